@@ -35,7 +35,8 @@ TC_ALL_ROWS_MAX_V = 131072
 EXPORTS = ("tail_create", "tail_run", "tail_run_ex", "tail_run_host", "tail_check", "tail_get_info",
            "tail_destroy", "tail_status_string", "tail_profile_enable", "tail_profile_read",
            "tail_set_wait_limit", "tail_debug_drop_stage", "tail_last_error", "tail_run_noalloc",
-           "tail_merge_shards", "tail_run_moe", "tail_tap_shape", "tail_run_taps", "tail_prepare_weight")
+           "tail_merge_shards", "tail_run_moe", "tail_tap_shape", "tail_run_taps", "tail_prepare_weight",
+           "tail_verify", "tail_verify_logits", "tail_verify_logits_workspace")
 KERNELS = ("rms_rows", "lm_head", "merge")
 
 
@@ -104,6 +105,13 @@ def lib(path: str | None = None):
         L.tail_run_noalloc.restype = ctypes.c_int
         L.tail_merge_shards.argtypes = [i32, i32, i32, i32, P, P, ctypes.POINTER(i32), P, i32, P, P, P, P]
         L.tail_merge_shards.restype = ctypes.c_int
+        i64 = ctypes.c_int64
+        L.tail_verify.argtypes = [i32, i32, i32, P, P, P, i32, P, P, P, P, i32, i64, i32, P, P, P]
+        L.tail_verify.restype = ctypes.c_int
+        L.tail_verify_logits_workspace.argtypes = [i32, i32, i32, ctypes.POINTER(i64)]
+        L.tail_verify_logits_workspace.restype = ctypes.c_int
+        L.tail_verify_logits.argtypes = [i32, i32, i32, P, i32, i64, P, P, P, P, P, P, i32, i64, P, i64, P, P, P]
+        L.tail_verify_logits.restype = ctypes.c_int
         L.tail_check.argtypes = [P]
         L.tail_check.restype = ctypes.c_int
         L.tail_get_info.argtypes = [P, ctypes.POINTER(tail_info)]
@@ -403,3 +411,6 @@ def merge_shards(cand_vals, cand_idx, shard_offsets, k, params=None, out_tokens=
     if rc != TAIL_OK:
         raise TailError(rc, "tail_merge_shards")
     return out_tokens
+
+
+from .speculative import verify, verify_logits, verify_logits_workspace  # noqa: E402,F401

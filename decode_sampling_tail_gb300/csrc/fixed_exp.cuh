@@ -1,0 +1,115 @@
+// Exponentials as fixed-point integers, for draws that have to be decided as in
+// 64-bit arithmetic.
+//
+// A draw compares u * sum(e) with running sums of e_i = exp((l_i - m) / T).  Over
+// a whole vocabulary an error of 2^-24 in the running sum moves 200,000
+// boundaries by more than some of them are wide, so one draw in a few hundred
+// would land on a neighbour.  FP64 is no way out (2 operations a clock and SM);
+// here e is formed in pairs of fp32 (a value and its rounding error, Dekker 1971)
+// with a relative error below 2^-36 and then rounded once to an integer multiple
+// of 2^-shift.  Integer sums are exact and do not depend on their order, so a
+// row can be split over any number of threads and CTAs and still give the same
+// bits.
+//
+// exp((l - m) / T) = 2^y, y = (l - m) * (log2 e / T) in a pair; the table-driven
+// method of Tang (1989): y = n + j / 32 + f, |f| <= 1 / 64, 2^y = 2^n * 2^(j/32)
+// * (1 + p(f)) with 2^(j/32) in a pair and p the Taylor series of 2^f - 1 to the
+// fifth power (next term below 2^-48), its linear term in a pair.
+#pragma once
+
+#include <stdint.h>
+
+namespace tail {
+
+constexpr int EXP_TABLE = 32;
+constexpr int EXP_MANT_BITS = 52;  // the significand below is an integer multiple of 2^-52
+
+// 2^(j / 32) = first + second, second the fp32 rounding of the remainder
+__device__ const float2 EXP2_TABLE[EXP_TABLE] = {
+    {0x1.000000p+0f, 0x0.0p+0f},       {0x1.059b0ep+0f, -0x1.9d4f52p-25f}, {0x1.0b5586p+0f, 0x1.9f3122p-25f},
+    {0x1.11301ep+0f, -0x1.fdb496p-25f}, {0x1.172b84p+0f, -0x1.c15742p-27f}, {0x1.1d4874p+0f, -0x1.d2e8cap-25f},
+    {0x1.2387a6p+0f, 0x1.ceac48p-25f},  {0x1.29e9e0p+0f, -0x1.5c0424p-25f}, {0x1.306fe0p+0f, 0x1.4636e2p-25f},
+    {0x1.371a74p+0f, -0x1.18aac6p-25f}, {0x1.3dea64p+0f, 0x1.824684p-25f},  {0x1.44e086p+0f, 0x1.8624b4p-30f},
+    {0x1.4bfdaep+0f, -0x1.593abcp-25f}, {0x1.5342b6p+0f, -0x1.2c5610p-25f}, {0x1.5ab07ep+0f, -0x1.5bd5ecp-27f},
+    {0x1.6247ecp+0f, -0x1.f8b550p-25f}, {0x1.6a09e6p+0f, 0x1.9fcef4p-26f},  {0x1.71f75ep+0f, 0x1.1d8beep-25f},
+    {0x1.7a1148p+0f, -0x1.829fd0p-25f}, {0x1.82589ap+0f, -0x1.accc7cp-26f}, {0x1.8ace54p+0f, 0x1.15506ep-27f},
+    {0x1.93737cp+0f, -0x1.e64744p-25f}, {0x1.9c4918p+0f, 0x1.51f848p-27f},  {0x1.a5503cp+0f, -0x1.b83b54p-25f},
+    {0x1.ae89fap+0f, -0x1.a94b14p-26f}, {0x1.b7f770p+0f, -0x1.a09438p-25f}, {0x1.c199bep+0f, -0x1.3d56b2p-27f},
+    {0x1.cb720ep+0f, -0x1.8837ccp-27f}, {0x1.d5818ep+0f, -0x1.822dbcp-27f}, {0x1.dfc974p+0f, -0x1.908c94p-25f},
+    {0x1.ea4afap+0f, 0x1.52486cp-27f},  {0x1.f50766p+0f, -0x1.246eb0p-26f},
+};
+
+// log2(e) / T as a pair (one fp64 division a row).
+struct ExpScale {
+  float h, l;
+};
+__device__ __forceinline__ ExpScale exp_scale(float temp) {
+  const double c = 1.4426950408889634 / static_cast<double>(temp);
+  ExpScale s;
+  s.h = static_cast<float>(c);
+  s.l = isinf(s.h) ? 0.f : static_cast<float>(c - static_cast<double>(s.h));
+  return s;
+}
+
+// The significand of exp((l - m) / T) in units of 2^-52 (below 2^54) and its
+// binary exponent n <= 0: the value is mant * 2^(n - 52).  mant = 0 stands for
+// anything below 2^-60, for l = -inf and for NaN.  l == m gives exactly 1, also
+// when both are infinite.  `table` is EXP2_TABLE, in shared memory.
+__device__ __forceinline__ int64_t exp_mant(float l, float m, ExpScale c, const float2* table, int& n) {
+  n = 0;
+  if (l == m) return int64_t(1) << EXP_MANT_BITS;
+  const float d = l - m;  // with its rounding error: Knuth's two-sum
+  const float dl = d - l;
+  const float err = (l - (d - dl)) + (-m - dl);
+  const float yh = d * c.h;
+  if (!(yh >= -60.0f)) return 0;
+  const float yl = fmaf(d, c.h, -yh) + fmaf(d, c.l, err * c.h);
+  const int k = __float2int_rn(yh * 32.0f);
+  n = k >> 5;
+  const float2 t = table[k & 31];
+  const float f0 = fmaf(static_cast<float>(k), -0.03125f, yh);  // exact
+  const float fh = f0 + yl;
+  const float fl = (f0 - fh) + yl;
+  // 2^f - 1 = f ln 2 + f^2 (ln^2 2 / 2! + f ln^3 2 / 3! + ...)
+  constexpr float L1H = 0x1.62e430p-1f, L1L = -0x1.05c610p-29f;
+  const float a = fh * L1H;
+  const float b = fmaf(fh, L1H, -a) + fmaf(fh, L1L, fl * L1H);
+  float q = fmaf(fh, 0x1.5d87fep-10f, 0x1.3b2ab6p-7f);
+  q = fmaf(fh, q, 0x1.c6b08ep-5f);
+  q = fmaf(fh, q, 0x1.ebfbe0p-3f);
+  const float s = fmaf(fh * fh, q, b);
+  const float g = t.x * a;
+  const float rest = fmaf(t.x, s, fmaf(t.x, a, -g)) + fmaf(t.y, a, t.y);
+  const float e0 = t.x + g;
+  const float e1 = ((t.x - e0) + g) + rest;
+  const float eh = e0 + e1;
+  const float el = (e0 - eh) + e1;
+  // eh is in [0.98, 2): a multiple of 2^-24; |el| <= 2^-24
+  return (static_cast<int64_t>(__float2int_rn(eh * 16777216.0f)) << (EXP_MANT_BITS - 24)) +
+         __float2int_rn(el * 4503599627370496.0f);
+}
+
+// exp((l - m) / T) rounded to a multiple of 2^-shift, shift <= 52.
+__device__ __forceinline__ int64_t exp_fixed(float l, float m, ExpScale c, const float2* table, int shift) {
+  int n;
+  const int64_t mant = exp_mant(l, m, c, table, n);
+  const int r = EXP_MANT_BITS - shift - n;  // bits to drop
+  if (r > 56) return 0;                     // below half a step: mant < 2^54
+  return r > 0 ? (mant + (int64_t(1) << (r - 1))) >> r : mant;
+}
+
+// exp((l - m) / T) as fp64 (a few values a row).
+__device__ __forceinline__ double exp_double(float l, float m, ExpScale c, const float2* table) {
+  int n;
+  const int64_t mant = exp_mant(l, m, c, table, n);
+  return ldexp(static_cast<double>(mant), n - EXP_MANT_BITS);
+}
+
+// q * (zh + zl) rounded to a multiple of 2^-shift (q * z < 2^(62 - shift)).
+__device__ __forceinline__ int64_t prod_fixed(float q, float zh, float zl, float scale) {
+  const float h = q * zh;
+  const float l = fmaf(q, zh, -h) + q * zl;
+  return __float2ll_rn(h * scale) + __float2ll_rn(l * scale);
+}
+
+}  // namespace tail

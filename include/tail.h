@@ -363,6 +363,76 @@ int tail_merge_shards(int32_t nshard, int32_t k_in, int32_t k, int32_t gbs, cons
                       int32_t* out_topk_idx_opt, void* stream);
 
 /*
+ * Verification of drafted tokens (speculative decoding): which of a sequence's
+ * drafts stand against the tail's own distribution, and the token that follows
+ * them.  The page has no counterpart; the target distribution is that of its
+ * `sampling_params`.
+ *
+ * A sequence with d drafts has d + 1 consecutive rows: row j's logits predict the
+ * position of draft j, the last row the position after all of them.  With P_j the
+ * target distribution of row j and q_j the draft model's:
+ *   draft x_j is accepted iff u_accept[j] * q_j(x_j) < P_j(x_j) and every draft
+ *   before it was (P_j(x_j) = 0 for a token outside P_j's support or the vocabulary);
+ *   at the first refused row the token is the smallest candidate i, in the order of
+ *   the list (tail_verify) or of the vocabulary (tail_verify_logits), with
+ *   u * sum(r) < r_0 + .. + r_i, r = max(P_j - q_j, 0), or r = P_j where that is zero
+ *   everywhere; after d accepted drafts it is drawn from P_d in the same way.
+ * Tokens so emitted are distributed as draws from P.
+ *
+ *   rows           rows of the call (row-indexed arrays have that many); 0 allowed.
+ *   nseq           sequences; 0 is a no-op.
+ *   cu_rows        [nseq + 1] int32 (device): sequence s has the rows
+ *                  [cu_rows[s], cu_rows[s + 1]), non-decreasing, at most rows.  An empty
+ *                  sequence gets a count of 0.  Rows behind the last sequence are not
+ *                  read and keep what out_tokens holds.  (Values outside [0, rows] are cut.)
+ *   drafts         [rows] int32: the drafted token of each row; a sequence's last entry is
+ *                  not used.  Any value is allowed (-1 marks a slot without a draft: refused).
+ *   u_accept       [rows] fp32 uniforms in [0, 1) of the acceptance tests.
+ *   draft_probs_opt [rows][draft_ld] q_j of draft_dtype (tail_dtype), V columns, or NULL:
+ *                  the drafts are certain (q_j is 1 at x_j).  Values count as cut to [0, 1].
+ *   out_tokens     [rows] int32: per sequence the accepted drafts, the token, then -1.
+ *   out_count      [nseq] int32: tokens emitted (accepted drafts + 1).
+ * A row whose every candidate is -inf has nothing to draw from: its draft is refused
+ * and its token is -1 (counted).  A candidate at -inf has probability 0; among logits
+ * of +inf the mass is shared.  NaN is outside the domain.  Decisions and draws are
+ * made with weights of 2^-36 relative error and exact sums, so they agree with 64-bit
+ * arithmetic except where u lies within about 2^-36 of a boundary; they do not depend
+ * on the batch.  No handle and no allocation; the current device and `stream`.
+ */
+
+/*
+ * Against the tail's sorted top-k: P_j is the sampler's distribution of the row (its
+ * top_k and top_p cuts, temperature; greedy rows put 1 on the first candidate).
+ *   topk_vals, topk_idx  [rows][k] as tail_run_ex and tail_merge_shards write them, 1 <= k <= 1024.
+ *   params, n_param_cols [rows][3 or 4] as in tail_run; the fourth column (0.5 when absent)
+ *                  is the draw's u.
+ *   V              columns of draft_probs_opt (not used without it).
+ * One launch.
+ */
+int tail_verify(int32_t rows, int32_t nseq, int32_t k, const float* topk_vals, const int32_t* topk_idx,
+                const float* params, int32_t n_param_cols, const int32_t* cu_rows, const int32_t* drafts,
+                const float* u_accept, const void* draft_probs_opt, int32_t draft_dtype, int64_t draft_ld,
+                int32_t V, int32_t* out_tokens, int32_t* out_count, void* stream);
+
+/*
+ * Against the whole vocabulary: P_j = softmax(logits_j / temperature_j), or 1 at the lowest
+ * index of the maximum when temperature_j <= 0 or NaN.
+ *   logits         [rows][logits_ld] of logits_dtype (tail_dtype), V columns, aligned to its
+ *                  element; whole 16-byte vectors are read where rows allow.  (out_logits_opt of
+ *                  tail_run is such an array.)
+ *   temperature, u_draw  [rows] fp32.
+ *   workspace      device memory of tail_verify_logits_workspace(rows, nseq, V) bytes, 16-byte
+ *                  aligned, any contents; calls that may overlap need one each.
+ * Two launches.  Limits: V <= 1048576, rows and nseq <= 65535 (TAIL_ERR_UNSUPPORTED beyond).
+ */
+int tail_verify_logits_workspace(int32_t rows, int32_t nseq, int32_t V, int64_t* bytes);
+int tail_verify_logits(int32_t rows, int32_t nseq, int32_t V, const void* logits, int32_t logits_dtype,
+                       int64_t logits_ld, const float* temperature, const int32_t* cu_rows, const int32_t* drafts,
+                       const float* u_accept, const float* u_draw, const void* draft_probs_opt,
+                       int32_t draft_dtype, int64_t draft_ld, void* workspace, int64_t workspace_bytes,
+                       int32_t* out_tokens, int32_t* out_count, void* stream);
+
+/*
  * The calls below are the library's own plumbing (error reporting, timing, the
  * bound on device waits, a test hook, static facts, lifetime); no page defines
  * them.
