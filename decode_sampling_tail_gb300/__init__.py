@@ -19,7 +19,7 @@ import threading
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtail.so")
 
-TAIL_F32, TAIL_F16, TAIL_BF16 = 0, 1, 2
+TAIL_F32, TAIL_F16, TAIL_BF16, TAIL_MXFP4 = 0, 1, 2, 3
 TAIL_OK = 0
 TAIL_ERR_INVALID_ARG = -1
 TAIL_ERR_UNSUPPORTED = -2
@@ -36,7 +36,8 @@ EXPORTS = ("tail_create", "tail_run", "tail_run_ex", "tail_run_host", "tail_chec
            "tail_destroy", "tail_status_string", "tail_profile_enable", "tail_profile_read",
            "tail_set_wait_limit", "tail_debug_drop_stage", "tail_last_error", "tail_run_noalloc",
            "tail_merge_shards", "tail_run_moe", "tail_tap_shape", "tail_run_taps", "tail_prepare_weight",
-           "tail_verify", "tail_verify_logits", "tail_verify_logits_workspace")
+           "tail_verify", "tail_verify_logits", "tail_verify_logits_workspace",
+           "tail_moe_create", "tail_moe_run", "tail_moe_get_info", "tail_moe_destroy")
 KERNELS = ("rms_rows", "lm_head", "merge")
 
 
@@ -68,6 +69,14 @@ class tail_info(ctypes.Structure):
                 ("lmhead_path", ctypes.c_int32), ("rows_per_pass", ctypes.c_int32),
                 ("kernels_per_run", ctypes.c_int32), ("scratch_bytes", ctypes.c_int64),
                 ("tc_min_rows", ctypes.c_int32)]
+
+
+class tail_moe_config(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int32), ("I", ctypes.c_int32), ("E", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("n_shared", ctypes.c_int32), ("t_max", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("weight_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("act_alpha", ctypes.c_float),
+                ("act_beta", ctypes.c_float), ("act_limit", ctypes.c_float), ("interleaved", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("route_scale", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -112,6 +121,14 @@ def lib(path: str | None = None):
         L.tail_verify_logits_workspace.restype = ctypes.c_int
         L.tail_verify_logits.argtypes = [i32, i32, i32, P, i32, i64, P, P, P, P, P, P, i32, i64, P, i64, P, P, P]
         L.tail_verify_logits.restype = ctypes.c_int
+        L.tail_moe_create.argtypes = [ctypes.POINTER(tail_moe_config), ctypes.c_int, ctypes.POINTER(P)]
+        L.tail_moe_create.restype = ctypes.c_int
+        L.tail_moe_run.argtypes = [P, P, P, P, P, P, P, P, P, P, P, i32, P, P, P, P, P]
+        L.tail_moe_run.restype = ctypes.c_int
+        L.tail_moe_get_info.argtypes = [P, ctypes.POINTER(i64)]
+        L.tail_moe_get_info.restype = ctypes.c_int
+        L.tail_moe_destroy.argtypes = [P]
+        L.tail_moe_destroy.restype = None
         L.tail_check.argtypes = [P]
         L.tail_check.restype = ctypes.c_int
         L.tail_get_info.argtypes = [P, ctypes.POINTER(tail_info)]
@@ -414,3 +431,4 @@ def merge_shards(cand_vals, cand_idx, shard_offsets, k, params=None, out_tokens=
 
 
 from .speculative import verify, verify_logits, verify_logits_workspace  # noqa: E402,F401
+from .moe_layer import Moe  # noqa: E402,F401

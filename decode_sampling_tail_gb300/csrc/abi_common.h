@@ -21,6 +21,19 @@ inline int elem_bytes(int dtype) { return dtype == TAIL_F32 ? 4 : 2; }
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Makes a device current for a scope; the caller's comes back at its end.
+struct DeviceGuard {
+  int prev = -1;
+  bool ok = false;
+  explicit DeviceGuard(int dev) {
+    if (cudaGetDevice(&prev) != cudaSuccess) return;
+    ok = cudaSetDevice(dev) == cudaSuccess;
+  }
+  ~DeviceGuard() {
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+};
+
 // Vocabulary slabs (= lm_head CTAs): one per SM, at least 8 column pairs
 // (128 columns) per slab, at most `max_slabs`.
 inline int slab_count(int64_t npairs, int num_sms, int max_slabs) {

@@ -1,0 +1,209 @@
+// Entry points of the mixture-of-experts layer: handle lifetime, argument checks,
+// scratch and the launch sequence (router, experts, combine).
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <new>
+
+#include "../../include/tail.h"
+#include "abi_common.h"
+#include "moe_internal.h"
+#include "moe_layer.cuh"
+#include "moe_layer_internal.h"
+
+using namespace tail;
+
+struct tail_moe_s {
+  tail_moe_config cfg;
+  int device;
+  int num_sms;
+  int max_smem;
+  int S, N1, n_all;
+  uint8_t* scratch;
+  int64_t scratch_bytes;
+  // within scratch
+  float* logits;
+  float2* stats;
+  float* act;
+  uint32_t* amax;
+  float* slots;
+  float* slot_w;
+};
+
+namespace {
+
+bool valid(const tail_moe_config* c) {
+  if (!c) return false;
+  if (c->H < 1 || c->I < 1 || c->E < 1 || c->topk < 1 || c->topk > c->E || c->n_shared < 0) return false;
+  if (c->t_max < 1 || !(c->eps >= 0.0f)) return false;
+  if (c->weight_dtype != TAIL_BF16 && c->weight_dtype != TAIL_MXFP4) return false;
+  if (c->act != TAIL_MOE_GLU && c->act != TAIL_MOE_RELU2) return false;
+  if (c->score != TAIL_MOE_SOFTMAX && c->score != TAIL_MOE_SIGMOID) return false;
+  if (!(c->act_limit >= 0.0f) || c->act_alpha != c->act_alpha || c->act_beta != c->act_beta) return false;
+  return c->route_scale == c->route_scale;
+}
+
+bool supported(const tail_moe_config* c) {
+  const int m = c->weight_dtype == TAIL_MXFP4 ? 32 : 16;
+  return c->H % m == 0 && c->I % m == 0 && c->H <= ML_MAX_DIM && c->I <= ML_MAX_DIM && c->topk <= ML_MAX_TOPK &&
+         c->n_shared <= ML_MAX_SHARED && c->E <= ML_MAX_EXPERTS - c->n_shared && c->t_max <= ML_MAX_T;
+}
+
+int64_t round256(int64_t v) { return (v + 255) & ~int64_t(255); }
+
+// Whether two byte ranges meet.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uint8_t* x = static_cast<const uint8_t*>(a);
+  const uint8_t* y = static_cast<const uint8_t*>(b);
+  return x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+extern "C" {
+
+int tail_moe_create(const tail_moe_config* cfg, int device, tail_moe_t** out) {
+  if (!out) return TAIL_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!valid(cfg)) return TAIL_ERR_INVALID_ARG;
+  if (!supported(cfg)) {
+    set_last_error("tail_moe_create: H and I multiples of 16 (mxfp4: 32) up to 16384, E + n_shared <= 512, "
+                   "topk <= 16, n_shared <= 8, t_max <= 64");
+    return TAIL_ERR_UNSUPPORTED;
+  }
+  int ndev = 0;
+  if (cudaGetDeviceCount(&ndev) != cudaSuccess || device < 0 || device >= ndev) return TAIL_ERR_INVALID_ARG;
+  DeviceGuard guard(device);
+  if (!guard.ok) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
+  cudaDeviceProp prop;
+  cudaError_t e = cudaGetDeviceProperties(&prop, device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDeviceProperties");
+  if (prop.major != 10 || prop.minor != 3) {
+    set_last_error("tail_moe_create: built for sm_103a only");
+    return TAIL_ERR_UNSUPPORTED;
+  }
+  tail_moe_t* m = new (std::nothrow) tail_moe_t();
+  if (!m) return TAIL_ERR_OOM;
+  memset(m, 0, sizeof(*m));
+  m->cfg = *cfg;
+  m->device = device;
+  m->num_sms = prop.multiProcessorCount;
+  m->max_smem = static_cast<int>(prop.sharedMemPerBlockOptin);
+  m->S = cfg->topk + cfg->n_shared;
+  m->N1 = cfg->act == TAIL_MOE_GLU ? 2 * cfg->I : cfg->I;
+  m->n_all = cfg->E + cfg->n_shared;
+  const int64_t T = cfg->t_max, pairs = T * m->S;
+  const int64_t sizes[] = {T * cfg->E * 4, T * 8, pairs * cfg->I * 4, pairs * 4, pairs * cfg->H * 4, pairs * 4};
+  for (int64_t n : sizes) m->scratch_bytes += round256(n);
+  e = cudaMalloc(reinterpret_cast<void**>(&m->scratch), static_cast<size_t>(m->scratch_bytes));
+  if (e != cudaSuccess) {
+    delete m;
+    return cuda_fail(e, "tail_moe_create: scratch allocation");
+  }
+  uint8_t* p = m->scratch;
+  m->logits = reinterpret_cast<float*>(p);
+  m->stats = reinterpret_cast<float2*>(p += round256(sizes[0]));
+  m->act = reinterpret_cast<float*>(p += round256(sizes[1]));
+  m->amax = reinterpret_cast<uint32_t*>(p += round256(sizes[2]));
+  m->slots = reinterpret_cast<float*>(p += round256(sizes[3]));
+  m->slot_w = reinterpret_cast<float*>(p += round256(sizes[4]));
+  *out = m;
+  return TAIL_OK;
+}
+
+int tail_moe_run(tail_moe_t* m, const uint16_t* x, const float* gamma_opt, const uint16_t* router_w,
+                 const float* router_bias_opt, const void* w1, const uint8_t* w1_scale, const float* b1_opt,
+                 const void* w2, const uint8_t* w2_scale, const float* b2_opt, int32_t n_tokens,
+                 uint16_t* out_hidden_opt, float* out_slots_opt, float* out_slot_w_opt, int32_t* out_ids_opt,
+                 void* stream) {
+  if (!m || n_tokens < 0 || n_tokens > m->cfg.t_max) return TAIL_ERR_INVALID_ARG;
+  if (n_tokens == 0) return TAIL_OK;
+  const tail_moe_config& c = m->cfg;
+  const bool fp4 = c.weight_dtype == TAIL_MXFP4;
+  if (!x || !router_w || !w1 || !w2 || (fp4 && (!w1_scale || !w2_scale))) return TAIL_ERR_INVALID_ARG;
+  if (!out_hidden_opt && !out_slots_opt) return TAIL_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(router_w, 16) || !aligned(gamma_opt, 16) || !aligned(w1, 32) || !aligned(w2, 32))
+    return TAIL_ERR_INVALID_ARG;
+  if (!aligned(router_bias_opt, 4) || !aligned(b1_opt, 4) || !aligned(b2_opt, 4) || !aligned(out_hidden_opt, 16) ||
+      !aligned(out_slots_opt, 16) || !aligned(out_slot_w_opt, 4) || !aligned(out_ids_opt, 4))
+    return TAIL_ERR_INVALID_ARG;
+  // x is read again when the slots are combined: h in place of x is an element-wise replacement and
+  // allowed, any other overlap is not
+  const int64_t xb = static_cast<int64_t>(n_tokens) * c.H * 2;
+  if (out_hidden_opt && out_hidden_opt != x && overlap(out_hidden_opt, xb, x, xb)) return TAIL_ERR_INVALID_ARG;
+  DeviceGuard guard(m->device);
+  if (!guard.ok) return TAIL_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const MoeLayerPlan plan = plan_moe_layer(n_tokens, m->S, c.H, c.I, fp4, m->max_smem, m->num_sms);
+  if (!plan.ok) return TAIL_ERR_UNSUPPORTED;  // not reached within the limits of create
+  MoeLayerArgs a;
+  a.x = x;
+  a.gamma = gamma_opt;
+  a.wr = router_w;
+  a.br = router_bias_opt;
+  a.w1 = static_cast<const uint8_t*>(w1);
+  a.s1 = w1_scale;
+  a.b1 = b1_opt;
+  a.w2 = static_cast<const uint8_t*>(w2);
+  a.s2 = w2_scale;
+  a.b2 = b2_opt;
+  a.logits = m->logits;
+  a.stats = m->stats;
+  a.act = m->act;
+  a.amax = m->amax;
+  a.slots = out_slots_opt ? out_slots_opt : m->slots;
+  a.slot_w = out_slot_w_opt ? out_slot_w_opt : m->slot_w;
+  a.ids = out_ids_opt;
+  a.T = n_tokens;
+  a.H = c.H;
+  a.I = c.I;
+  a.N1 = m->N1;
+  a.E = c.E;
+  a.topk = c.topk;
+  a.nsh = c.n_shared;
+  a.S = m->S;
+  a.gated = c.act == TAIL_MOE_GLU;
+  a.interleaved = c.interleaved ? 1 : 0;
+  a.score = c.score == TAIL_MOE_SIGMOID;
+  a.alpha = c.act_alpha;
+  a.beta = c.act_beta;
+  a.limit = c.act_limit;
+  a.route_scale = c.route_scale;
+  a.eps = c.eps;
+  a.G = plan.G;
+  cudaError_t e = launch_moe_layer(a, plan, fp4, s);
+  if (e != cudaSuccess) return cuda_fail(e, "tail_moe_run: kernel launch");
+  if (out_hidden_opt) {
+    MoeIn in;
+    in.x = x;
+    in.slots = a.slots;
+    in.slot_dtype = 0;
+    in.w = a.slot_w;
+    in.S = m->S;
+    in.n_routed = c.topk;
+    in.h_out = out_hidden_opt;
+    e = launch_moe_combine(in, n_tokens, c.H, s, false);
+    if (e != cudaSuccess) return cuda_fail(e, "tail_moe_run: kernel launch (combine)");
+  }
+  return TAIL_OK;
+}
+
+int tail_moe_get_info(const tail_moe_t* m, int64_t* scratch_bytes) {
+  if (!m || !scratch_bytes) return TAIL_ERR_INVALID_ARG;
+  *scratch_bytes = m->scratch_bytes;
+  return TAIL_OK;
+}
+
+void tail_moe_destroy(tail_moe_t* m) {
+  if (!m) return;
+  DeviceGuard guard(m->device);
+  if (guard.ok) {
+    cudaDeviceSynchronize();
+    cudaFree(m->scratch);
+    cudaGetLastError();
+  }
+  delete m;
+}
+
+}  // extern "C"

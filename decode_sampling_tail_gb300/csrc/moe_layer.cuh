@@ -1,0 +1,254 @@
+// A mixture-of-experts layer for a few tokens: arguments and device pieces
+// (moe_layer.cu holds the kernels, moe_api.cu the entry points).
+//
+//   t = x * rsqrt(mean(x^2) + eps) * gamma
+//   z = Wr t + br;  the topk experts of largest score, and the shared ones
+//   a = act(W1[e] t + b1[e]);  y[slot] = W2[e] a + b2[e]
+//   h = bf16(x + bf16(sum of routed w y + sum of shared y))   (moe.cuh)
+//
+// A few tokens select a few experts each, so the layer is a stream of weights:
+// every selected expert's W1 and W2 once.  The matrix products run on mma.sync
+// with 16 weight rows as the M side and up to 8 tokens as the N side; for so few
+// columns the tensor pipe idles either way, and registers fed straight from
+// global memory need no staging.
+//
+// Weight fragments.  A lane (g = lane / 4, q = lane % 4) of an m16n8k16 product
+// holds k slots {2q, 2q+1, 2q+8, 2q+9} of rows g and g + 8.  A sum does not mind
+// the order of k, so lane q takes 16 consecutive bf16 (32 bytes; 32 consecutive
+// 4-bit values, one scale block) of each of its rows and feeds them as the
+// slots of 4 (8) products; its activations are the same 16 (32) columns.  One
+// load instruction then covers whole 128-byte (64-byte) lines of 8 rows, and
+// nothing is shuffled.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace tail {
+
+constexpr int ML_THREADS = 512;
+constexpr int ML_WARPS = ML_THREADS / 32;
+constexpr int ML_MAX_T = 64;
+constexpr int ML_MAX_EXPERTS = 512;  // routed and shared together: one thread each when the plan is made
+constexpr int ML_MAX_TOPK = 16;
+constexpr int ML_MAX_SHARED = 8;
+constexpr int ML_MAX_DIM = 16384;
+
+struct MoeLayerArgs {
+  const uint16_t* x;      // [T][H] bf16
+  const float* gamma;     // [H] or null: x is used as it is
+  const uint16_t* wr;     // [E][H] bf16
+  const float* br;        // [E] or null
+  const uint8_t* w1;      // [n][N1][H]
+  const uint8_t* s1;      // [n][N1][H / 32] scales, or null
+  const float* b1;        // [n][N1] or null
+  const uint8_t* w2;      // [n][H][I]
+  const uint8_t* s2;
+  const float* b2;        // [n][H] or null
+  float* logits;          // [T][E]
+  float2* stats;          // [T] 1 / rms and the largest |t|
+  float* act;             // [T * S][I]
+  uint32_t* amax;         // [T * S] largest |a|, as bits
+  float* slots;           // [T * S][H]
+  float* slot_w;          // [T][S]
+  int32_t* ids;           // [T][S] or null
+  int T, H, I, N1, E, topk, nsh, S;
+  int gated, interleaved, score;
+  float alpha, beta, limit, route_scale, eps;
+  int G;                  // tokens of one expert that share a pass over its weights
+};
+
+// ---------------------------------------------------------------- loads
+__device__ __forceinline__ void ldg_stream(const uint8_t* p, uint32_t (&v)[8]) {
+  uint64_t a, b, c, d;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.b64 {%0,%1,%2,%3}, [%4];"
+               : "=l"(a), "=l"(b), "=l"(c), "=l"(d)
+               : "l"(p));
+  v[0] = static_cast<uint32_t>(a), v[1] = static_cast<uint32_t>(a >> 32);
+  v[2] = static_cast<uint32_t>(b), v[3] = static_cast<uint32_t>(b >> 32);
+  v[4] = static_cast<uint32_t>(c), v[5] = static_cast<uint32_t>(c >> 32);
+  v[6] = static_cast<uint32_t>(d), v[7] = static_cast<uint32_t>(d >> 32);
+}
+__device__ __forceinline__ void ldg_stream(const uint8_t* p, uint32_t (&v)[4]) {
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "l"(p));
+}
+
+// D (16x8 fp32) += A (16x16 fp16, row) * B (16x8 fp16, col)
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Eight 4-bit values (e2m1, low nibble first) times the scale pair: four fp16 pairs.
+__device__ __forceinline__ void fp4_to_half(uint32_t w, uint32_t scale, uint32_t (&h)[4]) {
+  asm("{\n.reg .b8 a, b, c, d;\n"
+      "mov.b32 {a, b, c, d}, %4;\n"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 v = __hmul2(reinterpret_cast<const __half2&>(h[i]), reinterpret_cast<const __half2&>(scale));
+    h[i] = reinterpret_cast<const uint32_t&>(v);
+  }
+}
+
+// 2^(s - ref) as an fp16 pair for s <= ref; 0 below the smallest subnormal.
+__device__ __forceinline__ uint32_t half_pow2(int s, int ref) {
+  const int d = s - ref;
+  const uint32_t b = d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
+  return b | (b << 16);
+}
+
+// 2^(s - 127) of an e8m0 scale; 255 is NaN.
+__device__ __forceinline__ float e8m0(int s) {
+  return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7fc00000u : static_cast<uint32_t>(s) << 23);
+}
+
+// The power of two that brings amax into [2^12, 2^13), as the biased exponent of an fp32; 127 (one)
+// for an amax that is not finite.  Its inverse has the exponent 254 - e.
+__device__ __forceinline__ int scale_exponent(uint32_t amax_bits) {
+  const int e = static_cast<int>(amax_bits >> 23);
+  return e >= 255 ? 127 : min(266 - e, 253);
+}
+__device__ __forceinline__ float pow2_field(int e) { return __uint_as_float(static_cast<uint32_t>(e) << 23); }
+
+// ---------------------------------------------------------------- plan
+// Which experts run, on which tokens: made by every CTA from the router's logits
+// (the same integers in each), kept in shared memory.
+struct MoePlan {
+  uint16_t* pair_e;  // [pairs padded to 8] expert of pair t * S + s
+  uint16_t* list;    // [pairs] pairs ordered by expert, then token
+  uint32_t* unit;    // [<= pairs] expert | first list entry << 10 | entries << 21: one pass over an expert
+  uint32_t* cnt;     // [ML_MAX_EXPERTS]
+  uint32_t* red;     // [ML_WARPS + 1]
+  int nunits;
+};
+__host__ __device__ inline int plan_bytes(int pairs) {
+  const int p8 = (pairs + 7) & ~7;
+  return p8 * 2 * 2 + p8 * 4 + ML_MAX_EXPERTS * 4 + (ML_WARPS + 4) * 4;
+}
+__device__ __forceinline__ int unit_expert(uint32_t u) { return u & 1023; }
+__device__ __forceinline__ int unit_first(uint32_t u) { return (u >> 10) & 2047; }
+__device__ __forceinline__ int unit_size(uint32_t u) { return u >> 21; }
+
+// One warp: token t's experts and weights.
+__device__ __forceinline__ void route_token(const MoeLayerArgs& a, int t, uint16_t* pair_e, bool write) {
+  const int lane = threadIdx.x & 31;
+  const float* z = a.logits + static_cast<int64_t>(t) * a.E;
+  constexpr int PER = ML_MAX_EXPERTS / 32;
+  uint32_t key[PER];
+  // softmax: z with its bias ranks and weighs; sigmoid: sigmoid(z) weighs, plus the bias ranks
+  auto score = [&](float v) { return a.score ? 1.0f / (1.0f + expf(-v)) : v; };
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = i * 32 + lane;
+    key[i] = 0u;
+    if (e < a.E) {
+      const float v = __ldcg(z + e);
+      key[i] = float_key(a.br ? score(v) + a.br[e] : v);
+    }
+  }
+  float w = 0.f;
+  int mine = 0;
+  for (int j = 0; j < a.topk; ++j) {
+    uint64_t best = 0ull;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const uint64_t c = (static_cast<uint64_t>(key[i]) << 32) | static_cast<uint32_t>(~(i * 32 + lane));
+      if (i * 32 + lane < a.E && key[i] != 0u && c > best) best = c;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const uint64_t c = __shfl_xor_sync(0xffffffffu, best, o);
+      best = c > best ? c : best;
+    }
+    const int e = static_cast<int>(~static_cast<uint32_t>(best)) & (ML_MAX_EXPERTS - 1);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i * 32 + lane == e) key[i] = 0u;
+    if (lane == j) {
+      mine = e;
+      const float v = __ldcg(z + e);
+      w = a.score ? score(v) : v + (a.br ? a.br[e] : 0.f);
+    }
+  }
+  if (lane < a.topk) pair_e[t * a.S + lane] = static_cast<uint16_t>(mine);
+  if (lane < a.nsh) pair_e[t * a.S + a.topk + lane] = static_cast<uint16_t>(a.E + lane);
+  if (!write) return;
+  if (!a.score) {  // the first is the largest
+    const float top = __shfl_sync(0xffffffffu, w, 0);
+    w = lane < a.topk ? expf(w - top) : 0.f;
+  } else if (lane >= a.topk) {
+    w = 0.f;
+  }
+  float sum = w;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane < a.topk) a.slot_w[t * a.S + lane] = a.route_scale * w / sum;
+  if (lane < a.nsh) a.slot_w[t * a.S + a.topk + lane] = 1.0f;
+  if (a.ids) {
+    if (lane < a.topk) a.ids[t * a.S + lane] = mine;
+    if (lane < a.nsh) a.ids[t * a.S + a.topk + lane] = a.E + lane;
+  }
+}
+
+// The whole CTA.
+__device__ __forceinline__ void make_plan(const MoeLayerArgs& a, MoePlan& p, bool write) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int pairs = a.T * a.S, p8 = (pairs + 7) & ~7;
+  for (int t = warp; t < a.T; t += ML_WARPS) route_token(a, t, p.pair_e, write);
+  if (tid < 8 && pairs + tid < p8) p.pair_e[pairs + tid] = 0xffffu;
+  if (tid < ML_MAX_EXPERTS) p.cnt[tid] = 0u;
+  __syncthreads();
+  for (int i = tid; i < pairs; i += ML_THREADS) atomicAdd(&p.cnt[p.pair_e[i]], 1u);
+  __syncthreads();
+  // exclusive sums of the pairs (low half) and the units (high half) before each expert
+  const uint32_t n = p.cnt[tid];
+  const uint32_t units = (n + a.G - 1) / a.G;
+  uint32_t v = n | (units << 16), incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) p.red[warp] = incl;
+  __syncthreads();
+  uint32_t before = incl - v, total = 0u;
+  for (int w = 0; w < ML_WARPS; ++w) {
+    if (w < warp) before += p.red[w];
+    total += p.red[w];
+  }
+  if (n > 0u) {
+    int at = static_cast<int>(before & 0xffffu);
+    uint32_t u = before >> 16;
+    for (uint32_t f = 0; f < n; f += a.G, ++u)
+      p.unit[u] = static_cast<uint32_t>(tid) | ((at + f) << 10) | (min(n - f, static_cast<uint32_t>(a.G)) << 21);
+    for (int i = 0; i < p8; i += 8) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p.pair_e + i);
+      const uint32_t ws[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if ((ws[k] & 0xffffu) == static_cast<uint32_t>(tid)) p.list[at++] = static_cast<uint16_t>(i + 2 * k);
+        if ((ws[k] >> 16) == static_cast<uint32_t>(tid)) p.list[at++] = static_cast<uint16_t>(i + 2 * k + 1);
+      }
+    }
+  }
+  p.nunits = static_cast<int>(total >> 16);
+  __syncthreads();
+}
+
+}  // namespace tail

@@ -113,18 +113,6 @@ int validate_config(const tail_config* c) {
 
 namespace {
 
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = false;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) return;
-    ok = cudaSetDevice(dev) == cudaSuccess;
-  }
-  ~DeviceGuard() {
-    if (prev >= 0) cudaSetDevice(prev);
-  }
-};
-
 template <typename T>
 cudaError_t dalloc(T** p, size_t n, int64_t* total) {
   *p = nullptr;

@@ -1,0 +1,113 @@
+"""A mixture-of-experts layer for a few tokens on torch CUDA tensors (tail_moe_create, tail_moe_run).
+
+It forms the hidden state that the tail reads (``out_hidden``, for ``Tail.run``), or the slots and weights
+that ``Tail.run_moe`` combines inside its first kernel.  ``include/tail.h`` states the formulas.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import TAIL_BF16, TAIL_ERR_UNSUPPORTED, TAIL_MXFP4, TAIL_OK, TailError, _ptr, _stream_ptr, lib, tail_moe_config
+
+WEIGHTS = {"bf16": TAIL_BF16, "mxfp4": TAIL_MXFP4}
+ACTS = {"glu": 0, "relu2": 1}
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+class Moe:
+    """A layer handle bound to one device; the weights stay the caller's tensors.
+
+    ``w1`` is [n, N1, H] and ``w2`` [n, H, I] bfloat16 with n = E + n_shared and N1 = 2 I ("glu") or I ("relu2");
+    with ``weight_dtype="mxfp4"`` they are uint8 [n, N1, H / 2] and [n, H, I / 2] and ``w1_scale`` [n, N1, H / 32],
+    ``w2_scale`` [n, H, I / 32] uint8 hold the block exponents.  Runs of one handle share its scratch: one at a time.
+    """
+
+    def __init__(self, H: int, I: int, E: int, topk: int, t_max: int = 64, *, n_shared: int = 0, eps: float = 1e-5,
+                 weight_dtype: str = "bf16", act: str = "glu", act_alpha: float = 1.0, act_beta: float = 0.0,
+                 act_limit: float = 0.0, interleaved: bool = False, score: str = "softmax", route_scale: float = 1.0,
+                 device: int = 0):
+        self.h = None
+        self.cfg = tail_moe_config(H, I, E, topk, n_shared, t_max, eps, WEIGHTS[weight_dtype], ACTS[act], act_alpha,
+                                   act_beta, act_limit, int(interleaved), SCORES[score], route_scale)
+        self.device = device
+        h = ctypes.c_void_p()
+        rc = lib().tail_moe_create(ctypes.byref(self.cfg), device, ctypes.byref(h))
+        if rc == TAIL_ERR_UNSUPPORTED:
+            raise TailError(rc, "tail_moe_create [" + lib().tail_last_error().decode() + "]")
+        if rc != TAIL_OK:
+            raise TailError(rc, "tail_moe_create")
+        self.h = h.value
+
+    def close(self):
+        if self.h:
+            lib().tail_moe_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def _need(self, t, what, dtype, shape):
+        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device.type != "cuda" \
+                or t.device.index != self.device:
+            raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on cuda:{self.device}; got "
+                             f"{t.dtype}, {tuple(t.shape)}, strides {t.stride()}, {t.device}")
+
+    def run(self, x, gamma, router_w, w1, w2, *, router_bias=None, w1_scale=None, w2_scale=None, b1=None, b2=None,
+            out_hidden=None, out_slots=None, out_slot_w=None, out_ids=None, stream=None):
+        """One run over x [T, H] bfloat16 (tail_moe_run).  gamma [H] float32 or None (x is already normalised),
+        router_w [E, H] bfloat16, router_bias [E], b1 [n, N1], b2 [n, H] float32 or None.  Outputs: out_hidden
+        [T, H] bfloat16 (may be x), out_slots [T, S, H] and out_slot_w [T, S] float32, out_ids [T, S] int32 with
+        S = topk + n_shared; out_hidden is allocated when neither it nor out_slots is given.  Returns out_hidden."""
+        import torch
+        if not self.h:
+            raise ValueError("the handle is closed")
+        c = self.cfg
+        if x.dim() != 2 or not 0 <= int(x.shape[0]) <= c.t_max:
+            raise ValueError(f"x must be [T, {c.H}] with T <= {c.t_max}; got {tuple(x.shape)}")
+        T, H, I, E, n, S = int(x.shape[0]), c.H, c.I, c.E, c.E + c.n_shared, c.topk + c.n_shared
+        N1 = 2 * I if c.act == 0 else I
+        bf16, f32 = torch.bfloat16, torch.float32
+        self._need(x, "x", bf16, (T, H))
+        self._need(router_w, "router_w", bf16, (E, H))
+        if c.weight_dtype == TAIL_MXFP4:
+            if w1_scale is None or w2_scale is None:
+                raise ValueError("mxfp4 weights need w1_scale and w2_scale")
+            self._need(w1, "w1", torch.uint8, (n, N1, H // 2))
+            self._need(w2, "w2", torch.uint8, (n, H, I // 2))
+            self._need(w1_scale, "w1_scale", torch.uint8, (n, N1, H // 32))
+            self._need(w2_scale, "w2_scale", torch.uint8, (n, H, I // 32))
+        else:
+            if w1_scale is not None or w2_scale is not None:
+                raise ValueError("bf16 weights take no scales")
+            self._need(w1, "w1", bf16, (n, N1, H))
+            self._need(w2, "w2", bf16, (n, H, I))
+        for t, what, shape in ((gamma, "gamma", (H,)), (router_bias, "router_bias", (E,)), (b1, "b1", (n, N1)),
+                               (b2, "b2", (n, H)), (out_slots, "out_slots", (T, S, H)),
+                               (out_slot_w, "out_slot_w", (T, S))):
+            if t is not None:
+                self._need(t, what, f32, shape)
+        if out_ids is not None:
+            self._need(out_ids, "out_ids", torch.int32, (T, S))
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        if out_hidden is None and out_slots is None:
+            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), self.device)
+            with torch.cuda.stream(s):
+                out_hidden = torch.empty((T, H), dtype=bf16, device=x.device)
+        if out_hidden is not None:
+            self._need(out_hidden, "out_hidden", bf16, (T, H))
+        rc = lib().tail_moe_run(self.h, _ptr(x), _ptr(gamma), _ptr(router_w), _ptr(router_bias), _ptr(w1),
+                                _ptr(w1_scale), _ptr(b1), _ptr(w2), _ptr(w2_scale), _ptr(b2), T, _ptr(out_hidden),
+                                _ptr(out_slots), _ptr(out_slot_w), _ptr(out_ids), _stream_ptr(stream, x.device))
+        if rc != TAIL_OK:
+            raise TailError(rc, "tail_moe_run")
+        return out_hidden

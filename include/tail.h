@@ -45,8 +45,9 @@ extern "C" {
 
 typedef struct tail_s tail_t;
 
-/* Element type of `hidden` (parameter `hidden_states`: fp32, fp16 or bf16). */
-typedef enum { TAIL_F32 = 0, TAIL_F16 = 1, TAIL_BF16 = 2 } tail_dtype;
+/* Element type of `hidden` (parameter `hidden_states`: fp32, fp16 or bf16).  TAIL_MXFP4 is a weight
+   type of tail_moe_create alone. */
+typedef enum { TAIL_F32 = 0, TAIL_F16 = 1, TAIL_BF16 = 2, TAIL_MXFP4 = 3 } tail_dtype;
 
 typedef enum {
   TAIL_OK = 0,
@@ -431,6 +432,81 @@ int tail_verify_logits(int32_t rows, int32_t nseq, int32_t V, const void* logits
                        const float* u_accept, const float* u_draw, const void* draft_probs_opt,
                        int32_t draft_dtype, int64_t draft_ld, void* workspace, int64_t workspace_bytes,
                        int32_t* out_tokens, int32_t* out_count, void* stream);
+
+/*
+ * A mixture-of-experts layer for a few tokens: what forms the slots that tail_run_moe
+ * combines (same sources; the layer itself follows the public GPT-OSS and Nemotron
+ * definitions that the config's fields span).  For every token:
+ *   t = x * rsqrt(mean(x^2) + eps) * gamma          (gamma NULL: t = x)
+ *   z = router_w t
+ *   TAIL_MOE_SOFTMAX: the topk experts of largest z + bias, weights softmax over those;
+ *   TAIL_MOE_SIGMOID: the topk experts of largest sigmoid(z) + bias, weights sigmoid(z)
+ *     over their sum; both times route_scale.  Ties go to the lower index; slots are
+ *     in falling order of the score.  n_shared experts E, E + 1, .. follow with weight 1.
+ *   per slot: u = W1[e] t + b1[e];  y = W2[e] a + b2[e], with
+ *   TAIL_MOE_GLU   (W1 has 2 I rows): a = g * sigmoid(act_alpha * g) * (v + act_beta), gate
+ *                  row i at 2i and up row at 2i + 1 when interleaved, else at i and I + i; with
+ *                  act_limit > 0 first g = min(g, limit), v = clamp(v, -limit, limit);
+ *   TAIL_MOE_RELU2 (W1 has I rows): a = max(u, 0)^2.
+ *   h = bf16(x + bf16(r + sh)): the combine of tail_run_moe over these slots.
+ * (GPT-OSS: softmax, interleaved GLU with alpha 1.702, beta 1, limit 7; a SiLU-gated layer:
+ * alpha 1, beta 0, limit 0; Nemotron: sigmoid with bias, RELU2, 2 shared experts.)
+ * Selected experts' weights are read once for up to 16 tokens (fewer when H or I is above
+ * about 3000); products and sums are fp32, with activations carried as two 16-bit parts.
+ */
+typedef enum { TAIL_MOE_GLU = 0, TAIL_MOE_RELU2 = 1 } tail_moe_act;
+typedef enum { TAIL_MOE_SOFTMAX = 0, TAIL_MOE_SIGMOID = 1 } tail_moe_score;
+
+typedef struct {
+  int32_t H;            /* hidden width: H % 16 == 0 (mxfp4: 32), at most 16384 */
+  int32_t I;            /* intermediate width of an expert: the same */
+  int32_t E;            /* routed experts; E + n_shared <= 512 */
+  int32_t topk;         /* experts a token selects: 1 .. min(E, 16) */
+  int32_t n_shared;     /* experts every token runs, stored behind the routed ones: 0 .. 8 */
+  int32_t t_max;        /* largest n_tokens of a run: 1 .. 64 */
+  float eps;            /* under the norm's root */
+  int32_t weight_dtype; /* TAIL_BF16 or TAIL_MXFP4 */
+  int32_t act;          /* tail_moe_act */
+  float act_alpha;      /* TAIL_MOE_GLU only */
+  float act_beta;
+  float act_limit;      /* 0: no clamp */
+  int32_t interleaved;  /* TAIL_MOE_GLU only: layout of W1's rows */
+  int32_t score;        /* tail_moe_score */
+  float route_scale;    /* factor of the routed weights */
+} tail_moe_config;
+
+typedef struct tail_moe_s tail_moe_t;
+
+/* Creates a handle on CUDA device `device` with scratch for t_max tokens.  TAIL_ERR_INVALID_ARG for a
+   bad config, TAIL_ERR_UNSUPPORTED beyond the limits above or off sm_103, TAIL_ERR_OOM. */
+int tail_moe_create(const tail_moe_config* cfg, int device, tail_moe_t** out);
+
+/*
+ * One run, asynchronous on `stream`.  n below is E + n_shared, N1 the rows of W1, S = topk + n_shared.
+ *   x              [n_tokens][H] bf16, 16-byte aligned.
+ *   gamma_opt      [H] fp32, 16-byte aligned, or NULL (x is already normalised).
+ *   router_w       [E][H] bf16, 16-byte aligned; router_bias_opt [E] fp32 or NULL.
+ *   w1, w2         [n][N1][H] and [n][H][I], 32-byte aligned: bf16, or (TAIL_MXFP4) two e2m1
+ *                  values a byte, the lower column in the low nibble; then w1_scale [n][N1][H / 32]
+ *                  and w2_scale [n][H][I / 32] hold the e8m0 exponents of blocks of 32 columns.
+ *   b1_opt, b2_opt [n][N1] and [n][H] fp32, or NULL.
+ *   n_tokens       0 .. t_max (0 is a no-op).
+ *   out_hidden_opt [n_tokens][H] bf16 h, 16-byte aligned (may be x itself), or NULL.
+ *   out_slots_opt  [n_tokens][S][H] fp32 y, 16-byte aligned, or NULL: with out_slot_w_opt the
+ *                  `slots` and `slot_w` of tail_run_moe (n_routed = topk).  One of the two is needed.
+ *   out_slot_w_opt [n_tokens][S] fp32, out_ids_opt [n_tokens][S] int32, or NULL.
+ * Inputs must not alias outputs otherwise.  One run per handle at a time (its scratch is shared),
+ * also between captured graphs.  Results are deterministic, and a token's do not depend on the
+ * others except through how many tokens share an expert (fp32 summation order).  Non-finite
+ * activations give non-finite outputs in their own token's row only.
+ */
+int tail_moe_run(tail_moe_t* m, const uint16_t* x, const float* gamma_opt, const uint16_t* router_w,
+                 const float* router_bias_opt, const void* w1, const uint8_t* w1_scale, const float* b1_opt,
+                 const void* w2, const uint8_t* w2_scale, const float* b2_opt, int32_t n_tokens,
+                 uint16_t* out_hidden_opt, float* out_slots_opt, float* out_slot_w_opt, int32_t* out_ids_opt,
+                 void* stream);
+int tail_moe_get_info(const tail_moe_t* m, int64_t* scratch_bytes);
+void tail_moe_destroy(tail_moe_t* m);
 
 /*
  * The calls below are the library's own plumbing (error reporting, timing, the
