@@ -1,5 +1,5 @@
 // Entry points of the mixture-of-experts layer: handle lifetime, argument checks,
-// scratch and the launch sequence (router, experts, combine).
+// scratch and the launch.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>
@@ -8,7 +8,7 @@
 
 #include "../../include/tail.h"
 #include "abi_common.h"
-#include "moe_internal.h"
+#include "internal.h"
 #include "moe_layer.cuh"
 #include "moe_layer_internal.h"
 
@@ -29,6 +29,8 @@ struct tail_moe_s {
   uint32_t* amax;
   float* slots;
   float* slot_w;
+  MoeControl* ctl;  // zero between launches
+  int* err;
 };
 
 namespace {
@@ -94,10 +96,14 @@ int tail_moe_create(const tail_moe_config* cfg, int device, tail_moe_t** out) {
   m->N1 = cfg->act == TAIL_MOE_GLU ? 2 * cfg->I : cfg->I;
   m->n_all = cfg->E + cfg->n_shared;
   const int64_t T = cfg->t_max, pairs = T * m->S;
-  const int64_t sizes[] = {T * cfg->E * 4, T * 8, pairs * cfg->I * 4, pairs * 4, pairs * cfg->H * 4, pairs * 4};
+  const int64_t sizes[] = {T * cfg->E * 4, T * 8, pairs * cfg->I * 4, pairs * 4, pairs * cfg->H * 4, pairs * 4,
+                           static_cast<int64_t>(sizeof(MoeControl)), 4};
   for (int64_t n : sizes) m->scratch_bytes += round256(n);
   e = cudaMalloc(reinterpret_cast<void**>(&m->scratch), static_cast<size_t>(m->scratch_bytes));
+  if (e == cudaSuccess) e = cudaMemset(m->scratch, 0, static_cast<size_t>(m->scratch_bytes));
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
+    if (m->scratch) cudaFree(m->scratch);
     delete m;
     return cuda_fail(e, "tail_moe_create: scratch allocation");
   }
@@ -108,6 +114,8 @@ int tail_moe_create(const tail_moe_config* cfg, int device, tail_moe_t** out) {
   m->amax = reinterpret_cast<uint32_t*>(p += round256(sizes[2]));
   m->slots = reinterpret_cast<float*>(p += round256(sizes[3]));
   m->slot_w = reinterpret_cast<float*>(p += round256(sizes[4]));
+  m->ctl = reinterpret_cast<MoeControl*>(p += round256(sizes[5]));
+  m->err = reinterpret_cast<int*>(p += round256(sizes[6]));
   *out = m;
   return TAIL_OK;
 }
@@ -122,6 +130,7 @@ int tail_moe_run(tail_moe_t* m, const uint16_t* x, const float* gamma_opt, const
   const tail_moe_config& c = m->cfg;
   const bool fp4 = c.weight_dtype == TAIL_MXFP4;
   if (!x || !router_w || !w1 || !w2 || (fp4 && (!w1_scale || !w2_scale))) return TAIL_ERR_INVALID_ARG;
+  if (fp4 && (!aligned(w1_scale, 16) || !aligned(w2_scale, 16))) return TAIL_ERR_INVALID_ARG;
   if (!out_hidden_opt && !out_slots_opt) return TAIL_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(router_w, 16) || !aligned(gamma_opt, 16) || !aligned(w1, 32) || !aligned(w2, 32))
     return TAIL_ERR_INVALID_ARG;
@@ -135,7 +144,8 @@ int tail_moe_run(tail_moe_t* m, const uint16_t* x, const float* gamma_opt, const
   DeviceGuard guard(m->device);
   if (!guard.ok) return TAIL_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const MoeLayerPlan plan = plan_moe_layer(n_tokens, m->S, c.H, c.I, fp4, m->max_smem, m->num_sms);
+  const MoeLayerPlan plan = plan_moe_layer(n_tokens, c.topk, c.n_shared, c.E, c.H, c.I, fp4, m->max_smem,
+                                           m->num_sms);
   if (!plan.ok) return TAIL_ERR_UNSUPPORTED;  // not reached within the limits of create
   MoeLayerArgs a;
   a.x = x;
@@ -172,21 +182,25 @@ int tail_moe_run(tail_moe_t* m, const uint16_t* x, const float* gamma_opt, const
   a.route_scale = c.route_scale;
   a.eps = c.eps;
   a.G = plan.G;
-  cudaError_t e = launch_moe_layer(a, plan, fp4, s);
+  a.h_out = out_hidden_opt;
+  a.ctl = m->ctl;
+  a.err = m->err;
+  a.timeout_ns = DEFAULT_TIMEOUT_NS;
+  const cudaError_t e = launch_moe_layer(a, plan, s);
   if (e != cudaSuccess) return cuda_fail(e, "tail_moe_run: kernel launch");
-  if (out_hidden_opt) {
-    MoeIn in;
-    in.x = x;
-    in.slots = a.slots;
-    in.slot_dtype = 0;
-    in.w = a.slot_w;
-    in.S = m->S;
-    in.n_routed = c.topk;
-    in.h_out = out_hidden_opt;
-    e = launch_moe_combine(in, n_tokens, c.H, s, false);
-    if (e != cudaSuccess) return cuda_fail(e, "tail_moe_run: kernel launch (combine)");
-  }
   return TAIL_OK;
+}
+
+int tail_moe_check(tail_moe_t* m) {
+  if (!m) return TAIL_ERR_INVALID_ARG;
+  DeviceGuard guard(m->device);
+  if (!guard.ok) return TAIL_ERR_CUDA;
+  cudaError_t e = cudaDeviceSynchronize();
+  int code = 0;
+  if (e == cudaSuccess) e = cudaMemcpy(&code, m->err, sizeof(int), cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess && code != 0) e = cudaMemset(m->err, 0, sizeof(int));
+  if (e != cudaSuccess) return cuda_fail(e, "tail_moe_check");
+  return code != 0 ? TAIL_ERR_DEVICE : TAIL_OK;
 }
 
 int tail_moe_get_info(const tail_moe_t* m, int64_t* scratch_bytes) {

@@ -1,16 +1,27 @@
-// Kernels of the mixture-of-experts layer for a few tokens (moe_layer.cuh states
-// the formulas and the fragment layout).
+// The kernel of the mixture-of-experts layer for a few tokens (moe_layer.cuh
+// states the formulas and the fragment layout).
+//
+// One launch, one CTA per SM, four stages: router logits; the first product and
+// the activation; the second product; combine and residual.  A stage needs all of
+// the one before, and the streams of two stages should not drain in between, so
+// the CTAs stay: a stage is cut into one share per CTA, shares are taken in order
+// from a ticket counter, and a CTA that ends a stage asks for its first weights of
+// the next before it waits for the others.
+//
+// No CTA needs another to be resident: shares are handed out in stage order, so a
+// share that a CTA waits on is held by a CTA that runs and, in its turn, waits on
+// earlier stages only.  CTAs that start late find their shares done by others.
+// Waits are bounded; one that runs out raises the error word, and the CTA leaves.
+#include <math.h>
+
 #include "internal.h"
+#include "moe.cuh"
 #include "moe_layer.cuh"
 #include "moe_layer_internal.h"
 
 namespace tail {
 
 namespace {
-
-// ---------------------------------------------------------------- router
-constexpr int ROUTER_THREADS = 256;
-constexpr int ROUTER_WARPS = ROUTER_THREADS / 32;
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -37,70 +48,77 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// CTA e < E: the logits of expert e for every token, a warp a token.  CTA E + t: 1 / rms and the
-// largest |t| of token t, and the largest-activation words of its pairs cleared.
-__global__ void __launch_bounds__(ROUTER_THREADS) moe_router_kernel(const MoeLayerArgs a) {
+// ---------------------------------------------------------------- router
+// The logits of experts [e0, e1) for every token, and per token in [t0, t1) 1 / rms, the largest |t| and its
+// pairs' largest-activation words cleared.  A warp a (token, expert), or several warps, K split, when there are
+// fewer of them than warps.  The norm factors out: z = (1 / rms) * sum(x gamma w).
+__device__ __forceinline__ void router_share(const MoeLayerArgs& a, int e0, int e1, int t0, int t1, float* s_part) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  __shared__ float s_sum[ROUTER_WARPS], s_max[ROUTER_WARPS];
-  if (static_cast<int>(blockIdx.x) < a.E) {
-    const int e = blockIdx.x;
-    const uint16_t* w = a.wr + static_cast<int64_t>(e) * a.H;
-    for (int t = warp; t < a.T; t += ROUTER_WARPS) {
+  const int items = (e1 - e0) * a.T + (t1 - t0);
+  if (items == 0) return;  // more CTAs than experts and tokens
+  const int nw = blockDim.x >> 5;
+  const int split = items >= nw ? 1 : 1 << (31 - __clz(nw / items));
+  const int groups = nw / split;
+  const int grp = warp / split, part = warp - grp * split;
+  for (int i0 = 0; i0 < items; i0 += groups) {
+    const int i = i0 + grp;
+    const bool live = grp < groups && i < items;
+    float dot = 0.f, ss = 0.f;
+    bool stat = false;
+    int t = 0, e = 0;
+    if (live) {
+      stat = i >= (e1 - e0) * a.T;
+      e = stat ? 0 : e0 + i / a.T;
+      t = stat ? t0 + i - (e1 - e0) * a.T : i % a.T;
       const uint16_t* x = a.x + static_cast<int64_t>(t) * a.H;
-      float dot = 0.f, ss = 0.f;
-      for (int k = lane * 8; k < a.H; k += 256) {
+      const uint16_t* w = a.wr + static_cast<int64_t>(e) * a.H;
+#pragma unroll 4
+      for (int k = (part * 32 + lane) * 8; k < a.H; k += split * 256) {
         float xf[8], wf[8], g[8];
         unpack8(__ldg(reinterpret_cast<const uint4*>(x + k)), xf);
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w + k)), wf);
         load_gamma(a.gamma, k, g);
+        if (!stat) unpack8(__ldg(reinterpret_cast<const uint4*>(w + k)), wf);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = fmaf(xf[i], xf[i], ss);
-          dot = fmaf(xf[i] * wf[i], g[i], dot);
+        for (int j = 0; j < 8; ++j) {
+          ss = fmaf(xf[j], xf[j], ss);
+          if (stat) {
+            const float v = fabsf(xf[j] * g[j]);
+            dot = v <= 3.402823466e38f ? fmaxf(dot, v) : INFINITY;
+          } else {
+            dot = fmaf(xf[j] * wf[j], g[j], dot);
+          }
         }
       }
-      dot = warp_sum(dot);
       ss = warp_sum(ss);
-      if (lane == 0) {
-        const float r = a.gamma ? 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps) : 1.0f;
-        a.logits[static_cast<int64_t>(t) * a.E + e] = dot * r;
+      if (stat) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot = fmaxf(dot, __shfl_xor_sync(0xffffffffu, dot, o));
+      } else {
+        dot = warp_sum(dot);
       }
     }
-    return;
-  }
-  const int t = blockIdx.x - a.E;
-  const uint16_t* x = a.x + static_cast<int64_t>(t) * a.H;
-  float ss = 0.f, mx = 0.f;
-  bool bad = false;
-  for (int k = tid * 8; k < a.H; k += ROUTER_THREADS * 8) {
-    float xf[8], g[8];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(x + k)), xf);
-    load_gamma(a.gamma, k, g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      ss = fmaf(xf[i], xf[i], ss);
-      const float v = fabsf(xf[i] * g[i]);
-      mx = fmaxf(mx, v);
-      bad |= !(v <= 3.402823466e38f);
+    __syncthreads();
+    if (live && lane == 0) {
+      s_part[2 * warp] = dot;
+      s_part[2 * warp + 1] = ss;
     }
-  }
-  if (bad) mx = INFINITY;
-  ss = warp_sum(ss);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) {
-    s_sum[warp] = ss;
-    s_max[warp] = mx;
-  }
-  for (int s = tid; s < a.S; s += ROUTER_THREADS) a.amax[t * a.S + s] = 0u;
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < ROUTER_WARPS; ++w) {
-      ss += s_sum[w];
-      mx = fmaxf(mx, s_max[w]);
+    __syncthreads();
+    if (live && part == 0) {
+      if (stat)
+        for (int s = lane; s < a.S; s += 32) a.amax[t * a.S + s] = 0u;
+      if (lane == 0) {
+        for (int k = 1; k < split; ++k) {
+          const float d = s_part[2 * (warp + k)];
+          dot = stat ? fmaxf(dot, d) : dot + d;
+          ss += s_part[2 * (warp + k) + 1];
+        }
+        const float r = a.gamma ? 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps) : 1.0f;
+        if (stat)
+          a.stats[t] = make_float2(r, dot * r);
+        else
+          a.logits[static_cast<int64_t>(t) * a.E + e] = dot * r;
+      }
     }
-    const float r = a.gamma ? 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps) : 1.0f;
-    a.stats[t] = make_float2(r, mx * r);
   }
 }
 
@@ -109,16 +127,25 @@ __global__ void __launch_bounds__(ROUTER_THREADS) moe_router_kernel(const MoeLay
 // up to 16 tokens' activations in shared memory.
 //
 // Work is cut into tiles of a unit (an expert and up to G of its tokens): RG subtiles of 16 * RT
-// rows, whose K is split over 16 / RG warps.  A CTA takes a contiguous share of all tiles.  Each warp
-// keeps the fragments of its next DEPTH k-steps in registers, across tile borders; at the end of a
-// tile the warps' partial sums meet in shared memory (two buffers, one barrier a tile) and one warp a
-// subtile adds them in a fixed order and finishes the rows while the others go on.
-template <bool FP4>
+// rows, whose K is split over MAIN / RG warps.  A share is a contiguous run of tiles.  Each main
+// warp keeps the fragments of its next DEPTH k-steps in registers, across tile borders (12 warps of 4
+// steps of 2 KB: 96 KB in flight an SM); at the end of a tile it leaves its partial sums in shared
+// memory and goes on.  A finishing warp adds them in a fixed order and finishes the rows: its chain of
+// bias loads, sums and exponentials held up every warp of the CTA when a main warp did it between two
+// barriers (64 tokens over 128 experts: 1640 us).
+// Formats: BF16; MXFP4; MXFP4_WIDE, for rows that are whole pieces of 64 columns.  The number of lines
+// an SM can wait for is bounded, so a load should ask for whole ones: with 16 bytes a lane (half lines)
+// 4-bit weights streamed at 3.3 TB/s whatever the depth.
+enum Format : int { BF16 = 0, MXFP4 = 1, MXFP4_WIDE = 2 };
+
+template <int FMT>
 struct Step {
-  static constexpr int COLS = FP4 ? 128 : 64;     // columns of one k-step of a warp
-  static constexpr int LANE_BYTES = FP4 ? 16 : 32;
+  static constexpr bool FP4 = FMT != BF16;
+  static constexpr int LANE_BYTES = FMT == MXFP4 ? 16 : 32;
   static constexpr int WORDS = LANE_BYTES / 4;
-  static constexpr int STEP_BYTES = 4 * LANE_BYTES;
+  static constexpr int LANE_COLS = FP4 ? 2 * LANE_BYTES : LANE_BYTES / 2;
+  static constexpr int COLS = 4 * LANE_COLS;  // columns of one k-step of a warp
+  static constexpr int BLOCKS = FP4 ? LANE_COLS / 32 : 1;  // scales a lane needs
 };
 
 struct Phase {
@@ -127,30 +154,90 @@ struct Phase {
   const float* bias;
   int N, K;
   int row_bytes, scale_bytes;
-  int a_mul, rt_step, b_step;  // row of (subtile, rt, half, g): sub * a_mul * RT * .. (row_of)
+  int a_mul, rt_step, b_step;  // rows from a lane's first to those of its other fragments (row_of)
+  int w_rt, w_b, s_rt, s_b;    // the same steps in bytes of the weight and of its scales
   int nsub, tiles;             // subtiles and tiles of a unit
   int steps;                   // k-steps
   int pitch;                   // bytes of one activation row in shared memory
+  int ahead;                   // tiles brought into L2 ahead of the one at work
 };
 
-template <bool FP4, int RT>
+template <int FMT, int RT>
 struct Frag {
-  uint32_t w[RT][2][Step<FP4>::WORDS];
-  uint32_t s[RT][2];
+  uint32_t w[RT][2][Step<FMT>::WORDS];
+  uint32_t s[RT][2][1];  // scales, a byte each
 };
 
-template <bool FP4, int RT, int NB, int PHASE, int DEPTH>
+// State of a CTA that outlives a share.
+template <int MAIN>
+struct Cta {
+  MoePlan plan;
+  uint32_t act;        // shared memory: 2 G activation rows
+  float4* red;         // [ML_BUFS][MAIN][RT * NACC][32]
+  uint32_t full, empty;  // mbarriers [ML_BUFS]: partial sums written, and read
+  volatile int* abort;   // a bounded wait ran out: no one waits any more
+  uint32_t seq;        // tiles so far, over all shares
+};
+
+template <int MAIN>
+__device__ __forceinline__ void main_warps_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * MAIN) : "memory");
+}
+
+__device__ __forceinline__ void wait_or_abort(const MoeLayerArgs& a, volatile int* abort, uint32_t bar, uint32_t parity, int code) {
+  if (*abort) return;
+  if (!mbar_wait_bounded(bar, parity, a.timeout_ns)) {
+    raise_error(a.err, code);
+    *abort = 1;
+  }
+}
+
+// The whole CTA: until `shares` shares of an earlier stage are done and their writes are visible.
+__device__ __forceinline__ void wait_stage(const MoeLayerArgs& a, volatile int* abort, const uint32_t* done, uint32_t shares) {
+  if (threadIdx.x == 0 && !*abort) {
+    uint32_t v;
+    uint64_t t0 = 0;
+    for (;;) {
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(done) : "memory");
+      if (v >= shares) break;
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > a.timeout_ns) {
+        raise_error(a.err, DEV_TIMEOUT_BARRIER);
+        *abort = 1;
+        break;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+template <int FMT, int RT, int NB, int PHASE, int DEPTH, int MAIN>
 struct Experts {
   static constexpr int NACC = NB == 4 ? 2 : 1;
-  using S = Step<FP4>;
+  static constexpr int JOBS = RT * NACC;
+  using S = Step<FMT>;
+  static constexpr bool FP4 = S::FP4;
+  static constexpr int BLOCKS = S::BLOCKS;
 
   const MoeLayerArgs& a;
   const Phase& ph;
+  Cta<MAIN>& cta;
   const MoePlan& plan;
-  uint32_t act;        // shared memory: 2 G activation rows
-  float4* red;         // [2][ML_WARPS][RT * NACC][32]
+  uint32_t act;
   int ksplit, rg_warp, kw, RG;
   int lane, warp, g, q;
+
+  __device__ __forceinline__ Experts(const MoeLayerArgs& a_, const Phase& ph_, Cta<MAIN>& c, int ks)
+      : a(a_), ph(ph_), cta(c), plan(c.plan), act(c.act), ksplit(ks) {
+    lane = threadIdx.x & 31;
+    warp = threadIdx.x >> 5;
+    g = lane >> 2;
+    q = lane & 3;
+    RG = MAIN / ksplit;
+    rg_warp = warp / ksplit;
+    kw = warp - rg_warp * ksplit;
+  }
 
   __device__ __forceinline__ int64_t row_of(int sub) const {
     // first row (rt = 0, half 0) of this lane's fragment
@@ -168,7 +255,7 @@ struct Experts {
   __device__ __forceinline__ void stage(uint32_t unit) const {
     const int n = unit_size(unit), first = unit_first(unit);
     const int kpad = ph.steps * S::COLS, chunks = kpad / 8;
-    for (int i = threadIdx.x; i < n * chunks; i += ML_THREADS) {
+    for (int i = threadIdx.x; i < n * chunks; i += 32 * MAIN) {
       const int tok = i / chunks, k = (i - tok * chunks) * 8;
       const int pair = plan.list[first + tok];
       float v[8];
@@ -208,126 +295,205 @@ struct Experts {
           lo[j] = reinterpret_cast<const uint32_t&>(l);
         }
       }
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(act_row(0, tok) + k * 2), "r"(hi[0]), "r"(hi[1]),
+      // within a k-step, the pieces that the four lanes of a row read together lie side by side
+      constexpr int PIECES = S::COLS / 8, PER = PIECES / 4;
+      const int piece = (k / 8) % PIECES;
+      const uint32_t at = k / S::COLS * (S::COLS * 2) + ((piece % PER) * 4 + piece / PER) * 16;
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(act_row(0, tok) + at), "r"(hi[0]), "r"(hi[1]),
                    "r"(hi[2]), "r"(hi[3])
                    : "memory");
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(act_row(1, tok) + k * 2), "r"(lo[0]), "r"(lo[1]),
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(act_row(1, tok) + at), "r"(lo[0]), "r"(lo[1]),
                    "r"(lo[2]), "r"(lo[3])
                    : "memory");
     }
   }
 
   struct Cursor {
-    int tile, i;
-    const uint8_t* w;  // null: no rows here for this warp
+    int u, tile;       // unit and tile in it
+    int left;          // tiles that follow, this one included
+    int i, rounds;     // k-step of the warp in the tile; rounds of DEPTH steps a tile
+    int k;             // this lane's first column in the warp's next k-step
+    const uint8_t* w;  // its first row
     const uint8_t* s;
   };
 
   __device__ __forceinline__ void aim(Cursor& c) const {
-    const int u = c.tile / ph.tiles;
-    const int sub = (c.tile - u * ph.tiles) * RG + rg_warp;
-    c.w = nullptr;
-    if (sub < ph.nsub) {
-      const int64_t row = static_cast<int64_t>(unit_expert(plan.unit[u])) * ph.N + row_of(sub);
-      c.w = ph.w + row * ph.row_bytes + q * S::LANE_BYTES;
-      if (FP4) c.s = ph.s + row * ph.scale_bytes + q;
-    }
+    const int sub = c.tile * RG + rg_warp;  // past the last subtile: any rows, their sums are not used
+    const int64_t row = static_cast<int64_t>(unit_expert(plan.unit[c.u])) * ph.N + row_of(sub < ph.nsub ? sub : 0);
+    c.k = kw * S::COLS + q * (S::LANE_COLS);
+    c.w = ph.w + row * ph.row_bytes;
+    if (FP4) c.s = ph.s + row * ph.scale_bytes;
   }
 
-  __device__ __forceinline__ void load(Frag<FP4, RT>& f, Cursor& c, int nk) const {
-    if (c.i == 0) aim(c);
-    const int ks = kw + c.i * ksplit;
-    const bool in = c.w != nullptr && ks * S::COLS + q * (S::COLS / 4) < ph.K;
+  // The next k-step's fragment.  Past the end of the rows it holds their first columns, which meet
+  // activations of zero; past the share's last tile, that tile's.
+  __device__ __forceinline__ void load(Frag<FMT, RT>& f, Cursor& c) const {
+    if (c.i == 0 && c.left > 0) aim(c);
+    const int k = c.k < ph.K ? c.k : 0;
+    const uint8_t* w = c.w + (FP4 ? k >> 1 : k << 1);
+    const uint8_t* s = FP4 ? c.s + (k >> 5) : nullptr;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t r = rt * ph.rt_step + h * ph.b_step;
-        if (in) {
-          ldg_stream(c.w + r * ph.row_bytes + ks * S::STEP_BYTES, f.w[rt][h]);
-          if (FP4) f.s[rt][h] = __ldg(c.s + r * ph.scale_bytes + ks * 4);
-        } else {
-#pragma unroll
-          for (int j = 0; j < S::WORDS; ++j) f.w[rt][h][j] = 0u;
-          f.s[rt][h] = 0u;
-        }
+        ldg_stream(w + (rt * ph.w_rt + h * ph.w_b), f.w[rt][h]);
+        if (FMT == MXFP4) ldg_scale(s + (rt * ph.s_rt + h * ph.s_b), f.s[rt][h]);
+        if (FMT == MXFP4_WIDE) ldg_scale2(s + (rt * ph.s_rt + h * ph.s_b), f.s[rt][h]);
       }
-    if (++c.i == nk) {
+    c.k += ksplit * S::COLS;
+    if (++c.i == c.rounds * DEPTH) {
       c.i = 0;
-      ++c.tile;
+      --c.left;
+      if (++c.tile == ph.tiles) {
+        c.tile = 0;
+        ++c.u;
+      }
     }
   }
 
-  // acc += the fragment's products; nb n-tiles of 8 columns (nb == 1: 4 high, 4 low columns)
-  __device__ __forceinline__ void products(Frag<FP4, RT>& f, int ks, const uint32_t (&bp)[NB], int nb,
-                                           float (&acc)[RT][NACC][4]) const {
-    if constexpr (!FP4) {
+  // One thread: the weights of a tile into L2.  The fragments in flight cover L2's latency, not the
+  // memory's.
+  __device__ __forceinline__ void prefetch(int u, int tile) const {
+    const int64_t row0 = static_cast<int64_t>(unit_expert(plan.unit[u])) * ph.N;
+    const int subs = min(RG, ph.nsub - tile * RG);
+    const bool halves = PHASE == 1 && a.gated && !a.interleaved;  // gate and up rows lie apart
+    const int rows = subs * RT * (halves ? 8 : 16);
+    const int64_t r = row0 + static_cast<int64_t>(tile) * RG * RT * (halves ? 8 : 16);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        if (b < nb) {
-          uint32_t v[8];
-          lds128(bp[b] + ks * 128, v[0], v[1], v[2], v[3]);
-          lds128(bp[b] + ks * 128 + 16, v[4], v[5], v[6], v[7]);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              mma_bf16_16816(acc[rt][b >> 1], f.w[rt][0][2 * j], f.w[rt][1][2 * j], f.w[rt][0][2 * j + 1],
-                             f.w[rt][1][2 * j + 1], v[2 * j], v[2 * j + 1]);
-        }
-      }
-    } else {
-      // Each lane's scale relative to the largest of the four blocks of its row goes into the values
-      // (a power of two: exact), the largest itself into the fp32 sums.
-      float d[RT][NACC][4];
-      float fac[RT][2];
-      uint32_t sc[RT][2];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-        for (int n = 0; n < NACC; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) d[rt][n][j] = 0.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          int m = f.s[rt][h];
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          sc[rt][h] = half_pow2(f.s[rt][h], m);
-          fac[rt][h] = e8m0(m);
-        }
-      }
-      const bool swap = q >= 2;  // lanes 2 and 3 take their words in another order: no two share banks
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const int piece = swap ? w ^ 1 : w;
-        uint32_t v[NB][4];
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          if (b < nb) lds128(bp[b] + ks * 256 + piece * 16, v[b][0], v[b][1], v[b][2], v[b][3]);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          uint32_t x[4], y[4];
-          fp4_to_half(swap ? f.w[rt][0][w ^ 1] : f.w[rt][0][w], sc[rt][0], x);
-          fp4_to_half(swap ? f.w[rt][1][w ^ 1] : f.w[rt][1][w], sc[rt][1], y);
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            if (b < nb) {
-              mma_f16_16816(d[rt][b >> 1], x[0], y[0], x[1], y[1], v[b][0], v[b][1]);
-              mma_f16_16816(d[rt][b >> 1], x[2], y[2], x[3], y[3], v[b][2], v[b][3]);
-            }
-        }
-      }
+    for (int h = 0; h < 2; ++h) {
+      if (h == 1 && !halves) break;
+      const int64_t at = r + (h ? a.I : 0);
+      prefetch_l2(ph.w + at * ph.row_bytes, rows * ph.row_bytes);
+      if (FP4 && (at * ph.scale_bytes) % 16 == 0 && rows * ph.scale_bytes % 16 == 0)
+        prefetch_l2(ph.s + at * ph.scale_bytes, rows * ph.scale_bytes);
+    }
+  }
+
+  // Sums of a tile.  4-bit weights: d counts in units of 2^(ref - 127), acc in ones.
+  struct Sums {
+    float acc[RT][NACC][4];
+    float d[FP4 ? RT : 1][FP4 ? NACC : 1][4];
+    int ref;
+  };
+
+  __device__ __forceinline__ void flush(Sums& t) const {
+    if constexpr (FP4) {
+      const float f = e8m0(t.ref);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int n = 0; n < NACC; ++n) {
-          acc[rt][n][0] = fmaf(d[rt][n][0], fac[rt][0], acc[rt][n][0]);
-          acc[rt][n][1] = fmaf(d[rt][n][1], fac[rt][0], acc[rt][n][1]);
-          acc[rt][n][2] = fmaf(d[rt][n][2], fac[rt][1], acc[rt][n][2]);
-          acc[rt][n][3] = fmaf(d[rt][n][3], fac[rt][1], acc[rt][n][3]);
-        }
+        for (int n = 0; n < NACC; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            t.acc[rt][n][j] = fmaf(t.d[rt][n][j], f, t.acc[rt][n][j]);
+            t.d[rt][n][j] = 0.f;
+          }
     }
+  }
+
+  // d += the fragment's products with its values times the scale pairs
+  template <int N>
+  __device__ __forceinline__ void products_fp4(const Frag<FMT, RT>& f, const uint32_t (&sc)[RT][2][BLOCKS], uint32_t at,
+                                               const uint32_t (&bp)[NB], float (&d)[RT][NACC][4]) const {
+#pragma unroll
+    for (int w = 0; w < S::WORDS; ++w) {
+      uint32_t v[N][4];
+#pragma unroll
+      for (int b = 0; b < N; ++b) lds128(bp[b] + at + w * 64, v[b][0], v[b][1], v[b][2], v[b][3]);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        uint32_t x[4], y[4];
+        fp4_to_half(f.w[rt][0][w], sc[rt][0][w / 4], x);
+        fp4_to_half(f.w[rt][1][w], sc[rt][1][w / 4], y);
+#pragma unroll
+        for (int b = 0; b < N; ++b) {
+          mma_f16_16816(d[rt][b >> 1], x[0], y[0], x[1], y[1], v[b][0], v[b][1]);
+          mma_f16_16816(d[rt][b >> 1], x[2], y[2], x[3], y[3], v[b][2], v[b][3]);
+        }
+      }
+    }
+  }
+
+  // Adds the fragment's products with N n-tiles of 8 columns (N == 1: 4 high, 4 low columns).
+  template <int N>
+  __device__ __forceinline__ void products(const Frag<FMT, RT>& f, int ks, const uint32_t (&bp)[NB], Sums& t) const {
+    const uint32_t at = ks * (S::COLS * 2);
+    if constexpr (!FP4) {
+#pragma unroll
+      for (int b = 0; b < N; ++b) {
+        uint32_t v[8];
+        lds128(bp[b] + at, v[0], v[1], v[2], v[3]);
+        lds128(bp[b] + at + 64, v[4], v[5], v[6], v[7]);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_bf16_16816(t.acc[rt][b >> 1], f.w[rt][0][2 * j], f.w[rt][1][2 * j], f.w[rt][0][2 * j + 1],
+                           f.w[rt][1][2 * j + 1], v[2 * j], v[2 * j + 1]);
+      }
+    } else {
+      // A block's scale relative to ref goes into its values: a power of two from 2^-14 to 2^12, so
+      // fp16 holds them exactly.  Trained weights stay in one such window for whole tiles; where they
+      // leave it, ref moves, and blocks too far apart for any window are summed quad by quad.
+      const uint32_t low = static_cast<uint32_t>(t.ref - 14);
+      uint32_t e[RT][2][BLOCKS];
+      bool ok = true;
+#pragma unroll
+      for (int i = 0; i < RT * 2 * BLOCKS; ++i) {
+        const int rt = i / (2 * BLOCKS), h = i / BLOCKS % 2, k = i % BLOCKS;
+        e[rt][h][k] = f.s[rt][h][0] >> (8 * k) & 255u;
+        ok = ok && e[rt][h][k] - low <= 26u;
+      }
+      bool apart = false;
+      if (!__all_sync(0xffffffffu, ok)) {
+        uint32_t mx = 0u, mn = 255u;
+#pragma unroll
+        for (int i = 0; i < RT * 2 * BLOCKS; ++i) {
+          const uint32_t v = e[i / (2 * BLOCKS)][i / BLOCKS % 2][i % BLOCKS];
+          mx = max(mx, v);
+          mn = min(mn, v);
+        }
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        mn = __reduce_min_sync(0xffffffffu, mn);
+        flush(t);
+        apart = mx > mn + 26u || mn + 14u > 242u;
+        if (!apart) t.ref = static_cast<int>(mn) + 14;
+      }
+      uint32_t sc[RT][2][BLOCKS];
+      const uint32_t one = (15u - static_cast<uint32_t>(t.ref)) * 0x04000400u;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int top = apart ? row_max(e[rt][h]) : 0;
+#pragma unroll
+          for (int k = 0; k < BLOCKS; ++k)  // (e - ref + 15) << 10, twice
+            sc[rt][h][k] = apart ? half_pow2(static_cast<int>(e[rt][h][k]), top) : e[rt][h][k] * 0x04000400u + one;
+        }
+      products_fp4<N>(f, sc, at, bp, t.d);
+      if (apart) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const float f0 = e8m0(row_max(e[rt][0])), f1 = e8m0(row_max(e[rt][1]));
+#pragma unroll
+          for (int n = 0; n < NACC; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              t.acc[rt][n][j] = fmaf(t.d[rt][n][j], j < 2 ? f0 : f1, t.acc[rt][n][j]);
+              t.d[rt][n][j] = 0.f;
+            }
+        }
+      }
+    }
+  }
+
+  // the largest scale of a row's blocks in the k-step
+  static __device__ __forceinline__ int row_max(const uint32_t (&e)[BLOCKS]) {
+    int m = static_cast<int>(e[0]);
+#pragma unroll
+    for (int k = 1; k < BLOCKS; ++k) m = max(m, static_cast<int>(e[k]));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   }
 
   __device__ __forceinline__ float glu(float gate, float up) const {
@@ -338,44 +504,59 @@ struct Experts {
     return gate / (1.0f + expf(-a.alpha * gate)) * (up + a.beta);
   }
 
-  // One warp: the rows of subtile (rg, rt) for the tokens 8 * n .. of the unit.
-  __device__ __forceinline__ void finish(uint32_t unit, int tile_in_unit, int job, const float4* part) const {
+  // One warp: the rows of subtile (rg, rt) for the tokens 8 * n .. of the unit.  `wait` is called once
+  // the loads that need no partial sums are under way.
+  template <typename Wait>
+  __device__ __forceinline__ void finish(uint32_t unit, int tile_in_unit, int job, const float4* part, Wait wait) const {
     const int n = job % NACC, rt = (job / NACC) % RT, rg = job / (NACC * RT);
     const int sub = tile_in_unit * RG + rg;
-    if (sub >= ph.nsub) return;
+    const int size = unit_size(unit), first = unit_first(unit), e = unit_expert(unit);
+    const bool rows = sub < ph.nsub && n * 8 < size;
+    const int64_t ra = row_of(sub) + rt * ph.rt_step, rb = ra + ph.b_step;
+    const int tok0 = n * 8 + 2 * q;
+    float ba = 0.f, bb = 0.f;
+    uint32_t am[2] = {0u, 0u};
+    int pair[2] = {0, 0};
+    if (rows) {
+      if (ph.bias) {
+        const float* bias = ph.bias + static_cast<int64_t>(e) * ph.N;
+        ba = __ldg(bias + ra);
+        bb = __ldg(bias + rb);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (tok0 + j < size) {
+          pair[j] = plan.list[first + tok0 + j];
+          if (FP4)
+            am[j] = PHASE == 1 ? __float_as_uint(__ldcg(&a.stats[pair[j] / a.S].y)) : __ldcg(a.amax + pair[j]);
+        }
+    }
+    wait();
+    if (!rows) return;
     float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int k = 0; k < ksplit; ++k) {
-      const float4 p = part[((rg * ksplit + k) * (RT * NACC) + rt * NACC + n) * 32 + lane];
+      const float4 p = part[((rg * ksplit + k) * JOBS + rt * NACC + n) * 32 + lane];
       c.x += p.x, c.y += p.y, c.z += p.z, c.w += p.w;
     }
-    const int size = unit_size(unit), first = unit_first(unit), e = unit_expert(unit);
     if (NB == 1 || size <= 4) {  // columns 0-3 high parts, 4-7 low parts
       c.x += __shfl_xor_sync(0xffffffffu, c.x, 2);
       c.y += __shfl_xor_sync(0xffffffffu, c.y, 2);
       c.z += __shfl_xor_sync(0xffffffffu, c.z, 2);
       c.w += __shfl_xor_sync(0xffffffffu, c.w, 2);
     }
-    const int tok0 = n * 8 + 2 * q;
-    const int64_t ra = row_of(sub) + rt * ph.rt_step, rb = ra + ph.b_step;
-    const float* bias = ph.bias ? ph.bias + static_cast<int64_t>(e) * ph.N : nullptr;
-    const float ba = bias ? __ldg(bias + ra) : 0.f, bb = bias ? __ldg(bias + rb) : 0.f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int tok = tok0 + j;
-      const bool live = tok < size;
-      const int pair = live ? plan.list[first + tok] : 0;
+      const bool live = tok0 + j < size;
       float va = j ? c.y : c.x, vb = j ? c.w : c.z;
       if (FP4) {
-        const uint32_t am = !live ? 0u
-                            : PHASE == 1 ? __float_as_uint(__ldcg(&a.stats[pair / a.S].y))
-                                         : __ldcg(a.amax + pair);
-        const float inv = pow2_field(254 - scale_exponent(am));
+        const float inv = pow2_field(254 - scale_exponent(am[j]));
         va *= inv, vb *= inv;
       }
       va += ba, vb += bb;
       if (PHASE == 2) {
         if (live) {
-          float* y = a.slots + static_cast<int64_t>(pair) * a.H;
+          float* y = a.slots + static_cast<int64_t>(pair[j]) * a.H;
           y[ra] = va;
           y[rb] = vb;
         }
@@ -384,22 +565,22 @@ struct Experts {
       float m;
       if (a.gated) {
         const float v = glu(va, vb);
-        if (live) a.act[static_cast<int64_t>(pair) * a.I + sub * 8 * RT + rt * 8 + g] = v;
+        if (live) a.act[static_cast<int64_t>(pair[j]) * a.I + sub * 8 * RT + rt * 8 + g] = v;
         m = fabsf(v);
         if (!(m >= 0.f)) m = INFINITY;
       } else {
         va = va > 0.f ? va * va : va != va ? va : 0.f;
         vb = vb > 0.f ? vb * vb : vb != vb ? vb : 0.f;
         if (live) {
-          a.act[static_cast<int64_t>(pair) * a.I + ra] = va;
-          a.act[static_cast<int64_t>(pair) * a.I + rb] = vb;
+          a.act[static_cast<int64_t>(pair[j]) * a.I + ra] = va;
+          a.act[static_cast<int64_t>(pair[j]) * a.I + rb] = vb;
         }
         m = va == va && vb == vb ? fmaxf(va, vb) : INFINITY;
       }
       if (FP4) {  // the largest of the row: a maximum does not depend on the order
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (live && g == 0) atomicMax(a.amax + pair, __float_as_uint(m));
+        if (live && g == 0) atomicMax(a.amax + pair[j], __float_as_uint(m));
       }
     }
   }
@@ -409,184 +590,338 @@ struct Experts {
     nb = NB == 1 || size <= 4 ? 1 : NB == 2 || size <= 8 ? 2 : NB;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      bp[b] = (nb == 1 ? act_row(g >> 2, g & 3) : act_row(b & 1, (b >> 1) * 8 + g)) + q * (S::COLS / 4) * 2;
+      bp[b] = (nb == 1 ? act_row(g >> 2, g & 3) : act_row(b & 1, (b >> 1) * 8 + g)) + q * 16;
   }
 
-  __device__ __forceinline__ void run(int lo, int hi) {
-    if (lo >= hi) return;
-    const int nk = (ph.steps + ksplit - 1) / ksplit;
-    const int total = (hi - lo) * nk;
-    Cursor c;
-    c.tile = lo;
-    c.i = 0;
-    Frag<FP4, RT> f[DEPTH];
-#pragma unroll
-    for (int s = 0; s < DEPTH; ++s)
-      if (s < total) load(f[s], c, nk);
-    int u = lo / ph.tiles;
-    int in_unit = lo - u * ph.tiles;
-    uint32_t unit = plan.unit[u];
-    stage(unit);
-    __syncthreads();
-    uint32_t bp[NB];
-    int nb;
-    aim_columns(unit, bp, nb);
-    float acc[RT][NACC][4] = {};
-    int i = 0, done = 0, turn = 0;
-    for (int base = 0; base < total; base += DEPTH) {
-#pragma unroll
-      for (int s = 0; s < DEPTH; ++s) {
-        if (base + s >= total) break;
-        const int ks = kw + i * ksplit;
-        if (ks < ph.steps) products(f[s], ks, bp, nb, acc);
-        if (base + s + DEPTH < total) load(f[s], c, nk);
-        if (++i == nk) {  // the tile's end
-          i = 0;
-          float4* part = red + (done & 1) * (ML_WARPS * RT * NACC * 32);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int n = 0; n < NACC; ++n) {
-              part[(warp * (RT * NACC) + rt * NACC + n) * 32 + lane] =
-                  make_float4(acc[rt][n][0], acc[rt][n][1], acc[rt][n][2], acc[rt][n][3]);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) acc[rt][n][j] = 0.f;
-            }
-          __syncthreads();
-          const int jobs = RG * RT * NACC;
-          for (int job = (warp - turn) & (ML_WARPS - 1); job < jobs; job += ML_WARPS)
-            if (NACC == 1 || job % NACC == 0 || unit_size(unit) > 8) finish(unit, in_unit, job, part);
-          turn += jobs;
-          ++done;
-          if (++in_unit == ph.tiles && lo + done < hi) {
-            in_unit = 0;
-            unit = plan.unit[++u];
-            stage(unit);  // every warp is past the barrier: the old rows are not read any more
-            __syncthreads();
-            aim_columns(unit, bp, nb);
-          }
-        }
+  __device__ __forceinline__ float4* partial(uint32_t seq) const {
+    return cta.red + (seq % ML_BUFS) * (MAIN * JOBS * 32);
+  }
+
+  // Tiles [lo, hi) on a finishing warp: every ML_FINISH-th of them.
+  __device__ __forceinline__ void finish_share(int lo, int hi) const {
+    int u = lo / ph.tiles, tile = lo - u * ph.tiles;
+    for (int t = lo; t < hi; ++t) {
+      const uint32_t s = cta.seq + (t - lo);
+      if (static_cast<int>(s % ML_FINISH) == warp - MAIN) {
+        const uint32_t unit = plan.unit[u];
+        for (int job = 0; job < RG * JOBS; ++job)
+          finish(unit, tile, job, partial(s), [&] {
+            if (job == 0)
+              wait_or_abort(a, cta.abort, cta.full + 8 * (s % ML_BUFS), (s / ML_BUFS) & 1, DEV_TIMEOUT_FULL);
+          });
+        __syncwarp();
+        if (lane == 0) mbar_arrive(cta.empty + 8 * (s % ML_BUFS));
+      }
+      if (++tile == ph.tiles) {
+        tile = 0;
+        ++u;
       }
     }
   }
+
+  // The k-steps of one tile, in rounds of DEPTH; each slot of the ring is refilled as it is used.
+  __device__ __forceinline__ void tile_steps(Frag<FMT, RT> (&f)[DEPTH], Cursor& c, const uint32_t (&bp)[NB], int nb,
+                                             Sums& t) const {
+    int ks = kw;
+    for (int r = 0; r < c.rounds; ++r) {
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        if (ks < ph.steps) {
+          if (NB == 1 || nb == 1)
+            products<1>(f[d], ks, bp, t);
+          else if (NB == 2 || nb == 2)
+            products<NB < 2 ? 1 : 2>(f[d], ks, bp, t);
+          else
+            products<NB>(f[d], ks, bp, t);
+        }
+        load(f[d], c);
+        ks += ksplit;
+      }
+    }
+  }
+
+  // Tiles [lo, hi) on a main warp; the fragments of the first DEPTH steps are in f.
+  __device__ __forceinline__ void main_share(int lo, int hi, Frag<FMT, RT> (&f)[DEPTH], Cursor& c) const {
+    int u = lo / ph.tiles, tile = lo - u * ph.tiles;
+    uint32_t unit = plan.unit[u];
+    stage(unit);
+    main_warps_sync<MAIN>();
+    uint32_t bp[NB];
+    int nb;
+    aim_columns(unit, bp, nb);
+    Sums t = {};
+    t.ref = 127;
+    int pu = u, pt = tile, pn = lo;  // the next tile to prefetch
+    for (int n = lo; n < hi; ++n) {
+      if (threadIdx.x == 0) {
+        for (; pn < hi && pn <= n + ph.ahead; ++pn) {
+          if (pn > n) prefetch(pu, pt);
+          if (++pt == ph.tiles) {
+            pt = 0;
+            ++pu;
+          }
+        }
+      }
+      if (tile == ph.tiles) {
+        tile = 0;
+        unit = plan.unit[++u];
+        main_warps_sync<MAIN>();  // the old unit's rows are not read any more
+        stage(unit);
+        main_warps_sync<MAIN>();
+        aim_columns(unit, bp, nb);
+      }
+      ++tile;
+      tile_steps(f, c, bp, nb, t);
+      flush(t);
+      const uint32_t s = cta.seq + (n - lo);
+      if (s >= ML_BUFS)
+        wait_or_abort(a, cta.abort, cta.empty + 8 * (s % ML_BUFS), (s / ML_BUFS - 1) & 1, DEV_TIMEOUT_EMPTY);
+      float4* part = partial(s) + warp * JOBS * 32 + lane;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int m = 0; m < NACC; ++m) {
+          part[(rt * NACC + m) * 32] =
+              make_float4(t.acc[rt][m][0], t.acc[rt][m][1], t.acc[rt][m][2], t.acc[rt][m][3]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t.acc[rt][m][j] = 0.f;
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(cta.full + 8 * (s % ML_BUFS));
+    }
+  }
+
+  // The whole CTA: tiles [lo, hi), once the stage before is done.
+  __device__ __forceinline__ void share(int lo, int hi, const uint32_t* done, uint32_t shares) {
+    if (warp < MAIN) {
+      Cursor c;
+      c.u = lo / ph.tiles;
+      c.tile = lo - c.u * ph.tiles;
+      c.left = hi - lo;
+      c.rounds = (ph.steps + ksplit * DEPTH - 1) / (ksplit * DEPTH);
+      c.i = 0;
+      c.k = 0;
+      c.w = ph.w;
+      c.s = ph.s;
+      Frag<FMT, RT> f[DEPTH];
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) load(f[d], c);
+      if (done) wait_stage(a, cta.abort, done, shares);
+      if (lo < hi) main_share(lo, hi, f, c);
+    } else {
+      if (done) wait_stage(a, cta.abort, done, shares);
+      finish_share(lo, hi);
+    }
+    cta.seq += hi - lo;
+  }
 };
 
-template <bool FP4, int RT, int NB, int PHASE, int DEPTH>
-__global__ void __launch_bounds__(ML_THREADS, 1) moe_experts_kernel(const MoeLayerArgs a, const Phase ph, int ksplit) {
+template <int FMT, int RT, int NB, int DEPTH, int MAIN>
+__global__ void __launch_bounds__(32 * (MAIN + ML_FINISH), 1)
+    moe_layer_kernel(const __grid_constant__ MoeLayerArgs a, const __grid_constant__ Phase ph1,
+                     const __grid_constant__ Phase ph2, int ksplit1, int ksplit2) {
   extern __shared__ __align__(128) uint8_t smem[];
-  const int pairs = a.T * a.S, p8 = (pairs + 7) & ~7;
-  MoePlan plan;
-  plan.pair_e = reinterpret_cast<uint16_t*>(smem);
-  plan.list = plan.pair_e + p8;
-  plan.unit = reinterpret_cast<uint32_t*>(plan.list + p8);
-  plan.cnt = plan.unit + p8;
-  plan.red = plan.cnt + ML_MAX_EXPERTS;
-  make_plan(a, plan, PHASE == 1 && blockIdx.x == 0);
-  uint8_t* act = smem + ((plan_bytes(pairs) + 127) & ~127);
+  __shared__ __align__(8) uint64_t s_bar[2 * ML_BUFS];
+  __shared__ float s_part[2 * ML_MAX_WARPS];
+  __shared__ uint32_t s_ticket;
+  __shared__ int s_abort;
   const int tid = threadIdx.x;
-  Experts<FP4, RT, NB, PHASE, DEPTH> x{a, ph, plan};
-  x.act = smem_u32(act);
-  x.red = reinterpret_cast<float4*>(act + ((2 * a.G * ph.pitch + 127) & ~127));
-  x.lane = tid & 31;
-  x.warp = tid >> 5;
-  x.g = x.lane >> 2;
-  x.q = x.lane & 3;
-  x.ksplit = ksplit;
-  x.RG = ML_WARPS / ksplit;
-  x.rg_warp = x.warp / ksplit;
-  x.kw = x.warp - x.rg_warp * ksplit;
-  const int64_t tiles = static_cast<int64_t>(plan.nunits) * ph.tiles;
-  x.run(static_cast<int>(tiles * blockIdx.x / gridDim.x), static_cast<int>(tiles * (blockIdx.x + 1) / gridDim.x));
+  const int pairs = a.T * a.S, p8 = (pairs + 7) & ~7;
+  constexpr int THREADS = 32 * (MAIN + ML_FINISH);
+  Cta<MAIN> cta;
+  cta.plan.pair_e = reinterpret_cast<uint16_t*>(smem);
+  cta.plan.list = cta.plan.pair_e + p8;
+  cta.plan.unit = reinterpret_cast<uint32_t*>(cta.plan.list + p8);
+  cta.plan.cnt = cta.plan.unit + p8;
+  cta.plan.red = cta.plan.cnt + ML_MAX_EXPERTS;
+  cta.plan.nunits = -1;
+  uint8_t* rows = smem + ((plan_bytes(pairs) + 127) & ~127);
+  cta.act = smem_u32(rows);
+  cta.red = reinterpret_cast<float4*>(rows + ((2 * a.G * max(ph1.pitch, ph2.pitch) + 127) & ~127));
+  cta.full = smem_u32(s_bar);
+  cta.empty = cta.full + 8 * ML_BUFS;
+  cta.abort = &s_abort;
+  cta.seq = 0;
+  if (tid == 0) {
+    for (int i = 0; i < ML_BUFS; ++i) {
+      mbar_init(cta.full + 8 * i, MAIN);
+      mbar_init(cta.empty + 8 * i, 1);
+    }
+    fence_mbar_init();
+    s_abort = 0;
+    s_ticket = atomicAdd(&a.ctl->ticket, 1u);
+  }
+  __syncthreads();
+  const uint32_t n = gridDim.x, last = (a.h_out ? 4u : 3u) * n;
+  uint32_t ticket = s_ticket;
+  while (ticket < last) {
+    __syncthreads();
+    if (tid == THREADS - 1) s_ticket = atomicAdd(&a.ctl->ticket, 1u);  // the next share, early
+    const uint32_t stage = ticket / n;
+    const int64_t i = ticket - stage * n;
+    auto cut = [&](int64_t total, int64_t k) { return static_cast<int>(total * k / n); };
+    if (stage == 0) {
+      const int64_t r = n - 1 - i;  // the tokens' statistics go to the last shares first
+      router_share(a, cut(a.E, i), cut(a.E, i + 1), cut(a.T, r), cut(a.T, r + 1), s_part);
+    } else if (stage == 3) {
+      wait_stage(a, cta.abort, a.ctl->done + 2, n);
+      MoeIn m;
+      m.x = a.x;
+      m.slots = a.slots;
+      m.slot_dtype = 0;
+      m.w = a.slot_w;
+      m.S = a.S;
+      m.n_routed = a.topk;
+      const int half = a.H / 2;
+      const int lo = cut(static_cast<int64_t>(a.T) * half, i), hi = cut(static_cast<int64_t>(a.T) * half, i + 1);
+      for (int p = lo + tid; p < hi && !s_abort; p += THREADS) {
+        const int t = p / half, j = 2 * (p - t * half);
+        const uint32_t h0 = moe_lane_h(m, t, a.H, j), h1 = moe_lane_h(m, t, a.H, j + 1);
+        *reinterpret_cast<uint32_t*>(a.h_out + static_cast<int64_t>(t) * a.H + j) = h0 | (h1 << 16);
+      }
+    } else {
+      if (cta.plan.nunits < 0) {
+        wait_stage(a, cta.abort, a.ctl->done, n);
+        if (!s_abort) make_plan(a, cta.plan, ticket == n);
+      }
+      if (!s_abort) {
+        const int64_t tiles = static_cast<int64_t>(cta.plan.nunits) * (stage == 1 ? ph1.tiles : ph2.tiles);
+        if (stage == 1) {
+          Experts<FMT, RT, NB, 1, DEPTH, MAIN> x(a, ph1, cta, ksplit1);
+          x.share(cut(tiles, i), cut(tiles, i + 1), nullptr, 0u);
+        } else {
+          Experts<FMT, RT, NB, 2, DEPTH, MAIN> x(a, ph2, cta, ksplit2);
+          x.share(cut(tiles, i), cut(tiles, i + 1), a.ctl->done + 1, n);
+        }
+      }
+    }
+    __syncthreads();
+    if (tid == 0 && stage < 3) {
+      __threadfence();
+      atomicAdd(&a.ctl->done[stage], 1u);
+    }
+    ticket = s_ticket;
+  }
+  if (tid == 0) {
+    __threadfence();
+    if (atomicAdd(&a.ctl->left, 1u) == n - 1) {  // every other CTA is past its last use of these words
+      a.ctl->ticket = 0u;
+      for (int k = 0; k < 3; ++k) a.ctl->done[k] = 0u;
+      a.ctl->left = 0u;
+    }
+  }
 }
 
 // ---------------------------------------------------------------- host
-template <bool FP4, int RT>
-Phase make_phase(const MoeLayerArgs& a, int phase, int ksplit) {
+constexpr int AHEAD_BYTES = 64 * 1024;
+constexpr int STATIC_SMEM = 512;  // at least moe_layer_kernel's __shared__ variables
+
+// Main warps, steps in flight of each and 16-row groups a warp takes at a time, for a format and the
+// number of n-tiles.
+constexpr int main_warps(int fmt) { return fmt == MXFP4 ? 8 : 12; }
+constexpr int depth_of(int fmt) { return fmt == BF16 ? 4 : 3; }
+constexpr int groups_of(int fmt, int nb) { return fmt == MXFP4 && nb < 4 ? 2 : 1; }
+int step_cols(int fmt) { return fmt == BF16 ? 64 : fmt == MXFP4 ? 128 : 256; }
+int columns_of(int G) { return G <= 4 ? 1 : G <= 8 ? 2 : 4; }
+
+// An activation row: whole k-steps, and 64 bytes more so that two rows fill the 128 bytes of all banks.
+int pitch_of(int fmt, int K) {
+  const int cols = step_cols(fmt);
+  return (K + cols - 1) / cols * cols * 2 + 64;
+}
+
+// Warps that split K: as many as keep at least nine tenths of their rounds of k-steps busy, else those
+// that keep the most.
+int ksplit_of(int fmt, int K) {
+  const int steps = (K + step_cols(fmt) - 1) / step_cols(fmt), depth = depth_of(fmt), main = main_warps(fmt);
+  int best = 1, best_slots = (steps + depth - 1) / depth * depth;
+  for (int k = 2; k <= main; ++k) {
+    const int slots = (steps + k * depth - 1) / (k * depth) * (k * depth);
+    if (main % k == 0 && (10 * steps >= 9 * slots || slots <= best_slots)) {
+      best = k;
+      best_slots = slots;
+    }
+  }
+  return best;
+}
+
+Phase make_phase(const MoeLayerArgs& a, int fmt, int nb, int phase, int ksplit) {
   Phase p;
   const bool gated = phase == 1 && a.gated;
+  const int RT = groups_of(fmt, nb), RG = main_warps(fmt) / ksplit;
   p.w = phase == 1 ? a.w1 : a.w2;
   p.s = phase == 1 ? a.s1 : a.s2;
   p.bias = phase == 1 ? a.b1 : a.b2;
   p.N = phase == 1 ? a.N1 : a.H;
   p.K = phase == 1 ? a.H : a.I;
-  p.row_bytes = FP4 ? p.K / 2 : p.K * 2;
+  p.row_bytes = fmt == BF16 ? p.K * 2 : p.K / 2;
   p.scale_bytes = p.K / 32;
   p.a_mul = gated && a.interleaved ? 2 : 1;
   p.rt_step = gated ? (a.interleaved ? 16 : 8) : 16;
   p.b_step = gated ? (a.interleaved ? 1 : a.I) : 8;
+  p.w_rt = p.rt_step * p.row_bytes;
+  p.w_b = p.b_step * p.row_bytes;
+  p.s_rt = p.rt_step * p.scale_bytes;
+  p.s_b = p.b_step * p.scale_bytes;
   p.nsub = p.N / (16 * RT);
-  const int RG = ML_WARPS / ksplit;
   p.tiles = (p.nsub + RG - 1) / RG;
-  p.steps = (p.K + Step<FP4>::COLS - 1) / Step<FP4>::COLS;
-  p.pitch = p.steps * Step<FP4>::COLS * 2 + (FP4 ? 32 : 16);
+  p.steps = (p.K + step_cols(fmt) - 1) / step_cols(fmt);
+  p.pitch = pitch_of(fmt, p.K);
+  p.ahead = 1 + AHEAD_BYTES / (RG * RT * 16 * p.row_bytes);
   return p;
 }
 
-int pitch_of(bool fp4, int K) {
-  const int cols = fp4 ? 128 : 64;
-  return (K + cols - 1) / cols * cols * 2 + (fp4 ? 32 : 16);
-}
-
-// Warps that split K: as many as leave every warp two k-steps.
-int ksplit_of(bool fp4, int K) {
-  const int steps = (K + (fp4 ? 127 : 63)) / (fp4 ? 128 : 64);
-  int k = ML_WARPS;
-  while (k > 1 && steps < 2 * k) k >>= 1;
-  return k;
-}
-
-int columns_of(int G) { return G <= 4 ? 1 : G <= 8 ? 2 : 4; }
-
-template <bool FP4, int RT, int NB, int DEPTH>
-cudaError_t launch_experts(const MoeLayerArgs& a, int phase, int grid, int smem, int ksplit, cudaStream_t stream) {
-  const Phase ph = make_phase<FP4, RT>(a, phase, ksplit);
-  const void* f = phase == 1 ? reinterpret_cast<const void*>(moe_experts_kernel<FP4, RT, NB, 1, DEPTH>)
-                             : reinterpret_cast<const void*>(moe_experts_kernel<FP4, RT, NB, 2, DEPTH>);
-  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <int FMT, int NB>
+cudaError_t launch_as(const MoeLayerArgs& a, const MoeLayerPlan& p, cudaStream_t stream) {
+  constexpr int MAIN = main_warps(FMT);
+  const Phase ph1 = make_phase(a, FMT, NB, 1, p.ksplit1), ph2 = make_phase(a, FMT, NB, 2, p.ksplit2);
+  auto f = moe_layer_kernel<FMT, groups_of(FMT, NB), NB, depth_of(FMT), MAIN>;
+  const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
   if (e != cudaSuccess) return e;
-  void* args[] = {const_cast<MoeLayerArgs*>(&a), const_cast<Phase*>(&ph), &ksplit};
-  return cudaLaunchKernel(f, dim3(grid), dim3(ML_THREADS), args, smem, stream);
+  f<<<p.grid, 32 * (MAIN + ML_FINISH), p.smem, stream>>>(a, ph1, ph2, p.ksplit1, p.ksplit2);
+  return cudaGetLastError();
 }
 
-template <bool FP4>
-cudaError_t launch_phase(const MoeLayerArgs& a, const MoeLayerPlan& p, int phase, cudaStream_t s) {
-  const int ks = phase == 1 ? p.ksplit1 : p.ksplit2;
+template <int FMT>
+cudaError_t launch_columns(const MoeLayerArgs& a, const MoeLayerPlan& p, cudaStream_t s) {
   switch (columns_of(a.G)) {
-    case 1: return launch_experts<FP4, FP4 ? 2 : 1, 1, FP4 ? 3 : 4>(a, phase, p.grid, p.smem, ks, s);
-    case 2: return launch_experts<FP4, FP4 ? 2 : 1, 2, FP4 ? 3 : 4>(a, phase, p.grid, p.smem, ks, s);
-    default: return launch_experts<FP4, 1, 4, 4>(a, phase, p.grid, p.smem, ks, s);
+    case 1: return launch_as<FMT, 1>(a, p, s);
+    case 2: return launch_as<FMT, 2>(a, p, s);
+    default: return launch_as<FMT, 4>(a, p, s);
   }
 }
 
 }  // namespace
 
-// Tokens a unit may hold and the shared memory, for `pairs` pairs and activation rows of the wider
-// of the two products.
-MoeLayerPlan plan_moe_layer(int T, int S, int H, int I, bool fp4, int max_smem, int num_sms) {
+// Tokens a unit may hold and the shared memory, with activation rows of the wider of the two products.
+MoeLayerPlan plan_moe_layer(int T, int topk, int nsh, int E, int H, int I, bool fp4, int max_smem, int num_sms) {
   MoeLayerPlan p;
+  max_smem -= STATIC_SMEM;  // the limit counts the kernel's own variables too
   p.grid = num_sms;
-  const int pitch = pitch_of(fp4, H > I ? H : I);
-  const int fixed = ((plan_bytes(T * S) + 127) & ~127) + 128;
-  p.G = T < 16 ? T : 16;
+  p.format = !fp4 ? BF16 : H % 64 == 0 && I % 64 == 0 ? MXFP4_WIDE : MXFP4;
+  const int pitch = pitch_of(p.format, H > I ? H : I);
+  const int fixed = ((plan_bytes(T * (topk + nsh)) + 127) & ~127) + 128;
+  // room for the tokens that share an expert when they spread evenly, and three standard deviations
+  const float mean = static_cast<float>(T) * topk / E;
+  const float room = mean + 3.0f * sqrtf(mean);
+  const int most = nsh > 0 ? 16 : room <= 4.0f ? 4 : room <= 8.0f ? 8 : 16;
+  p.G = T < most ? T : most;
   for (;; --p.G) {
     const int nb = columns_of(p.G);
-    const int rt = fp4 && nb < 4 ? 2 : 1;
-    const int red = 2 * ML_WARPS * rt * (nb == 4 ? 2 : 1) * 512;
+    const int red = ML_BUFS * main_warps(p.format) * groups_of(p.format, nb) * (nb == 4 ? 2 : 1) * 512;
     p.smem = fixed + 2 * p.G * pitch + red;
     if (p.smem <= max_smem || p.G == 1) break;
   }
   p.ok = p.smem <= max_smem;
-  p.ksplit1 = ksplit_of(fp4, H);
-  p.ksplit2 = ksplit_of(fp4, I);
+  p.ksplit1 = ksplit_of(p.format, H);
+  p.ksplit2 = ksplit_of(p.format, I);
   return p;
 }
 
-cudaError_t launch_moe_layer(const MoeLayerArgs& a, const MoeLayerPlan& p, bool fp4, cudaStream_t s) {
-  moe_router_kernel<<<a.E + a.T, ROUTER_THREADS, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
-  for (int phase = 1; phase <= 2 && e == cudaSuccess; ++phase)
-    e = fp4 ? launch_phase<true>(a, p, phase, s) : launch_phase<false>(a, p, phase, s);
-  return e;
+cudaError_t launch_moe_layer(const MoeLayerArgs& a, const MoeLayerPlan& p, cudaStream_t s) {
+  return p.format == BF16 ? launch_columns<BF16>(a, p, s)
+         : p.format == MXFP4 ? launch_columns<MXFP4>(a, p, s)
+                             : launch_columns<MXFP4_WIDE>(a, p, s);
 }
 
 }  // namespace tail

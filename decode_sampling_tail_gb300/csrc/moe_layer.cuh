@@ -30,13 +30,24 @@
 
 namespace tail {
 
-constexpr int ML_THREADS = 512;
-constexpr int ML_WARPS = ML_THREADS / 32;
+constexpr int ML_FINISH = 4;  // warps that add the partial sums and finish the rows, besides 8 or 12 main warps
+constexpr int ML_MAX_WARPS = 16;
+constexpr int ML_BUFS = 4;    // tiles whose partial sums may wait for a finishing warp
 constexpr int ML_MAX_T = 64;
-constexpr int ML_MAX_EXPERTS = 512;  // routed and shared together: one thread each when the plan is made
+constexpr int ML_MAX_EXPERTS = 512;  // routed and shared together
 constexpr int ML_MAX_TOPK = 16;
 constexpr int ML_MAX_SHARED = 8;
 constexpr int ML_MAX_DIM = 16384;
+
+// Words the CTAs of one launch share; all zero between launches (the last CTA to leave clears them).
+struct MoeControl {
+  uint32_t ticket;   // next share of work
+  uint32_t pad0[31];
+  uint32_t done[3];  // finished shares of the router, the first and the second product
+  uint32_t pad1[29];
+  uint32_t left;     // CTAs that took their last ticket
+  uint32_t pad2[31];
+};
 
 struct MoeLayerArgs {
   const uint16_t* x;      // [T][H] bf16
@@ -56,6 +67,10 @@ struct MoeLayerArgs {
   float* slots;           // [T * S][H]
   float* slot_w;          // [T][S]
   int32_t* ids;           // [T][S] or null
+  uint16_t* h_out;        // [T][H] or null
+  MoeControl* ctl;
+  int* err;
+  uint64_t timeout_ns;
   int T, H, I, N1, E, topk, nsh, S;
   int gated, interleaved, score;
   float alpha, beta, limit, route_scale, eps;
@@ -63,20 +78,28 @@ struct MoeLayerArgs {
 };
 
 // ---------------------------------------------------------------- loads
+// Read once, so not kept in L1.  Unconditional: a predicated load, or one in a branch, would join its
+// result with other values by moves, which wait for the data and undo the prefetch.
 __device__ __forceinline__ void ldg_stream(const uint8_t* p, uint32_t (&v)[8]) {
-  uint64_t a, b, c, d;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.b64 {%0,%1,%2,%3}, [%4];"
-               : "=l"(a), "=l"(b), "=l"(c), "=l"(d)
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                : "l"(p));
-  v[0] = static_cast<uint32_t>(a), v[1] = static_cast<uint32_t>(a >> 32);
-  v[2] = static_cast<uint32_t>(b), v[3] = static_cast<uint32_t>(b >> 32);
-  v[4] = static_cast<uint32_t>(c), v[5] = static_cast<uint32_t>(c >> 32);
-  v[6] = static_cast<uint32_t>(d), v[7] = static_cast<uint32_t>(d >> 32);
 }
 __device__ __forceinline__ void ldg_stream(const uint8_t* p, uint32_t (&v)[4]) {
   asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.b32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                : "l"(p));
+}
+// Brings [p, p + bytes) into L2: both multiples of 16.
+__device__ __forceinline__ void prefetch_l2(const uint8_t* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void ldg_scale(const uint8_t* p, uint32_t (&v)[1]) {
+  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v[0]) : "l"(p));
+}
+// two neighbouring scales, both in v[0]
+__device__ __forceinline__ void ldg_scale2(const uint8_t* p, uint32_t (&v)[1]) {
+  asm volatile("{\n.reg .u16 t;\nld.global.nc.u16 t, [%1];\ncvt.u32.u16 %0, t;\n}" : "=r"(v[0]) : "l"(p));
 }
 
 // D (16x8 fp32) += A (16x16 fp16, row) * B (16x8 fp16, col)
@@ -133,13 +156,13 @@ struct MoePlan {
   uint16_t* pair_e;  // [pairs padded to 8] expert of pair t * S + s
   uint16_t* list;    // [pairs] pairs ordered by expert, then token
   uint32_t* unit;    // [<= pairs] expert | first list entry << 10 | entries << 21: one pass over an expert
-  uint32_t* cnt;     // [ML_MAX_EXPERTS]
-  uint32_t* red;     // [ML_WARPS + 1]
+  uint32_t* cnt;     // [ML_MAX_EXPERTS] pairs of each expert, then those before it
+  uint32_t* red;     // [ML_MAX_WARPS]
   int nunits;
 };
 __host__ __device__ inline int plan_bytes(int pairs) {
   const int p8 = (pairs + 7) & ~7;
-  return p8 * 2 * 2 + p8 * 4 + ML_MAX_EXPERTS * 4 + (ML_WARPS + 4) * 4;
+  return p8 * 2 * 2 + p8 * 4 + ML_MAX_EXPERTS * 4 + (ML_MAX_WARPS + 4) * 4;
 }
 __device__ __forceinline__ int unit_expert(uint32_t u) { return u & 1023; }
 __device__ __forceinline__ int unit_first(uint32_t u) { return (u >> 10) & 2047; }
@@ -156,44 +179,40 @@ __device__ __forceinline__ void route_token(const MoeLayerArgs& a, int t, uint16
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = i * 32 + lane;
-    key[i] = 0u;
-    if (e < a.E) {
+    key[i] = 0u;  // below every score's key
+    if (i * 32 < a.E && e < a.E) {
       const float v = __ldcg(z + e);
-      key[i] = float_key(a.br ? score(v) + a.br[e] : v);
+      key[i] = float_key(a.br ? score(v) + __ldg(a.br + e) : v);
     }
   }
-  float w = 0.f;
   int mine = 0;
   for (int j = 0; j < a.topk; ++j) {
-    uint64_t best = 0ull;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const uint64_t c = (static_cast<uint64_t>(key[i]) << 32) | static_cast<uint32_t>(~(i * 32 + lane));
-      if (i * 32 + lane < a.E && key[i] != 0u && c > best) best = c;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const uint64_t c = __shfl_xor_sync(0xffffffffu, best, o);
-      best = c > best ? c : best;
-    }
-    const int e = static_cast<int>(~static_cast<uint32_t>(best)) & (ML_MAX_EXPERTS - 1);
+    uint32_t best = 0u;
+    int at = ML_MAX_EXPERTS - 1;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (i * 32 + lane == e) key[i] = 0u;
-    if (lane == j) {
-      mine = e;
-      const float v = __ldcg(z + e);
-      w = a.score ? score(v) : v + (a.br ? a.br[e] : 0.f);
-    }
+      if (i * 32 < a.E && key[i] > best) {
+        best = key[i];
+        at = i * 32 + lane;
+      }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const int e = __reduce_min_sync(0xffffffffu, best == top ? at : ML_MAX_EXPERTS - 1);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i * 32 < a.E && i * 32 + lane == e) key[i] = 0u;
+    if (lane == j) mine = e;
   }
   if (lane < a.topk) pair_e[t * a.S + lane] = static_cast<uint16_t>(mine);
   if (lane < a.nsh) pair_e[t * a.S + a.topk + lane] = static_cast<uint16_t>(a.E + lane);
   if (!write) return;
+  float w = 0.f;
+  if (lane < a.topk) {
+    const float v = __ldcg(z + mine);
+    w = a.score ? score(v) : v + (a.br ? __ldg(a.br + mine) : 0.f);
+  }
   if (!a.score) {  // the first is the largest
     const float top = __shfl_sync(0xffffffffu, w, 0);
     w = lane < a.topk ? expf(w - top) : 0.f;
-  } else if (lane >= a.topk) {
-    w = 0.f;
   }
   float sum = w;
 #pragma unroll
@@ -209,17 +228,24 @@ __device__ __forceinline__ void route_token(const MoeLayerArgs& a, int t, uint16
 // The whole CTA.
 __device__ __forceinline__ void make_plan(const MoeLayerArgs& a, MoePlan& p, bool write) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nt = blockDim.x, nw = nt >> 5;
   const int pairs = a.T * a.S, p8 = (pairs + 7) & ~7;
-  for (int t = warp; t < a.T; t += ML_WARPS) route_token(a, t, p.pair_e, write);
-  if (tid < 8 && pairs + tid < p8) p.pair_e[pairs + tid] = 0xffffu;
-  if (tid < ML_MAX_EXPERTS) p.cnt[tid] = 0u;
+  for (int i = tid; i < ML_MAX_EXPERTS; i += nt) p.cnt[i] = 0u;
+  if (tid < p8 - pairs) p.pair_e[pairs + tid] = 0xffffu;
+  for (int t = warp; t < a.T; t += nw) route_token(a, t, p.pair_e, write);
   __syncthreads();
-  for (int i = tid; i < pairs; i += ML_THREADS) atomicAdd(&p.cnt[p.pair_e[i]], 1u);
+  for (int i = tid; i < pairs; i += nt) atomicAdd(&p.cnt[p.pair_e[i]], 1u);
   __syncthreads();
-  // exclusive sums of the pairs (low half) and the units (high half) before each expert
-  const uint32_t n = p.cnt[tid];
-  const uint32_t units = (n + a.G - 1) / a.G;
-  uint32_t v = n | (units << 16), incl = v;
+  // the pairs (low half) and the units (high half) before each expert; a thread takes two experts
+  constexpr int HALF = ML_MAX_EXPERTS / 2;
+  uint32_t n0 = 0u, n1 = 0u;
+  if (tid < HALF) {
+    const uint2 n = reinterpret_cast<const uint2*>(p.cnt)[tid];
+    n0 = n.x, n1 = n.y;
+  }
+  auto units = [&](uint32_t n) { return (n + a.G - 1) / a.G; };
+  const uint32_t v0 = n0 | (units(n0) << 16), v = v0 + (n1 | (units(n1) << 16));
+  uint32_t incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
@@ -228,26 +254,36 @@ __device__ __forceinline__ void make_plan(const MoeLayerArgs& a, MoePlan& p, boo
   if (lane == 31) p.red[warp] = incl;
   __syncthreads();
   uint32_t before = incl - v, total = 0u;
-  for (int w = 0; w < ML_WARPS; ++w) {
-    if (w < warp) before += p.red[w];
-    total += p.red[w];
+  for (int w = 0; w < nw; ++w) {
+    const uint32_t r = p.red[w];
+    if (w < warp) before += r;
+    total += r;
   }
-  if (n > 0u) {
-    int at = static_cast<int>(before & 0xffffu);
-    uint32_t u = before >> 16;
-    for (uint32_t f = 0; f < n; f += a.G, ++u)
-      p.unit[u] = static_cast<uint32_t>(tid) | ((at + f) << 10) | (min(n - f, static_cast<uint32_t>(a.G)) << 21);
-    for (int i = 0; i < p8; i += 8) {
-      const uint4 q = *reinterpret_cast<const uint4*>(p.pair_e + i);
-      const uint32_t ws[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if ((ws[k] & 0xffffu) == static_cast<uint32_t>(tid)) p.list[at++] = static_cast<uint16_t>(i + 2 * k);
-        if ((ws[k] >> 16) == static_cast<uint32_t>(tid)) p.list[at++] = static_cast<uint16_t>(i + 2 * k + 1);
-      }
-    }
+  if (tid < HALF) {
+    auto write_units = [&](uint32_t e, uint32_t n, uint32_t at) {
+      p.cnt[e] = at & 0xffffu;
+      uint32_t u = at >> 16;
+      for (uint32_t f = 0; f < n; f += a.G, ++u)
+        p.unit[u] = e | (((at & 0xffffu) + f) << 10) | (min(n - f, static_cast<uint32_t>(a.G)) << 21);
+    };
+    write_units(2 * tid, n0, before);
+    write_units(2 * tid + 1, n1, before + v0);
   }
   p.nunits = static_cast<int>(total >> 16);
+  __syncthreads();
+  // a pair's place: the pairs of its expert before it
+  for (int i = tid; i < pairs; i += nt) {
+    const uint32_t e = p.pair_e[i], ee = e | (e << 16);
+    uint32_t at = p.cnt[e];
+    int j = 0;
+    for (; j + 8 <= i; j += 8) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p.pair_e + j);
+      at += (__popc(__vcmpeq2(q.x, ee)) + __popc(__vcmpeq2(q.y, ee)) + __popc(__vcmpeq2(q.z, ee)) +
+             __popc(__vcmpeq2(q.w, ee))) >> 4;
+    }
+    for (; j < i; ++j) at += p.pair_e[j] == e ? 1u : 0u;
+    p.list[at] = static_cast<uint16_t>(i);
+  }
   __syncthreads();
 }
 

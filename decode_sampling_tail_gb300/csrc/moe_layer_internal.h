@@ -10,13 +10,14 @@ struct MoeLayerArgs;
 
 struct MoeLayerPlan {
   bool ok;
+  int format;   // Format of moe_layer.cu
   int G;        // tokens of one expert that share a pass over its weights
   int smem;     // dynamic shared memory of the expert kernels
   int grid;
   int ksplit1, ksplit2;  // warps that split the columns of W1's and W2's rows
 };
 
-MoeLayerPlan plan_moe_layer(int T, int S, int H, int I, bool fp4, int max_smem, int num_sms);
-cudaError_t launch_moe_layer(const MoeLayerArgs& a, const MoeLayerPlan& p, bool fp4, cudaStream_t stream);
+MoeLayerPlan plan_moe_layer(int T, int topk, int nsh, int E, int H, int I, bool fp4, int max_smem, int num_sms);
+cudaError_t launch_moe_layer(const MoeLayerArgs& a, const MoeLayerPlan& p, cudaStream_t stream);
 
 }  // namespace tail

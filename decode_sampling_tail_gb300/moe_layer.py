@@ -111,3 +111,9 @@ class Moe:
         if rc != TAIL_OK:
             raise TailError(rc, "tail_moe_run")
         return out_hidden
+
+    def check(self):
+        """Synchronises and raises when a bounded device wait of a run ran out (tail_moe_check)."""
+        rc = lib().tail_moe_check(self.h)
+        if rc != TAIL_OK:
+            raise TailError(rc, "tail_moe_check")

@@ -482,13 +482,14 @@ typedef struct tail_moe_s tail_moe_t;
 int tail_moe_create(const tail_moe_config* cfg, int device, tail_moe_t** out);
 
 /*
- * One run, asynchronous on `stream`.  n below is E + n_shared, N1 the rows of W1, S = topk + n_shared.
+ * One run, one launch, asynchronous on `stream`.  n below is E + n_shared, N1 the rows of W1, S = topk + n_shared.
  *   x              [n_tokens][H] bf16, 16-byte aligned.
  *   gamma_opt      [H] fp32, 16-byte aligned, or NULL (x is already normalised).
  *   router_w       [E][H] bf16, 16-byte aligned; router_bias_opt [E] fp32 or NULL.
  *   w1, w2         [n][N1][H] and [n][H][I], 32-byte aligned: bf16, or (TAIL_MXFP4) two e2m1
  *                  values a byte, the lower column in the low nibble; then w1_scale [n][N1][H / 32]
- *                  and w2_scale [n][H][I / 32] hold the e8m0 exponents of blocks of 32 columns.
+ *                  and w2_scale [n][H][I / 32], 16-byte aligned, hold the e8m0 exponents of blocks of
+ *                  32 columns.
  *   b1_opt, b2_opt [n][N1] and [n][H] fp32, or NULL.
  *   n_tokens       0 .. t_max (0 is a no-op).
  *   out_hidden_opt [n_tokens][H] bf16 h, 16-byte aligned (may be x itself), or NULL.
@@ -505,6 +506,9 @@ int tail_moe_run(tail_moe_t* m, const uint16_t* x, const float* gamma_opt, const
                  const void* w2, const uint8_t* w2_scale, const float* b2_opt, int32_t n_tokens,
                  uint16_t* out_hidden_opt, float* out_slots_opt, float* out_slot_w_opt, int32_t* out_ids_opt,
                  void* stream);
+/* Synchronises the device and reads the handle's error word: TAIL_ERR_DEVICE (and clears it) when a
+   bounded device wait of a run ran out (its outputs are then undefined), else TAIL_OK. */
+int tail_moe_check(tail_moe_t* m);
 int tail_moe_get_info(const tail_moe_t* m, int64_t* scratch_bytes);
 void tail_moe_destroy(tail_moe_t* m);
 

@@ -4,7 +4,8 @@ The kernels carry an activation as two 16-bit parts: what they leave out is at m
 half-steps of 2^-8 multiply) or 2^-20 (fp16 parts, 2^-11 each, with room for the smallest elements of a row); sums
 run in fp32 over chains of well under 128 additions, each off by at most 2^-23 of the running magnitude.  So a product
 W v is off by at most (part + 2^-16) |W| |v|, and errors of v pass through |W|.  Elementary functions are off by a few
-units of 2^-24.
+units of 2^-24.  An fp32 value below 2^-126 is a multiple of 2^-149, so an activation or an output of that size is off
+by up to TINY whatever it was computed from.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import torch
 FP4 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 PART = {"bf16": 2.0 ** -16, "mxfp4": 2.0 ** -20}
 SUM = 2.0 ** -16
+TINY = 2.0 ** -149
 
 
 def widen(w, scale):
@@ -26,7 +28,8 @@ def widen(w, scale):
 
 
 def route(x, gamma, router_w, bias, topk, n_shared, score, scale, eps):
-    """t, ids, weights and the smallest gap between a selected and a passed-over expert of each token."""
+    """t, ids, weights and the smallest gap between a selected expert and the next one of each token, relative to its
+    largest score (fp32 scores are off by about 1e-6 of that)."""
     t = x.double()
     if gamma is not None:
         t = t / torch.sqrt((t * t).mean(-1, keepdim=True) + eps) * gamma.double()
@@ -35,7 +38,7 @@ def route(x, gamma, router_w, bias, topk, n_shared, score, scale, eps):
     rank = weigh if bias is None else weigh + bias.double()
     order = torch.sort(rank, dim=-1, descending=True, stable=True)
     ids = order.indices[:, :topk]
-    gaps = order.values[:, :-1] - order.values[:, 1:]
+    gaps = (order.values[:, :-1] - order.values[:, 1:]) / rank.abs().amax(-1, keepdim=True)
     gap = gaps[:, :topk].amin(-1) if gaps.shape[1] else torch.ones(len(t), dtype=torch.float64, device=t.device)
     if score == "sigmoid":
         w = torch.gather(weigh, 1, ids)
@@ -75,8 +78,9 @@ def experts(t, ids, w1, s1, b1, w2, s2, b2, weight_dtype, act, alpha, beta, limi
             a = silu * (u + beta)
             slope = 1.0 + 0.28 * max(1.0, abs(alpha))  # |d silu / d g| <= sigmoid + |alpha g| sigmoid' < 1.28
             da = slope * dg * ((u + beta).abs() + du) + silu.abs() * du + 2.0 ** -20 * a.abs()
+        da = da + TINY
         out = a @ m2.T + (0 if b2 is None else b2[e].double())
-        dy = da @ m2.abs().T + rel * ((a.abs() + da) @ m2.abs().T) + 2.0 ** -22 * out.abs()
+        dy = da @ m2.abs().T + rel * ((a.abs() + da) @ m2.abs().T) + 2.0 ** -22 * out.abs() + TINY
         y[at[:, 0], at[:, 1]] = out
         bound[at[:, 0], at[:, 1]] = dy
     return y, bound
