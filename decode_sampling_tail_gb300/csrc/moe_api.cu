@@ -182,6 +182,8 @@ int tail_moe_run(tail_moe_t* m, const uint16_t* x, const float* gamma_opt, const
   a.route_scale = c.route_scale;
   a.eps = c.eps;
   a.G = plan.G;
+  a.R = plan.R;
+  a.all_rows = plan.all_rows;
   a.h_out = out_hidden_opt;
   a.ctl = m->ctl;
   a.err = m->err;

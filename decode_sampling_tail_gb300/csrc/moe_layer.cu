@@ -50,73 +50,86 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // ---------------------------------------------------------------- router
 // The logits of experts [e0, e1) for every token, and per token in [t0, t1) 1 / rms, the largest |t| and its
-// pairs' largest-activation words cleared.  A warp a (token, expert), or several warps, K split, when there are
-// fewer of them than warps.  The norm factors out: z = (1 / rms) * sum(x gamma w).
-__device__ __forceinline__ void router_share(const MoeLayerArgs& a, int e0, int e1, int t0, int t1, float* s_part) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int items = (e1 - e0) * a.T + (t1 - t0);
-  if (items == 0) return;  // more CTAs than experts and tokens
-  const int nw = blockDim.x >> 5;
-  const int split = items >= nw ? 1 : 1 << (31 - __clz(nw / items));
-  const int groups = nw / split;
-  const int grp = warp / split, part = warp - grp * split;
-  for (int i0 = 0; i0 < items; i0 += groups) {
-    const int i = i0 + grp;
-    const bool live = grp < groups && i < items;
-    float dot = 0.f, ss = 0.f;
-    bool stat = false;
-    int t = 0, e = 0;
-    if (live) {
-      stat = i >= (e1 - e0) * a.T;
-      e = stat ? 0 : e0 + i / a.T;
-      t = stat ? t0 + i - (e1 - e0) * a.T : i % a.T;
-      const uint16_t* x = a.x + static_cast<int64_t>(t) * a.H;
-      const uint16_t* w = a.wr + static_cast<int64_t>(e) * a.H;
-#pragma unroll 4
-      for (int k = (part * 32 + lane) * 8; k < a.H; k += split * 256) {
-        float xf[8], wf[8], g[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(x + k)), xf);
-        load_gamma(a.gamma, k, g);
-        if (!stat) unpack8(__ldg(reinterpret_cast<const uint4*>(w + k)), wf);
+// pairs' largest-activation words cleared.  The whole CTA; a warp a token, or several, K split, when there are
+// fewer tokens than warps.  The norm factors out: z = (1 / rms) * sum(x gamma w), and gamma w is formed once, in
+// shared memory (v: H floats).
+__device__ __forceinline__ void router_share(const MoeLayerArgs& a, int e0, int e1, int t0, int t1, float* v,
+                                             float* s_part) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nt = blockDim.x, nw = nt >> 5;
+#pragma unroll 1
+  for (int e = e0; e <= e1; ++e) {
+    const bool stat = e == e1;  // the last pass: statistics
+    const int first = stat ? t0 : 0, n = (stat ? t1 : a.T) - first;
+    if (n == 0) continue;
+    const uint16_t* w = a.wr + static_cast<int64_t>(stat ? 0 : e) * a.H;
+    __syncthreads();  // v and s_part are read by the pass before
+#pragma unroll 1
+    for (int k = tid * 8; k < a.H; k += nt * 8) {
+      float wf[8], g[8];
+      load_gamma(a.gamma, k, g);
+      if (!stat) unpack8(__ldg(reinterpret_cast<const uint4*>(w + k)), wf);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          ss = fmaf(xf[j], xf[j], ss);
-          if (stat) {
-            const float v = fabsf(xf[j] * g[j]);
-            dot = v <= 3.402823466e38f ? fmaxf(dot, v) : INFINITY;
-          } else {
-            dot = fmaf(xf[j] * wf[j], g[j], dot);
+      for (int j = 0; j < 8; ++j) g[j] = stat ? g[j] : g[j] * wf[j];
+      *reinterpret_cast<float4*>(v + k) = make_float4(g[0], g[1], g[2], g[3]);
+      *reinterpret_cast<float4*>(v + k + 4) = make_float4(g[4], g[5], g[6], g[7]);
+    }
+    __syncthreads();
+    const int split = n >= nw ? 1 : 1 << (31 - __clz(nw / n));
+    const int groups = nw / split, grp = warp / split, part = warp - grp * split;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += groups) {
+      const bool live = grp < groups && i0 + grp < n;
+      const int t = first + i0 + grp;
+      float dot = 0.f, ss = 0.f;
+      if (live) {
+        const uint16_t* x = a.x + static_cast<int64_t>(t) * a.H;
+#pragma unroll 4
+        for (int k = (part * 32 + lane) * 8; k < a.H; k += split * 256) {
+          float xf[8];
+          unpack8(__ldg(reinterpret_cast<const uint4*>(x + k)), xf);
+          const float4 p = *reinterpret_cast<const float4*>(v + k), q = *reinterpret_cast<const float4*>(v + k + 4);
+          const float vf[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            ss = fmaf(xf[j], xf[j], ss);
+            if (stat) {
+              const float m = fabsf(xf[j] * vf[j]);
+              dot = m <= 3.402823466e38f ? fmaxf(dot, m) : INFINITY;
+            } else {
+              dot = fmaf(xf[j], vf[j], dot);
+            }
           }
         }
-      }
-      ss = warp_sum(ss);
-      if (stat) {
+        ss = warp_sum(ss);
+        if (stat) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot = fmaxf(dot, __shfl_xor_sync(0xffffffffu, dot, o));
-      } else {
-        dot = warp_sum(dot);
-      }
-    }
-    __syncthreads();
-    if (live && lane == 0) {
-      s_part[2 * warp] = dot;
-      s_part[2 * warp + 1] = ss;
-    }
-    __syncthreads();
-    if (live && part == 0) {
-      if (stat)
-        for (int s = lane; s < a.S; s += 32) a.amax[t * a.S + s] = 0u;
-      if (lane == 0) {
-        for (int k = 1; k < split; ++k) {
-          const float d = s_part[2 * (warp + k)];
-          dot = stat ? fmaxf(dot, d) : dot + d;
-          ss += s_part[2 * (warp + k) + 1];
+          for (int o = 16; o > 0; o >>= 1) dot = fmaxf(dot, __shfl_xor_sync(0xffffffffu, dot, o));
+        } else {
+          dot = warp_sum(dot);
         }
-        const float r = a.gamma ? 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps) : 1.0f;
+      }
+      __syncthreads();
+      if (live && lane == 0) {
+        s_part[2 * warp] = dot;
+        s_part[2 * warp + 1] = ss;
+      }
+      __syncthreads();
+      if (live && part == 0) {
         if (stat)
-          a.stats[t] = make_float2(r, dot * r);
-        else
-          a.logits[static_cast<int64_t>(t) * a.E + e] = dot * r;
+          for (int s = lane; s < a.S; s += 32) a.amax[t * a.S + s] = 0u;
+        if (lane == 0) {
+#pragma unroll 1
+          for (int k = 1; k < split; ++k) {
+            const float d = s_part[2 * (warp + k)];
+            dot = stat ? fmaxf(dot, d) : dot + d;
+            ss += s_part[2 * (warp + k) + 1];
+          }
+          const float r = a.gamma ? rsqrtf(__fdividef(ss, static_cast<float>(a.H)) + a.eps) : 1.0f;
+          if (stat)
+            a.stats[t] = make_float2(r, dot * r);
+          else
+            a.logits[static_cast<int64_t>(t) * a.E + e] = dot * r;
+        }
       }
     }
   }
@@ -159,7 +172,7 @@ struct Phase {
   int nsub, tiles;             // subtiles and tiles of a unit
   int steps;                   // k-steps
   int pitch;                   // bytes of one activation row in shared memory
-  int ahead;                   // tiles brought into L2 ahead of the one at work
+  int ahead;                   // whether the next tiles are brought into L2 early
 };
 
 template <int FMT, int RT>
@@ -194,7 +207,7 @@ __device__ __forceinline__ void wait_or_abort(const MoeLayerArgs& a, volatile in
 
 // The whole CTA: until `shares` shares of an earlier stage are done and their writes are visible.
 __device__ __forceinline__ void wait_stage(const MoeLayerArgs& a, volatile int* abort, const uint32_t* done, uint32_t shares) {
-  if (threadIdx.x == 0 && !*abort) {
+  if (threadIdx.x == blockDim.x - 32 && !*abort) {  // a finishing warp's: no loads of its own to wait for
     uint32_t v;
     uint64_t t0 = 0;
     for (;;) {
@@ -245,90 +258,174 @@ struct Experts {
     return static_cast<int64_t>(sub) * 16 * RT + g;
   }
 
-  // the activation row of a token's high (plane 0) or low (plane 1) part
-  __device__ __forceinline__ uint32_t act_row(int plane, int tok) const {
-    return act + static_cast<uint32_t>(plane * a.G + min(tok, a.G - 1)) * ph.pitch;
+  // row `row` of the high (plane 0) or low (plane 1) parts
+  __device__ __forceinline__ uint32_t act_row(int plane, int row) const {
+    return act + static_cast<uint32_t>(plane * a.R + row) * ph.pitch;
+  }
+  // the row of a unit's token (any row past its tokens: those columns are not used)
+  __device__ __forceinline__ int row_of_token(uint32_t unit, int tok) const {
+    const int i = min(tok, unit_size(unit) - 1);
+    return PHASE == 1 && a.all_rows ? plan.list[unit_first(unit) + i] / a.S : i;
   }
 
-  // Activations of a unit into shared memory, split into a high and a low 16-bit part so that the
-  // products carry them to about 2^-17 (bf16) or 2^-22 (fp16, scaled by a power of two a token).
+  // Eight activations v times mult into shared memory, split into a high and a low 16-bit part so that
+  // the products carry them to about 2^-17 (bf16) or 2^-22 (fp16, scaled by a power of two a token).
+  // Within a k-step, the pieces that the four lanes of a row read together lie side by side.
+  __device__ __forceinline__ void put8(int row, int k, const float (&v)[8], float mult) const {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (FP4) {
+        const float x = v[2 * j] * mult, y = v[2 * j + 1] * mult;
+        const __half2 h = __floats2half2_rn(x, y);
+        const __half2 l = __floats2half2_rn(x - __low2float(h), y - __high2float(h));
+        hi[j] = reinterpret_cast<const uint32_t&>(h);
+        lo[j] = reinterpret_cast<const uint32_t&>(l);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        const __nv_bfloat162 l = __floats2bfloat162_rn(v[2 * j] - __low2float(h), v[2 * j + 1] - __high2float(h));
+        hi[j] = reinterpret_cast<const uint32_t&>(h);
+        lo[j] = reinterpret_cast<const uint32_t&>(l);
+      }
+    }
+    constexpr int PIECES = S::COLS / 8, PER = PIECES / 4;
+    const int piece = (k / 8) % PIECES;
+    const uint32_t at = k / S::COLS * (S::COLS * 2) + ((piece % PER) * 4 + piece / PER) * 16;
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(act_row(0, row) + at), "r"(hi[0]), "r"(hi[1]),
+                 "r"(hi[2]), "r"(hi[3])
+                 : "memory");
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(act_row(1, row) + at), "r"(lo[0]), "r"(lo[1]),
+                 "r"(lo[2]), "r"(lo[3])
+                 : "memory");
+  }
+
+  // t of `token` at columns k .. k + 7, from its 1 / rms
+  __device__ __forceinline__ void normed8(int token, int k, float r, float (&v)[8]) const {
+    float gm[8];
+    unpack8(__ldg(reinterpret_cast<const uint4*>(a.x + static_cast<int64_t>(token) * a.H + k)), v);
+    load_gamma(a.gamma, k, gm);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * r * gm[j];
+  }
+
+  // The main warps: the rows of a unit.
   __device__ __forceinline__ void stage(uint32_t unit) const {
     const int n = unit_size(unit), first = unit_first(unit);
-    const int kpad = ph.steps * S::COLS, chunks = kpad / 8;
-    for (int i = threadIdx.x; i < n * chunks; i += 32 * MAIN) {
-      const int tok = i / chunks, k = (i - tok * chunks) * 8;
-      const int pair = plan.list[first + tok];
-      float v[8];
-      float mult = 1.f;
-      if (k >= ph.K) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.f;
-      } else if (PHASE == 1) {
-        const int t = pair / a.S;
-        const float2 st = __ldcg(a.stats + t);
-        float gm[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(a.x + static_cast<int64_t>(t) * a.H + k)), v);
-        load_gamma(a.gamma, k, gm);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = v[j] * st.x * gm[j];
-        if (FP4) mult = pow2_field(scale_exponent(__float_as_uint(st.y)));
-      } else {
-        const float4* p = reinterpret_cast<const float4*>(a.act + static_cast<int64_t>(pair) * a.I + k);
-        const float4 x = __ldcg(p), y = __ldcg(p + 1);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-        if (FP4) mult = pow2_field(scale_exponent(__ldcg(a.amax + pair)));
+    const int chunks = ph.steps * (S::COLS / 8);
+#pragma unroll 1
+    for (int row = 0; row < n; ++row) {  // a row at a time, all warps on it
+      const int pair = plan.list[first + row];
+      const int token = pair / a.S;
+      float r = 1.f;
+      uint32_t top = 0u;
+      if (PHASE == 1) {
+        const float2 st = __ldcg(a.stats + token);
+        r = st.x;
+        top = __float_as_uint(st.y);
+      } else if (FP4) {
+        top = __ldcg(a.amax + pair);
       }
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (FP4) {
-          const float x = v[2 * j] * mult, y = v[2 * j + 1] * mult;
-          const __half2 h = __floats2half2_rn(x, y);
-          const __half2 l = __floats2half2_rn(x - __low2float(h), y - __high2float(h));
-          hi[j] = reinterpret_cast<const uint32_t&>(h);
-          lo[j] = reinterpret_cast<const uint32_t&>(l);
-        } else {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-          const __nv_bfloat162 l =
-              __floats2bfloat162_rn(v[2 * j] - __low2float(h), v[2 * j + 1] - __high2float(h));
-          hi[j] = reinterpret_cast<const uint32_t&>(h);
-          lo[j] = reinterpret_cast<const uint32_t&>(l);
+#pragma unroll 1
+      for (int c = warp * 32 + lane; c < chunks; c += 32 * MAIN) {
+        const int k = c * 8;
+        float v[8] = {};
+        if (k < ph.K) {
+          if (PHASE == 1) {
+            normed8(token, k, r, v);
+          } else {
+            const float4* p = reinterpret_cast<const float4*>(a.act + static_cast<int64_t>(pair) * a.I + k);
+            const float4 x = __ldcg(p), y = __ldcg(p + 1);
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+          }
         }
+        put8(row, k, v, FP4 ? pow2_field(scale_exponent(top)) : 1.f);
       }
-      // within a k-step, the pieces that the four lanes of a row read together lie side by side
-      constexpr int PIECES = S::COLS / 8, PER = PIECES / 4;
-      const int piece = (k / 8) % PIECES;
-      const uint32_t at = k / S::COLS * (S::COLS * 2) + ((piece % PER) * 4 + piece / PER) * 16;
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(act_row(0, tok) + at), "r"(hi[0]), "r"(hi[1]),
-                   "r"(hi[2]), "r"(hi[3])
-                   : "memory");
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(act_row(1, tok) + at), "r"(lo[0]), "r"(lo[1]),
-                   "r"(lo[2]), "r"(lo[3])
-                   : "memory");
     }
   }
 
+  // The whole CTA, while the router's other shares finish: the first product's rows of every token, each
+  // with a 1 / rms and a largest value formed here.
+  __device__ __forceinline__ void stage_all(float* s_part) const {
+    const int nw = blockDim.x >> 5;
+    const int split = a.T >= nw ? 1 : 1 << (31 - __clz(nw / a.T));
+    const int groups = nw / split, grp = warp / split, part = warp - grp * split;
+    const int kpad = ph.steps * S::COLS;
+#pragma unroll 1
+    for (int i0 = 0; i0 < a.T; i0 += groups) {
+      const int t = i0 + grp;
+      const bool live = grp < groups && t < a.T;
+      float ss = 0.f, mx = 0.f;
+      if (live) {
+#pragma unroll 4
+        for (int k = (part * 32 + lane) * 8; k < a.H; k += split * 256) {
+          float v[8], gm[8];
+          unpack8(__ldg(reinterpret_cast<const uint4*>(a.x + static_cast<int64_t>(t) * a.H + k)), v);
+          load_gamma(a.gamma, k, gm);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            ss = fmaf(v[j], v[j], ss);
+            const float m = fabsf(v[j] * gm[j]);
+            mx = m <= 3.402823466e38f ? fmaxf(mx, m) : INFINITY;
+          }
+        }
+        ss = warp_sum(ss);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      }
+      __syncthreads();
+      if (live && lane == 0) {
+        s_part[2 * warp] = mx;
+        s_part[2 * warp + 1] = ss;
+      }
+      __syncthreads();
+      if (!live) continue;
+      mx = 0.f, ss = 0.f;
+#pragma unroll 1
+      for (int k = 0; k < split; ++k) {
+        mx = fmaxf(mx, s_part[2 * (grp * split + k)]);
+        ss += s_part[2 * (grp * split + k) + 1];
+      }
+      const float r = a.gamma ? rsqrtf(__fdividef(ss, static_cast<float>(a.H)) + a.eps) : 1.0f;
+      const float mult = FP4 ? pow2_field(scale_exponent(__float_as_uint(mx * r))) : 1.f;
+#pragma unroll 2
+      for (int k = (part * 32 + lane) * 8; k < kpad; k += split * 256) {
+        float v[8] = {};
+        if (k < a.H) normed8(t, k, r, v);
+        put8(t, k, v, mult);
+      }
+    }
+    __syncthreads();
+  }
+
+  // A share's tiles fall into segments, one a unit; a segment's k-steps, nk a tile, are padded to whole
+  // rounds of the ring.
   struct Cursor {
     int u, tile;       // unit and tile in it
-    int left;          // tiles that follow, this one included
-    int i, rounds;     // k-step of the warp in the tile; rounds of DEPTH steps a tile
+    int left;          // tiles of the share that follow, this one included
+    int i, nk;         // k-step of the warp in the tile, and their number
+    int steps, slots;  // k-steps and ring slots left in the segment
     int k;             // this lane's first column in the warp's next k-step
     const uint8_t* w;  // its first row
     const uint8_t* s;
   };
 
-  __device__ __forceinline__ void aim(Cursor& c) const {
-    const int sub = c.tile * RG + rg_warp;  // past the last subtile: any rows, their sums are not used
-    const int64_t row = static_cast<int64_t>(unit_expert(plan.unit[c.u])) * ph.N + row_of(sub < ph.nsub ? sub : 0);
-    c.k = kw * S::COLS + q * (S::LANE_COLS);
-    c.w = ph.w + row * ph.row_bytes;
-    if (FP4) c.s = ph.s + row * ph.scale_bytes;
-  }
+  static __device__ __forceinline__ int whole_rounds(int steps) { return (steps + DEPTH - 1) / DEPTH * DEPTH; }
 
   // The next k-step's fragment.  Past the end of the rows it holds their first columns, which meet
-  // activations of zero; past the share's last tile, that tile's.
+  // activations of zero; in a padding slot and past the share, anything that may be read.
   __device__ __forceinline__ void load(Frag<FMT, RT>& f, Cursor& c) const {
-    if (c.i == 0 && c.left > 0) aim(c);
+    if (c.slots == 0 && c.left > 0) {  // the next segment
+      const int n = min(ph.tiles - c.tile, c.left);
+      c.steps = n * c.nk;
+      c.slots = whole_rounds(c.steps);
+    }
+    if (c.i == 0 && c.steps > 0) {
+      const int sub = c.tile * RG + rg_warp;  // past the last subtile: any rows, their sums are not used
+      const int64_t row = static_cast<int64_t>(unit_expert(plan.unit[c.u])) * ph.N + row_of(sub < ph.nsub ? sub : 0);
+      c.k = kw * S::COLS + q * S::LANE_COLS;
+      c.w = ph.w + row * ph.row_bytes;
+      if (FP4) c.s = ph.s + row * ph.scale_bytes;
+    }
     const int k = c.k < ph.K ? c.k : 0;
     const uint8_t* w = c.w + (FP4 ? k >> 1 : k << 1);
     const uint8_t* s = FP4 ? c.s + (k >> 5) : nullptr;
@@ -340,13 +437,16 @@ struct Experts {
         if (FMT == MXFP4) ldg_scale(s + (rt * ph.s_rt + h * ph.s_b), f.s[rt][h]);
         if (FMT == MXFP4_WIDE) ldg_scale2(s + (rt * ph.s_rt + h * ph.s_b), f.s[rt][h]);
       }
-    c.k += ksplit * S::COLS;
-    if (++c.i == c.rounds * DEPTH) {
-      c.i = 0;
-      --c.left;
-      if (++c.tile == ph.tiles) {
-        c.tile = 0;
-        ++c.u;
+    --c.slots;
+    if (--c.steps >= 0) {
+      c.k += ksplit * S::COLS;
+      if (++c.i == c.nk) {
+        c.i = 0;
+        --c.left;
+        if (++c.tile == ph.tiles) {
+          c.tile = 0;
+          ++c.u;
+        }
       }
     }
   }
@@ -432,49 +532,58 @@ struct Experts {
                            f.w[rt][1][2 * j + 1], v[2 * j], v[2 * j + 1]);
       }
     } else {
-      // A block's scale relative to ref goes into its values: a power of two from 2^-14 to 2^12, so
+      // A block's scale relative to ref goes into its values: a power of two from 2^-8 to 2^7, so that
       // fp16 holds them exactly.  Trained weights stay in one such window for whole tiles; where they
       // leave it, ref moves, and blocks too far apart for any window are summed quad by quad.
-      const uint32_t low = static_cast<uint32_t>(t.ref - 14);
-      uint32_t e[RT][2][BLOCKS];
-      bool ok = true;
+      const uint32_t low = static_cast<uint32_t>(t.ref - 8) * 0x01010101u;
+      uint32_t off[RT][2], out = 0u;  // scales above the window's lower end, a byte each
 #pragma unroll
-      for (int i = 0; i < RT * 2 * BLOCKS; ++i) {
-        const int rt = i / (2 * BLOCKS), h = i / BLOCKS % 2, k = i % BLOCKS;
-        e[rt][h][k] = f.s[rt][h][0] >> (8 * k) & 255u;
-        ok = ok && e[rt][h][k] - low <= 26u;
+      for (int i = 0; i < 2 * RT; ++i) {
+        off[i / 2][i % 2] = f.s[i / 2][i % 2][0] - (BLOCKS == 2 ? low & 0xffffu : low & 0xffu);
+        out |= off[i / 2][i % 2];  // a borrow leaves a byte that is out too
       }
       bool apart = false;
-      if (!__all_sync(0xffffffffu, ok)) {
+      if (__any_sync(0xffffffffu, (out & ~0x0f0fu) != 0u)) {
         uint32_t mx = 0u, mn = 255u;
 #pragma unroll
-        for (int i = 0; i < RT * 2 * BLOCKS; ++i) {
-          const uint32_t v = e[i / (2 * BLOCKS)][i / BLOCKS % 2][i % BLOCKS];
+        for (int i = 0; i < 2 * RT * BLOCKS; ++i) {
+          const uint32_t v = f.s[i / (2 * BLOCKS)][i / BLOCKS % 2][0] >> (8 * (i % BLOCKS)) & 255u;
           mx = max(mx, v);
           mn = min(mn, v);
         }
         mx = __reduce_max_sync(0xffffffffu, mx);
         mn = __reduce_min_sync(0xffffffffu, mn);
         flush(t);
-        apart = mx > mn + 26u || mn + 14u > 242u;
-        if (!apart) t.ref = static_cast<int>(mn) + 14;
+        apart = mx > mn + 15u || mn > 239u;  // (255 is NaN, and below 16 no difference wraps into the window)
+        if (!apart) {
+          t.ref = static_cast<int>(mn) + 8;
+#pragma unroll
+          for (int i = 0; i < 2 * RT; ++i)
+            off[i / 2][i % 2] = f.s[i / 2][i % 2][0] - mn * (BLOCKS == 2 ? 0x0101u : 1u);
+        }
       }
       uint32_t sc[RT][2][BLOCKS];
-      const uint32_t one = (15u - static_cast<uint32_t>(t.ref)) * 0x04000400u;
+      if (!apart) {  // 2^(offset - 8), twice: exponent field offset + 7
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int top = apart ? row_max(e[rt][h]) : 0;
-#pragma unroll
-          for (int k = 0; k < BLOCKS; ++k)  // (e - ref + 15) << 10, twice
-            sc[rt][h][k] = apart ? half_pow2(static_cast<int>(e[rt][h][k]), top) : e[rt][h][k] * 0x04000400u + one;
+        for (int i = 0; i < 2 * RT * BLOCKS; ++i) {
+          const uint32_t o = off[i / (2 * BLOCKS)][i / BLOCKS % 2];
+          sc[i / (2 * BLOCKS)][i / BLOCKS % 2][i % BLOCKS] =
+              (BLOCKS == 1 ? o : i % BLOCKS ? o >> 8 : o & 0xffu) * 0x04000400u + 0x1c001c00u;
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2 * RT; ++i) {
+          const int top = row_max(f.s[i / 2][i % 2][0]);
+#pragma unroll
+          for (int k = 0; k < BLOCKS; ++k)
+            sc[i / 2][i % 2][k] = half_pow2(static_cast<int>(f.s[i / 2][i % 2][0] >> (8 * k) & 255u), top);
+        }
+      }
       products_fp4<N>(f, sc, at, bp, t.d);
       if (apart) {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          const float f0 = e8m0(row_max(e[rt][0])), f1 = e8m0(row_max(e[rt][1]));
+          const float f0 = e8m0(row_max(f.s[rt][0][0])), f1 = e8m0(row_max(f.s[rt][1][0]));
 #pragma unroll
           for (int n = 0; n < NACC; ++n)
 #pragma unroll
@@ -488,10 +597,9 @@ struct Experts {
   }
 
   // the largest scale of a row's blocks in the k-step
-  static __device__ __forceinline__ int row_max(const uint32_t (&e)[BLOCKS]) {
-    int m = static_cast<int>(e[0]);
-#pragma unroll
-    for (int k = 1; k < BLOCKS; ++k) m = max(m, static_cast<int>(e[k]));
+  static __device__ __forceinline__ int row_max(uint32_t s) {
+    int m = static_cast<int>(s & 255u);
+    if (BLOCKS == 2) m = max(m, static_cast<int>(s >> 8 & 255u));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   }
@@ -501,7 +609,7 @@ struct Experts {
       gate = gate > a.limit ? a.limit : gate;  // NaN stays
       up = up > a.limit ? a.limit : up < -a.limit ? -a.limit : up;
     }
-    return gate / (1.0f + expf(-a.alpha * gate)) * (up + a.beta);
+    return __fdividef(gate, 1.0f + expf(-a.alpha * gate)) * (up + a.beta);
   }
 
   // One warp: the rows of subtile (rg, rt) for the tokens 8 * n .. of the unit.  `wait` is called once
@@ -534,7 +642,7 @@ struct Experts {
     wait();
     if (!rows) return;
     float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 4
     for (int k = 0; k < ksplit; ++k) {
       const float4 p = part[((rg * ksplit + k) * JOBS + rt * NACC + n) * 32 + lane];
       c.x += p.x, c.y += p.y, c.z += p.z, c.w += p.w;
@@ -590,7 +698,9 @@ struct Experts {
     nb = NB == 1 || size <= 4 ? 1 : NB == 2 || size <= 8 ? 2 : NB;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      bp[b] = (nb == 1 ? act_row(g >> 2, g & 3) : act_row(b & 1, (b >> 1) * 8 + g)) + q * 16;
+      bp[b] = (nb == 1 ? act_row(g >> 2, row_of_token(unit, g & 3))
+                       : act_row(b & 1, row_of_token(unit, (b >> 1) * 8 + g))) +
+              q * 16;
   }
 
   __device__ __forceinline__ float4* partial(uint32_t seq) const {
@@ -600,10 +710,12 @@ struct Experts {
   // Tiles [lo, hi) on a finishing warp: every ML_FINISH-th of them.
   __device__ __forceinline__ void finish_share(int lo, int hi) const {
     int u = lo / ph.tiles, tile = lo - u * ph.tiles;
+#pragma unroll 1
     for (int t = lo; t < hi; ++t) {
       const uint32_t s = cta.seq + (t - lo);
       if (static_cast<int>(s % ML_FINISH) == warp - MAIN) {
         const uint32_t unit = plan.unit[u];
+#pragma unroll 1
         for (int job = 0; job < RG * JOBS; ++job)
           finish(unit, tile, job, partial(s), [&] {
             if (job == 0)
@@ -619,75 +731,80 @@ struct Experts {
     }
   }
 
-  // The k-steps of one tile, in rounds of DEPTH; each slot of the ring is refilled as it is used.
-  __device__ __forceinline__ void tile_steps(Frag<FMT, RT> (&f)[DEPTH], Cursor& c, const uint32_t (&bp)[NB], int nb,
-                                             Sums& t) const {
-    int ks = kw;
-    for (int r = 0; r < c.rounds; ++r) {
+  // A tile's end: this warp's partial sums to the finishing warp.
+  __device__ __forceinline__ void hand_over(uint32_t s, Sums& t) const {
+    flush(t);
+    if (s >= ML_BUFS)
+      wait_or_abort(a, cta.abort, cta.empty + 8 * (s % ML_BUFS), (s / ML_BUFS - 1) & 1, DEV_TIMEOUT_EMPTY);
+    float4* part = partial(s) + warp * JOBS * 32 + lane;
 #pragma unroll
-      for (int d = 0; d < DEPTH; ++d) {
-        if (ks < ph.steps) {
-          if (NB == 1 || nb == 1)
-            products<1>(f[d], ks, bp, t);
-          else if (NB == 2 || nb == 2)
-            products<NB < 2 ? 1 : 2>(f[d], ks, bp, t);
-          else
-            products<NB>(f[d], ks, bp, t);
-        }
-        load(f[d], c);
-        ks += ksplit;
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int m = 0; m < NACC; ++m) {
+        part[(rt * NACC + m) * 32] = make_float4(t.acc[rt][m][0], t.acc[rt][m][1], t.acc[rt][m][2], t.acc[rt][m][3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t.acc[rt][m][j] = 0.f;
       }
-    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(cta.full + 8 * (s % ML_BUFS));
   }
 
   // Tiles [lo, hi) on a main warp; the fragments of the first DEPTH steps are in f.
   __device__ __forceinline__ void main_share(int lo, int hi, Frag<FMT, RT> (&f)[DEPTH], Cursor& c) const {
     int u = lo / ph.tiles, tile = lo - u * ph.tiles;
-    uint32_t unit = plan.unit[u];
-    stage(unit);
-    main_warps_sync<MAIN>();
-    uint32_t bp[NB];
-    int nb;
-    aim_columns(unit, bp, nb);
     Sums t = {};
     t.ref = 127;
-    int pu = u, pt = tile, pn = lo;  // the next tile to prefetch
-    for (int n = lo; n < hi; ++n) {
-      if (threadIdx.x == 0) {
-        for (; pn < hi && pn <= n + ph.ahead; ++pn) {
-          if (pn > n) prefetch(pu, pt);
-          if (++pt == ph.tiles) {
-            pt = 0;
-            ++pu;
-          }
-        }
-      }
-      if (tile == ph.tiles) {
-        tile = 0;
-        unit = plan.unit[++u];
+    uint32_t s = cta.seq;
+    int n = lo;
+#pragma unroll 1
+    while (n < hi) {  // a segment
+      const uint32_t unit = plan.unit[u];
+      if (!(PHASE == 1 && a.all_rows)) {
         main_warps_sync<MAIN>();  // the old unit's rows are not read any more
         stage(unit);
         main_warps_sync<MAIN>();
-        aim_columns(unit, bp, nb);
       }
-      ++tile;
-      tile_steps(f, c, bp, nb, t);
-      flush(t);
-      const uint32_t s = cta.seq + (n - lo);
-      if (s >= ML_BUFS)
-        wait_or_abort(a, cta.abort, cta.empty + 8 * (s % ML_BUFS), (s / ML_BUFS - 1) & 1, DEV_TIMEOUT_EMPTY);
-      float4* part = partial(s) + warp * JOBS * 32 + lane;
+      uint32_t bp[NB];
+      int nb;
+      aim_columns(unit, bp, nb);
+      const int end = min(hi, n + ph.tiles - tile);
+      int steps = (end - n) * c.nk, i = 0, ks = kw;
+      if (threadIdx.x == 0 && n == lo && ph.ahead && tile + 1 < ph.tiles && n + 1 < end) prefetch(u, tile + 1);
+#pragma unroll 1
+      for (int r = whole_rounds(steps); r > 0; r -= DEPTH) {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int m = 0; m < NACC; ++m) {
-          part[(rt * NACC + m) * 32] =
-              make_float4(t.acc[rt][m][0], t.acc[rt][m][1], t.acc[rt][m][2], t.acc[rt][m][3]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) t.acc[rt][m][j] = 0.f;
+        for (int d = 0; d < DEPTH; ++d) {
+          const bool live = steps > 0;
+          if (live && ks < ph.steps) {
+            if (NB == 1 || nb == 1)
+              products<1>(f[d], ks, bp, t);
+            else if (NB == 2 || nb == 2)
+              products<NB < 2 ? 1 : 2>(f[d], ks, bp, t);
+            else
+              products<NB>(f[d], ks, bp, t);
+          }
+          load(f[d], c);
+          --steps;
+          ks += ksplit;
+          if (live && ++i == c.nk) {
+            i = 0;
+            ks = kw;
+            ++tile;
+            // the tile after the next into L2, or the next unit's first
+            if (threadIdx.x == 0 && ph.ahead && n + 2 < hi) {
+              if (tile + 1 < ph.tiles)
+                prefetch(u, tile + 1);
+              else
+                prefetch(u + 1, tile + 1 - ph.tiles < ph.tiles ? tile + 1 - ph.tiles : 0);
+            }
+            hand_over(s, t);
+            ++s;
+            ++n;
+          }
         }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(cta.full + 8 * (s % ML_BUFS));
+      }
+      tile = 0;
+      ++u;
     }
   }
 
@@ -698,8 +815,10 @@ struct Experts {
       c.u = lo / ph.tiles;
       c.tile = lo - c.u * ph.tiles;
       c.left = hi - lo;
-      c.rounds = (ph.steps + ksplit * DEPTH - 1) / (ksplit * DEPTH);
+      c.nk = (ph.steps + ksplit - 1) / ksplit;
       c.i = 0;
+      c.steps = 0;
+      c.slots = 0;
       c.k = 0;
       c.w = ph.w;
       c.s = ph.s;
@@ -707,7 +826,7 @@ struct Experts {
 #pragma unroll
       for (int d = 0; d < DEPTH; ++d) load(f[d], c);
       if (done) wait_stage(a, cta.abort, done, shares);
-      if (lo < hi) main_share(lo, hi, f, c);
+      main_share(lo, hi, f, c);
     } else {
       if (done) wait_stage(a, cta.abort, done, shares);
       finish_share(lo, hi);
@@ -715,6 +834,31 @@ struct Experts {
     cta.seq += hi - lo;
   }
 };
+
+// h of token t at columns j and j + 1: the arithmetic of moe.cuh, a batch of slots' loads at a time.
+__device__ __forceinline__ void combine2(const MoeLayerArgs& a, int t, int j) {
+  constexpr int BATCH = 8;
+  float r0 = 0.f, r1 = 0.f, s0 = 0.f, s1 = 0.f;
+  const uint32_t x = *reinterpret_cast<const uint32_t*>(a.x + static_cast<int64_t>(t) * a.H + j);
+  for (int b = 0; b < a.S; b += BATCH) {
+    float2 y[BATCH];
+    float w[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (b + i < a.S) {
+        y[i] = __ldcg(reinterpret_cast<const float2*>(a.slots + static_cast<int64_t>(t * a.S + b + i) * a.H + j));
+        w[i] = __ldcg(a.slot_w + t * a.S + b + i);
+      }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (b + i < a.S) {
+        moe_accumulate(b + i, a.topk, w[i], y[i].x, r0, s0);
+        moe_accumulate(b + i, a.topk, w[i], y[i].y, r1, s1);
+      }
+  }
+  *reinterpret_cast<uint32_t*>(a.h_out + static_cast<int64_t>(t) * a.H + j) =
+      moe_finish(x & 0xffffu, r0, s0) | (moe_finish(x >> 16, r1, s1) << 16);
+}
 
 template <int FMT, int RT, int NB, int DEPTH, int MAIN>
 __global__ void __launch_bounds__(32 * (MAIN + ML_FINISH), 1)
@@ -737,7 +881,7 @@ __global__ void __launch_bounds__(32 * (MAIN + ML_FINISH), 1)
   cta.plan.nunits = -1;
   uint8_t* rows = smem + ((plan_bytes(pairs) + 127) & ~127);
   cta.act = smem_u32(rows);
-  cta.red = reinterpret_cast<float4*>(rows + ((2 * a.G * max(ph1.pitch, ph2.pitch) + 127) & ~127));
+  cta.red = reinterpret_cast<float4*>(rows + ((2 * a.R * max(ph1.pitch, ph2.pitch) + 127) & ~127));
   cta.full = smem_u32(s_bar);
   cta.empty = cta.full + 8 * ML_BUFS;
   cta.abort = &s_abort;
@@ -749,60 +893,60 @@ __global__ void __launch_bounds__(32 * (MAIN + ML_FINISH), 1)
     }
     fence_mbar_init();
     s_abort = 0;
+    pdl_wait();  // the run before may still use the shared words
     s_ticket = atomicAdd(&a.ctl->ticket, 1u);
+  } else {
+    pdl_wait();
   }
   __syncthreads();
   const uint32_t n = gridDim.x, last = (a.h_out ? 4u : 3u) * n;
   uint32_t ticket = s_ticket;
+#pragma unroll 1
   while (ticket < last) {
     __syncthreads();
     if (tid == THREADS - 1) s_ticket = atomicAdd(&a.ctl->ticket, 1u);  // the next share, early
     const uint32_t stage = ticket / n;
-    const int64_t i = ticket - stage * n;
-    auto cut = [&](int64_t total, int64_t k) { return static_cast<int>(total * k / n); };
+    const uint32_t i = ticket - stage * n;
+    // the first of `total` things that belong to share k of n
+    auto cut = [&](uint32_t total, uint32_t k) {
+      const uint32_t q = total / n;
+      return static_cast<int>(q * k + (total - q * n) * k / n);
+    };
     if (stage == 0) {
-      const int64_t r = n - 1 - i;  // the tokens' statistics go to the last shares first
-      router_share(a, cut(a.E, i), cut(a.E, i + 1), cut(a.T, r), cut(a.T, r + 1), s_part);
+      const uint32_t r = n - 1 - i;  // the tokens' statistics go to the last shares first
+      router_share(a, cut(a.E, i), cut(a.E, i + 1), cut(a.T, r), cut(a.T, r + 1), reinterpret_cast<float*>(rows), s_part);
     } else if (stage == 3) {
       wait_stage(a, cta.abort, a.ctl->done + 2, n);
-      MoeIn m;
-      m.x = a.x;
-      m.slots = a.slots;
-      m.slot_dtype = 0;
-      m.w = a.slot_w;
-      m.S = a.S;
-      m.n_routed = a.topk;
       const int half = a.H / 2;
-      const int lo = cut(static_cast<int64_t>(a.T) * half, i), hi = cut(static_cast<int64_t>(a.T) * half, i + 1);
-      for (int p = lo + tid; p < hi && !s_abort; p += THREADS) {
-        const int t = p / half, j = 2 * (p - t * half);
-        const uint32_t h0 = moe_lane_h(m, t, a.H, j), h1 = moe_lane_h(m, t, a.H, j + 1);
-        *reinterpret_cast<uint32_t*>(a.h_out + static_cast<int64_t>(t) * a.H + j) = h0 | (h1 << 16);
-      }
+      const int lo = cut(a.T * half, i), hi = cut(a.T * half, i + 1);
+#pragma unroll 1
+      for (int p = lo + tid; p < hi && !s_abort; p += THREADS) combine2(a, p / half, 2 * (p % half));
     } else {
       if (cta.plan.nunits < 0) {
+        if (a.all_rows && stage == 1) Experts<FMT, RT, NB, 1, DEPTH, MAIN>(a, ph1, cta, ksplit1).stage_all(s_part);
         wait_stage(a, cta.abort, a.ctl->done, n);
-        if (!s_abort) make_plan(a, cta.plan, ticket == n);
+        if (!s_abort) make_plan(a, cta.plan);
       }
+      if (ticket == n && tid >= 32 * MAIN && !s_abort)
+#pragma unroll 1
+        for (int t = (tid >> 5) - MAIN; t < a.T; t += ML_FINISH) write_routes(a, t, cta.plan.pair_e);
       if (!s_abort) {
-        const int64_t tiles = static_cast<int64_t>(cta.plan.nunits) * (stage == 1 ? ph1.tiles : ph2.tiles);
-        if (stage == 1) {
-          Experts<FMT, RT, NB, 1, DEPTH, MAIN> x(a, ph1, cta, ksplit1);
-          x.share(cut(tiles, i), cut(tiles, i + 1), nullptr, 0u);
-        } else {
-          Experts<FMT, RT, NB, 2, DEPTH, MAIN> x(a, ph2, cta, ksplit2);
-          x.share(cut(tiles, i), cut(tiles, i + 1), a.ctl->done + 1, n);
-        }
+        const uint32_t tiles = cta.plan.nunits * (stage == 1 ? ph1.tiles : ph2.tiles);
+        const int lo = cut(tiles, i), hi = cut(tiles, i + 1);
+        if (stage == 1)
+          Experts<FMT, RT, NB, 1, DEPTH, MAIN>(a, ph1, cta, ksplit1).share(lo, hi, nullptr, 0u);
+        else
+          Experts<FMT, RT, NB, 2, DEPTH, MAIN>(a, ph2, cta, ksplit2).share(lo, hi, a.ctl->done + 1, n);
       }
     }
     __syncthreads();
-    if (tid == 0 && stage < 3) {
+    if (tid == THREADS - 32 && stage < 3) {
       __threadfence();
       atomicAdd(&a.ctl->done[stage], 1u);
     }
     ticket = s_ticket;
   }
-  if (tid == 0) {
+  if (tid == THREADS - 32) {
     __threadfence();
     if (atomicAdd(&a.ctl->left, 1u) == n - 1) {  // every other CTA is past its last use of these words
       a.ctl->ticket = 0u;
@@ -813,7 +957,7 @@ __global__ void __launch_bounds__(32 * (MAIN + ML_FINISH), 1)
 }
 
 // ---------------------------------------------------------------- host
-constexpr int AHEAD_BYTES = 64 * 1024;
+constexpr int AHEAD_BYTES = 128 * 1024;
 constexpr int STATIC_SMEM = 512;  // at least moe_layer_kernel's __shared__ variables
 
 // Main warps, steps in flight of each and 16-row groups a warp takes at a time, for a format and the
@@ -830,18 +974,13 @@ int pitch_of(int fmt, int K) {
   return (K + cols - 1) / cols * cols * 2 + 64;
 }
 
-// Warps that split K: as many as keep at least nine tenths of their rounds of k-steps busy, else those
-// that keep the most.
+// Warps that split K: as many as keep 85 % of their k-steps busy (small tiles spread evenly over the
+// SMs: with 192 rows a tile instead of 48, 8 tokens over 66 experts took 165 us instead of 136).
 int ksplit_of(int fmt, int K) {
-  const int steps = (K + step_cols(fmt) - 1) / step_cols(fmt), depth = depth_of(fmt), main = main_warps(fmt);
-  int best = 1, best_slots = (steps + depth - 1) / depth * depth;
-  for (int k = 2; k <= main; ++k) {
-    const int slots = (steps + k * depth - 1) / (k * depth) * (k * depth);
-    if (main % k == 0 && (10 * steps >= 9 * slots || slots <= best_slots)) {
-      best = k;
-      best_slots = slots;
-    }
-  }
+  const int steps = (K + step_cols(fmt) - 1) / step_cols(fmt), main = main_warps(fmt);
+  int best = 1;
+  for (int k = 2; k <= main; ++k)
+    if (main % k == 0 && 100 * steps >= 85 * ((steps + k - 1) / k * k) && (fmt == BF16 || steps >= 3 * k)) best = k;
   return best;
 }
 
@@ -867,7 +1006,7 @@ Phase make_phase(const MoeLayerArgs& a, int fmt, int nb, int phase, int ksplit) 
   p.tiles = (p.nsub + RG - 1) / RG;
   p.steps = (p.K + step_cols(fmt) - 1) / step_cols(fmt);
   p.pitch = pitch_of(fmt, p.K);
-  p.ahead = 1 + AHEAD_BYTES / (RG * RT * 16 * p.row_bytes);
+  p.ahead = RG * RT * 16 * p.row_bytes <= AHEAD_BYTES;
   return p;
 }
 
@@ -878,8 +1017,17 @@ cudaError_t launch_as(const MoeLayerArgs& a, const MoeLayerPlan& p, cudaStream_t
   auto f = moe_layer_kernel<FMT, groups_of(FMT, NB), NB, depth_of(FMT), MAIN>;
   const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
   if (e != cudaSuccess) return e;
-  f<<<p.grid, 32 * (MAIN + ML_FINISH), p.smem, stream>>>(a, ph1, ph2, p.ksplit1, p.ksplit2);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.grid);
+  cfg.blockDim = dim3(32 * (MAIN + ML_FINISH));
+  cfg.dynamicSmemBytes = p.smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f, a, ph1, ph2, p.ksplit1, p.ksplit2);
 }
 
 template <int FMT>
@@ -909,7 +1057,9 @@ MoeLayerPlan plan_moe_layer(int T, int topk, int nsh, int E, int H, int I, bool 
   for (;; --p.G) {
     const int nb = columns_of(p.G);
     const int red = ML_BUFS * main_warps(p.format) * groups_of(p.format, nb) * (nb == 4 ? 2 : 1) * 512;
-    p.smem = fixed + 2 * p.G * pitch + red;
+    p.all_rows = T <= p.G;
+    p.R = p.G;
+    p.smem = fixed + 2 * p.R * pitch + red;
     if (p.smem <= max_smem || p.G == 1) break;
   }
   p.ok = p.smem <= max_smem;

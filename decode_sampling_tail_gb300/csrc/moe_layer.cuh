@@ -75,6 +75,8 @@ struct MoeLayerArgs {
   int gated, interleaved, score;
   float alpha, beta, limit, route_scale, eps;
   int G;                  // tokens of one expert that share a pass over its weights
+  int R;                  // activation rows in shared memory: G, or all T tokens (all_rows)
+  int all_rows;           // the first product's rows are staged once, for every token
 };
 
 // ---------------------------------------------------------------- loads
@@ -168,30 +170,34 @@ __device__ __forceinline__ int unit_expert(uint32_t u) { return u & 1023; }
 __device__ __forceinline__ int unit_first(uint32_t u) { return (u >> 10) & 2047; }
 __device__ __forceinline__ int unit_size(uint32_t u) { return u >> 21; }
 
-// One warp: token t's experts and weights.
-__device__ __forceinline__ void route_token(const MoeLayerArgs& a, int t, uint16_t* pair_e, bool write) {
+// What ranks an expert's logit: softmax: z with its bias; sigmoid: sigmoid(z) with its bias.
+__device__ __forceinline__ float route_score(const MoeLayerArgs& a, float z) {
+  return a.score ? __fdividef(1.0f, 1.0f + expf(-z)) : z;
+}
+
+// One warp: token t's experts, in falling order of the score; at most 32 * PER experts.
+template <int PER>
+__device__ __forceinline__ void route_token(const MoeLayerArgs& a, int t, uint16_t* pair_e) {
   const int lane = threadIdx.x & 31;
   const float* z = a.logits + static_cast<int64_t>(t) * a.E;
-  constexpr int PER = ML_MAX_EXPERTS / 32;
   uint32_t key[PER];
-  // softmax: z with its bias ranks and weighs; sigmoid: sigmoid(z) weighs, plus the bias ranks
-  auto score = [&](float v) { return a.score ? 1.0f / (1.0f + expf(-v)) : v; };
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = i * 32 + lane;
     key[i] = 0u;  // below every score's key
-    if (i * 32 < a.E && e < a.E) {
+    if (e < a.E) {
       const float v = __ldcg(z + e);
-      key[i] = float_key(a.br ? score(v) + __ldg(a.br + e) : v);
+      key[i] = float_key(a.br ? route_score(a, v) + __ldg(a.br + e) : v);
     }
   }
   int mine = 0;
+#pragma unroll 1
   for (int j = 0; j < a.topk; ++j) {
     uint32_t best = 0u;
     int at = ML_MAX_EXPERTS - 1;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (i * 32 < a.E && key[i] > best) {
+      if (key[i] > best) {
         best = key[i];
         at = i * 32 + lane;
       }
@@ -199,16 +205,22 @@ __device__ __forceinline__ void route_token(const MoeLayerArgs& a, int t, uint16
     const int e = __reduce_min_sync(0xffffffffu, best == top ? at : ML_MAX_EXPERTS - 1);
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (i * 32 < a.E && i * 32 + lane == e) key[i] = 0u;
+      if (i * 32 + lane == e) key[i] = 0u;
     if (lane == j) mine = e;
   }
   if (lane < a.topk) pair_e[t * a.S + lane] = static_cast<uint16_t>(mine);
   if (lane < a.nsh) pair_e[t * a.S + a.topk + lane] = static_cast<uint16_t>(a.E + lane);
-  if (!write) return;
+}
+
+// One warp: token t's weights and ids to memory, its experts known.
+__device__ __forceinline__ void write_routes(const MoeLayerArgs& a, int t, const uint16_t* pair_e) {
+  const int lane = threadIdx.x & 31;
   float w = 0.f;
+  int e = 0;
   if (lane < a.topk) {
-    const float v = __ldcg(z + mine);
-    w = a.score ? score(v) : v + (a.br ? __ldg(a.br + mine) : 0.f);
+    e = pair_e[t * a.S + lane];
+    const float v = __ldcg(a.logits + static_cast<int64_t>(t) * a.E + e);
+    w = a.score ? route_score(a, v) : v + (a.br ? __ldg(a.br + e) : 0.f);
   }
   if (!a.score) {  // the first is the largest
     const float top = __shfl_sync(0xffffffffu, w, 0);
@@ -220,20 +232,28 @@ __device__ __forceinline__ void route_token(const MoeLayerArgs& a, int t, uint16
   if (lane < a.topk) a.slot_w[t * a.S + lane] = a.route_scale * w / sum;
   if (lane < a.nsh) a.slot_w[t * a.S + a.topk + lane] = 1.0f;
   if (a.ids) {
-    if (lane < a.topk) a.ids[t * a.S + lane] = mine;
+    if (lane < a.topk) a.ids[t * a.S + lane] = e;
     if (lane < a.nsh) a.ids[t * a.S + a.topk + lane] = a.E + lane;
   }
 }
 
 // The whole CTA.
-__device__ __forceinline__ void make_plan(const MoeLayerArgs& a, MoePlan& p, bool write) {
+__device__ __forceinline__ void make_plan(const MoeLayerArgs& a, MoePlan& p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nt = blockDim.x, nw = nt >> 5;
   const int pairs = a.T * a.S, p8 = (pairs + 7) & ~7;
+#pragma unroll 1
   for (int i = tid; i < ML_MAX_EXPERTS; i += nt) p.cnt[i] = 0u;
   if (tid < p8 - pairs) p.pair_e[pairs + tid] = 0xffffu;
-  for (int t = warp; t < a.T; t += nw) route_token(a, t, p.pair_e, write);
+#pragma unroll 1
+  for (int t = warp; t < a.T; t += nw) {
+    if (a.E <= 128)
+      route_token<4>(a, t, p.pair_e);
+    else
+      route_token<ML_MAX_EXPERTS / 32>(a, t, p.pair_e);
+  }
   __syncthreads();
+#pragma unroll 1
   for (int i = tid; i < pairs; i += nt) atomicAdd(&p.cnt[p.pair_e[i]], 1u);
   __syncthreads();
   // the pairs (low half) and the units (high half) before each expert; a thread takes two experts
@@ -254,6 +274,7 @@ __device__ __forceinline__ void make_plan(const MoeLayerArgs& a, MoePlan& p, boo
   if (lane == 31) p.red[warp] = incl;
   __syncthreads();
   uint32_t before = incl - v, total = 0u;
+#pragma unroll 1
   for (int w = 0; w < nw; ++w) {
     const uint32_t r = p.red[w];
     if (w < warp) before += r;
@@ -263,7 +284,8 @@ __device__ __forceinline__ void make_plan(const MoeLayerArgs& a, MoePlan& p, boo
     auto write_units = [&](uint32_t e, uint32_t n, uint32_t at) {
       p.cnt[e] = at & 0xffffu;
       uint32_t u = at >> 16;
-      for (uint32_t f = 0; f < n; f += a.G, ++u)
+  #pragma unroll 1
+    for (uint32_t f = 0; f < n; f += a.G, ++u)
         p.unit[u] = e | (((at & 0xffffu) + f) << 10) | (min(n - f, static_cast<uint32_t>(a.G)) << 21);
     };
     write_units(2 * tid, n0, before);
@@ -272,15 +294,18 @@ __device__ __forceinline__ void make_plan(const MoeLayerArgs& a, MoePlan& p, boo
   p.nunits = static_cast<int>(total >> 16);
   __syncthreads();
   // a pair's place: the pairs of its expert before it
+#pragma unroll 1
   for (int i = tid; i < pairs; i += nt) {
     const uint32_t e = p.pair_e[i], ee = e | (e << 16);
     uint32_t at = p.cnt[e];
     int j = 0;
+#pragma unroll 1
     for (; j + 8 <= i; j += 8) {
       const uint4 q = *reinterpret_cast<const uint4*>(p.pair_e + j);
       at += (__popc(__vcmpeq2(q.x, ee)) + __popc(__vcmpeq2(q.y, ee)) + __popc(__vcmpeq2(q.z, ee)) +
              __popc(__vcmpeq2(q.w, ee))) >> 4;
     }
+#pragma unroll 1
     for (; j < i; ++j) at += p.pair_e[j] == e ? 1u : 0u;
     p.list[at] = static_cast<uint16_t>(i);
   }

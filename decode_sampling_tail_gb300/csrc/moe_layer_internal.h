@@ -12,6 +12,8 @@ struct MoeLayerPlan {
   bool ok;
   int format;   // Format of moe_layer.cu
   int G;        // tokens of one expert that share a pass over its weights
+  int R;        // activation rows in shared memory
+  int all_rows; // every token's rows of the first product stay there
   int smem;     // dynamic shared memory of the expert kernels
   int grid;
   int ksplit1, ksplit2;  // warps that split the columns of W1's and W2's rows
