@@ -98,11 +98,39 @@ __device__ __forceinline__ int64_t exp_fixed(float l, float m, ExpScale c, const
   return r > 0 ? (mant + (int64_t(1) << (r - 1))) >> r : mant;
 }
 
-// exp((l - m) / T) as fp64 (a few values a row).
+// exp((l - m) / T) in fp32, scale = log2(e) / T: a relative error of a few 2^-24 times the exponent's
+// size.  l == m gives 1.
+__device__ __forceinline__ float exp_fast(float l, float m, float scale) {
+  const float e = exp2f((l - m) * scale);
+  return l == m ? 1.0f : l == -INFINITY ? 0.0f : e;
+}
+
+// 2^e as fp64, e a normal exponent.
+__device__ __forceinline__ double pow2_double(int e) {
+  return __longlong_as_double(static_cast<long long>(1023 + e) << 52);
+}
+
+// exp((l - m) / T) as fp64 (a few values a row: fp64 is slow here).
 __device__ __forceinline__ double exp_double(float l, float m, ExpScale c, const float2* table) {
   int n;
   const int64_t mant = exp_mant(l, m, c, table, n);
-  return ldexp(static_cast<double>(mant), n - EXP_MANT_BITS);
+  return static_cast<double>(mant) * pow2_double(n - EXP_MANT_BITS);
+}
+
+// s * exp((l - m) / T) for s >= 0 in units of 2^-from, in units of 2^-to (rounded down).
+__device__ __forceinline__ int64_t scale_fixed(int64_t s, int from, float l, float m, ExpScale c, const float2* table,
+                                               int to) {
+  int n;
+  const uint64_t mant = static_cast<uint64_t>(exp_mant(l, m, c, table, n));
+  const uint64_t hi = __umul64hi(static_cast<uint64_t>(s), mant), lo = static_cast<uint64_t>(s) * mant;
+  const int r = from + EXP_MANT_BITS - n - to;  // bits to drop; at least 52
+  if (r >= 128) return 0;
+  return static_cast<int64_t>(r >= 64 ? hi >> (r - 64) : (hi << (64 - r)) | (lo >> r));
+}
+
+// The largest integer at most u * total: an integer sum S exceeds u * total iff it exceeds this.
+__device__ __forceinline__ int64_t draw_threshold(float u, int64_t total) {
+  return __double2ll_rd(static_cast<double>(u) * static_cast<double>(total));
 }
 
 // q * (zh + zl) rounded to a multiple of 2^-shift (q * z < 2^(62 - shift)).

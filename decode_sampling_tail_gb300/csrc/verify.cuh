@@ -61,6 +61,23 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v) {  // inclusive
   return v;
 }
 
+// Launches with programmatic dependent launch: the kernel's start overlaps the end of the one before
+// it, up to its pdl_wait.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(VERIFY_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // A sequence's tokens around its settled row: the drafts before it, -1 behind it; its own token is
 // written by whoever drew it.
 __device__ __forceinline__ void write_sequence(int lo, int hi, int sel, const int32_t* drafts, int32_t* out_tokens,

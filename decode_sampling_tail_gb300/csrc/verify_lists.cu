@@ -67,44 +67,36 @@ __device__ __forceinline__ Chunks sum_chunks(const int64_t* w, int n) {
   return c;
 }
 
-// The smallest i whose running sum S_i satisfies S_i > t (strict) or S_i >= t; n when there is none.
-// *sum receives S_i.
-template <bool STRICT>
-__device__ __forceinline__ int first_above(const Chunks& c, double t, int64_t* sum) {
-  auto over = [&](int64_t s) { return STRICT ? static_cast<double>(s) > t : static_cast<double>(s) >= t; };
+// The smallest i whose running sum S_i exceeds t; n when there is none.  *sum receives S_i.
+__device__ __forceinline__ int first_above(const Chunks& c, int64_t t, int64_t* sum) {
   const int lane = threadIdx.x & 31;
-  const uint32_t who = __ballot_sync(0xffffffffu, over(c.incl));
+  const uint32_t who = __ballot_sync(0xffffffffu, c.incl > t);
   if (who == 0u) return c.n;
   const int src = __ffs(who) - 1;
   const int64_t upto = __shfl_sync(0xffffffffu, c.incl, src > 0 ? src - 1 : 0);
   const int i = src * c.E + lane;
-  const int64_t S = (src > 0 ? upto : 0) + warp_scan(lane < c.E && i < c.n ? c.w[i] : 0);
-  const uint32_t in = __ballot_sync(0xffffffffu, lane < c.E && i < c.n && over(S));
+  const bool mine = lane < c.E && i < c.n;
+  const int64_t S = (src > 0 ? upto : 0) + warp_scan(mine ? c.w[i] : 0);
+  const uint32_t in = __ballot_sync(0xffffffffu, mine && S > t);
   if (in == 0u) return c.n;  // not reached: the chunk's last sum is the one that was found
   *sum = __shfl_sync(0xffffffffu, S, __ffs(in) - 1);
   return src * c.E + __ffs(in) - 1;
 }
 
-// The draw: the smallest i with u * total < S_i; past the end (u >= 1) the last candidate with weight.
+// The draw: the smallest i with weight and u * total < S_i; past the end (u >= 1) the last with weight.
 __device__ __forceinline__ int draw(const Chunks& c, float u) {
   int64_t s;
-  const int i = first_above<true>(c, static_cast<double>(u) * static_cast<double>(c.total), &s);
+  const int i = first_above(c, draw_threshold(u, c.total), &s);
   if (i < c.n && c.w[i] > 0) return i;
-  int best = -1;
+  const bool past = i >= c.n;  // else u < 0, before the first weight
+  int v = past ? -1 : 0x7fffffff;
   for (int j = threadIdx.x & 31; j < c.n; j += 32)
-    if (c.w[j] > 0) {
-      if (best < 0 || i >= c.n) best = j;  // u < 0 lands before the first weight: take that one
-    }
-  const uint32_t has = __ballot_sync(0xffffffffu, best >= 0);
-  if (has == 0u) return -1;
-  int v = i >= c.n ? best : (best < 0 ? 0x7fffffff : best);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const int t = __shfl_xor_sync(0xffffffffu, v, o);
-    v = i >= c.n ? max(v, t) : min(v, t);
-  }
-  return v;
+    if (c.w[j] > 0) v = past ? max(v, j) : min(v, j);
+  v = past ? __reduce_max_sync(0xffffffffu, v) : __reduce_min_sync(0xffffffffu, v);
+  return v >= 0 && v < c.n ? v : -1;
 }
+
+constexpr int BATCH = 8;  // candidates whose loads a lane has under way together
 
 __global__ void __launch_bounds__(VERIFY_THREADS) verify_lists_kernel(const VerifyArgs a) {
   extern __shared__ __align__(16) int64_t s_w[];  // [VERIFY_WARPS][k]
@@ -113,6 +105,7 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_lists_kernel(const Veri
   __shared__ int32_t s_token[VERIFY_WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid < EXP_TABLE) s_table[tid] = EXP2_TABLE[tid];
+  pdl_wait();
   int lo, hi;
   sequence_rows(a.cu, blockIdx.x, a.rows, lo, hi);
   int64_t* w = s_w + static_cast<int64_t>(warp) * a.k;
@@ -142,21 +135,38 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_lists_kernel(const Veri
         const ExpScale c = exp_scale(p.temp);
         int64_t ex = 0;
         int at = k;
-        for (int i = lane; i < kk; i += 32) {
-          const int64_t e = exp_fixed(vals[i], l0, c, s_table, 52);
-          w[i] = e;
-          if (idx[i] == x && !bonus) {
-            at = i;
-            ex = e;
+        auto weigh = [&] {
+          for (int i0 = lane; i0 < kk; i0 += 32 * BATCH) {
+            float v[BATCH];
+            int32_t id[BATCH];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+              const int i = i0 + 32 * b;
+              v[b] = i < kk ? __ldg(vals + i) : 0.f;
+              id[b] = i < kk ? __ldg(idx + i) : 0;
+            }
+#pragma unroll 2
+            for (int b = 0; b < BATCH; ++b) {
+              const int i = i0 + 32 * b;
+              if (i < kk) {
+                const int64_t e = exp_fixed(v[b], l0, c, s_table, 52);
+                w[i] = e;
+                if (id[b] == x && !bonus) {
+                  at = i;
+                  ex = e;
+                }
+              }
+            }
           }
-        }
-        __syncwarp();
+          __syncwarp();
+        };
+        weigh();
         Chunks ch = sum_chunks(w, kk);
         int m = kk;
-        if (p.top_p < 1.0f) {
-          int64_t cm = ch.total;
-          const int i = first_above<false>(
-              ch, static_cast<double>(p.top_p) * static_cast<double>(ch.total), &cm);
+        if (p.top_p < 1.0f) {  // the first candidate whose sum reaches top_p of all
+          int64_t cm;
+          const double cut = static_cast<double>(p.top_p) * static_cast<double>(ch.total);
+          const int i = first_above(ch, __double2ll_ru(cut) - 1, &cm);
           if (i < kk) m = i + 1;
           if (m < kk) ch = sum_chunks(w, m);  // the kept prefix alone
         }
@@ -165,18 +175,29 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_lists_kernel(const Veri
           ok = __any_sync(0xffffffffu, at < m && t < static_cast<double>(ex));
         }
         if (!ok && !bonus && ch.total > 0) {  // the residual max(P - q, 0), in the same units
-          const double total = static_cast<double>(ch.total);
+          const float zh = static_cast<float>(ch.total), zl = static_cast<float>(ch.total - static_cast<int64_t>(zh));
           __syncwarp();  // the list's weights have been read
-          for (int i = lane; i < m; i += 32) {
-            const float q = a.q.p ? draft_prob(a.q, row, idx[i]) : (idx[i] == x ? 1.f : 0.f);
-            const int64_t r = w[i] - __double2ll_rn(static_cast<double>(q) * total);
-            w[i] = r > 0 ? r : 0;
+          for (int i0 = lane; i0 < m; i0 += 32 * BATCH) {
+            float q[BATCH];
+            int32_t id[BATCH];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) id[b] = i0 + 32 * b < m ? __ldg(idx + i0 + 32 * b) : -1;
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b)
+              q[b] = a.q.p ? draft_prob(a.q, row, id[b]) : (id[b] == x ? 1.f : 0.f);
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+              const int i = i0 + 32 * b;
+              if (i < m) {
+                const int64_t r = w[i] - prod_fixed(q[b], zh, zl, 1.f);
+                w[i] = r > 0 ? r : 0;
+              }
+            }
           }
           __syncwarp();
           ch = sum_chunks(w, m);
           if (ch.total == 0) {  // q covers P: the draw is from P itself
-            for (int i = lane; i < m; i += 32) w[i] = exp_fixed(vals[i], l0, c, s_table, 52);
-            __syncwarp();
+            weigh();
             ch = sum_chunks(w, m);
           }
         }
@@ -243,8 +264,7 @@ extern "C" int tail_verify(int32_t rows, int32_t nseq, int32_t k, const float* t
     e = cudaFuncSetAttribute(verify_lists_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              VERIFY_WARPS * MAX_K * static_cast<int>(sizeof(int64_t)));
   if (e != cudaSuccess) return cuda_fail(e, "tail_verify: shared memory opt-in");
-  verify_lists_kernel<<<nseq, VERIFY_THREADS, smem, static_cast<cudaStream_t>(stream)>>>(a);
-  e = cudaGetLastError();
+  e = launch_overlapped(verify_lists_kernel, dim3(nseq), smem, static_cast<cudaStream_t>(stream), a);
   if (e != cudaSuccess) return cuda_fail(e, "tail_verify: kernel launch");
   return TAIL_OK;
 }

@@ -7,7 +7,8 @@ from __future__ import annotations
 
 import ctypes
 
-from . import TAIL_BF16, TAIL_ERR_UNSUPPORTED, TAIL_MXFP4, TAIL_OK, TailError, _ptr, _stream_ptr, lib, tail_moe_config
+from . import TAIL_BF16, TAIL_MXFP4, TAIL_OK, TailError, lib, tail_moe_config
+from ._args import allocating_on, fail, need, need_opt, raw_stream
 
 WEIGHTS = {"bf16": TAIL_BF16, "mxfp4": TAIL_MXFP4}
 ACTS = {"glu": 0, "relu2": 1}
@@ -32,10 +33,8 @@ class Moe:
         self.device = device
         h = ctypes.c_void_p()
         rc = lib().tail_moe_create(ctypes.byref(self.cfg), device, ctypes.byref(h))
-        if rc == TAIL_ERR_UNSUPPORTED:
-            raise TailError(rc, "tail_moe_create [" + lib().tail_last_error().decode() + "]")
         if rc != TAIL_OK:
-            raise TailError(rc, "tail_moe_create")
+            fail(rc, "tail_moe_create")
         self.h = h.value
 
     def close(self):
@@ -55,12 +54,6 @@ class Moe:
     def __exit__(self, *exc):
         self.close()
 
-    def _need(self, t, what, dtype, shape):
-        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device.type != "cuda" \
-                or t.device.index != self.device:
-            raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on cuda:{self.device}; got "
-                             f"{t.dtype}, {tuple(t.shape)}, strides {t.stride()}, {t.device}")
-
     def run(self, x, gamma, router_w, w1, w2, *, router_bias=None, w1_scale=None, w2_scale=None, b1=None, b2=None,
             out_hidden=None, out_slots=None, out_slot_w=None, out_ids=None, stream=None):
         """One run over x [T, H] bfloat16 (tail_moe_run).  gamma [H] float32 or None (x is already normalised),
@@ -70,44 +63,33 @@ class Moe:
         import torch
         if not self.h:
             raise ValueError("the handle is closed")
-        c = self.cfg
-        if x.dim() != 2 or not 0 <= int(x.shape[0]) <= c.t_max:
+        c, d = self.cfg, self.device
+        if x.dim() != 2 or x.shape[0] > c.t_max:
             raise ValueError(f"x must be [T, {c.H}] with T <= {c.t_max}; got {tuple(x.shape)}")
-        T, H, I, E, n, S = int(x.shape[0]), c.H, c.I, c.E, c.E + c.n_shared, c.topk + c.n_shared
+        T, H, I, E, n, S = x.shape[0], c.H, c.I, c.E, c.E + c.n_shared, c.topk + c.n_shared
         N1 = 2 * I if c.act == 0 else I
-        bf16, f32 = torch.bfloat16, torch.float32
-        self._need(x, "x", bf16, (T, H))
-        self._need(router_w, "router_w", bf16, (E, H))
+        bf16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
         if c.weight_dtype == TAIL_MXFP4:
             if w1_scale is None or w2_scale is None:
                 raise ValueError("mxfp4 weights need w1_scale and w2_scale")
-            self._need(w1, "w1", torch.uint8, (n, N1, H // 2))
-            self._need(w2, "w2", torch.uint8, (n, H, I // 2))
-            self._need(w1_scale, "w1_scale", torch.uint8, (n, N1, H // 32))
-            self._need(w2_scale, "w2_scale", torch.uint8, (n, H, I // 32))
+            p1, p2 = need(w1, "w1", u8, (n, N1, H // 2), d), need(w2, "w2", u8, (n, H, I // 2), d)
+            s1 = need(w1_scale, "w1_scale", u8, (n, N1, H // 32), d)
+            s2 = need(w2_scale, "w2_scale", u8, (n, H, I // 32), d)
         else:
             if w1_scale is not None or w2_scale is not None:
                 raise ValueError("bf16 weights take no scales")
-            self._need(w1, "w1", bf16, (n, N1, H))
-            self._need(w2, "w2", bf16, (n, H, I))
-        for t, what, shape in ((gamma, "gamma", (H,)), (router_bias, "router_bias", (E,)), (b1, "b1", (n, N1)),
-                               (b2, "b2", (n, H)), (out_slots, "out_slots", (T, S, H)),
-                               (out_slot_w, "out_slot_w", (T, S))):
-            if t is not None:
-                self._need(t, what, f32, shape)
-        if out_ids is not None:
-            self._need(out_ids, "out_ids", torch.int32, (T, S))
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
+            p1, p2, s1, s2 = need(w1, "w1", bf16, (n, N1, H), d), need(w2, "w2", bf16, (n, H, I), d), None, None
         if out_hidden is None and out_slots is None:
-            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), self.device)
-            with torch.cuda.stream(s):
-                out_hidden = torch.empty((T, H), dtype=bf16, device=x.device)
-        if out_hidden is not None:
-            self._need(out_hidden, "out_hidden", bf16, (T, H))
-        rc = lib().tail_moe_run(self.h, _ptr(x), _ptr(gamma), _ptr(router_w), _ptr(router_bias), _ptr(w1),
-                                _ptr(w1_scale), _ptr(b1), _ptr(w2), _ptr(w2_scale), _ptr(b2), T, _ptr(out_hidden),
-                                _ptr(out_slots), _ptr(out_slot_w), _ptr(out_ids), _stream_ptr(stream, x.device))
+            with allocating_on(stream, d):
+                out_hidden = torch.empty((T, H), dtype=bf16, device=d)
+        rc = lib().tail_moe_run(
+            self.h, need(x, "x", bf16, (T, H), d), need_opt(gamma, "gamma", f32, (H,), d),
+            need(router_w, "router_w", bf16, (E, H), d), need_opt(router_bias, "router_bias", f32, (E,), d), p1, s1,
+            need_opt(b1, "b1", f32, (n, N1), d), p2, s2, need_opt(b2, "b2", f32, (n, H), d), T,
+            need_opt(out_hidden, "out_hidden", bf16, (T, H), d),
+            need_opt(out_slots, "out_slots", f32, (T, S, H), d),
+            need_opt(out_slot_w, "out_slot_w", f32, (T, S), d), need_opt(out_ids, "out_ids", torch.int32, (T, S), d),
+            raw_stream(stream, d))
         if rc != TAIL_OK:
             raise TailError(rc, "tail_moe_run")
         return out_hidden

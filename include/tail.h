@@ -395,10 +395,11 @@ int tail_merge_shards(int32_t nshard, int32_t k_in, int32_t k, int32_t gbs, cons
  *   out_count      [nseq] int32: tokens emitted (accepted drafts + 1).
  * A row whose every candidate is -inf has nothing to draw from: its draft is refused
  * and its token is -1 (counted).  A candidate at -inf has probability 0; among logits
- * of +inf the mass is shared.  NaN is outside the domain.  Decisions and draws are
- * made with weights of 2^-36 relative error and exact sums, so they agree with 64-bit
- * arithmetic except where u lies within about 2^-36 of a boundary; they do not depend
- * on the batch.  No handle and no allocation; the current device and `stream`.
+ * of +inf the mass is shared.  NaN is outside the domain.  Draws are made with weights
+ * of 2^-36 relative error and exact sums, so they agree with 64-bit arithmetic except
+ * where u lies within about 2^-36 of a boundary (acceptances: u_accept q within 2^-36 of
+ * P, tail_verify_logits 2^-20); they do not depend on the batch.  No handle and no
+ * allocation; the current device and `stream`.
  */
 
 /*
@@ -424,7 +425,7 @@ int tail_verify(int32_t rows, int32_t nseq, int32_t k, const float* topk_vals, c
  *   temperature, u_draw  [rows] fp32.
  *   workspace      device memory of tail_verify_logits_workspace(rows, nseq, V) bytes, 16-byte
  *                  aligned, any contents; calls that may overlap need one each.
- * Two launches.  Limits: V <= 1048576, rows and nseq <= 65535 (TAIL_ERR_UNSUPPORTED beyond).
+ * Three launches.  Limits: V <= 1048576, rows and nseq <= 65535 (TAIL_ERR_UNSUPPORTED beyond).
  */
 int tail_verify_logits_workspace(int32_t rows, int32_t nseq, int32_t V, int64_t* bytes);
 int tail_verify_logits(int32_t rows, int32_t nseq, int32_t V, const void* logits, int32_t logits_dtype,
