@@ -7,14 +7,13 @@
 //     in fp32.  Every row has to be read, since which one is settled is not known yet; this pass is
 //     bound by memory and only has to decide acceptances (a relative 2^-21 of Z).
 //   verify_settle (chunk, sequence): each CTA judges the sequence's rows from those statistics (all
-//     of them compute the same bits, none waits) and finds the settled row; then the chunk's sum of that
-//     row alone as an integer (fixed_exp.cuh, units of 2^-49: 8192 of at most 1 stay below 2^63).
+//     of them compute the same bits, none waits) and finds the settled row; then the sums of that row's
+//     segments (1024 columns, a warp's part) as integers (fixed_exp.cuh, units of 2^-49 relative to m_c).
 //   verify_draw (chunk, sequence): after d accepted drafts, or with one-hot drafts (P without x_j), the
-//     chunk sums already say which chunk holds the token, and that chunk's CTA alone reads its columns
-//     again.  The residual max(P - q, 0) needs one pass over that row's l and q: every CTA sums its
-//     chunk, the last of the sequence to finish (a counter that verify_settle cleared) picks the chunk
-//     and the token.
-// Sums over chunks are integers of 2^-shift relative to the row's maximum, with V 2^shift below 2^62;
+//     segments' sums already say which one holds the token; one CTA reads its columns again.  The
+//     residual max(P - q, 0) needs one pass over that row's l and q: every CTA sums its chunk's segments,
+//     the last of the sequence to finish (a counter that verify_settle cleared) picks one and the token.
+// Sums over segments are integers of 2^-shift relative to the row's maximum, with V 2^shift below 2^62;
 // the residual is max(e - q Z, 0) in the same units.  The draft's row is read only for sequences that
 // refuse a draft.
 #include "../../include/tail.h"
@@ -30,8 +29,8 @@ constexpr int VL_WARP_COLS = 128 * VL_GROUPS;                 // a warp's column
 constexpr int VL_CHUNK = VL_WARP_COLS * VERIFY_WARPS;         // 8192
 constexpr int VL_SHIFT = 49;
 constexpr int VL_MAX_V = 1 << 20;
-constexpr int VL_MAX_CHUNKS = (VL_MAX_V + 3) / VL_CHUNK + 1;  // a thread each in the draw kernel
-static_assert(VL_MAX_CHUNKS <= VERIFY_THREADS, "one thread a chunk");
+constexpr int VL_MAX_CHUNKS = (VL_MAX_V + 3) / VL_CHUNK + 1;
+constexpr int VL_MAX_SEGS = VL_MAX_CHUNKS * VERIFY_WARPS;
 constexpr int VL_MAX_ROWS = 65535;                            // a grid dimension
 
 struct ChunkStat {
@@ -59,8 +58,8 @@ struct LogitsArgs {
   const float* u;
   DraftProbs q;
   ChunkStat* stats;    // [rows][nchunk]
-  int64_t* sums;       // [nseq][nchunk] the settled row's chunk sums, units of 2^-49 relative to m_c
-  int64_t* rsum;       // [nseq][nchunk] its residual sums
+  int64_t* sums;       // [nseq][nseg] the settled row's segment sums, units of 2^-49 relative to m_c
+  int64_t* rsum;       // [nseq][nseg] its residual sums
   Settled* settled;    // [nseq]
   uint32_t* done;      // [nseq] CTAs whose residual sum is written
   int32_t* tokens;
@@ -97,12 +96,12 @@ __device__ __forceinline__ void unpack4(const __nv_bfloat16* p, float (&v)[4]) {
 // A thread's groups of 4 columns of a row, at col0 + 128 i; `fill` outside [0, V).  All vector loads are
 // under way together; a group across a row's end takes single loads, and so do rows that do not lie on
 // whole vectors (draft probabilities whose rows start elsewhere than the logits').
-template <typename T>
-__device__ __forceinline__ void load_groups(const T* row, int col0, int V, float fill, float (&v)[VL_GROUPS][4]) {
+template <typename T, int N>
+__device__ __forceinline__ void load_groups(const T* row, int col0, int V, float fill, float (&v)[N][4]) {
   const bool whole = (reinterpret_cast<uintptr_t>(row + col0) & (4 * sizeof(T) - 1)) == 0;
   bool rest = false;
 #pragma unroll
-  for (int i = 0; i < VL_GROUPS; ++i) {
+  for (int i = 0; i < N; ++i) {
     const int col = col0 + i * 128;
     const bool inside = col >= 0 && col + 4 <= V;
 #pragma unroll
@@ -112,7 +111,7 @@ __device__ __forceinline__ void load_groups(const T* row, int col0, int V, float
   }
   if (!rest) return;
 #pragma unroll
-  for (int i = 0; i < VL_GROUPS; ++i)
+  for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int col = col0 + i * 128;
@@ -172,14 +171,12 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_stats_kernel(const Logi
     for (int e = 0; e < 4; ++e) m = fmaxf(m, v[i][e]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) s_max[warp] = m;
-  __syncthreads();
-  m = s_max[0];
-#pragma unroll
-  for (int w = 1; w < VERIFY_WARPS; ++w) m = fmaxf(m, s_max[w]);
+  // each warp relative to its own maximum: no barrier between the loads and the exponentials
+  const bool greedy = !(temp > 0.0f);
+  const float scale = greedy ? 0.f : exp_scale(temp).h;
   float sum = 0.f;
   int arg = a.V;
-  if (!(temp > 0.0f)) {
+  if (greedy) {
 #pragma unroll
     for (int i = VL_GROUPS - 1; i >= 0; --i)
 #pragma unroll
@@ -187,7 +184,6 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_stats_kernel(const Logi
         if (v[i][e] == m && col0 + i * 128 + e >= 0) arg = col0 + i * 128 + e;
     arg = __reduce_min_sync(0xffffffffu, arg);
   } else if (m != -INFINITY) {
-    const float scale = exp_scale(temp).h;
 #pragma unroll
     for (int i = 0; i < VL_GROUPS; ++i)
 #pragma unroll
@@ -196,17 +192,21 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_stats_kernel(const Logi
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
   if (lane == 0) {
+    s_max[warp] = m;
     s_sum[warp] = sum;
     s_arg[warp] = arg;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    ChunkStat st = {m, 0.f, a.V, 0};
-    for (int w = 0; w < VERIFY_WARPS; ++w) {
-      st.sum += s_sum[w];
-      st.arg = min(st.arg, s_arg[w]);
-    }
-    a.stats[static_cast<int64_t>(row) * a.nchunk + c] = st;
+  if (warp == 0) {
+    const float mw = lane < VERIFY_WARPS ? s_max[lane] : -INFINITY;
+    float top = mw;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float z = mw > -INFINITY && !greedy ? s_sum[lane] * exp_fast(mw, top, scale) : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    const int at = __reduce_min_sync(0xffffffffu, lane < VERIFY_WARPS && mw == top ? s_arg[lane] : a.V);
+    if (lane == 0) a.stats[static_cast<int64_t>(row) * a.nchunk + c] = ChunkStat{top, z, at, 0};
   }
 }
 
@@ -272,7 +272,6 @@ template <typename T>
 __global__ void __launch_bounds__(VERIFY_THREADS) verify_settle_kernel(const LogitsArgs a) {
   __shared__ float2 s_table[EXP_TABLE];
   __shared__ Settled s_row[VERIFY_WARPS];
-  __shared__ int64_t s_sum[VERIFY_WARPS];
   __shared__ ChunkVals s_vals;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seq = blockIdx.y, c = blockIdx.x;
@@ -323,12 +322,7 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_settle_kernel(const Log
     }
     sum = warp_sum(sum);
   }
-  if (lane == 0) s_sum[warp] = sum;
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < VERIFY_WARPS; ++w) sum += s_sum[w];
-    a.sums[static_cast<int64_t>(seq) * a.nchunk + c] = sum;
-  }
+  if (lane == 0) a.sums[(static_cast<int64_t>(seq) * a.nchunk + c) * VERIFY_WARPS + warp] = sum;
 }
 
 enum DrawMode : int {
@@ -345,115 +339,38 @@ struct Weigh {
   ExpScale sc;
 };
 
-// Shared memory of the draw kernel.
-struct DrawVals {
-  ChunkVals v;
-  float4 q[VL_GROUPS][VERIFY_THREADS];
-  int64_t g[VL_GROUPS][VERIFY_THREADS];  // the groups' sums
-};
-
 __device__ __forceinline__ int64_t weight_of(float l, float q, int col, const Weigh& g, const float2* table) {
   int64_t r = exp_fixed(l, g.max, g.sc, table, g.shift);
   if (g.mode == DRAW_RESIDUAL) r = max(r - prod_fixed(as_prob(q), g.zh, g.zl, g.scale), static_cast<int64_t>(0));
   return l == -INFINITY || (g.mode == DRAW_OTHERS && col == g.x) ? 0 : r;
 }
 
-// The whole CTA: chunk c's values, the groups' sums, and their sum over the warp.
-template <typename T>
-__device__ __noinline__ int64_t weigh_chunk(const LogitsArgs& a, int row, int c, const Weigh& g, const float2* table,
-                                            DrawVals& s) {
-  const int tid = threadIdx.x;
-  const int col0 = stage_chunk(static_cast<const T*>(a.logits) + row * a.ld, c, a.V, s.v);
-  if (g.mode == DRAW_RESIDUAL) {
-    float v[VL_GROUPS][4];
-    const int64_t o = row * a.q.ld;
-    if (a.q.dtype == 0)
-      load_groups(static_cast<const float*>(a.q.p) + o, col0, a.V, 0.f, v);
-    else if (a.q.dtype == 1)
-      load_groups(static_cast<const __half*>(a.q.p) + o, col0, a.V, 0.f, v);
-    else
-      load_groups(static_cast<const __nv_bfloat16*>(a.q.p) + o, col0, a.V, 0.f, v);
-#pragma unroll
-    for (int i = 0; i < VL_GROUPS; ++i) s.q[i][tid] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-  }
-  int64_t sum = 0;
-#pragma unroll 1
-  for (int i = 0; i < VL_GROUPS; ++i) {
-    const float4 l = s.v.l[i][tid];
-    const float4 q = g.mode == DRAW_RESIDUAL ? s.q[i][tid] : make_float4(0.f, 0.f, 0.f, 0.f);
-    const int col = col0 + i * 128;
-    const int64_t w = weight_of(l.x, q.x, col, g, table) + weight_of(l.y, q.y, col + 1, g, table) +
-                      weight_of(l.z, q.z, col + 2, g, table) + weight_of(l.w, q.w, col + 3, g, table);
-    s.g[i][tid] = w;
-    sum += w;
-  }
-  return warp_sum(sum);
-}
+// The draw kernel's columns, each value read back by the thread that wrote it, and the residual's segments.
+struct DrawVals {
+  float4 l[VL_GROUPS][VERIFY_THREADS];
+  float4 q[VL_GROUPS][VERIFY_THREADS];
+  int64_t r[VL_MAX_SEGS];
+};
 
-// The whole CTA, after weigh_chunk of chunk c (`sum` its result): the first column whose running weight
-// exceeds t, the last with any weight when none does; -1 when the chunk has no weight.
-template <typename T>
-__device__ __noinline__ int find_column(const LogitsArgs& a, int row, int c, const Weigh& g, const float2* table,
-                                        const DrawVals& s, int64_t sum, int64_t t, int64_t* s_sum, int* s_col) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  __syncthreads();  // s_sum may still be read
-  if (lane == 0) s_sum[warp] = sum;
-  if (tid == 0) *s_col = -1;
-  __syncthreads();
-  int at = -1, some = -1;
-  int64_t before = 0, upto = 0;
-#pragma unroll
-  for (int k = 0; k < VERIFY_WARPS; ++k) {
-    if (s_sum[k] > 0) some = k;
-    if (at < 0 && s_sum[k] > 0 && upto + s_sum[k] > t) {
-      at = k;
-      before = upto;
-    }
-    upto += s_sum[k];
-  }
-  const bool past = at < 0;
-  if (past) at = some;
-  if (warp == at) {
-    int gi = -1, src = -1;  // the group: index and lane
-    int64_t S = 0;          // the sum before it
-#pragma unroll 1
-    for (int i = 0; i < VL_GROUPS; ++i) {
-      const int64_t w = s.g[i][tid];
-      const int64_t incl = before + warp_scan(w);
-      const uint32_t any = __ballot_sync(0xffffffffu, w > 0);
-      const uint32_t hit = past ? 0u : __ballot_sync(0xffffffffu, w > 0 && incl > t);
-      if (any) {
-        gi = i;
-        src = hit ? __ffs(hit) - 1 : 31 - __clz(any);
-        S = __shfl_sync(0xffffffffu, incl - w, src);
-      }
-      if (hit) break;
-      before = __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (gi >= 0 && lane == src) {
-      const float l[4] = {s.v.l[gi][tid].x, s.v.l[gi][tid].y, s.v.l[gi][tid].z, s.v.l[gi][tid].w};
-      const float q[4] = {s.q[gi][tid].x, s.q[gi][tid].y, s.q[gi][tid].z, s.q[gi][tid].w};
-      const int col0 = first_col(static_cast<const T*>(a.logits) + row * a.ld, c) + gi * 128;
-      int found = -1, last = -1;
-      for (int e = 0; e < 4; ++e) {
-        const int64_t w = weight_of(l[e], q[e], col0 + e, g, table);
-        S += w;
-        if (w > 0) {
-          last = col0 + e;
-          if (found < 0 && !past && S > t) found = last;
-        }
-      }
-      *s_col = found >= 0 ? found : last;
-    }
-  }
-  __syncthreads();
-  return *s_col;
+// Draft probabilities of the groups at col0 + 128 i.
+template <int N>
+__device__ __forceinline__ void load_draft(const LogitsArgs& a, int row, int col0, float (&v)[N][4]) {
+  const int64_t o = row * a.q.ld;
+  if (a.q.dtype == 0)
+    load_groups(static_cast<const float*>(a.q.p) + o, col0, a.V, 0.f, v);
+  else if (a.q.dtype == 1)
+    load_groups(static_cast<const __half*>(a.q.p) + o, col0, a.V, 0.f, v);
+  else
+    load_groups(static_cast<const __nv_bfloat16*>(a.q.p) + o, col0, a.V, 0.f, v);
 }
 
 // One warp: the first of n weights whose running sum exceeds u * total, the last with weight when none
 // does (-1 when none has any); `left` receives u * total less the sum before it.
-__device__ __forceinline__ int find_chunk(const int64_t* w, int n, float u, int64_t total, double& left) {
+__device__ __forceinline__ int find_segment(const int64_t* w, int n, float u, double& left) {
   const int lane = threadIdx.x & 31;
+  int64_t total = 0;
+  for (int k = lane; k < n; k += 32) total += w[k];
+  total = warp_sum(total);
   const int64_t t = draw_threshold(u, total);
   int64_t upto = 0, before = 0;
   int at = -1, some = -1;
@@ -474,15 +391,57 @@ __device__ __forceinline__ int find_chunk(const int64_t* w, int n, float u, int6
   return at >= 0 ? at : some;
 }
 
+// The whole CTA: the first column of segment `seg` whose running weight exceeds t, the last with any
+// weight when none does, to tokens[row]; -1 when it has none.
+template <typename T>
+__device__ __forceinline__ void draw_in_segment(const LogitsArgs& a, int row, int seg, const Weigh& g, int64_t t,
+                                                const float2* table, int64_t* s_sum) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const T* lrow = static_cast<const T*>(a.logits) + row * a.ld;
+  const int col = chunk_col(lrow, seg / VERIFY_WARPS) + seg % VERIFY_WARPS * VL_WARP_COLS + tid * 4;
+  static_assert(VL_WARP_COLS == 4 * VERIFY_THREADS, "a group a thread");
+  float l[1][4], q[1][4] = {};
+  load_groups(lrow, col, a.V, -INFINITY, l);
+  if (g.mode == DRAW_RESIDUAL) load_draft(a, row, col, q);
+  int64_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = weight_of(l[0][e], q[0][e], col + e, g, table);
+  const int64_t sum = w[0] + w[1] + w[2] + w[3];
+  int64_t incl = warp_scan(sum);
+  __syncthreads();  // s_sum may still be read
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int k = 0; k < VERIFY_WARPS; ++k) {
+    if (k < warp) incl += s_sum[k];
+    total += s_sum[k];
+  }
+  // the group that takes the sum past t; past the end (t at or above the total) the last with weight
+  const int64_t cut = t < total ? t : total - 1;
+  int64_t S = incl - sum;
+  if (sum > 0 && S <= max(cut, static_cast<int64_t>(0)) && incl > cut) {
+    int token = -1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      S += w[e];
+      if (w[e] > 0 && S > cut && token < 0) token = col + e;
+    }
+    a.tokens[row] = token;
+  } else if (tid == 0 && total <= 0) {
+    a.tokens[row] = -1;
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(VERIFY_THREADS) verify_draw_kernel(const LogitsArgs a) {
   __shared__ float2 s_table[EXP_TABLE];
-  __shared__ int64_t s_w[VL_MAX_CHUNKS], s_all[VL_MAX_CHUNKS];
-  __shared__ int64_t s_sum[VERIFY_WARPS];
-  __shared__ int s_col, s_chunk, s_flag;
-  __shared__ int64_t s_t;
   extern __shared__ __align__(16) uint8_t smem[];
-  DrawVals& vals = *reinterpret_cast<DrawVals*>(smem);
+  DrawVals& s_vals = *reinterpret_cast<DrawVals*>(smem);
+  __shared__ int64_t s_w[VL_MAX_SEGS];
+  __shared__ int64_t s_sum[VERIFY_WARPS];
+  __shared__ int s_seg, s_flag;
+  __shared__ int64_t s_t;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seq = blockIdx.y, c = blockIdx.x;
   if (tid < EXP_TABLE) s_table[tid] = EXP2_TABLE[tid];
@@ -490,106 +449,104 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_draw_kernel(const Logit
   pdl_wait();
   const Settled st = a.settled[seq];
   if (st.token > -2) return;  // empty, greedy, or nothing to draw from
-  const int row = st.row;
+  const bool residual = st.refused && a.q.p;
+  if (!residual && c != 0) return;
+  const int row = st.row, nseg = a.nchunk * VERIFY_WARPS;
+  const T* lrow = static_cast<const T*>(a.logits) + row * a.ld;
   const ChunkStat* cs = a.stats + static_cast<int64_t>(row) * a.nchunk;
-  const int64_t* sums = a.sums + static_cast<int64_t>(seq) * a.nchunk;
+  const int64_t* sums = a.sums + static_cast<int64_t>(seq) * nseg;
   const float u = __ldg(a.u + row);
   Weigh g;
-  g.mode = !st.refused ? DRAW_P : a.q.p ? DRAW_RESIDUAL : DRAW_OTHERS;
+  g.mode = !st.refused ? DRAW_P : residual ? DRAW_RESIDUAL : DRAW_OTHERS;
   g.x = st.refused ? __ldg(a.drafts + row) : -1;
   g.sc = exp_scale(__ldg(a.temp + row));
-  // the chunks' sums relative to the row's maximum: all of P (s_all), and without a one-hot draft (s_w)
-  if (tid < a.nchunk) {
-    const float m = cs[tid].max;
-    const int64_t all = sums[tid];
-    int64_t own = 0;
-    if (g.mode == DRAW_OTHERS && g.x >= 0 && g.x < a.V) {
-      const T* lrow = static_cast<const T*>(a.logits) + row * a.ld;
-      const int k0 = chunk_col(lrow, tid);
-      if (g.x >= k0 && g.x < k0 + VL_CHUNK) {
-        const float l = widen<T>(lrow[g.x]);
-        if (l > -INFINITY) own = exp_fixed(l, m, g.sc, s_table, VL_SHIFT);
-      }
-    }
-    s_all[tid] = scale_fixed(all, VL_SHIFT, m, st.max, g.sc, s_table, a.shift);
-    s_w[tid] = scale_fixed(all - own, VL_SHIFT, m, st.max, g.sc, s_table, a.shift);
-  }
-  __syncthreads();
-  auto total_of = [&](const int64_t* w) {
-    int64_t t = 0;
-    for (int k = lane; k < a.nchunk; k += 32) t += w[k];
-    return warp_sum(t);
-  };
+  float v[VL_GROUPS][4];  // this CTA's columns, under way while the sums are scaled
+  const int col0 = first_col(lrow, c);
+  if (residual) load_groups(lrow, col0, a.V, -INFINITY, v);
 
-  if (g.mode == DRAW_RESIDUAL) {
-    const double Z = static_cast<double>(total_of(s_all)) * pow2_double(-a.shift);
+  // the segments' sums relative to the row's maximum, a one-hot draft's own weight taken out unless that
+  // leaves nothing (the draft holds all of P: a refusal by an a of 1 or more)
+  auto scale_sums = [&](bool others) {
+    const int k0 = others ? g.x - chunk_col(lrow, 0) : -1;  // the draft's place in the chunks
+    int64_t any = 0;
+#pragma unroll 1
+    for (int k = tid; k < nseg; k += VERIFY_THREADS) {
+      const float m = cs[k / VERIFY_WARPS].max;
+      int64_t s = sums[k];
+      if (others && k0 / VL_WARP_COLS == k && g.x >= 0 && g.x < a.V) {
+        const float l = widen<T>(lrow[g.x]);
+        if (l > -INFINITY) s -= exp_fixed(l, m, g.sc, s_table, VL_SHIFT);
+      }
+      const int64_t w = scale_fixed(s, VL_SHIFT, m, st.max, g.sc, s_table, a.shift);
+      s_w[k] = w;
+      any |= w;
+    }
+    return __syncthreads_or(any != 0);
+  };
+  if (!scale_sums(g.mode == DRAW_OTHERS) && g.mode == DRAW_OTHERS) {
+    g.mode = DRAW_P;
+    scale_sums(false);
+  }
+
+  if (residual) {
+    int64_t total = 0;
+    for (int k = lane; k < nseg; k += 32) total += s_w[k];
+    const double Z = static_cast<double>(warp_sum(total)) * pow2_double(-a.shift);
     g.shift = a.shift;
     g.scale = ldexpf(1.f, a.shift);
     g.max = st.max;
     g.zh = static_cast<float>(Z);
     g.zl = static_cast<float>(Z - static_cast<double>(g.zh));
-    const int64_t mine = weigh_chunk<T>(a, row, c, g, s_table, vals);
-    if (lane == 0) s_sum[warp] = mine;
-    __syncthreads();
-    if (tid == 0) {
-      int64_t sum = mine;
-      for (int k = 1; k < VERIFY_WARPS; ++k) sum += s_sum[k];
-      __stcg(reinterpret_cast<long long*>(a.rsum) + static_cast<int64_t>(seq) * a.nchunk + c, sum);
-      __threadfence();
-      s_flag = atomicAdd(a.done + seq, 1u) == static_cast<uint32_t>(a.nchunk - 1);
+#pragma unroll
+    for (int i = 0; i < VL_GROUPS; ++i) s_vals.l[i][tid] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+    load_draft(a, row, col0, v);
+    int64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < VL_GROUPS; ++i) s_vals.q[i][tid] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+#pragma unroll 1
+    for (int i = 0; i < VL_GROUPS; ++i) {
+      const float4 l = s_vals.l[i][tid], q = s_vals.q[i][tid];
+      sum += weight_of(l.x, q.x, 0, g, s_table) + weight_of(l.y, q.y, 0, g, s_table) +
+             weight_of(l.z, q.z, 0, g, s_table) + weight_of(l.w, q.w, 0, g, s_table);
     }
+    sum = warp_sum(sum);
+    long long* rsum = reinterpret_cast<long long*>(a.rsum) + static_cast<int64_t>(seq) * nseg;
+    if (lane == 0) __stcg(rsum + c * VERIFY_WARPS + warp, sum);
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) s_flag = atomicAdd(a.done + seq, 1u) == static_cast<uint32_t>(a.nchunk - 1);
     __syncthreads();
     if (!s_flag) return;
     __threadfence();
-    if (tid < a.nchunk)
-      s_w[tid] = __ldcg(reinterpret_cast<const long long*>(a.rsum) + static_cast<int64_t>(seq) * a.nchunk + tid);
-    __syncthreads();
-    if (warp == 0) {
-      double left;
-      const int at = find_chunk(s_w, a.nchunk, u, total_of(s_w), left);
-      if (lane == 0) {
-        s_chunk = at;
-        s_t = __double2ll_rd(left);
-      }
+    int64_t any = 0;
+    for (int k = tid; k < nseg; k += VERIFY_THREADS) {
+      s_vals.r[k] = __ldcg(rsum + k);
+      any |= s_vals.r[k];
     }
-    __syncthreads();
-    const int at = s_chunk;
-    if (at >= 0) {
-      const int64_t sum = at == c ? mine : weigh_chunk<T>(a, row, at, g, s_table, vals);
-      const int col = find_column<T>(a, row, at, g, s_table, vals, sum, s_t, s_sum, &s_col);
-      if (tid == 0) a.tokens[row] = col;
-      return;
-    }
-    g.mode = DRAW_P;  // q covers P: the draw is from P itself, by this CTA
+    if (!__syncthreads_or(any != 0)) g.mode = DRAW_P;  // q covers P: the draw is from P itself
   }
 
-  const bool alone = st.refused && a.q.p;  // the last CTA of a residual without weight does any chunk
-  g.shift = VL_SHIFT;
   if (warp == 0) {
-    int64_t total = total_of(alone ? s_all : s_w);
-    const bool others = !alone && total > 0;
-    if (!others) total = total_of(s_all);  // the draft holds all of P (a refusal by an a of 1 or more): from P
     double left;
-    const int at = find_chunk(others ? s_w : s_all, a.nchunk, u, total, left);
+    const int seg = find_segment(g.mode == DRAW_RESIDUAL ? s_vals.r : s_w, nseg, u, left);
     if (lane == 0) {
-      s_chunk = at;
-      s_flag = others ? g.mode : DRAW_P;
-      if (at >= 0)  // in units of the chunk's own weights
-        s_t = __double2ll_rd(left * pow2_double(VL_SHIFT - a.shift) / exp_double(cs[at].max, st.max, g.sc, s_table));
+      s_seg = seg;
+      if (g.mode != DRAW_RESIDUAL && seg >= 0)  // in units of the chunk's own weights
+        left *= pow2_double(VL_SHIFT - a.shift) / exp_double(cs[seg / VERIFY_WARPS].max, st.max, g.sc, s_table);
+      s_t = __double2ll_rd(left);
     }
   }
   __syncthreads();
-  g.mode = s_flag;
-  const int at = s_chunk;
-  if (at < 0) {
-    if ((c == 0 || alone) && tid == 0) a.tokens[row] = -1;
+  const int seg = s_seg;
+  if (seg < 0) {
+    if (tid == 0) a.tokens[row] = -1;
     return;
   }
-  if (!alone && at != c) return;
-  g.max = cs[at].max;
-  const int64_t sum = weigh_chunk<T>(a, row, at, g, s_table, vals);
-  const int col = find_column<T>(a, row, at, g, s_table, vals, sum, s_t, s_sum, &s_col);
-  if (tid == 0) a.tokens[row] = col;
+  if (g.mode != DRAW_RESIDUAL) {
+    g.shift = VL_SHIFT;
+    g.max = cs[seg / VERIFY_WARPS].max;
+  }
+  draw_in_segment<T>(a, row, seg, g, s_t, s_table, s_sum);
 }
 
 int64_t round256(int64_t v) { return (v + 255) & ~int64_t(255); }
@@ -602,7 +559,7 @@ struct Parts {
 };
 Parts parts(int rows, int nseq, int V) {
   const int64_t nc = chunks(V);
-  return Parts{round256(rows * nc * static_cast<int64_t>(sizeof(ChunkStat))), round256(nseq * nc * 8),
+  return Parts{round256(rows * nc * static_cast<int64_t>(sizeof(ChunkStat))), round256(nseq * nc * VERIFY_WARPS * 8),
                round256(nseq * static_cast<int64_t>(sizeof(Settled))), round256(nseq * 4LL)};
 }
 
