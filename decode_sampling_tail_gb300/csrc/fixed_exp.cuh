@@ -39,15 +39,17 @@ __device__ const float2 EXP2_TABLE[EXP_TABLE] = {
     {0x1.ea4afap+0f, 0x1.52486cp-27f},  {0x1.f50766p+0f, -0x1.246eb0p-26f},
 };
 
-// log2(e) / T as a pair (one fp64 division a row).
+// log2(e) / T as a pair: the quotient and, from the exact remainder, the rest.  (An fp64 division by
+// every thread kept the fp64 pipe, two operations a clock, busy for 41 of a kernel's 57 us.)
 struct ExpScale {
   float h, l;
 };
 __device__ __forceinline__ ExpScale exp_scale(float temp) {
-  const double c = 1.4426950408889634 / static_cast<double>(temp);
+  constexpr float LH = 0x1.715476p+0f, LL = 0x1.4ae0c0p-26f;  // log2(e)
   ExpScale s;
-  s.h = static_cast<float>(c);
-  s.l = isinf(s.h) ? 0.f : static_cast<float>(c - static_cast<double>(s.h));
+  s.h = LH / temp;
+  const float rest = fmaf(-s.h, temp, LH) + LL;
+  s.l = s.h > 0.f && s.h < INFINITY ? rest / temp : 0.f;
   return s;
 }
 
@@ -98,6 +100,92 @@ __device__ __forceinline__ int64_t exp_fixed(float l, float m, ExpScale c, const
   return r > 0 ? (mant + (int64_t(1) << (r - 1))) >> r : mant;
 }
 
+// Two values at a time on the packed fp32 pipe (half the instructions): exp_fixed(l0), exp_fixed(l1)
+// rounded to multiples of 2^-shift, off by at most one of them.  m is finite.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ void unpack(F2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 sub(F2 a, F2 b) { return fma(b, f2(-1.f), a); }  // exact product: a - b rounded once
+
+// (h 2^28 + w) / 2^r, rounded; r in [0, 63).  By 32-bit conversions and shifts: a conversion to 64 bits
+// runs on the fp64 pipe.
+__device__ __forceinline__ int64_t drop_bits(float h, float w, int r) {
+  const int64_t mant = (static_cast<int64_t>(__float2int_rn(h)) << (EXP_MANT_BITS - 24)) + __float2int_rn(w);
+  return (mant + ((int64_t(1) << r) >> 1)) >> r;
+}
+
+__device__ __forceinline__ void exp_fixed2(float l0, float l1, float m, ExpScale c, const float2* table, int shift,
+                                           int64_t& r0, int64_t& r1) {
+  const F2 l = f2(l0, l1), nm = f2(-m), ch = f2(c.h);
+  const F2 d = add(l, nm), dl = sub(d, l);
+  const F2 err = add(sub(l, sub(d, dl)), sub(nm, dl));
+  const F2 yh = mul(d, ch);
+  const F2 yl = add(fma(d, ch, mul(d, f2(-c.h))), fma(d, f2(c.l), mul(err, ch)));
+  constexpr float ROUND = 12582912.0f;  // 1.5 * 2^23: its sum with a small number ends in that number's integer
+  const F2 t = fma(yh, f2(32.0f), f2(ROUND));
+  const F2 f0 = fma(sub(t, f2(ROUND)), f2(-0.03125f), yh);
+  const F2 fh = add(f0, yl), fl = add(sub(f0, fh), yl);
+  float t0, t1, y0, y1;
+  unpack(t, t0, t1);
+  unpack(yh, y0, y1);
+  const int k0 = __float_as_int(t0) - __float_as_int(ROUND), k1 = __float_as_int(t1) - __float_as_int(ROUND);
+  const float2 b0 = table[k0 & 31], b1 = table[k1 & 31];
+  const F2 tx = f2(b0.x, b1.x), ty = f2(b0.y, b1.y);
+  constexpr float L1H = 0x1.62e430p-1f, L1L = -0x1.05c610p-29f;
+  const F2 a = mul(fh, f2(L1H)), na = mul(fh, f2(-L1H));
+  const F2 b = add(fma(fh, f2(L1H), na), fma(fh, f2(L1L), mul(fl, f2(L1H))));
+  F2 q = fma(fh, f2(0x1.5d87fep-10f), f2(0x1.3b2ab6p-7f));
+  q = fma(fh, q, f2(0x1.c6b08ep-5f));
+  q = fma(fh, q, f2(0x1.ebfbe0p-3f));
+  const F2 s = fma(mul(fh, fh), q, b);
+  const F2 g = mul(tx, a);
+  const F2 rest = add(fma(tx, s, fma(tx, a, mul(tx, na))), fma(ty, a, ty));
+  const F2 e0 = add(tx, g);
+  const F2 e1 = add(add(sub(tx, e0), g), rest);
+  const F2 eh = add(e0, e1), el = add(sub(e0, eh), e1);
+  float h0, h1, w0, w1;
+  unpack(mul(eh, f2(16777216.0f)), h0, h1);
+  unpack(mul(el, f2(4503599627370496.0f)), w0, w1);
+  r0 = y0 >= -60.0f ? drop_bits(h0, w0, EXP_MANT_BITS - shift - (k0 >> 5)) : 0;  // also 0 for -inf and NaN
+  r1 = y1 >= -60.0f ? drop_bits(h1, w1, EXP_MANT_BITS - shift - (k1 >> 5)) : 0;
+}
+
+// Four of them; among logits of +inf (m too) each of those weighs 1 and the others nothing.
+__device__ __forceinline__ void exp_fixed4(float4 l, float m, ExpScale c, const float2* table, int shift,
+                                           int64_t (&r)[4]) {
+  if (m == INFINITY) {
+    r[0] = l.x == m ? int64_t(1) << shift : 0;
+    r[1] = l.y == m ? int64_t(1) << shift : 0;
+    r[2] = l.z == m ? int64_t(1) << shift : 0;
+    r[3] = l.w == m ? int64_t(1) << shift : 0;
+    return;
+  }
+  exp_fixed2(l.x, l.y, m, c, table, shift, r[0], r[1]);
+  exp_fixed2(l.z, l.w, m, c, table, shift, r[2], r[3]);
+}
+
 // exp((l - m) / T) in fp32, scale = log2(e) / T: a relative error of a few 2^-24 times the exponent's
 // size.  l == m gives 1.
 __device__ __forceinline__ float exp_fast(float l, float m, float scale) {
@@ -133,11 +221,16 @@ __device__ __forceinline__ int64_t draw_threshold(float u, int64_t total) {
   return __double2ll_rd(static_cast<double>(u) * static_cast<double>(total));
 }
 
-// q * (zh + zl) rounded to a multiple of 2^-shift (q * z < 2^(62 - shift)).
-__device__ __forceinline__ int64_t prod_fixed(float q, float zh, float zl, float scale) {
-  const float h = q * zh;
-  const float l = fmaf(q, zh, -h) + q * zl;
-  return __float2ll_rn(h * scale) + __float2ll_rn(l * scale);
+// q * z, rounded down, for q in [0, 1] and 0 <= z < 2^62.
+__device__ __forceinline__ int64_t prod_fixed(float q, int64_t z) {
+  const uint32_t b = __float_as_uint(q);
+  const uint32_t e = b >> 23;
+  const uint32_t m = (b & 0x7fffffu) | (e ? 0x800000u : 0u);  // q = m * 2^(max(e, 1) - 150)
+  const int r = 150 - static_cast<int>(e ? e : 1u);           // bits to drop: at least 23
+  const uint64_t lo = static_cast<uint64_t>(m) * static_cast<uint32_t>(z);
+  const uint64_t hi = static_cast<uint64_t>(m) * static_cast<uint32_t>(z >> 32) + (lo >> 32);
+  if (r >= 96) return 0;
+  return static_cast<int64_t>(r >= 32 ? hi >> (r - 32) : (hi << (32 - r)) | (static_cast<uint32_t>(lo) >> r));
 }
 
 }  // namespace tail

@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_lists_kernel(const Veri
           ok = __any_sync(0xffffffffu, at < m && t < static_cast<double>(ex));
         }
         if (!ok && !bonus && ch.total > 0) {  // the residual max(P - q, 0), in the same units
-          const float zh = static_cast<float>(ch.total), zl = static_cast<float>(ch.total - static_cast<int64_t>(zh));
+          const int64_t total = ch.total;
           __syncwarp();  // the list's weights have been read
           for (int i0 = lane; i0 < m; i0 += 32 * BATCH) {
             float q[BATCH];
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_lists_kernel(const Veri
             for (int b = 0; b < BATCH; ++b) {
               const int i = i0 + 32 * b;
               if (i < m) {
-                const int64_t r = w[i] - prod_fixed(q[b], zh, zl, 1.f);
+                const int64_t r = w[i] - prod_fixed(q[b], total);
                 w[i] = r > 0 ? r : 0;
               }
             }

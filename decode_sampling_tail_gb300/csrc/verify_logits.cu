@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_stats_kernel(const Logi
 
 // One warp: whether the row's draft is accepted, and what its token is if it is settled here.
 template <typename T>
-__device__ __forceinline__ bool judge_row(const LogitsArgs& a, int row, bool bonus, const float2* table, Settled& s) {
+__device__ __forceinline__ bool judge_row(const LogitsArgs& a, int row, bool bonus, Settled& s) {
   const int lane = threadIdx.x & 31;
   const ChunkStat* st = a.stats + static_cast<int64_t>(row) * a.nchunk;
   const float temp = __ldg(a.temp + row);
@@ -241,7 +241,7 @@ __device__ __forceinline__ bool judge_row(const LogitsArgs& a, int row, bool bon
   s.row = row;
   s.max = m;
   s.token = -2;
-  double ex = 0.0, Z = 1.0;
+  float ex = 0.f, z = 1.f;
   if (m == -INFINITY) {
     s.token = -1;
   } else if (greedy) {
@@ -251,19 +251,18 @@ __device__ __forceinline__ bool judge_row(const LogitsArgs& a, int row, bool bon
       if (cm[i] == m) arg = min(arg, ca[i]);
     arg = __reduce_min_sync(0xffffffffu, arg);
     s.token = arg < a.V ? arg : -1;
-    ex = known && x == arg ? 1.0 : 0.0;
+    ex = known && x == arg ? 1.f : 0.f;
   } else {
     const ExpScale sc = exp_scale(temp);
-    float z = 0.f;
+    z = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) z = fmaf(cz[i], exp_fast(cm[i], m, sc.h), z);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    Z = static_cast<double>(z);
-    if (known) ex = exp_double(lx, m, sc, table);
+    if (known) ex = exp_fast(lx, m, sc.h);
     if (!(z > 0.f)) s.token = -1;
   }
-  const bool ok = !bonus && static_cast<double>(u_a) * qx * Z < ex;
+  const bool ok = !bonus && u_a * qx * z < ex;
   s.refused = !bonus && !ok;
   return ok;
 }
@@ -284,7 +283,7 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_settle_kernel(const Log
   for (int j0 = lo; j0 < hi; j0 += VERIFY_WARPS) {
     if (j0 + warp < hi) {
       Settled s;
-      const bool ok = judge_row<T>(a, j0 + warp, j0 + warp == hi - 1, s_table, s);
+      const bool ok = judge_row<T>(a, j0 + warp, j0 + warp == hi - 1, s);
       if (lane == 0) {
         if (ok) s.row = hi;  // goes on
         s_row[warp] = s;
@@ -317,8 +316,9 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_settle_kernel(const Log
 #pragma unroll 1
     for (int i = 0; i < VL_GROUPS; ++i) {
       const float4 v = s_vals.l[i][tid];
-      sum += exp_fixed(v.x, m, sc, s_table, VL_SHIFT) + exp_fixed(v.y, m, sc, s_table, VL_SHIFT) +
-             exp_fixed(v.z, m, sc, s_table, VL_SHIFT) + exp_fixed(v.w, m, sc, s_table, VL_SHIFT);
+      int64_t r[4];
+      exp_fixed4(v, m, sc, s_table, VL_SHIFT, r);
+      sum += (r[0] + r[1]) + (r[2] + r[3]);
     }
     sum = warp_sum(sum);
   }
@@ -335,14 +335,25 @@ enum DrawMode : int {
 // (DRAW_P, DRAW_OTHERS), or the residual in units of 2^-shift relative to the row's.
 struct Weigh {
   int mode, x, shift;
-  float max, zh, zl, scale;
+  float max;
+  int64_t z;  // the row's Z in units of 2^-shift
   ExpScale sc;
 };
 
-__device__ __forceinline__ int64_t weight_of(float l, float q, int col, const Weigh& g, const float2* table) {
-  int64_t r = exp_fixed(l, g.max, g.sc, table, g.shift);
-  if (g.mode == DRAW_RESIDUAL) r = max(r - prod_fixed(as_prob(q), g.zh, g.zl, g.scale), static_cast<int64_t>(0));
-  return l == -INFINITY || (g.mode == DRAW_OTHERS && col == g.x) ? 0 : r;
+// Weights of columns col .. col + 3.
+__device__ __forceinline__ void weigh4(float4 l, float4 q, int col, const Weigh& g, const float2* table,
+                                       int64_t (&w)[4]) {
+  exp_fixed4(l, g.max, g.sc, table, g.shift, w);
+  if (g.mode == DRAW_RESIDUAL) {
+    const float qf[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = max(w[e] - prod_fixed(as_prob(qf[e]), g.z), static_cast<int64_t>(0));
+  } else if (g.mode == DRAW_OTHERS) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (col + e == g.x) w[e] = 0;
+  }
 }
 
 // The draw kernel's columns, each value read back by the thread that wrote it, and the residual's segments.
@@ -404,8 +415,8 @@ __device__ __forceinline__ void draw_in_segment(const LogitsArgs& a, int row, in
   load_groups(lrow, col, a.V, -INFINITY, l);
   if (g.mode == DRAW_RESIDUAL) load_draft(a, row, col, q);
   int64_t w[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = weight_of(l[0][e], q[0][e], col + e, g, table);
+  weigh4(make_float4(l[0][0], l[0][1], l[0][2], l[0][3]), make_float4(q[0][0], q[0][1], q[0][2], q[0][3]), col, g,
+         table, w);
   const int64_t sum = w[0] + w[1] + w[2] + w[3];
   int64_t incl = warp_scan(sum);
   __syncthreads();  // s_sum may still be read
@@ -475,7 +486,9 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_draw_kernel(const Logit
       int64_t s = sums[k];
       if (others && k0 / VL_WARP_COLS == k && g.x >= 0 && g.x < a.V) {
         const float l = widen<T>(lrow[g.x]);
-        if (l > -INFINITY) s -= exp_fixed(l, m, g.sc, s_table, VL_SHIFT);
+        int64_t own[4];  // by the arithmetic of the segment's sum
+        exp_fixed4(make_float4(l, l, l, l), m, g.sc, s_table, VL_SHIFT, own);
+        s -= own[0];
       }
       const int64_t w = scale_fixed(s, VL_SHIFT, m, st.max, g.sc, s_table, a.shift);
       s_w[k] = w;
@@ -491,12 +504,10 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_draw_kernel(const Logit
   if (residual) {
     int64_t total = 0;
     for (int k = lane; k < nseg; k += 32) total += s_w[k];
-    const double Z = static_cast<double>(warp_sum(total)) * pow2_double(-a.shift);
+    total = warp_sum(total);
     g.shift = a.shift;
-    g.scale = ldexpf(1.f, a.shift);
     g.max = st.max;
-    g.zh = static_cast<float>(Z);
-    g.zl = static_cast<float>(Z - static_cast<double>(g.zh));
+    g.z = total;
 #pragma unroll
     for (int i = 0; i < VL_GROUPS; ++i) s_vals.l[i][tid] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
     load_draft(a, row, col0, v);
@@ -506,8 +517,9 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_draw_kernel(const Logit
 #pragma unroll 1
     for (int i = 0; i < VL_GROUPS; ++i) {
       const float4 l = s_vals.l[i][tid], q = s_vals.q[i][tid];
-      sum += weight_of(l.x, q.x, 0, g, s_table) + weight_of(l.y, q.y, 0, g, s_table) +
-             weight_of(l.z, q.z, 0, g, s_table) + weight_of(l.w, q.w, 0, g, s_table);
+      int64_t w[4];
+      weigh4(l, q, 0, g, s_table, w);
+      sum += (w[0] + w[1]) + (w[2] + w[3]);
     }
     sum = warp_sum(sum);
     long long* rsum = reinterpret_cast<long long*>(a.rsum) + static_cast<int64_t>(seq) * nseg;
