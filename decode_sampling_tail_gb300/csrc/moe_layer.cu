@@ -141,24 +141,21 @@ __device__ __forceinline__ void router_share(const MoeLayerArgs& a, int e0, int 
 //
 // Work is cut into tiles of a unit (an expert and up to G of its tokens): RG subtiles of 16 * RT
 // rows, whose K is split over MAIN / RG warps.  A share is a contiguous run of tiles.  Each main
-// warp keeps the fragments of its next DEPTH k-steps in registers, across tile borders (12 warps of 4
-// steps of 2 KB: 96 KB in flight an SM); at the end of a tile it leaves its partial sums in shared
-// memory and goes on.  A finishing warp adds them in a fixed order and finishes the rows: its chain of
-// bias loads, sums and exponentials held up every warp of the CTA when a main warp did it between two
-// barriers (64 tokens over 128 experts: 1640 us).
-// Formats: BF16; MXFP4; MXFP4_WIDE, for rows that are whole pieces of 64 columns.  The number of lines
-// an SM can wait for is bounded, so a load should ask for whole ones: with 16 bytes a lane (half lines)
-// 4-bit weights streamed at 3.3 TB/s whatever the depth.
+// warp keeps DEPTH k-steps of 2 KB under way, across tile borders (12 warps of 4: 96 KB an SM); at
+// the end of a tile it leaves its partial sums in shared memory and goes on.  A finishing warp adds
+// them in a fixed order and finishes the rows: its chain of bias loads, sums and exponentials held up
+// every warp of the CTA when a main warp did it between two barriers (64 tokens over 128 experts:
+// 1640 us).
+//
+// Formats: BF16; MXFP4; MXFP4_WIDE, for rows that are whole pieces of 64 columns.
 enum Format : int { BF16 = 0, MXFP4 = 1, MXFP4_WIDE = 2 };
 
 template <int FMT>
 struct Step {
   static constexpr bool FP4 = FMT != BF16;
-  static constexpr int LANE_BYTES = FMT == MXFP4 ? 16 : 32;
-  static constexpr int WORDS = LANE_BYTES / 4;
-  static constexpr int LANE_COLS = FP4 ? 2 * LANE_BYTES : LANE_BYTES / 2;
-  static constexpr int COLS = 4 * LANE_COLS;  // columns of one k-step of a warp
-  static constexpr int BLOCKS = FP4 ? LANE_COLS / 32 : 1;  // scales a lane needs
+  static constexpr int PIECES = FMT == MXFP4 ? 1 : 2;       // 16-byte pieces of a row that a lane takes
+  static constexpr int PIECE_COLS = FP4 ? 32 : 8;
+  static constexpr int COLS = 4 * PIECES * PIECE_COLS;      // columns of one k-step of a warp
 };
 
 struct Phase {
@@ -175,17 +172,25 @@ struct Phase {
   int ahead;                   // whether the next tiles are brought into L2 early
 };
 
+// A k-step's fragments in registers: scales a word each, the lane's byte at the bottom.
 template <int FMT, int RT>
 struct Frag {
-  uint32_t w[RT][2][Step<FMT>::WORDS];
-  uint32_t s[RT][2][1];  // scales, a byte each
+  uint32_t w[RT][2][Step<FMT>::PIECES][4];
+  uint32_t s[RT][2][Step<FMT>::PIECES];
 };
+
+// Bytes of one k-step of a warp in the ring.
+template <int FMT, int RT>
+__host__ __device__ constexpr int slot_bytes() {
+  return RT * 2 * Step<FMT>::PIECES * (512 + (Step<FMT>::FP4 ? 128 : 0));
+}
 
 // State of a CTA that outlives a share.
 template <int MAIN>
 struct Cta {
   MoePlan plan;
-  uint32_t act;        // shared memory: 2 G activation rows
+  uint32_t act;        // shared memory: 2 R activation rows
+  uint32_t ring;       // [MAIN][DEPTH] slots
   float4* red;         // [ML_BUFS][MAIN][RT * NACC][32]
   uint32_t full, empty;  // mbarriers [ML_BUFS]: partial sums written, and read
   volatile int* abort;   // a bounded wait ran out: no one waits any more
@@ -231,7 +236,8 @@ struct Experts {
   static constexpr int JOBS = RT * NACC;
   using S = Step<FMT>;
   static constexpr bool FP4 = S::FP4;
-  static constexpr int BLOCKS = S::BLOCKS;
+  static constexpr int PIECES = S::PIECES;
+  static constexpr int SLOT = slot_bytes<FMT, RT>();
 
   const MoeLayerArgs& a;
   const Phase& ph;
@@ -270,7 +276,7 @@ struct Experts {
 
   // Eight activations v times mult into shared memory, split into a high and a low 16-bit part so that
   // the products carry them to about 2^-17 (bf16) or 2^-22 (fp16, scaled by a power of two a token).
-  // Within a k-step, the pieces that the four lanes of a row read together lie side by side.
+  // What the four lanes of a row read together lies side by side.
   __device__ __forceinline__ void put8(int row, int k, const float (&v)[8], float mult) const {
     uint32_t hi[4], lo[4];
 #pragma unroll
@@ -288,9 +294,12 @@ struct Experts {
         lo[j] = reinterpret_cast<const uint32_t&>(l);
       }
     }
-    constexpr int PIECES = S::COLS / 8, PER = PIECES / 4;
-    const int piece = (k / 8) % PIECES;
-    const uint32_t at = k / S::COLS * (S::COLS * 2) + ((piece % PER) * 4 + piece / PER) * 16;
+    int p = k / 8;
+    if (FP4) {  // word w of block 4 j + q stands at (4 j + w, q)
+      const int w = p & 3, block = p >> 2;
+      p = (block & ~3) * 4 + w * 4 + (block & 3);
+    }
+    const uint32_t at = p * 16;
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(act_row(0, row) + at), "r"(hi[0]), "r"(hi[1]),
                  "r"(hi[2]), "r"(hi[3])
                  : "memory");
@@ -397,49 +406,44 @@ struct Experts {
     __syncthreads();
   }
 
-  // A share's tiles fall into segments, one a unit; a segment's k-steps, nk a tile, are padded to whole
-  // rounds of the ring.
+  // Where the copies stand: D steps ahead of the products.
   struct Cursor {
     int u, tile;       // unit and tile in it
     int left;          // tiles of the share that follow, this one included
     int i, nk;         // k-step of the warp in the tile, and their number
-    int steps, slots;  // k-steps and ring slots left in the segment
-    int k;             // this lane's first column in the warp's next k-step
-    const uint8_t* w;  // its first row
+    const uint8_t* w;  // this lane's first row
     const uint8_t* s;
   };
 
-  static __device__ __forceinline__ int whole_rounds(int steps) { return (steps + DEPTH - 1) / DEPTH * DEPTH; }
-
-  // The next k-step's fragment.  Past the end of the rows it holds their first columns, which meet
-  // activations of zero; in a padding slot and past the share, anything that may be read.
-  __device__ __forceinline__ void load(Frag<FMT, RT>& f, Cursor& c) const {
-    if (c.slots == 0 && c.left > 0) {  // the next segment
-      const int n = min(ph.tiles - c.tile, c.left);
-      c.steps = n * c.nk;
-      c.slots = whole_rounds(c.steps);
-    }
-    if (c.i == 0 && c.steps > 0) {
-      const int sub = c.tile * RG + rg_warp;  // past the last subtile: any rows, their sums are not used
-      const int64_t row = static_cast<int64_t>(unit_expert(plan.unit[c.u])) * ph.N + row_of(sub < ph.nsub ? sub : 0);
-      c.k = kw * S::COLS + q * S::LANE_COLS;
-      c.w = ph.w + row * ph.row_bytes;
-      if (FP4) c.s = ph.s + row * ph.scale_bytes;
-    }
-    const int k = c.k < ph.K ? c.k : 0;
-    const uint8_t* w = c.w + (FP4 ? k >> 1 : k << 1);
-    const uint8_t* s = FP4 ? c.s + (k >> 5) : nullptr;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ldg_stream(w + (rt * ph.w_rt + h * ph.w_b), f.w[rt][h]);
-        if (FMT == MXFP4) ldg_scale(s + (rt * ph.s_rt + h * ph.s_b), f.s[rt][h]);
-        if (FMT == MXFP4_WIDE) ldg_scale2(s + (rt * ph.s_rt + h * ph.s_b), f.s[rt][h]);
+  // Copies the next k-step into a slot.  Past the end of the rows it takes their first columns, which meet
+  // activations of zero; past the share, nothing.
+  __device__ __forceinline__ void issue(Cursor& c, uint32_t slot) const {
+    if (c.left > 0) {
+      if (c.i == 0) {
+        const int sub = c.tile * RG + rg_warp;  // past the last subtile: any rows, their sums are not used
+        const int64_t row = static_cast<int64_t>(unit_expert(plan.unit[c.u])) * ph.N + row_of(sub < ph.nsub ? sub : 0);
+        c.w = ph.w + row * ph.row_bytes;
+        if (FP4) c.s = ph.s + row * ph.scale_bytes;
       }
-    --c.slots;
-    if (--c.steps >= 0) {
-      c.k += ksplit * S::COLS;
+      const int k = (kw + c.i * ksplit) * S::COLS + q * S::PIECE_COLS;
+#pragma unroll
+      for (int j = 0; j < PIECES; ++j) {
+        const int kj = k + j * 4 * S::PIECE_COLS;
+        const int col = kj < ph.K ? kj : 0;
+        const uint8_t* w = c.w + (FP4 ? col >> 1 : col << 1);
+        const uint32_t dst = slot + j * 512 + lane * 16;
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r) copy16(dst + r * (PIECES * 512), w + ((r >> 1) * ph.w_rt + (r & 1) * ph.w_b));
+        if (FP4) {  // the aligned word with the block's scale
+          const uint8_t* s = c.s + (col >> 5);
+          const uint32_t to = slot + 2 * RT * PIECES * 512 + j * 128 + lane * 4;
+#pragma unroll
+          for (int r = 0; r < 2 * RT; ++r) {
+            const uintptr_t p = reinterpret_cast<uintptr_t>(s + ((r >> 1) * ph.s_rt + (r & 1) * ph.s_b));
+            copy4(to + r * (PIECES * 128), reinterpret_cast<const uint8_t*>(p & ~static_cast<uintptr_t>(3)));
+          }
+        }
+      }
       if (++c.i == c.nk) {
         c.i = 0;
         --c.left;
@@ -449,6 +453,25 @@ struct Experts {
         }
       }
     }
+    copies_commit();
+  }
+
+  // The oldest k-step's fragments; `low` are the scale addresses' two low bits, by row (the step and the
+  // piece move them by whole words, a clamped one to column q of the row as well).
+  __device__ __forceinline__ void take(Frag<FMT, RT>& f, uint32_t slot, const uint32_t (&low)[RT][2], int ks) const {
+    copies_wait<DEPTH - 1>();
+#pragma unroll
+    for (int r = 0; r < 2 * RT; ++r)
+#pragma unroll
+      for (int j = 0; j < PIECES; ++j) {
+        uint32_t(&w)[4] = f.w[r >> 1][r & 1][j];
+        lds128(slot + (r * PIECES + j) * 512 + lane * 16, w[0], w[1], w[2], w[3]);
+        if (FP4) {
+          const uint32_t v = lds32(slot + 2 * RT * PIECES * 512 + (r * PIECES + j) * 128 + lane * 4);
+          const bool in = ks * S::COLS + (j * 4 + q) * S::PIECE_COLS < ph.K;
+          f.s[r >> 1][r & 1][j] = v >> (8 * ((low[r >> 1][r & 1] + (in ? q : 0)) & 3)) & 255u;
+        }
+      }
   }
 
   // One thread: the weights of a tile into L2.  The fragments in flight cover L2's latency, not the
@@ -493,18 +516,19 @@ struct Experts {
 
   // d += the fragment's products with its values times the scale pairs
   template <int N>
-  __device__ __forceinline__ void products_fp4(const Frag<FMT, RT>& f, const uint32_t (&sc)[RT][2][BLOCKS], uint32_t at,
+  __device__ __forceinline__ void products_fp4(const Frag<FMT, RT>& f, const uint32_t (&sc)[RT][2][PIECES], uint32_t at,
                                                const uint32_t (&bp)[NB], float (&d)[RT][NACC][4]) const {
 #pragma unroll
-    for (int w = 0; w < S::WORDS; ++w) {
+    for (int i = 0; i < 4 * PIECES; ++i) {
+      const int j = i / 4, w = i % 4;
       uint32_t v[N][4];
 #pragma unroll
-      for (int b = 0; b < N; ++b) lds128(bp[b] + at + w * 64, v[b][0], v[b][1], v[b][2], v[b][3]);
+      for (int b = 0; b < N; ++b) lds128(bp[b] + at + i * 64, v[b][0], v[b][1], v[b][2], v[b][3]);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         uint32_t x[4], y[4];
-        fp4_to_half(f.w[rt][0][w], sc[rt][0][w / 4], x);
-        fp4_to_half(f.w[rt][1][w], sc[rt][1][w / 4], y);
+        fp4_to_half(f.w[rt][0][j][w], sc[rt][0][j], x);
+        fp4_to_half(f.w[rt][1][j][w], sc[rt][1][j], y);
 #pragma unroll
         for (int b = 0; b < N; ++b) {
           mma_f16_16816(d[rt][b >> 1], x[0], y[0], x[1], y[1], v[b][0], v[b][1]);
@@ -520,70 +544,62 @@ struct Experts {
     const uint32_t at = ks * (S::COLS * 2);
     if constexpr (!FP4) {
 #pragma unroll
-      for (int b = 0; b < N; ++b) {
-        uint32_t v[8];
-        lds128(bp[b] + at, v[0], v[1], v[2], v[3]);
-        lds128(bp[b] + at + 64, v[4], v[5], v[6], v[7]);
+      for (int b = 0; b < N; ++b)
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int j = 0; j < PIECES; ++j) {
+          uint32_t v[4];
+          lds128(bp[b] + at + j * 64, v[0], v[1], v[2], v[3]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_bf16_16816(t.acc[rt][b >> 1], f.w[rt][0][2 * j], f.w[rt][1][2 * j], f.w[rt][0][2 * j + 1],
-                           f.w[rt][1][2 * j + 1], v[2 * j], v[2 * j + 1]);
-      }
+          for (int rt = 0; rt < RT; ++rt) {
+            const uint32_t(&x)[4] = f.w[rt][0][j];
+            const uint32_t(&y)[4] = f.w[rt][1][j];
+            mma_bf16_16816(t.acc[rt][b >> 1], x[0], y[0], x[1], y[1], v[0], v[1]);
+            mma_bf16_16816(t.acc[rt][b >> 1], x[2], y[2], x[3], y[3], v[2], v[3]);
+          }
+        }
     } else {
       // A block's scale relative to ref goes into its values: a power of two from 2^-8 to 2^7, so that
       // fp16 holds them exactly.  Trained weights stay in one such window for whole tiles; where they
       // leave it, ref moves, and blocks too far apart for any window are summed quad by quad.
-      const uint32_t low = static_cast<uint32_t>(t.ref - 8) * 0x01010101u;
-      uint32_t off[RT][2], out = 0u;  // scales above the window's lower end, a byte each
+      constexpr int NS = 2 * RT * PIECES;
+      auto scale = [&](int i) { return f.s[i / (2 * PIECES)][i / PIECES % 2][i % PIECES]; };
+      const uint32_t low = static_cast<uint32_t>(t.ref - 8);
+      uint32_t out = 0u;
 #pragma unroll
-      for (int i = 0; i < 2 * RT; ++i) {
-        off[i / 2][i % 2] = f.s[i / 2][i % 2][0] - (BLOCKS == 2 ? low & 0xffffu : low & 0xffu);
-        out |= off[i / 2][i % 2];  // a borrow leaves a byte that is out too
-      }
+      for (int i = 0; i < NS; ++i) out |= scale(i) - low;
       bool apart = false;
-      if (__any_sync(0xffffffffu, (out & ~0x0f0fu) != 0u)) {
+      if (__any_sync(0xffffffffu, out > 15u)) {
         uint32_t mx = 0u, mn = 255u;
 #pragma unroll
-        for (int i = 0; i < 2 * RT * BLOCKS; ++i) {
-          const uint32_t v = f.s[i / (2 * BLOCKS)][i / BLOCKS % 2][0] >> (8 * (i % BLOCKS)) & 255u;
-          mx = max(mx, v);
-          mn = min(mn, v);
+        for (int i = 0; i < NS; ++i) {
+          mx = max(mx, scale(i));
+          mn = min(mn, scale(i));
         }
         mx = __reduce_max_sync(0xffffffffu, mx);
         mn = __reduce_min_sync(0xffffffffu, mn);
         flush(t);
-        apart = mx > mn + 15u || mn > 239u;  // (255 is NaN, and below 16 no difference wraps into the window)
-        if (!apart) {
-          t.ref = static_cast<int>(mn) + 8;
-#pragma unroll
-          for (int i = 0; i < 2 * RT; ++i)
-            off[i / 2][i % 2] = f.s[i / 2][i % 2][0] - mn * (BLOCKS == 2 ? 0x0101u : 1u);
-        }
+        apart = mx > mn + 15u || mn > 239u;  // (255 is NaN)
+        if (!apart) t.ref = static_cast<int>(mn) + 8;
       }
-      uint32_t sc[RT][2][BLOCKS];
-      if (!apart) {  // 2^(offset - 8), twice: exponent field offset + 7
+      uint32_t sc[RT][2][PIECES];
+      if (!apart) {  // 2^(scale - ref), twice
+        const uint32_t one = (15u - static_cast<uint32_t>(t.ref)) * 0x04000400u;
 #pragma unroll
-        for (int i = 0; i < 2 * RT * BLOCKS; ++i) {
-          const uint32_t o = off[i / (2 * BLOCKS)][i / BLOCKS % 2];
-          sc[i / (2 * BLOCKS)][i / BLOCKS % 2][i % BLOCKS] =
-              (BLOCKS == 1 ? o : i % BLOCKS ? o >> 8 : o & 0xffu) * 0x04000400u + 0x1c001c00u;
-        }
+        for (int i = 0; i < NS; ++i) sc[i / (2 * PIECES)][i / PIECES % 2][i % PIECES] = scale(i) * 0x04000400u + one;
       } else {
 #pragma unroll
-        for (int i = 0; i < 2 * RT; ++i) {
-          const int top = row_max(f.s[i / 2][i % 2][0]);
+        for (int r = 0; r < 2 * RT; ++r) {
+          const int top = row_max(f.s[r >> 1][r & 1]);
 #pragma unroll
-          for (int k = 0; k < BLOCKS; ++k)
-            sc[i / 2][i % 2][k] = half_pow2(static_cast<int>(f.s[i / 2][i % 2][0] >> (8 * k) & 255u), top);
+          for (int j = 0; j < PIECES; ++j)
+            sc[r >> 1][r & 1][j] = half_pow2(static_cast<int>(f.s[r >> 1][r & 1][j]), top);
         }
       }
       products_fp4<N>(f, sc, at, bp, t.d);
       if (apart) {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          const float f0 = e8m0(row_max(f.s[rt][0][0])), f1 = e8m0(row_max(f.s[rt][1][0]));
+          const float f0 = e8m0(row_max(f.s[rt][0])), f1 = e8m0(row_max(f.s[rt][1]));
 #pragma unroll
           for (int n = 0; n < NACC; ++n)
 #pragma unroll
@@ -597,9 +613,10 @@ struct Experts {
   }
 
   // the largest scale of a row's blocks in the k-step
-  static __device__ __forceinline__ int row_max(uint32_t s) {
-    int m = static_cast<int>(s & 255u);
-    if (BLOCKS == 2) m = max(m, static_cast<int>(s >> 8 & 255u));
+  static __device__ __forceinline__ int row_max(const uint32_t (&s)[PIECES]) {
+    int m = static_cast<int>(s[0]);
+#pragma unroll
+    for (int j = 1; j < PIECES; ++j) m = max(m, static_cast<int>(s[j]));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   }
@@ -749,66 +766,66 @@ struct Experts {
     if (lane == 0) mbar_arrive(cta.full + 8 * (s % ML_BUFS));
   }
 
-  // Tiles [lo, hi) on a main warp; the fragments of the first DEPTH steps are in f.
-  __device__ __forceinline__ void main_share(int lo, int hi, Frag<FMT, RT> (&f)[DEPTH], Cursor& c) const {
+  // Tiles [lo, hi) on a main warp; the copies of the first DEPTH steps are under way.
+  __device__ __forceinline__ void main_share(int lo, int hi, Cursor& c, uint32_t ring) const {
     int u = lo / ph.tiles, tile = lo - u * ph.tiles;
     Sums t = {};
     t.ref = 127;
     uint32_t s = cta.seq;
-    int n = lo;
+    uint32_t bp[NB];
+    int nb = 1, slot = 0;
 #pragma unroll 1
-    while (n < hi) {  // a segment
-      const uint32_t unit = plan.unit[u];
-      if (!(PHASE == 1 && a.all_rows)) {
-        main_warps_sync<MAIN>();  // the old unit's rows are not read any more
-        stage(unit);
-        main_warps_sync<MAIN>();
+    for (int n = lo; n < hi; ++n, ++s, ++tile) {
+      if (tile == ph.tiles) {
+        tile = 0;
+        ++u;
       }
-      uint32_t bp[NB];
-      int nb;
-      aim_columns(unit, bp, nb);
-      const int end = min(hi, n + ph.tiles - tile);
-      int steps = (end - n) * c.nk, i = 0, ks = kw;
-      if (threadIdx.x == 0 && n == lo && ph.ahead && tile + 1 < ph.tiles && n + 1 < end) prefetch(u, tile + 1);
-#pragma unroll 1
-      for (int r = whole_rounds(steps); r > 0; r -= DEPTH) {
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-          const bool live = steps > 0;
-          if (live && ks < ph.steps) {
-            if (NB == 1 || nb == 1)
-              products<1>(f[d], ks, bp, t);
-            else if (NB == 2 || nb == 2)
-              products<NB < 2 ? 1 : 2>(f[d], ks, bp, t);
-            else
-              products<NB>(f[d], ks, bp, t);
-          }
-          load(f[d], c);
-          --steps;
-          ks += ksplit;
-          if (live && ++i == c.nk) {
-            i = 0;
-            ks = kw;
-            ++tile;
-            // the tile after the next into L2, or the next unit's first
-            if (threadIdx.x == 0 && ph.ahead && n + 2 < hi) {
-              if (tile + 1 < ph.tiles)
-                prefetch(u, tile + 1);
-              else
-                prefetch(u + 1, tile + 1 - ph.tiles < ph.tiles ? tile + 1 - ph.tiles : 0);
-            }
-            hand_over(s, t);
-            ++s;
-            ++n;
-          }
+      if (n == lo || tile == 0) {  // another unit
+        const uint32_t unit = plan.unit[u];
+        if (!(PHASE == 1 && a.all_rows)) {
+          main_warps_sync<MAIN>();  // the old unit's rows are not read any more
+          stage(unit);
+          main_warps_sync<MAIN>();
         }
+        aim_columns(unit, bp, nb);
       }
-      tile = 0;
-      ++u;
+      if (threadIdx.x == 0 && ph.ahead && n + 2 < hi) {  // the tile after the next into L2
+        const int far = tile + 2;
+        if (far < ph.tiles)
+          prefetch(u, far);
+        else
+          prefetch(u + 1, far - ph.tiles < ph.tiles ? far - ph.tiles : 0);
+      }
+      uint32_t low[RT][2] = {};
+      if (FP4) {
+        const int sub = tile * RG + rg_warp;
+        const uint32_t row = static_cast<uint32_t>(row_of(sub < ph.nsub ? sub : 0));
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r)  // an expert's scales are whole words
+          low[r >> 1][r & 1] = row * ph.scale_bytes + (r >> 1) * ph.s_rt + (r & 1) * ph.s_b;
+      }
+      int ks = kw;
+#pragma unroll 1
+      for (int i = 0; i < c.nk; ++i, ks += ksplit) {
+        const uint32_t at = ring + slot * SLOT;
+        Frag<FMT, RT> f;
+        take(f, at, low, ks);
+        if (ks < ph.steps) {
+          if (NB == 1 || nb == 1)
+            products<1>(f, ks, bp, t);
+          else if (NB == 2 || nb == 2)
+            products<NB < 2 ? 1 : 2>(f, ks, bp, t);
+          else
+            products<NB>(f, ks, bp, t);
+        }
+        issue(c, at);
+        slot = slot + 1 == DEPTH ? 0 : slot + 1;
+      }
+      hand_over(s, t);
     }
   }
 
-  // The whole CTA: tiles [lo, hi), once the stage before is done.
+  // The whole CTA: tiles [lo, hi), once the stage before is done; the first copies start before.
   __device__ __forceinline__ void share(int lo, int hi, const uint32_t* done, uint32_t shares) {
     if (warp < MAIN) {
       Cursor c;
@@ -817,16 +834,11 @@ struct Experts {
       c.left = hi - lo;
       c.nk = (ph.steps + ksplit - 1) / ksplit;
       c.i = 0;
-      c.steps = 0;
-      c.slots = 0;
-      c.k = 0;
-      c.w = ph.w;
-      c.s = ph.s;
-      Frag<FMT, RT> f[DEPTH];
-#pragma unroll
-      for (int d = 0; d < DEPTH; ++d) load(f[d], c);
+      const uint32_t ring = cta.ring + warp * (DEPTH * SLOT);
+#pragma unroll 1
+      for (int d = 0; d < DEPTH; ++d) issue(c, ring + d * SLOT);
       if (done) wait_stage(a, cta.abort, done, shares);
-      main_share(lo, hi, f, c);
+      main_share(lo, hi, c, ring);
     } else {
       if (done) wait_stage(a, cta.abort, done, shares);
       finish_share(lo, hi);
@@ -881,7 +893,9 @@ __global__ void __launch_bounds__(32 * (MAIN + ML_FINISH), 1)
   cta.plan.nunits = -1;
   uint8_t* rows = smem + ((plan_bytes(pairs) + 127) & ~127);
   cta.act = smem_u32(rows);
-  cta.red = reinterpret_cast<float4*>(rows + ((2 * a.R * max(ph1.pitch, ph2.pitch) + 127) & ~127));
+  uint8_t* red = rows + ((2 * a.R * max(ph1.pitch, ph2.pitch) + 127) & ~127);
+  cta.red = reinterpret_cast<float4*>(red);
+  cta.ring = smem_u32(red) + ML_BUFS * MAIN * RT * (NB == 4 ? 2 : 1) * 512;
   cta.full = smem_u32(s_bar);
   cta.empty = cta.full + 8 * ML_BUFS;
   cta.abort = &s_abort;
@@ -962,10 +976,13 @@ constexpr int STATIC_SMEM = 512;  // at least moe_layer_kernel's __shared__ vari
 
 // Main warps, steps in flight of each and 16-row groups a warp takes at a time, for a format and the
 // number of n-tiles.
-constexpr int main_warps(int fmt) { return fmt == MXFP4 ? 8 : 12; }
-constexpr int depth_of(int fmt) { return fmt == BF16 ? 4 : 3; }
+constexpr int MAIN_WARPS = 12;
+constexpr int depth_of(int nb) { return nb == 4 ? 2 : 4; }
 constexpr int groups_of(int fmt, int nb) { return fmt == MXFP4 && nb < 4 ? 2 : 1; }
 int step_cols(int fmt) { return fmt == BF16 ? 64 : fmt == MXFP4 ? 128 : 256; }
+int slot_of(int fmt, int rt) {
+  return fmt == BF16 ? slot_bytes<BF16, 1>() : fmt == MXFP4_WIDE ? slot_bytes<MXFP4_WIDE, 1>() : rt * slot_bytes<MXFP4, 1>();
+}
 int columns_of(int G) { return G <= 4 ? 1 : G <= 8 ? 2 : 4; }
 
 // An activation row: whole k-steps, and 64 bytes more so that two rows fill the 128 bytes of all banks.
@@ -977,17 +994,17 @@ int pitch_of(int fmt, int K) {
 // Warps that split K: as many as keep 85 % of their k-steps busy (small tiles spread evenly over the
 // SMs: with 192 rows a tile instead of 48, 8 tokens over 66 experts took 165 us instead of 136).
 int ksplit_of(int fmt, int K) {
-  const int steps = (K + step_cols(fmt) - 1) / step_cols(fmt), main = main_warps(fmt);
+  const int steps = (K + step_cols(fmt) - 1) / step_cols(fmt), main = MAIN_WARPS;
   int best = 1;
   for (int k = 2; k <= main; ++k)
-    if (main % k == 0 && 100 * steps >= 85 * ((steps + k - 1) / k * k) && (fmt == BF16 || steps >= 3 * k)) best = k;
+    if (main % k == 0 && 100 * steps >= 85 * ((steps + k - 1) / k * k) ) best = k;
   return best;
 }
 
 Phase make_phase(const MoeLayerArgs& a, int fmt, int nb, int phase, int ksplit) {
   Phase p;
   const bool gated = phase == 1 && a.gated;
-  const int RT = groups_of(fmt, nb), RG = main_warps(fmt) / ksplit;
+  const int RT = groups_of(fmt, nb), RG = MAIN_WARPS / ksplit;
   p.w = phase == 1 ? a.w1 : a.w2;
   p.s = phase == 1 ? a.s1 : a.s2;
   p.bias = phase == 1 ? a.b1 : a.b2;
@@ -1012,14 +1029,13 @@ Phase make_phase(const MoeLayerArgs& a, int fmt, int nb, int phase, int ksplit) 
 
 template <int FMT, int NB>
 cudaError_t launch_as(const MoeLayerArgs& a, const MoeLayerPlan& p, cudaStream_t stream) {
-  constexpr int MAIN = main_warps(FMT);
   const Phase ph1 = make_phase(a, FMT, NB, 1, p.ksplit1), ph2 = make_phase(a, FMT, NB, 2, p.ksplit2);
-  auto f = moe_layer_kernel<FMT, groups_of(FMT, NB), NB, depth_of(FMT), MAIN>;
+  auto f = moe_layer_kernel<FMT, groups_of(FMT, NB), NB, depth_of(NB), MAIN_WARPS>;
   const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.grid);
-  cfg.blockDim = dim3(32 * (MAIN + ML_FINISH));
+  cfg.blockDim = dim3(32 * (MAIN_WARPS + ML_FINISH));
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1056,7 +1072,8 @@ MoeLayerPlan plan_moe_layer(int T, int topk, int nsh, int E, int H, int I, bool 
   p.G = T < most ? T : most;
   for (;; --p.G) {
     const int nb = columns_of(p.G);
-    const int red = ML_BUFS * main_warps(p.format) * groups_of(p.format, nb) * (nb == 4 ? 2 : 1) * 512;
+    const int rt = groups_of(p.format, nb);
+    const int red = ML_BUFS * MAIN_WARPS * rt * (nb == 4 ? 2 : 1) * 512 + MAIN_WARPS * depth_of(nb) * slot_of(p.format, rt);
     p.all_rows = T <= p.G;
     p.R = p.G;
     p.smem = fixed + 2 * p.R * pitch + red;

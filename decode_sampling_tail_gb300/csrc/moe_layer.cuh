@@ -9,16 +9,19 @@
 // A few tokens select a few experts each, so the layer is a stream of weights:
 // every selected expert's W1 and W2 once.  The matrix products run on mma.sync
 // with 16 weight rows as the M side and up to 8 tokens as the N side; for so few
-// columns the tensor pipe idles either way, and registers fed straight from
-// global memory need no staging.
+// columns the tensor pipe idles either way, and registers are fed without
+// a barrier.
 //
 // Weight fragments.  A lane (g = lane / 4, q = lane % 4) of an m16n8k16 product
 // holds k slots {2q, 2q+1, 2q+8, 2q+9} of rows g and g + 8.  A sum does not mind
-// the order of k, so lane q takes 16 consecutive bf16 (32 bytes; 32 consecutive
-// 4-bit values, one scale block) of each of its rows and feeds them as the
-// slots of 4 (8) products; its activations are the same 16 (32) columns.  One
-// load instruction then covers whole 128-byte (64-byte) lines of 8 rows, and
-// nothing is shuffled.
+// the order of k, so lane q takes whole 16-byte pieces (8 bf16, or 32 4-bit
+// values: one scale block) of each of its rows and feeds them as the slots of 2
+// (8) products; its activations are the same columns.  The four lanes of a row
+// copy 64 neighbouring bytes at a time, and nothing is shuffled.
+//
+// Each lane copies its own pieces, by cp.async, into its own places of a ring in
+// shared memory and reads them back itself: no barrier guards the ring, any depth
+// fits a loop that is not unrolled, and the bytes in flight hold no registers.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -80,30 +83,27 @@ struct MoeLayerArgs {
 };
 
 // ---------------------------------------------------------------- loads
-// Read once, so not kept in L1.  Unconditional: a predicated load, or one in a branch, would join its
-// result with other values by moves, which wait for the data and undo the prefetch.
-__device__ __forceinline__ void ldg_stream(const uint8_t* p, uint32_t (&v)[8]) {
-  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "l"(p));
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void ldg_stream(const uint8_t* p, uint32_t (&v)[4]) {
-  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-               : "l"(p));
+__device__ __forceinline__ void copy4(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // Brings [p, p + bytes) into L2: both multiples of 16.
 __device__ __forceinline__ void prefetch_l2(const uint8_t* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void ldg_scale(const uint8_t* p, uint32_t (&v)[1]) {
-  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v[0]) : "l"(p));
-}
-// two neighbouring scales, both in v[0]
-__device__ __forceinline__ void ldg_scale2(const uint8_t* p, uint32_t (&v)[1]) {
-  asm volatile("{\n.reg .u16 t;\nld.global.nc.u16 t, [%1];\ncvt.u32.u16 %0, t;\n}" : "=r"(v[0]) : "l"(p));
-}
-
 // D (16x8 fp32) += A (16x16 fp16, row) * B (16x8 fp16, col)
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
