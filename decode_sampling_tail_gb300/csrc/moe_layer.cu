@@ -166,13 +166,13 @@ struct Phase {
   int row_bytes, scale_bytes;
   int a_mul, rt_step, b_step;  // rows from a lane's first to those of its other fragments (row_of)
   int w_rt, w_b, s_rt, s_b;    // the same steps in bytes of the weight and of its scales
+  uintptr_t s_end;             // behind the last scale
   int nsub, tiles;             // subtiles and tiles of a unit
   int steps;                   // k-steps
   int pitch;                   // bytes of one activation row in shared memory
-  int ahead;                   // whether the next tiles are brought into L2 early
 };
 
-// A k-step's fragments in registers: scales a word each, the lane's byte at the bottom.
+// A k-step's fragments in registers; a scale a word.
 template <int FMT, int RT>
 struct Frag {
   uint32_t w[RT][2][Step<FMT>::PIECES][4];
@@ -182,14 +182,15 @@ struct Frag {
 // Bytes of one k-step of a warp in the ring.
 template <int FMT, int RT>
 __host__ __device__ constexpr int slot_bytes() {
-  return RT * 2 * Step<FMT>::PIECES * (512 + (Step<FMT>::FP4 ? 128 : 0));
+  return RT * 2 * (Step<FMT>::PIECES * 512 + (Step<FMT>::FP4 ? 128 : 0));
 }
 
 // State of a CTA that outlives a share.
 template <int MAIN>
 struct Cta {
   MoePlan plan;
-  uint32_t act;        // shared memory: 2 R activation rows
+  const uint8_t* smem; // the dynamic shared memory
+  uint32_t act;        // 2 R activation rows
   uint32_t ring;       // [MAIN][DEPTH] slots
   float4* red;         // [ML_BUFS][MAIN][RT * NACC][32]
   uint32_t full, empty;  // mbarriers [ML_BUFS]: partial sums written, and read
@@ -425,7 +426,8 @@ struct Experts {
         c.w = ph.w + row * ph.row_bytes;
         if (FP4) c.s = ph.s + row * ph.scale_bytes;
       }
-      const int k = (kw + c.i * ksplit) * S::COLS + q * S::PIECE_COLS;
+      const int step = kw + c.i * ksplit;
+      const int k = step * S::COLS + q * S::PIECE_COLS;
 #pragma unroll
       for (int j = 0; j < PIECES; ++j) {
         const int kj = k + j * 4 * S::PIECE_COLS;
@@ -434,14 +436,18 @@ struct Experts {
         const uint32_t dst = slot + j * 512 + lane * 16;
 #pragma unroll
         for (int r = 0; r < 2 * RT; ++r) copy16(dst + r * (PIECES * 512), w + ((r >> 1) * ph.w_rt + (r & 1) * ph.w_b));
-        if (FP4) {  // the aligned word with the block's scale
-          const uint8_t* s = c.s + (col >> 5);
-          const uint32_t to = slot + 2 * RT * PIECES * 512 + j * 128 + lane * 4;
+      }
+      if (FP4) {
+        // a row's scales of the step, 4 * PIECES bytes, by the aligned words that hold them: lane q word q;
+        // the word behind 4 * PIECES aligned bytes is not touched, it may lie past the weight
+        const int b0 = step < ph.steps ? step * (4 * PIECES) : 0;
+        const uint32_t to = slot + 2 * RT * PIECES * 512 + lane * 4;
 #pragma unroll
-          for (int r = 0; r < 2 * RT; ++r) {
-            const uintptr_t p = reinterpret_cast<uintptr_t>(s + ((r >> 1) * ph.s_rt + (r & 1) * ph.s_b));
-            copy4(to + r * (PIECES * 128), reinterpret_cast<const uint8_t*>(p & ~static_cast<uintptr_t>(3)));
-          }
+        for (int r = 0; r < 2 * RT; ++r) {
+          const uintptr_t p = reinterpret_cast<uintptr_t>(c.s + (b0 + (r >> 1) * ph.s_rt + (r & 1) * ph.s_b));
+          const bool mine = q < PIECES || (q == PIECES && (p & 3) != 0);
+          const uintptr_t word = (p & ~static_cast<uintptr_t>(3)) + q * 4;
+          if (mine && word < ph.s_end) copy4(to + r * 128, reinterpret_cast<const uint8_t*>(word));
         }
       }
       if (++c.i == c.nk) {
@@ -456,46 +462,28 @@ struct Experts {
     copies_commit();
   }
 
-  // The oldest k-step's fragments; `low` are the scale addresses' two low bits, by row (the step and the
-  // piece move them by whole words, a clamped one to column q of the row as well).
+  // The oldest k-step's fragments; `low` are the two low bits of the rows' scale addresses (a step moves
+  // them by whole words).
   __device__ __forceinline__ void take(Frag<FMT, RT>& f, uint32_t slot, const uint32_t (&low)[RT][2], int ks) const {
+    const int blocks = ph.scale_bytes - ks * (4 * PIECES);  // of the row from this step on; a lane past them takes the first's
     copies_wait<DEPTH - 1>();
+    if (FP4) __syncwarp();  // the scales were copied by the four lanes of a row together
 #pragma unroll
     for (int r = 0; r < 2 * RT; ++r)
 #pragma unroll
       for (int j = 0; j < PIECES; ++j) {
         uint32_t(&w)[4] = f.w[r >> 1][r & 1][j];
         lds128(slot + (r * PIECES + j) * 512 + lane * 16, w[0], w[1], w[2], w[3]);
-        if (FP4) {
-          const uint32_t v = lds32(slot + 2 * RT * PIECES * 512 + (r * PIECES + j) * 128 + lane * 4);
-          const bool in = ks * S::COLS + (j * 4 + q) * S::PIECE_COLS < ph.K;
-          f.s[r >> 1][r & 1][j] = v >> (8 * ((low[r >> 1][r & 1] + (in ? q : 0)) & 3)) & 255u;
-        }
+        if (FP4)
+          f.s[r >> 1][r & 1][j] = lds8(slot + 2 * RT * PIECES * 512 + r * 128 + g * 16 + low[r >> 1][r & 1] +
+                                       (j * 4 + q < blocks ? j * 4 + q : 0));
       }
-  }
-
-  // One thread: the weights of a tile into L2.  The fragments in flight cover L2's latency, not the
-  // memory's.
-  __device__ __forceinline__ void prefetch(int u, int tile) const {
-    const int64_t row0 = static_cast<int64_t>(unit_expert(plan.unit[u])) * ph.N;
-    const int subs = min(RG, ph.nsub - tile * RG);
-    const bool halves = PHASE == 1 && a.gated && !a.interleaved;  // gate and up rows lie apart
-    const int rows = subs * RT * (halves ? 8 : 16);
-    const int64_t r = row0 + static_cast<int64_t>(tile) * RG * RT * (halves ? 8 : 16);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == 1 && !halves) break;
-      const int64_t at = r + (h ? a.I : 0);
-      prefetch_l2(ph.w + at * ph.row_bytes, rows * ph.row_bytes);
-      if (FP4 && (at * ph.scale_bytes) % 16 == 0 && rows * ph.scale_bytes % 16 == 0)
-        prefetch_l2(ph.s + at * ph.scale_bytes, rows * ph.scale_bytes);
-    }
   }
 
   // Sums of a tile.  4-bit weights: d counts in units of 2^(ref - 127), acc in ones.
   struct Sums {
     float acc[RT][NACC][4];
-    float d[FP4 ? RT : 1][FP4 ? NACC : 1][4];
+    float d[FP4 ? RT : 1][FP4 ? NACC : 1][2][4];  // two chains of products each: one's latency under the other's
     int ref;
   };
 
@@ -508,22 +496,27 @@ struct Experts {
         for (int n = 0; n < NACC; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            t.acc[rt][n][j] = fmaf(t.d[rt][n][j], f, t.acc[rt][n][j]);
-            t.d[rt][n][j] = 0.f;
+            t.acc[rt][n][j] = fmaf(t.d[rt][n][0][j] + t.d[rt][n][1][j], f, t.acc[rt][n][j]);
+            t.d[rt][n][0][j] = t.d[rt][n][1][j] = 0.f;
           }
     }
+  }
+
+  // 16 bytes of activations; plain loads, which the compiler may move up past products
+  __device__ __forceinline__ uint4 columns(uint32_t at) const {
+    return *reinterpret_cast<const uint4*>(cta.smem + at);
   }
 
   // d += the fragment's products with its values times the scale pairs
   template <int N>
   __device__ __forceinline__ void products_fp4(const Frag<FMT, RT>& f, const uint32_t (&sc)[RT][2][PIECES], uint32_t at,
-                                               const uint32_t (&bp)[NB], float (&d)[RT][NACC][4]) const {
+                                               const uint32_t (&bp)[NB], float (&d)[RT][NACC][2][4]) const {
 #pragma unroll
     for (int i = 0; i < 4 * PIECES; ++i) {
       const int j = i / 4, w = i % 4;
-      uint32_t v[N][4];
+      uint4 v[N];
 #pragma unroll
-      for (int b = 0; b < N; ++b) lds128(bp[b] + at + i * 64, v[b][0], v[b][1], v[b][2], v[b][3]);
+      for (int b = 0; b < N; ++b) v[b] = columns(bp[b] + at + i * 64);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         uint32_t x[4], y[4];
@@ -531,8 +524,8 @@ struct Experts {
         fp4_to_half(f.w[rt][1][j][w], sc[rt][1][j], y);
 #pragma unroll
         for (int b = 0; b < N; ++b) {
-          mma_f16_16816(d[rt][b >> 1], x[0], y[0], x[1], y[1], v[b][0], v[b][1]);
-          mma_f16_16816(d[rt][b >> 1], x[2], y[2], x[3], y[3], v[b][2], v[b][3]);
+          mma_f16_16816(d[rt][b >> 1][0], x[0], y[0], x[1], y[1], v[b].x, v[b].y);
+          mma_f16_16816(d[rt][b >> 1][1], x[2], y[2], x[3], y[3], v[b].z, v[b].w);
         }
       }
     }
@@ -547,14 +540,13 @@ struct Experts {
       for (int b = 0; b < N; ++b)
 #pragma unroll
         for (int j = 0; j < PIECES; ++j) {
-          uint32_t v[4];
-          lds128(bp[b] + at + j * 64, v[0], v[1], v[2], v[3]);
+          const uint4 v = columns(bp[b] + at + j * 64);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             const uint32_t(&x)[4] = f.w[rt][0][j];
             const uint32_t(&y)[4] = f.w[rt][1][j];
-            mma_bf16_16816(t.acc[rt][b >> 1], x[0], y[0], x[1], y[1], v[0], v[1]);
-            mma_bf16_16816(t.acc[rt][b >> 1], x[2], y[2], x[3], y[3], v[2], v[3]);
+            mma_bf16_16816(t.acc[rt][b >> 1], x[0], y[0], x[1], y[1], v.x, v.y);
+            mma_bf16_16816(t.acc[rt][b >> 1], x[2], y[2], x[3], y[3], v.z, v.w);
           }
         }
     } else {
@@ -604,8 +596,8 @@ struct Experts {
           for (int n = 0; n < NACC; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              t.acc[rt][n][j] = fmaf(t.d[rt][n][j], j < 2 ? f0 : f1, t.acc[rt][n][j]);
-              t.d[rt][n][j] = 0.f;
+              t.acc[rt][n][j] = fmaf(t.d[rt][n][0][j] + t.d[rt][n][1][j], j < 2 ? f0 : f1, t.acc[rt][n][j]);
+              t.d[rt][n][0][j] = t.d[rt][n][1][j] = 0.f;
             }
         }
       }
@@ -717,7 +709,7 @@ struct Experts {
     for (int b = 0; b < NB; ++b)
       bp[b] = (nb == 1 ? act_row(g >> 2, row_of_token(unit, g & 3))
                        : act_row(b & 1, row_of_token(unit, (b >> 1) * 8 + g))) +
-              q * 16;
+              q * 16 - smem_u32(cta.smem);
   }
 
   __device__ __forceinline__ float4* partial(uint32_t seq) const {
@@ -789,20 +781,13 @@ struct Experts {
         }
         aim_columns(unit, bp, nb);
       }
-      if (threadIdx.x == 0 && ph.ahead && n + 2 < hi) {  // the tile after the next into L2
-        const int far = tile + 2;
-        if (far < ph.tiles)
-          prefetch(u, far);
-        else
-          prefetch(u + 1, far - ph.tiles < ph.tiles ? far - ph.tiles : 0);
-      }
       uint32_t low[RT][2] = {};
       if (FP4) {
         const int sub = tile * RG + rg_warp;
         const uint32_t row = static_cast<uint32_t>(row_of(sub < ph.nsub ? sub : 0));
 #pragma unroll
         for (int r = 0; r < 2 * RT; ++r)  // an expert's scales are whole words
-          low[r >> 1][r & 1] = row * ph.scale_bytes + (r >> 1) * ph.s_rt + (r & 1) * ph.s_b;
+          low[r >> 1][r & 1] = (row * ph.scale_bytes + (r >> 1) * ph.s_rt + (r & 1) * ph.s_b) & 3u;
       }
       int ks = kw;
 #pragma unroll 1
@@ -818,6 +803,7 @@ struct Experts {
           else
             products<NB>(f, ks, bp, t);
         }
+        if (FP4) __syncwarp();  // the scales have been read by every lane
         issue(c, at);
         slot = slot + 1 == DEPTH ? 0 : slot + 1;
       }
@@ -891,6 +877,7 @@ __global__ void __launch_bounds__(32 * (MAIN + ML_FINISH), 1)
   cta.plan.cnt = cta.plan.unit + p8;
   cta.plan.red = cta.plan.cnt + ML_MAX_EXPERTS;
   cta.plan.nunits = -1;
+  cta.smem = smem;
   uint8_t* rows = smem + ((plan_bytes(pairs) + 127) & ~127);
   cta.act = smem_u32(rows);
   uint8_t* red = rows + ((2 * a.R * max(ph1.pitch, ph2.pitch) + 127) & ~127);
@@ -971,7 +958,6 @@ __global__ void __launch_bounds__(32 * (MAIN + ML_FINISH), 1)
 }
 
 // ---------------------------------------------------------------- host
-constexpr int AHEAD_BYTES = 128 * 1024;
 constexpr int STATIC_SMEM = 512;  // at least moe_layer_kernel's __shared__ variables
 
 // Main warps, steps in flight of each and 16-row groups a warp takes at a time, for a format and the
@@ -1019,11 +1005,11 @@ Phase make_phase(const MoeLayerArgs& a, int fmt, int nb, int phase, int ksplit) 
   p.w_b = p.b_step * p.row_bytes;
   p.s_rt = p.rt_step * p.scale_bytes;
   p.s_b = p.b_step * p.scale_bytes;
+  p.s_end = reinterpret_cast<uintptr_t>(p.s) + static_cast<uintptr_t>(a.E + a.nsh) * p.N * p.scale_bytes;
   p.nsub = p.N / (16 * RT);
   p.tiles = (p.nsub + RG - 1) / RG;
   p.steps = (p.K + step_cols(fmt) - 1) / step_cols(fmt);
   p.pitch = pitch_of(fmt, p.K);
-  p.ahead = RG * RT * 16 * p.row_bytes <= AHEAD_BYTES;
   return p;
 }
 
