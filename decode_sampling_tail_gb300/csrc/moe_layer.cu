@@ -204,10 +204,14 @@ __device__ __forceinline__ void main_warps_sync() {
 }
 
 __device__ __forceinline__ void wait_or_abort(const MoeLayerArgs& a, volatile int* abort, uint32_t bar, uint32_t parity, int code) {
-  if (*abort) return;
-  if (!mbar_wait_bounded(bar, parity, a.timeout_ns)) {
-    raise_error(a.err, code);
-    *abort = 1;
+  if (*abort || mbar_suspended_wait(bar, parity)) return;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_suspended_wait(bar, parity)) {
+    if (global_timer_ns() - t0 > a.timeout_ns) {
+      raise_error(a.err, code);
+      *abort = 1;
+      return;
+    }
   }
 }
 
@@ -407,49 +411,65 @@ struct Experts {
     __syncthreads();
   }
 
-  // Where the copies stand: D steps ahead of the products.
+  // Where the copies stand: DEPTH steps ahead of the products.
   struct Cursor {
-    int u, tile;       // unit and tile in it
-    int left;          // tiles of the share that follow, this one included
-    int i, nk;         // k-step of the warp in the tile, and their number
-    const uint8_t* w;  // this lane's first row
-    const uint8_t* s;
+    int u, tile;                // unit and tile in it
+    int left;                   // tiles of the share that follow, this one included
+    int i, nk;                  // k-step of the warp in the tile, and their number
+    int step;                   // the same of the row
+    const uint8_t* w[2 * RT];   // this lane's rows at the step
+    const uint8_t* s[2 * RT];   // the word of the rows' scales that this lane copies
+    uint32_t words;             // rows of which it copies one, a bit each
   };
 
-  // Copies the next k-step into a slot.  Past the end of the rows it takes their first columns, which meet
-  // activations of zero; past the share, nothing.
+  // Copies the next k-step into a slot; past the share, nothing.
   __device__ __forceinline__ void issue(Cursor& c, uint32_t slot) const {
     if (c.left > 0) {
       if (c.i == 0) {
         const int sub = c.tile * RG + rg_warp;  // past the last subtile: any rows, their sums are not used
         const int64_t row = static_cast<int64_t>(unit_expert(plan.unit[c.u])) * ph.N + row_of(sub < ph.nsub ? sub : 0);
-        c.w = ph.w + row * ph.row_bytes;
-        if (FP4) c.s = ph.s + row * ph.scale_bytes;
-      }
-      const int step = kw + c.i * ksplit;
-      const int k = step * S::COLS + q * S::PIECE_COLS;
-#pragma unroll
-      for (int j = 0; j < PIECES; ++j) {
-        const int kj = k + j * 4 * S::PIECE_COLS;
-        const int col = kj < ph.K ? kj : 0;
-        const uint8_t* w = c.w + (FP4 ? col >> 1 : col << 1);
-        const uint32_t dst = slot + j * 512 + lane * 16;
-#pragma unroll
-        for (int r = 0; r < 2 * RT; ++r) copy16(dst + r * (PIECES * 512), w + ((r >> 1) * ph.w_rt + (r & 1) * ph.w_b));
-      }
-      if (FP4) {
-        // a row's scales of the step, 4 * PIECES bytes, by the aligned words that hold them: lane q word q;
-        // the word behind 4 * PIECES aligned bytes is not touched, it may lie past the weight
-        const int b0 = step < ph.steps ? step * (4 * PIECES) : 0;
-        const uint32_t to = slot + 2 * RT * PIECES * 512 + lane * 4;
+        const uint8_t* w = ph.w + row * ph.row_bytes + kw * (PIECES * 64) + q * 16;
+        const uint8_t* sc = ph.s + row * ph.scale_bytes + kw * (4 * PIECES);
+        c.words = 0u;
+        c.step = kw;
 #pragma unroll
         for (int r = 0; r < 2 * RT; ++r) {
-          const uintptr_t p = reinterpret_cast<uintptr_t>(c.s + (b0 + (r >> 1) * ph.s_rt + (r & 1) * ph.s_b));
-          const bool mine = q < PIECES || (q == PIECES && (p & 3) != 0);
-          const uintptr_t word = (p & ~static_cast<uintptr_t>(3)) + q * 4;
-          if (mine && word < ph.s_end) copy4(to + r * 128, reinterpret_cast<const uint8_t*>(word));
+          c.w[r] = w + ((r >> 1) * ph.w_rt + (r & 1) * ph.w_b);
+          if (FP4) {
+            // a row's scales of a step, 4 * PIECES bytes, by the aligned words that hold them, lane q word q
+            const uintptr_t p = reinterpret_cast<uintptr_t>(sc + ((r >> 1) * ph.s_rt + (r & 1) * ph.s_b));
+            c.s[r] = reinterpret_cast<const uint8_t*>(p & ~static_cast<uintptr_t>(3)) + q * 4;
+            if (q < PIECES || (q == PIECES && (p & 3) != 0)) c.words |= 1u << r;
+          }
         }
       }
+      const uint32_t dst = slot + lane * 16, to = slot + 2 * RT * PIECES * 512 + lane * 4;
+      if ((c.step + 1) * S::COLS <= ph.K) {
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r) {
+#pragma unroll
+          for (int j = 0; j < PIECES; ++j) copy16(dst + (r * PIECES + j) * 512, c.w[r] + j * 64);
+          if (FP4 && (c.words >> r & 1u)) copy4(to + r * 128, c.s[r]);
+        }
+      } else if (c.step < ph.steps) {
+        // the end of the rows: a piece past it repeats the step's first, and the activations it meets are
+        // zero; words behind the last scale are not touched
+        const int left = ph.K - c.step * S::COLS;  // columns
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r) {
+#pragma unroll
+          for (int j = 0; j < PIECES; ++j)
+            copy16(dst + (r * PIECES + j) * 512,
+                   (j * 4 + q) * S::PIECE_COLS < left ? c.w[r] + j * 64 : c.w[r] - q * 16);
+          if (FP4 && (c.words >> r & 1u) && reinterpret_cast<uintptr_t>(c.s[r]) < ph.s_end) copy4(to + r * 128, c.s[r]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2 * RT; ++r) {
+        c.w[r] += ksplit * (PIECES * 64);
+        if (FP4) c.s[r] += ksplit * (4 * PIECES);
+      }
+      c.step += ksplit;
       if (++c.i == c.nk) {
         c.i = 0;
         --c.left;
@@ -900,52 +920,71 @@ __global__ void __launch_bounds__(32 * (MAIN + ML_FINISH), 1)
     pdl_wait();
   }
   __syncthreads();
-  const uint32_t n = gridDim.x, last = (a.h_out ? 4u : 3u) * n;
+  const uint32_t n = gridDim.x;
   uint32_t ticket = s_ticket;
-#pragma unroll 1
-  while (ticket < last) {
+  // the first of `total` things that belong to share k of n
+  auto cut = [&](uint32_t total, uint32_t k) {
+    const uint32_t q = total / n;
+    return static_cast<int>(q * k + (total - q * n) * k / n);
+  };
+  auto begin_share = [&] {  // asks for the next share
     __syncthreads();
-    if (tid == THREADS - 1) s_ticket = atomicAdd(&a.ctl->ticket, 1u);  // the next share, early
-    const uint32_t stage = ticket / n;
-    const uint32_t i = ticket - stage * n;
-    // the first of `total` things that belong to share k of n
-    auto cut = [&](uint32_t total, uint32_t k) {
-      const uint32_t q = total / n;
-      return static_cast<int>(q * k + (total - q * n) * k / n);
-    };
-    if (stage == 0) {
-      const uint32_t r = n - 1 - i;  // the tokens' statistics go to the last shares first
-      router_share(a, cut(a.E, i), cut(a.E, i + 1), cut(a.T, r), cut(a.T, r + 1), reinterpret_cast<float*>(rows), s_part);
-    } else if (stage == 3) {
-      wait_stage(a, cta.abort, a.ctl->done + 2, n);
-      const int half = a.H / 2;
-      const int lo = cut(a.T * half, i), hi = cut(a.T * half, i + 1);
-#pragma unroll 1
-      for (int p = lo + tid; p < hi && !s_abort; p += THREADS) combine2(a, p / half, 2 * (p % half));
-    } else {
-      if (cta.plan.nunits < 0) {
-        if (a.all_rows && stage == 1) Experts<FMT, RT, NB, 1, DEPTH, MAIN>(a, ph1, cta, ksplit1).stage_all(s_part);
-        wait_stage(a, cta.abort, a.ctl->done, n);
-        if (!s_abort) make_plan(a, cta.plan);
-      }
-      if (ticket == n && tid >= 32 * MAIN && !s_abort)
-#pragma unroll 1
-        for (int t = (tid >> 5) - MAIN; t < a.T; t += ML_FINISH) write_routes(a, t, cta.plan.pair_e);
-      if (!s_abort) {
-        const uint32_t tiles = cta.plan.nunits * (stage == 1 ? ph1.tiles : ph2.tiles);
-        const int lo = cut(tiles, i), hi = cut(tiles, i + 1);
-        if (stage == 1)
-          Experts<FMT, RT, NB, 1, DEPTH, MAIN>(a, ph1, cta, ksplit1).share(lo, hi, nullptr, 0u);
-        else
-          Experts<FMT, RT, NB, 2, DEPTH, MAIN>(a, ph2, cta, ksplit2).share(lo, hi, a.ctl->done + 1, n);
-      }
-    }
+    if (tid == THREADS - 1) s_ticket = atomicAdd(&a.ctl->ticket, 1u);
+  };
+  auto end_share = [&](int stage) {  // counts this one as done, and goes to the next
     __syncthreads();
     if (tid == THREADS - 32 && stage < 3) {
       __threadfence();
       atomicAdd(&a.ctl->done[stage], 1u);
     }
     ticket = s_ticket;
+  };
+
+#pragma unroll 1
+  while (ticket < n) {
+    begin_share();
+    const uint32_t r = n - 1 - ticket;  // the tokens' statistics go to the last shares first
+    router_share(a, cut(a.E, ticket), cut(a.E, ticket + 1), cut(a.T, r), cut(a.T, r + 1), reinterpret_cast<float*>(rows),
+                 s_part);
+    end_share(0);
+  }
+  if (ticket < 3 * n) {
+    if (a.all_rows && ticket < 2 * n) {
+      __syncthreads();
+      Experts<FMT, RT, NB, 1, DEPTH, MAIN>(a, ph1, cta, ksplit1).stage_all(s_part);
+    }
+    wait_stage(a, cta.abort, a.ctl->done, n);
+    if (!s_abort) {
+      make_plan(a, cta.plan);
+      if (ticket == n && tid >= 32 * MAIN)
+#pragma unroll 1
+        for (int t = (tid >> 5) - MAIN; t < a.T; t += ML_FINISH) write_routes(a, t, cta.plan.pair_e);
+    }
+  }
+#pragma unroll 1
+  while (ticket < 2 * n) {
+    begin_share();
+    const uint32_t i = ticket - n, tiles = s_abort ? 0u : cta.plan.nunits * ph1.tiles;
+    Experts<FMT, RT, NB, 1, DEPTH, MAIN>(a, ph1, cta, ksplit1).share(cut(tiles, i), cut(tiles, i + 1), nullptr, 0u);
+    end_share(1);
+  }
+#pragma unroll 1
+  while (ticket < 3 * n) {
+    begin_share();
+    const uint32_t i = ticket - 2 * n, tiles = s_abort ? 0u : cta.plan.nunits * ph2.tiles;
+    Experts<FMT, RT, NB, 2, DEPTH, MAIN>(a, ph2, cta, ksplit2).share(cut(tiles, i), cut(tiles, i + 1), a.ctl->done + 1, n);
+    end_share(2);
+  }
+#pragma unroll 1
+  while (a.h_out && ticket < 4 * n) {
+    begin_share();
+    wait_stage(a, cta.abort, a.ctl->done + 2, n);
+    const uint32_t i = ticket - 3 * n;
+    const int half = a.H / 2;
+    const int lo = cut(a.T * half, i), hi = cut(a.T * half, i + 1);
+#pragma unroll 1
+    for (int p = lo + tid; p < hi && !s_abort; p += THREADS) combine2(a, p / half, 2 * (p % half));
+    end_share(3);
   }
   if (tid == THREADS - 32) {
     __threadfence();
