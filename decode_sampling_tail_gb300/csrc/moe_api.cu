@@ -144,7 +144,7 @@ int tail_moe_run(tail_moe_t* m, const uint16_t* x, const float* gamma_opt, const
   DeviceGuard guard(m->device);
   if (!guard.ok) return TAIL_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const MoeLayerPlan plan = plan_moe_layer(n_tokens, c.topk, c.n_shared, c.E, c.H, c.I, fp4, m->max_smem,
+  const MoeLayerPlan plan = plan_moe_layer(n_tokens, c.topk, c.n_shared, c.E, c.H, c.I, m->N1, fp4, m->max_smem,
                                            m->num_sms);
   if (!plan.ok) return TAIL_ERR_UNSUPPORTED;  // not reached within the limits of create
   MoeLayerArgs a;

@@ -1016,14 +1016,25 @@ int pitch_of(int fmt, int K) {
   return (K + cols - 1) / cols * cols * 2 + 64;
 }
 
-// Warps that split K: as many as keep 85 % of their k-steps busy (small tiles spread evenly over the
-// SMs: with 192 rows a tile instead of 48, 8 tokens over 66 experts took 165 us instead of 136).
-int ksplit_of(int fmt, int K) {
+// Warps that split K: a divisor k of the main warps, and MAIN / k of them share a tile's rows.  The largest k that
+// keeps 85 % of their k-steps busy: small tiles spread evenly over the SMs (bf16, 8 tokens over 66 experts: 165 us
+// with 192 rows a tile, 136 with 48).  A 4-bit k-step holds four times the columns of a bf16 one, so that a warp
+// would often meet one of a tile, and a tile costs it as much as a k-step: there k falls while a warp's run is
+// below 6 k-steps and the units' tiles are at least 4 an SM (64 tokens over 128 experts of 2880 columns: k = 12, runs
+// of one, 263 us; 6: 222; 4: 211; 2, runs of six: 204; 1: 212.  One token, four experts: k = 12 36.7 us; 6, the
+// rule's: 35.4; 4: 38).  bf16 under the same rule: 8 tokens 129 -> 130 us, 64 tokens 870 -> 873.
+int ksplit_of(int fmt, int rt, int K, int N, int units, int sms) {
   const int steps = (K + step_cols(fmt) - 1) / step_cols(fmt), main = MAIN_WARPS;
-  int best = 1;
-  for (int k = 2; k <= main; ++k)
-    if (main % k == 0 && 100 * steps >= 85 * ((steps + k - 1) / k * k) ) best = k;
-  return best;
+  int best = 0;
+  for (int k = main; k >= 1; --k) {
+    const int run = (steps + k - 1) / k;  // k-steps of a warp in a tile
+    if (main % k != 0 || 100 * steps < 85 * run * k) continue;
+    if (best != 0 && (fmt == BF16 || steps >= 6 * best ||
+                      static_cast<int64_t>(units) * N < static_cast<int64_t>(4) * sms * 16 * rt * (main / k)))
+      break;
+    best = k;
+  }
+  return best;  // k = 1 keeps all of them busy
 }
 
 Phase make_phase(const MoeLayerArgs& a, int fmt, int nb, int phase, int ksplit) {
@@ -1083,7 +1094,7 @@ cudaError_t launch_columns(const MoeLayerArgs& a, const MoeLayerPlan& p, cudaStr
 }  // namespace
 
 // Tokens a unit may hold and the shared memory, with activation rows of the wider of the two products.
-MoeLayerPlan plan_moe_layer(int T, int topk, int nsh, int E, int H, int I, bool fp4, int max_smem, int num_sms) {
+MoeLayerPlan plan_moe_layer(int T, int topk, int nsh, int E, int H, int I, int N1, bool fp4, int max_smem, int num_sms) {
   MoeLayerPlan p;
   max_smem -= STATIC_SMEM;  // the limit counts the kernel's own variables too
   p.grid = num_sms;
@@ -1105,8 +1116,9 @@ MoeLayerPlan plan_moe_layer(int T, int topk, int nsh, int E, int H, int I, bool 
     if (p.smem <= max_smem || p.G == 1) break;
   }
   p.ok = p.smem <= max_smem;
-  p.ksplit1 = ksplit_of(p.format, H);
-  p.ksplit2 = ksplit_of(p.format, I);
+  const int units = (T * topk < E ? T * topk : E) + nsh, rt = groups_of(p.format, columns_of(p.G));
+  p.ksplit1 = ksplit_of(p.format, rt, H, N1, units, num_sms);
+  p.ksplit2 = ksplit_of(p.format, rt, I, H, units, num_sms);
   return p;
 }
 

@@ -19,7 +19,7 @@ struct MoeLayerPlan {
   int ksplit1, ksplit2;  // warps that split the columns of W1's and W2's rows
 };
 
-MoeLayerPlan plan_moe_layer(int T, int topk, int nsh, int E, int H, int I, bool fp4, int max_smem, int num_sms);
+MoeLayerPlan plan_moe_layer(int T, int topk, int nsh, int E, int H, int I, int N1, bool fp4, int max_smem, int num_sms);
 cudaError_t launch_moe_layer(const MoeLayerArgs& a, const MoeLayerPlan& p, cudaStream_t stream);
 
 }  // namespace tail
