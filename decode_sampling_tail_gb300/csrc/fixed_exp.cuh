@@ -40,16 +40,18 @@ __device__ const float2 EXP2_TABLE[EXP_TABLE] = {
 };
 
 // log2(e) / T as a pair: the quotient and, from the exact remainder, the rest.  (An fp64 division by
-// every thread kept the fp64 pipe, two operations a clock, busy for 41 of a kernel's 57 us.)
+// every thread kept the fp64 pipe, two operations a clock, busy for 41 of a kernel's 57 us.)  Below T = 2^-127
+// the quotient passes fp32's largest value and counts as that: an infinite one would make 0 times infinity of
+// the maximum's own exponent.
 struct ExpScale {
   float h, l;
 };
 __device__ __forceinline__ ExpScale exp_scale(float temp) {
   constexpr float LH = 0x1.715476p+0f, LL = 0x1.4ae0c0p-26f;  // log2(e)
   ExpScale s;
-  s.h = LH / temp;
+  s.h = fminf(LH / temp, 3.402823466e38f);
   const float rest = fmaf(-s.h, temp, LH) + LL;
-  s.l = s.h > 0.f && s.h < INFINITY ? rest / temp : 0.f;
+  s.l = s.h > 0.f && s.h < 3.402823466e38f ? rest / temp : 0.f;
   return s;
 }
 
@@ -187,10 +189,10 @@ __device__ __forceinline__ void exp_fixed4(float4 l, float m, ExpScale c, const 
 }
 
 // exp((l - m) / T) in fp32, scale = log2(e) / T: a relative error of a few 2^-24 times the exponent's
-// size.  l == m gives 1.
+// size.  l == m gives 1; l = -inf 0, also where the scale is 0 (fmaxf takes the number beside a NaN).
 __device__ __forceinline__ float exp_fast(float l, float m, float scale) {
   const float e = exp2f((l - m) * scale);
-  return l == m ? 1.0f : l == -INFINITY ? 0.0f : e;
+  return l == m ? 1.0f : fmaxf(e, 0.0f);
 }
 
 // 2^e as fp64, e a normal exponent.

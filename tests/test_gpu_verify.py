@@ -129,6 +129,28 @@ def test_lists_masked_and_extreme_rows(q):
     assert vc.compare(tokens, counts, _lists_want(c), c["cu"]) > 40
 
 
+@pytest.mark.parametrize("q", ["none", "f32"])
+def test_smallest_and_largest_temperatures(q):
+    # below 2^-127 the reciprocal of a temperature is no fp32 number; at +inf it is 0
+    def lists(prm, vals, idx):
+        prm[0::4, 2] = 1e-40
+        prm[1::4, 2] = 1.5e-45
+        prm[2::4, 2] = np.inf
+        vals[::2, 30:] = -np.inf
+    c = _lists_case(23, 40, 48, 500, q, params=lists)
+    tokens, counts = _lists_run(c)
+    assert vc.compare(tokens, counts, _lists_want(c), c["cu"]) > 25
+
+    def whole(z, temp):
+        temp[0::4] = 1e-40
+        temp[1::4] = 1.5e-45
+        temp[2::4] = np.inf
+        z[::2, 5000:] = -np.inf
+    c = _logits_case(24, 40, 9001, "f32", q, edit=whole)
+    tokens, counts = _logits_run(c)
+    assert vc.compare(tokens, counts, _logits_want(c), c["cu"]) > 25
+
+
 def test_lists_draft_covering_the_target_draws_from_it():
     # q is 1 at every id: the residual is zero, the draw is from P
     c = _lists_case(31, 40, 20, 100, "f32")
