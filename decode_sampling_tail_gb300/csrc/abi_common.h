@@ -21,6 +21,13 @@ inline int elem_bytes(int dtype) { return dtype == TAIL_F32 ? 4 : 2; }
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Whether two byte ranges meet.
+inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uint8_t* x = static_cast<const uint8_t*>(a);
+  const uint8_t* y = static_cast<const uint8_t*>(b);
+  return x < y + nb && y < x + na;
+}
+
 // Makes a device current for a scope; the caller's comes back at its end.
 struct DeviceGuard {
   int prev = -1;

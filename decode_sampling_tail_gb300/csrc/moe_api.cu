@@ -54,13 +54,6 @@ bool supported(const tail_moe_config* c) {
 
 int64_t round256(int64_t v) { return (v + 255) & ~int64_t(255); }
 
-// Whether two byte ranges meet.
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uint8_t* x = static_cast<const uint8_t*>(a);
-  const uint8_t* y = static_cast<const uint8_t*>(b);
-  return x < y + nb && y < x + na;
-}
-
 }  // namespace
 
 extern "C" {

@@ -7,10 +7,17 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "abi_common.h"
 #include "common.cuh"
 #include "fixed_exp.cuh"
 
 namespace tail {
+
+// Whether an output of n words meets another array of the call (rows or nseq + 1 words each): CTAs of one
+// sequence read its drafts and uniforms while another writes its tokens.
+inline bool meets(const void* out, int64_t n, const void* in, int64_t words) {
+  return overlap(out, n * 4, in, words * 4);
+}
 
 constexpr int VERIFY_THREADS = 256;
 constexpr int VERIFY_WARPS = VERIFY_THREADS / 32;

@@ -240,6 +240,15 @@ extern "C" int tail_verify(int32_t rows, int32_t nseq, int32_t k, const float* t
     if (!aligned(topk_vals, 4) || !aligned(topk_idx, 4) || !aligned(params, 4) || !aligned(drafts, 4) ||
         !aligned(u_accept, 4) || !aligned(out_tokens, 4))
       return TAIL_ERR_INVALID_ARG;
+    const int64_t n = rows;
+    const struct {
+      const void* p;
+      int64_t words;
+    } in[] = {{cu_rows, nseq + 1LL}, {drafts, n}, {u_accept, n}, {topk_vals, n * k}, {topk_idx, n * k},
+              {params, n * n_param_cols}};
+    for (const auto& i : in)
+      if (meets(out_tokens, n, i.p, i.words) || meets(out_count, nseq, i.p, i.words)) return TAIL_ERR_INVALID_ARG;
+    if (meets(out_tokens, n, out_count, nseq)) return TAIL_ERR_INVALID_ARG;
   }
   if (draft_probs_opt) {
     if (draft_dtype < TAIL_F32 || draft_dtype > TAIL_BF16 || V < 1 || draft_ld < V) return TAIL_ERR_INVALID_ARG;

@@ -622,6 +622,14 @@ extern "C" int tail_verify_logits(int32_t rows, int32_t nseq, int32_t V, const v
     if (!aligned(logits, elem_bytes(logits_dtype)) || !aligned(temperature, 4) || !aligned(drafts, 4) ||
         !aligned(u_accept, 4) || !aligned(u_draw, 4) || !aligned(out_tokens, 4))
       return TAIL_ERR_INVALID_ARG;
+    const int64_t n = rows;
+    const struct {
+      const void* p;
+      int64_t words;
+    } in[] = {{cu_rows, nseq + 1LL}, {drafts, n}, {u_accept, n}, {u_draw, n}, {temperature, n}, {workspace, need / 4}};
+    for (const auto& i : in)
+      if (meets(out_tokens, n, i.p, i.words) || meets(out_count, nseq, i.p, i.words)) return TAIL_ERR_INVALID_ARG;
+    if (meets(out_tokens, n, out_count, nseq)) return TAIL_ERR_INVALID_ARG;
   }
   if (draft_probs_opt) {
     if (draft_dtype < TAIL_F32 || draft_dtype > TAIL_BF16 || draft_ld < V) return TAIL_ERR_INVALID_ARG;

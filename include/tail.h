@@ -393,6 +393,8 @@ int tail_merge_shards(int32_t nshard, int32_t k_in, int32_t k, int32_t gbs, cons
  *                  the drafts are certain (q_j is 1 at x_j).  Values count as cut to [0, 1].
  *   out_tokens     [rows] int32: per sequence the accepted drafts, the token, then -1.
  *   out_count      [nseq] int32: tokens emitted (accepted drafts + 1).
+ * Outputs must not overlap an input, the workspace or one another (TAIL_ERR_INVALID_ARG where
+ * they meet the small arrays).  Everything is read in stream order.
  * A row whose every candidate is -inf has nothing to draw from: its draft is refused
  * and its token is -1 (counted).  A candidate at -inf has probability 0; among logits
  * of +inf the mass is shared.  NaN is outside the domain.  Draws are made with weights
@@ -452,8 +454,10 @@ int tail_verify_logits(int32_t rows, int32_t nseq, int32_t V, const void* logits
  *   h = bf16(x + bf16(r + sh)): the combine of tail_run_moe over these slots.
  * (GPT-OSS: softmax, interleaved GLU with alpha 1.702, beta 1, limit 7; a SiLU-gated layer:
  * alpha 1, beta 0, limit 0; Nemotron: sigmoid with bias, RELU2, 2 shared experts.)
- * Selected experts' weights are read once for up to 16 tokens (fewer when H or I is above
- * about 3000); products and sums are fp32, with activations carried as two 16-bit parts.
+ * A selected expert's weights are read once for its tokens up to a number between 4 and 16 (as
+ * many as an even spread of the call's tokens would bring it, with room; beyond 4 to 8 as shared
+ * memory allows: 10 at widths of 2880, 1 at 16384); products and sums are fp32, with activations
+ * carried as two 16-bit parts.
  */
 typedef enum { TAIL_MOE_GLU = 0, TAIL_MOE_RELU2 = 1 } tail_moe_act;
 typedef enum { TAIL_MOE_SOFTMAX = 0, TAIL_MOE_SIGMOID = 1 } tail_moe_score;
@@ -497,7 +501,7 @@ int tail_moe_create(const tail_moe_config* cfg, int device, tail_moe_t** out);
  *   out_slots_opt  [n_tokens][S][H] fp32 y, 16-byte aligned, or NULL: with out_slot_w_opt the
  *                  `slots` and `slot_w` of tail_run_moe (n_routed = topk).  One of the two is needed.
  *   out_slot_w_opt [n_tokens][S] fp32, out_ids_opt [n_tokens][S] int32, or NULL.
- * Inputs must not alias outputs otherwise.  One run per handle at a time (its scratch is shared),
+ * Inputs must not alias outputs otherwise, and everything is read in stream order.  One run per handle at a time (its scratch is shared),
  * also between captured graphs.  Results are deterministic, and a token's do not depend on the
  * others except through how many tokens share an expert (fp32 summation order).  Non-finite
  * activations give non-finite outputs in their own token's row only.

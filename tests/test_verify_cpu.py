@@ -10,6 +10,7 @@ from decode_sampling_tail_gb300 import build as dbuild
 from tests import verifycheck as vc
 
 P = 4096  # stands for an aligned device pointer; refused calls never read it
+OT, OC, WS = 1 << 24, 1 << 25, 1 << 26  # outputs and workspace, apart from it
 
 
 @pytest.fixture(scope="module")
@@ -20,7 +21,7 @@ def L():
 
 def verify(L, **kw):
     a = dict(rows=4, nseq=1, k=8, vals=P, idx=P, params=P, cols=4, cu=P, drafts=P, accept=P, q=None, qd=0, ld=0, V=0,
-             tokens=P, count=P)
+             tokens=OT, count=OC)
     a.update(kw)
     return L.tail_verify(a["rows"], a["nseq"], a["k"], a["vals"], a["idx"], a["params"], a["cols"], a["cu"],
                          a["drafts"], a["accept"], a["q"], a["qd"], a["ld"], a["V"], a["tokens"], a["count"], None)
@@ -36,13 +37,27 @@ def test_verify_refuses(L, kw):
     assert verify(L, **kw) == dst.TAIL_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("call,names", [
+    ("verify", ["cu", "drafts", "accept", "vals", "idx", "params"]),
+    ("logits", ["cu", "drafts", "accept", "u", "temp", "ws"])])
+@pytest.mark.parametrize("out", ["tokens", "count"])
+def test_outputs_over_inputs_are_refused(L, call, names, out):
+    run = verify if call == "verify" else logits
+    for name in names:
+        # one sequence of 4 rows: 16 bytes of tokens, 4 of counts
+        for by in ((0, -16) if name == "ws" else (0, 4, -4) if out == "tokens" else (0, -4)):
+            kw = {out: 1 << 28, name: (1 << 28) + by}
+            assert run(L, **kw) == dst.TAIL_ERR_INVALID_ARG, (name, by)
+    assert run(L, tokens=OT, count=OT + 12) == dst.TAIL_ERR_INVALID_ARG
+
+
 def test_no_sequences_is_a_no_op(L):
     assert verify(L, nseq=0, cu=None, count=None) == dst.TAIL_OK
 
 
 def logits(L, **kw):
     a = dict(rows=4, nseq=1, V=100, logits=P, ld_t=0, ld=100, temp=P, cu=P, drafts=P, accept=P, u=P, q=None, qd=0,
-             qld=0, ws=P, wb=1 << 20, tokens=P, count=P)
+             qld=0, ws=WS, wb=1 << 20, tokens=OT, count=OC)
     a.update(kw)
     return L.tail_verify_logits(a["rows"], a["nseq"], a["V"], a["logits"], a["ld_t"], a["ld"], a["temp"], a["cu"],
                                 a["drafts"], a["accept"], a["u"], a["q"], a["qd"], a["qld"], a["ws"], a["wb"],
@@ -52,7 +67,7 @@ def logits(L, **kw):
 @pytest.mark.parametrize("kw", [
     dict(rows=-1), dict(nseq=-1), dict(V=0), dict(logits=None), dict(temp=None), dict(cu=None), dict(drafts=None),
     dict(accept=None), dict(u=None), dict(tokens=None), dict(count=None), dict(ld_t=3), dict(ld_t=-1), dict(ld=99),
-    dict(logits=P + 2), dict(logits=P + 1, ld_t=2), dict(temp=P + 2), dict(ws=None), dict(ws=P + 8), dict(wb=100),
+    dict(logits=P + 2), dict(logits=P + 1, ld_t=2), dict(temp=P + 2), dict(ws=None), dict(ws=WS + 8), dict(wb=100),
     dict(q=P, qd=3, qld=100), dict(q=P, qld=99), dict(q=P + 2, qld=100)])
 def test_verify_logits_refuses(L, kw):
     assert logits(L, **kw) == dst.TAIL_ERR_INVALID_ARG
