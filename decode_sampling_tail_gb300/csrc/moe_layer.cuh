@@ -33,7 +33,7 @@
 
 namespace tail {
 
-constexpr int ML_FINISH = 4;  // warps that add the partial sums and finish the rows, besides 8 or 12 main warps
+constexpr int ML_FINISH = 4;  // warps that add the partial sums and finish the rows, besides the 12 main warps
 constexpr int ML_MAX_WARPS = 16;
 constexpr int ML_BUFS = 4;    // tiles whose partial sums may wait for a finishing warp
 constexpr int ML_MAX_T = 64;
@@ -197,7 +197,7 @@ __device__ __forceinline__ void route_token(const MoeLayerArgs& a, int t, uint16
     key[i] = 0u;  // below every score's key
     if (e < a.E) {
       const float v = __ldcg(z + e);
-      key[i] = float_key(a.br ? route_score(a, v) + __ldg(a.br + e) : v);
+      key[i] = max(float_key(a.br ? route_score(a, v) + __ldg(a.br + e) : v), 1u);  // (0: some NaN's key)
     }
   }
   int mine = 0;
@@ -294,8 +294,8 @@ __device__ __forceinline__ void make_plan(const MoeLayerArgs& a, MoePlan& p) {
     auto write_units = [&](uint32_t e, uint32_t n, uint32_t at) {
       p.cnt[e] = at & 0xffffu;
       uint32_t u = at >> 16;
-  #pragma unroll 1
-    for (uint32_t f = 0; f < n; f += a.G, ++u)
+#pragma unroll 1
+      for (uint32_t f = 0; f < n; f += a.G, ++u)
         p.unit[u] = e | (((at & 0xffffu) + f) << 10) | (min(n - f, static_cast<uint32_t>(a.G)) << 21);
     };
     write_units(2 * tid, n0, before);

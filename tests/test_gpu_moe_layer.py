@@ -246,6 +246,45 @@ def test_layer_runs_again_in_place_and_on_other_streams():
                      b1=c.b1, b2=c.b2).shape == (0, c.H)
 
 
+def test_two_handles_run_side_by_side():
+    # every CTA of a run wants a whole SM; runs of two handles share the device in any mix, eager and replayed
+    cases = [Case(12, 416, 288, 10, 4, w="mxfp4", shared=1, seed=15), Case(5, 512, 384, 9, 3, seed=16)]
+    want = [run_check(c)["out_hidden"] for c in cases]
+    streams = [torch.cuda.Stream(DEV) for _ in cases]
+    handles = [c.handle() for c in cases]
+    outs = [[torch.empty_like(w) for _ in range(6)] for w in want]
+    graphs = [torch.cuda.CUDAGraph() for _ in cases]
+    torch.cuda.synchronize()
+    for c, m, s, g, o in zip(cases, handles, streams, graphs, outs):
+        with torch.cuda.graph(g, stream=s):
+            for y in o[:3]:
+                c.run(m, dict(out_hidden=y), stream=s)
+    for _ in range(20):
+        for c, m, s, g, o in zip(cases, handles, streams, graphs, outs):
+            with torch.cuda.stream(s):
+                g.replay()
+            for y in o[3:]:
+                c.run(m, dict(out_hidden=y), stream=s)
+    torch.cuda.synchronize()
+    for m, o, w in zip(handles, outs, want):
+        m.check()
+        assert all(torch.equal(y, w) for y in o)
+        m.close()
+
+
+def test_layer_nan_router_bias_stays_within_the_experts():
+    # a NaN score ranks somewhere; the slots still name experts of the layer
+    c = Case(6, 96, 64, 5, 2, seed=17)
+    bits = torch.tensor([-1, 0x7fc00000, -1, -1, -1], dtype=torch.int32, device=DEV)
+    c.router_bias = bits.view(torch.float32)
+    out = c.outputs()
+    with c.handle() as m:
+        c.run(m, out)
+        torch.cuda.synchronize()
+        m.check()
+    assert ((out["out_ids"] >= 0) & (out["out_ids"] < 5)).all()
+
+
 def test_layer_slots_feed_the_tails_producer_step():
     # slots and weights through tail_run_moe give the h, the top-k and the tokens of out_hidden through the tail
     w = gen.custom(6, 256, 8192, 32, hidden_dtype="bf16", seed=330)
