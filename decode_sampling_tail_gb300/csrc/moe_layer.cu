@@ -12,6 +12,14 @@
 // share that a CTA waits on is held by a CTA that runs and, in its turn, waits on
 // earlier stages only.  CTAs that start late find their shares done by others.
 // Waits are bounded; one that runs out raises the error word, and the CTA leaves.
+//
+// Bound: bf16 by HBM, 4-bit weights by instructions.  Measured (copy rate 6.69 TB/s): bf16, 64 tokens over 128
+// experts of 2880 x 5760 and 2880 x 2880, 5.54 GB: 849-870 us, 6.4-6.5 TB/s (0.95-0.98); 8 tokens over 64 experts
+// and 2 shared, 737 MB: 122-125 us, 0.88-0.90; 5 tokens over 32 experts 0.88-0.92.  4 bits, 16 tokens over 128
+// experts, 677 MB: 200-204 us, 0.50: a 2 KB k-step of a warp takes about 350 instructions (196 of them conversions,
+// scalings and products), a scheduler's three main warps issue on 47 % of the cycles, and neither a deeper ring
+// (3, 4, 5 or 6 steps: 204.8, 204.2, 205.4, 206.2 us) nor k-steps of 32 rows (211) move it.  One token, 54 MB:
+// 35.4 us, a chain of stage latencies and of fetching code that runs once.
 #include <math.h>
 
 #include "internal.h"
@@ -52,7 +60,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 // The logits of experts [e0, e1) for every token, and per token in [t0, t1) 1 / rms, the largest |t| and its
 // pairs' largest-activation words cleared.  The whole CTA; a warp a token, or several, K split, when there are
 // fewer tokens than warps.  The norm factors out: z = (1 / rms) * sum(x gamma w), and gamma w is formed once, in
-// shared memory (v: H floats).
+// shared memory (v: H floats).  Latency: 16 bytes a lane and step from L2, and the barriers between.
 __device__ __forceinline__ void router_share(const MoeLayerArgs& a, int e0, int e1, int t0, int t1, float* v,
                                              float* s_part) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nt = blockDim.x, nw = nt >> 5;
@@ -144,8 +152,8 @@ __device__ __forceinline__ void router_share(const MoeLayerArgs& a, int e0, int 
 // warp keeps DEPTH k-steps of 2 KB under way, across tile borders (12 warps of 4: 96 KB an SM); at
 // the end of a tile it leaves its partial sums in shared memory and goes on.  A finishing warp adds
 // them in a fixed order and finishes the rows: its chain of bias loads, sums and exponentials held up
-// every warp of the CTA when a main warp did it between two barriers (64 tokens over 128 experts:
-// 1640 us).
+// every warp of the CTA when a main warp did it between two barriers (bf16, 64 tokens over 128
+// experts: 1640 us).
 //
 // Formats: BF16; MXFP4; MXFP4_WIDE, for rows that are whole pieces of 64 columns.
 enum Format : int { BF16 = 0, MXFP4 = 1, MXFP4_WIDE = 2 };
@@ -1020,9 +1028,9 @@ int pitch_of(int fmt, int K) {
 // keeps 85 % of their k-steps busy: small tiles spread evenly over the SMs (bf16, 8 tokens over 66 experts: 165 us
 // with 192 rows a tile, 136 with 48).  A 4-bit k-step holds four times the columns of a bf16 one, so that a warp
 // would often meet one of a tile, and a tile costs it as much as a k-step: there k falls while a warp's run is
-// below 6 k-steps and the units' tiles are at least 4 an SM (64 tokens over 128 experts of 2880 columns: k = 12, runs
+// below 6 k-steps and the units' tiles are at least 4 an SM (16 tokens over 128 experts of 2880 columns: k = 12, runs
 // of one, 263 us; 6: 222; 4: 211; 2, runs of six: 204; 1: 212.  One token, four experts: k = 12 36.7 us; 6, the
-// rule's: 35.4; 4: 38).  bf16 under the same rule: 8 tokens 129 -> 130 us, 64 tokens 870 -> 873.
+// rule's: 35.4; 4: 38).  bf16 under the same rule: 5 tokens 129 -> 130 us, 64 tokens 870 -> 873.
 int ksplit_of(int fmt, int rt, int K, int N, int units, int sms) {
   const int steps = (K + step_cols(fmt) - 1) / step_cols(fmt), main = MAIN_WARPS;
   int best = 0;

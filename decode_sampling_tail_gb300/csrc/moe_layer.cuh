@@ -9,8 +9,10 @@
 // A few tokens select a few experts each, so the layer is a stream of weights:
 // every selected expert's W1 and W2 once.  The matrix products run on mma.sync
 // with 16 weight rows as the M side and up to 8 tokens as the N side; for so few
-// columns the tensor pipe idles either way, and registers are fed without
-// a barrier.
+// columns the tensor pipe idles either way (8 tokens in bf16 need 0.18 of mma.sync's rate
+// at full memory bandwidth; a tcgen05 tile would be 128 rows by at least 8 columns, its
+// operands rounded to what one descriptor takes, its weights behind a barrier), and
+// registers are fed without one.
 //
 // Weight fragments.  A lane (g = lane / 4, q = lane % 4) of an m16n8k16 product
 // holds k slots {2q, 2q+1, 2q+8, 2q+9} of rows g and g + 8.  A sum does not mind
