@@ -2,25 +2,25 @@
 // rule of verify_lists.cu with P_j = softmax(l_j / T_j) over all V logits (the
 // lowest index of the maximum when T <= 0).
 //
-// Three kernels, over chunks of 8192 columns that a CTA holds in registers:
+// Three kernels, over chunks of 8192 columns, which a CTA holds in registers, or parts of them:
 //   verify_stats (chunk, row): the chunk's maximum m_c, its lowest column and sum exp((l - m_c) / T)
 //     in fp32.  Every row has to be read, since which one is settled is not known yet; this pass is
 //     bound by memory and only has to decide acceptances (a relative 2^-21 of Z).
-//   verify_settle (chunk, sequence): each CTA judges the sequence's rows from those statistics (all
+//   verify_settle (part, sequence): each CTA judges the sequence's rows from those statistics (all
 //     of them compute the same bits, none waits) and finds the settled row; then the sums of that row's
-//     segments (1024 columns, a warp's part) as integers (fixed_exp.cuh, units of 2^-49 relative to m_c).
-//   verify_draw (chunk, sequence): after d accepted drafts, or with one-hot drafts (P without x_j), the
+//     segments (1024 columns) as integers (fixed_exp.cuh, units of 2^-49 relative to m_c).
+//   verify_draw (part, sequence): after d accepted drafts, or with one-hot drafts (P without x_j), the
 //     segments' sums already say which one holds the token; one CTA reads its columns again.  The
-//     residual max(P - q, 0) needs one pass over that row's l and q: every CTA sums its chunk's segments,
+//     residual max(P - q, 0) needs one pass over that row's l and q: every CTA sums its segments,
 //     the last of the sequence to finish (a counter that verify_settle cleared) picks one and the token.
 // Sums over segments are integers of 2^-shift relative to the row's maximum, with V 2^shift below 2^62;
 // the residual is max(e - q Z, 0) in the same units.  The draft's row is read only for sequences that
 // refuse a draft.
 //
-// Measured at V = 201088: 96 sequences (384 fp32 rows, and fp32 draft rows where one is refused) 168 us back to back, of
+// Measured at V = 201088: 96 sequences (384 fp32 rows, and fp32 draft rows where one is refused) 167 us back to back, of
 // them stats 53-59 us (309 MB: 5.3-5.8 TB/s, 0.8-0.87 of the copy rate), settle 45-47 and draw 72-74: both form
-// 19 million exponentials to 2^-36, 50 and 70 instructions each, on 55-62 % of the issue slots; 16 sequences 44 us;
-// one sequence of 5 rows 18 us, the latency of three launches.
+// 19 million exponentials to 2^-36, 50 and 70 instructions each, on 55-62 % of the issue slots; 16 sequences 41 us;
+// one sequence of 5 rows 17 us, the latency of three launches.
 #include "../../include/tail.h"
 #include "abi_common.h"
 #include "verify.cuh"
@@ -133,26 +133,42 @@ __device__ __forceinline__ int chunk_col(const T* row, int c) {
   return c * VL_CHUNK - off;
 }
 
-// The first of a thread's columns of chunk c.
-template <typename T>
-__device__ __forceinline__ int first_col(const T* row, int c) {
-  return chunk_col(row, c) + (threadIdx.x >> 5) * VL_WARP_COLS + (threadIdx.x & 31) * 4;
+// The first of a thread's columns of part p of 1 / P of a chunk, p counted over the row; it has VL_GROUPS / P
+// groups of them.  A part is 8 / P segments, with P warps on each.
+template <int P, typename T>
+__device__ __forceinline__ int first_col(const T* row, int p) {
+  const int warp = threadIdx.x >> 5;
+  return chunk_col(row, p / P) + (p % P * (VERIFY_WARPS / P) + warp / P) * VL_WARP_COLS +
+         warp % P * (VL_WARP_COLS / P) + (threadIdx.x & 31) * 4;
 }
 
-// A chunk's values in shared memory, each read back by the thread that wrote it: the weights' loops stay
+// The sums of part p's segments, from its warps'; the whole CTA.
+template <int P>
+__device__ __forceinline__ void store_segments(int64_t sum, int64_t* out, int p, int64_t* s_sum) {
+  const int tid = threadIdx.x;
+  if ((tid & 31) == 0) s_sum[tid >> 5] = sum;
+  __syncthreads();
+  if (tid < VERIFY_WARPS / P) {
+    int64_t s = 0;
+#pragma unroll
+    for (int k = 0; k < P; ++k) s += s_sum[tid * P + k];
+    __stcg(reinterpret_cast<long long*>(out) + p * (VERIFY_WARPS / P) + tid, static_cast<long long>(s));
+  }
+}
+
+// A part's values in shared memory, each read back by the thread that wrote it: the weights' loops stay
 // rolled (code that runs once is bound by fetching it).
-struct ChunkVals {
-  float4 l[VL_GROUPS][VERIFY_THREADS];
+template <int P>
+struct PartVals {
+  float4 l[VL_GROUPS / P][VERIFY_THREADS];
 };
 
-template <typename T>
-__device__ __forceinline__ int stage_chunk(const T* row, int c, int V, ChunkVals& s) {
-  const int col0 = first_col(row, c);
-  float v[VL_GROUPS][4];
-  load_groups(row, col0, V, -INFINITY, v);
+template <int P, typename T>
+__device__ __forceinline__ void stage_part(const T* row, int p, int V, PartVals<P>& s) {
+  float v[VL_GROUPS / P][4];
+  load_groups(row, first_col<P>(row, p), V, -INFINITY, v);
 #pragma unroll
-  for (int i = 0; i < VL_GROUPS; ++i) s.l[i][threadIdx.x] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-  return col0;
+  for (int i = 0; i < VL_GROUPS / P; ++i) s.l[i][threadIdx.x] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
 }
 
 template <typename T>
@@ -166,7 +182,7 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_stats_kernel(const Logi
   if (row >= __ldg(a.cu + a.nseq)) return;  // behind the last sequence
   const T* lrow = static_cast<const T*>(a.logits) + row * a.ld;
   const float temp = __ldg(a.temp + row);
-  const int col0 = first_col(lrow, c);
+  const int col0 = first_col<1>(lrow, c);
   float v[VL_GROUPS][4];
   load_groups(lrow, col0, a.V, -INFINITY, v);
   float m = -INFINITY;
@@ -272,13 +288,14 @@ __device__ __forceinline__ bool judge_row(const LogitsArgs& a, int row, bool bon
   return ok;
 }
 
-template <typename T>
+template <typename T, int P>
 __global__ void __launch_bounds__(VERIFY_THREADS) verify_settle_kernel(const LogitsArgs a) {
   __shared__ float2 s_table[EXP_TABLE];
   __shared__ Settled s_row[VERIFY_WARPS];
-  __shared__ ChunkVals s_vals;
+  __shared__ PartVals<P> s_vals;
+  __shared__ int64_t s_sum[VERIFY_WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int seq = blockIdx.y, c = blockIdx.x;
+  const int seq = blockIdx.y, part = blockIdx.x;
   if (tid < EXP_TABLE) s_table[tid] = EXP2_TABLE[tid];
   __syncthreads();
   pdl_wait();
@@ -304,7 +321,7 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_settle_kernel(const Log
     }
     __syncthreads();
   }
-  if (c == 0) {
+  if (part == 0) {
     write_sequence(lo, hi, st.row, a.drafts, a.tokens, a.count + seq);
     if (tid == 0) {
       a.settled[seq] = st;
@@ -313,13 +330,13 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_settle_kernel(const Log
     }
   }
   if (st.token > -2) return;
-  const float m = a.stats[static_cast<int64_t>(st.row) * a.nchunk + c].max;
+  const float m = a.stats[static_cast<int64_t>(st.row) * a.nchunk + part / P].max;
   int64_t sum = 0;
   if (m != -INFINITY) {
-    stage_chunk(static_cast<const T*>(a.logits) + st.row * a.ld, c, a.V, s_vals);
+    stage_part<P>(static_cast<const T*>(a.logits) + st.row * a.ld, part, a.V, s_vals);
     const ExpScale sc = exp_scale(__ldg(a.temp + st.row));
 #pragma unroll 1
-    for (int i = 0; i < VL_GROUPS; ++i) {
+    for (int i = 0; i < VL_GROUPS / P; ++i) {
       const float4 v = s_vals.l[i][tid];
       int64_t r[4];
       exp_fixed4(v, m, sc, s_table, VL_SHIFT, r);
@@ -327,7 +344,7 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_settle_kernel(const Log
     }
     sum = warp_sum(sum);
   }
-  if (lane == 0) a.sums[(static_cast<int64_t>(seq) * a.nchunk + c) * VERIFY_WARPS + warp] = sum;
+  store_segments<P>(sum, a.sums + static_cast<int64_t>(seq) * a.nchunk * VERIFY_WARPS, part, s_sum);
 }
 
 enum DrawMode : int {
@@ -362,9 +379,10 @@ __device__ __forceinline__ void weigh4(float4 l, float4 q, int col, const Weigh&
 }
 
 // The draw kernel's columns, each value read back by the thread that wrote it, and the residual's segments.
+template <int P>
 struct DrawVals {
-  float4 l[VL_GROUPS][VERIFY_THREADS];
-  float4 q[VL_GROUPS][VERIFY_THREADS];
+  float4 l[VL_GROUPS / P][VERIFY_THREADS];
+  float4 q[VL_GROUPS / P][VERIFY_THREADS];
   int64_t r[VL_MAX_SEGS];
 };
 
@@ -449,24 +467,24 @@ __device__ __forceinline__ void draw_in_segment(const LogitsArgs& a, int row, in
   }
 }
 
-template <typename T>
+template <typename T, int P>
 __global__ void __launch_bounds__(VERIFY_THREADS) verify_draw_kernel(const LogitsArgs a) {
   __shared__ float2 s_table[EXP_TABLE];
   extern __shared__ __align__(16) uint8_t smem[];
-  DrawVals& s_vals = *reinterpret_cast<DrawVals*>(smem);
+  DrawVals<P>& s_vals = *reinterpret_cast<DrawVals<P>*>(smem);
   __shared__ int64_t s_w[VL_MAX_SEGS];
   __shared__ int64_t s_sum[VERIFY_WARPS];
   __shared__ int s_seg, s_flag;
   __shared__ int64_t s_t;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int seq = blockIdx.y, c = blockIdx.x;
+  const int seq = blockIdx.y, part = blockIdx.x;
   if (tid < EXP_TABLE) s_table[tid] = EXP2_TABLE[tid];
   __syncthreads();
   pdl_wait();
   const Settled st = a.settled[seq];
   if (st.token > -2) return;  // empty, greedy, or nothing to draw from
   const bool residual = st.refused && a.q.p;
-  if (!residual && c != 0) return;
+  if (!residual && part != 0) return;
   const int row = st.row, nseg = a.nchunk * VERIFY_WARPS;
   const T* lrow = static_cast<const T*>(a.logits) + row * a.ld;
   const ChunkStat* cs = a.stats + static_cast<int64_t>(row) * a.nchunk;
@@ -476,8 +494,8 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_draw_kernel(const Logit
   g.mode = !st.refused ? DRAW_P : residual ? DRAW_RESIDUAL : DRAW_OTHERS;
   g.x = st.refused ? __ldg(a.drafts + row) : -1;
   g.sc = exp_scale(__ldg(a.temp + row));
-  float v[VL_GROUPS][4];  // this CTA's columns, under way while the sums are scaled
-  const int col0 = first_col(lrow, c);
+  float v[VL_GROUPS / P][4];  // this CTA's columns, under way while the sums are scaled
+  const int col0 = first_col<P>(lrow, part);
   if (residual) load_groups(lrow, col0, a.V, -INFINITY, v);
 
   // the segments' sums relative to the row's maximum, a one-hot draft's own weight taken out unless that
@@ -514,30 +532,30 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_draw_kernel(const Logit
     g.max = st.max;
     g.z = total;
 #pragma unroll
-    for (int i = 0; i < VL_GROUPS; ++i) s_vals.l[i][tid] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+    for (int i = 0; i < VL_GROUPS / P; ++i) s_vals.l[i][tid] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
     load_draft(a, row, col0, v);
     int64_t sum = 0;
 #pragma unroll
-    for (int i = 0; i < VL_GROUPS; ++i) s_vals.q[i][tid] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+    for (int i = 0; i < VL_GROUPS / P; ++i) s_vals.q[i][tid] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
 #pragma unroll 1
-    for (int i = 0; i < VL_GROUPS; ++i) {
+    for (int i = 0; i < VL_GROUPS / P; ++i) {
       const float4 l = s_vals.l[i][tid], q = s_vals.q[i][tid];
       int64_t w[4];
       weigh4(l, q, 0, g, s_table, w);
       sum += (w[0] + w[1]) + (w[2] + w[3]);
     }
     sum = warp_sum(sum);
-    long long* rsum = reinterpret_cast<long long*>(a.rsum) + static_cast<int64_t>(seq) * nseg;
-    if (lane == 0) __stcg(rsum + c * VERIFY_WARPS + warp, sum);
+    int64_t* rsum = a.rsum + static_cast<int64_t>(seq) * nseg;
+    store_segments<P>(sum, rsum, part, s_sum);
     __threadfence();
     __syncthreads();
-    if (tid == 0) s_flag = atomicAdd(a.done + seq, 1u) == static_cast<uint32_t>(a.nchunk - 1);
+    if (tid == 0) s_flag = atomicAdd(a.done + seq, 1u) == static_cast<uint32_t>(a.nchunk * P - 1);
     __syncthreads();
     if (!s_flag) return;
     __threadfence();
     int64_t any = 0;
     for (int k = tid; k < nseg; k += VERIFY_THREADS) {
-      s_vals.r[k] = __ldcg(rsum + k);
+      s_vals.r[k] = __ldcg(reinterpret_cast<const long long*>(rsum) + k);
       any |= s_vals.r[k];
     }
     if (!__syncthreads_or(any != 0)) g.mode = DRAW_P;  // q covers P: the draw is from P itself
@@ -580,16 +598,28 @@ Parts parts(int rows, int nseq, int V) {
                round256(nseq * static_cast<int64_t>(sizeof(Settled))), round256(nseq * 4LL)};
 }
 
+template <typename T, int P>
+cudaError_t launch_parts(const LogitsArgs& a, cudaStream_t stream) {
+  const dim3 grid(a.nchunk * P, a.nseq);
+  cudaError_t e = launch_overlapped(verify_settle_kernel<T, P>, grid, 0, stream, a);
+  constexpr int smem = static_cast<int>(sizeof(DrawVals<P>));
+  if (e == cudaSuccess)  // idempotent, per device
+    e = cudaFuncSetAttribute(verify_draw_kernel<T, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = launch_overlapped(verify_draw_kernel<T, P>, grid, smem, stream, a);
+  return e;
+}
+
+// CTAs a chunk of the settled rows.  A few sequences leave SMs idle and take quarters, which end sooner; more
+// take halves, since every CTA judges the rows and scales the segments' sums again.  (us with quarters, halves and
+// whole chunks: 25 chunks 17.2, 17.9, 18.6; 259 32.3, 35.4, 37.9; 400 43.7, 41.5, 45.8; 2400 194, 167, 176.)
+constexpr int QUARTERS_UP_TO = 2 * 152;
+
 template <typename T>
 cudaError_t launch(const LogitsArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (a.rows > 0) e = launch_overlapped(verify_stats_kernel<T>, dim3(a.nchunk, a.rows), 0, stream, a);
-  if (e == cudaSuccess) e = launch_overlapped(verify_settle_kernel<T>, dim3(a.nchunk, a.nseq), 0, stream, a);
-  constexpr int smem = static_cast<int>(sizeof(DrawVals));
-  if (e == cudaSuccess)  // idempotent, per device
-    e = cudaFuncSetAttribute(verify_draw_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = launch_overlapped(verify_draw_kernel<T>, dim3(a.nchunk, a.nseq), smem, stream, a);
-  return e;
+  if (e != cudaSuccess) return e;
+  return a.nchunk * a.nseq <= QUARTERS_UP_TO ? launch_parts<T, 4>(a, stream) : launch_parts<T, 2>(a, stream);
 }
 
 }  // namespace

@@ -297,6 +297,19 @@ def test_logits_one_call_is_every_call():
         assert np.array_equal(t, tokens[lo:hi]) and n[0] == counts[s]
 
 
+@pytest.mark.parametrize("l,q", [("f32", "none"), ("bf16", "f32")])
+def test_logits_many_sequences(l, q):
+    # enough of them that a chunk is cut into fewer parts; the same tokens as the first ones alone
+    c = _logits_case(25, 110, 20011, l, q, most=3)
+    tokens, counts = _logits_run(c)
+    assert vc.compare(tokens, counts, _logits_want(c), c["cu"]) > 90
+    n, R = 5, int(c["cu"][5])
+    few = {**c, "cu": c["cu"][: n + 1], "R": R, "logits": c["logits"][:R], "q": None if c["q"] is None else c["q"][:R],
+           **{k: c[k][:R] for k in ("temp", "drafts", "accept", "u")}}
+    t, m = _logits_run(few)
+    assert np.array_equal(t, tokens[:R]) and np.array_equal(m, counts[:n])
+
+
 def test_captured_calls_replay():
     # both forms in one graph, two captured calls with a workspace each; inputs change between replays
     a, b = (_logits_case(s, 8, 9001, "f32", "bf16", pad=0) for s in (14, 15))
