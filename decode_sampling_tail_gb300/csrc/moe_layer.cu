@@ -14,8 +14,8 @@
 // Waits are bounded; one that runs out raises the error word, and the CTA leaves.
 //
 // Bound: bf16 by HBM, 4-bit weights by instructions.  Measured (copy rate 6.69 TB/s): bf16, 64 tokens over 128
-// experts of 2880 x 5760 and 2880 x 2880, 5.54 GB: 849-870 us, 6.4-6.5 TB/s (0.95-0.98); 8 tokens over 64 experts
-// and 2 shared, 737 MB: 122-125 us, 0.88-0.90; 5 tokens over 32 experts 0.88-0.92.  4 bits, 16 tokens over 128
+// experts of 2880 x 5760 and 2880 x 2880, 5.54 GB: 849-876 us, 6.3-6.5 TB/s (0.94-0.98); 8 tokens over 64 experts
+// and 2 shared, 737 MB: 122-126 us, 0.87-0.90; 5 tokens over 32 experts 0.88-0.92.  4 bits, 16 tokens over 128
 // experts, 677 MB: 200-204 us, 0.50: a 2 KB k-step of a warp takes about 350 instructions (196 of them conversions,
 // scalings and products), a scheduler's three main warps issue on 47 % of the cycles, and neither a deeper ring
 // (3, 4, 5 or 6 steps: 204.8, 204.2, 205.4, 206.2 us) nor k-steps of 32 rows (211) move it.  One token, 54 MB:

@@ -17,10 +17,10 @@
 // the residual is max(e - q Z, 0) in the same units.  The draft's row is read only for sequences that
 // refuse a draft.
 //
-// Measured at V = 201088: 96 sequences (384 fp32 rows, and fp32 draft rows where one is refused) 167 us back to back, of
-// them stats 53-59 us (309 MB: 5.3-5.8 TB/s, 0.8-0.87 of the copy rate), settle 45-47 and draw 72-74: both form
-// 19 million exponentials to 2^-36, 50 and 70 instructions each, on 55-62 % of the issue slots; 16 sequences 41 us;
-// one sequence of 5 rows 17 us, the latency of three launches.
+// Measured at V = 201088: 96 sequences (384 fp32 rows, and fp32 draft rows where one is refused) 164-167 us back to back, of
+// them stats 53-59 us (309 MB: 5.3-5.8 TB/s, 0.8-0.87 of the copy rate), settle 46 and draw 65: both form
+// 19 million exponentials to 2^-36, 55 to 75 instructions each, on 66 % of the issue slots; 16 sequences 42 us;
+// one sequence of 5 rows 17-18 us, the latency of three launches.
 #include "../../include/tail.h"
 #include "abi_common.h"
 #include "verify.cuh"
