@@ -297,6 +297,36 @@ def test_logits_one_call_is_every_call():
         assert np.array_equal(t, tokens[lo:hi]) and n[0] == counts[s]
 
 
+def test_rows_behind_32_bit_offsets():
+    # rows 2^30 elements apart: the fourth one's bytes and elements start past 2^32 and past 2^31
+    far = 1 << 30
+    room = torch.empty(5 * far, dtype=torch.bfloat16, device=DEV)
+
+    def spread(t):
+        view = room.as_strided(t.shape, (far, 1), 7)
+        view.copy_(t)
+        return view
+
+    c = _logits_case(26, 2, 3001, "bf16", "f32", most=1, pad=0)
+    c["cu"], c["R"] = np.array([0, 4, 5], np.int32), 5
+    g = np.random.default_rng(27)
+    for k in ("temp", "accept", "u"):
+        c[k] = (0.4 + 0.5 * g.random(5)).astype(np.float32)
+    z = torch.from_numpy(2.5 * g.standard_normal((5, 3001))).to(DEV, torch.bfloat16)
+    q = torch.softmax(z.float() + 0.3, -1)
+    c["logits"], c["q"], c["drafts"] = z, q, q.argmax(-1).int().cpu().numpy()
+    for accept in (1e-6, 0.99):
+        c["accept"][:] = accept
+        want = _logits_want(c)
+        tokens, counts = _logits_run({**c, "logits": spread(z)})
+        assert vc.compare(tokens, counts, want, c["cu"]) >= 1
+        c["q"] = q.to(torch.bfloat16)
+        want = _logits_want(c)
+        tokens, counts = _logits_run({**c, "q": spread(c["q"])})
+        assert vc.compare(tokens, counts, want, c["cu"]) >= 1
+        c["q"] = q
+
+
 @pytest.mark.parametrize("l,q", [("f32", "none"), ("bf16", "f32")])
 def test_logits_many_sequences(l, q):
     # enough of them that a chunk is cut into fewer parts; the same tokens as the first ones alone
