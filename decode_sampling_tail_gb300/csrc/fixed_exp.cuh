@@ -131,8 +131,8 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
 }
 __device__ __forceinline__ F2 sub(F2 a, F2 b) { return fma(b, f2(-1.f), a); }  // exact product: a - b rounded once
 
-// (h 2^28 + w) / 2^r, rounded; r in [0, 63).  By 32-bit conversions and shifts: a conversion to 64 bits
-// runs on the fp64 pipe.
+// (h 2^28 + w) / 2^r, rounded; r in [0, 56]: the value is below 2^54, and half of 2^r has to stay below 2^62.
+// By 32-bit conversions and shifts: a conversion to 64 bits runs on the fp64 pipe.
 __device__ __forceinline__ int64_t drop_bits(float h, float w, int r) {
   const int64_t mant = (static_cast<int64_t>(__float2int_rn(h)) << (EXP_MANT_BITS - 24)) + __float2int_rn(w);
   return (mant + ((int64_t(1) << r) >> 1)) >> r;
@@ -170,8 +170,10 @@ __device__ __forceinline__ void exp_fixed2(float l0, float l1, float m, ExpScale
   float h0, h1, w0, w1;
   unpack(mul(eh, f2(16777216.0f)), h0, h1);
   unpack(mul(el, f2(4503599627370496.0f)), w0, w1);
-  r0 = y0 >= -60.0f ? drop_bits(h0, w0, EXP_MANT_BITS - shift - (k0 >> 5)) : 0;  // also 0 for -inf and NaN
-  r1 = y1 >= -60.0f ? drop_bits(h1, w1, EXP_MANT_BITS - shift - (k1 >> 5)) : 0;
+  // 2^y below half a step is 0, and so are -inf and NaN; what is left drops at most 53 bits (k >> 5 >= -(shift + 1))
+  const float least = -static_cast<float>(shift + 1);
+  r0 = y0 >= least ? drop_bits(h0, w0, EXP_MANT_BITS - shift - (k0 >> 5)) : 0;
+  r1 = y1 >= least ? drop_bits(h1, w1, EXP_MANT_BITS - shift - (k1 >> 5)) : 0;
 }
 
 // Four of them; among logits of +inf (m too) each of those weighs 1 and the others nothing.

@@ -434,3 +434,43 @@ def test_wrappers_refuse_what_does_not_fit():
         dst.verify_logits(*b, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError):
         dst.verify_logits(*b, workspace=torch.empty(1 << 20, dtype=torch.float32, device=DEV))
+
+
+# ------------------------------------------------------------------ far below the chunk's largest
+
+def _deep(z, temp, most=1.0):
+    # per row: columns at 0 and -1 binary orders, one 1024-column segment of the same chunk at -59.03 to -59.97, the
+    # rest below -75: integer weights of nothing, on either side of where exponentials are formed at all
+    rng = np.random.default_rng(50)
+    R, V = z.shape
+    temp[:] = np.geomspace(0.05, most, R).astype(np.float32)
+    unit = (temp.astype(np.float64) * np.log(2.0))[:, None]
+    y = rng.uniform(-120.0, -75.0, (R, V))
+    y[:, 3072:4096] = rng.uniform(-59.97, -59.03, (R, 1024))
+    y[:, 5], y[:, 9] = 0.0, -1.0
+    z[:] = (y * unit).astype(np.float32)
+
+
+@pytest.mark.parametrize("accept", [0.0, 0.9])
+@pytest.mark.parametrize("q", ["none", "f32"])
+def test_logits_segments_without_weight_take_no_draw(q, accept):
+    c = _logits_case(51, 24, 20000, "f32", q, edit=_deep)
+    c["accept"][:] = accept
+    c["drafts"][::2] = 5
+    c["drafts"][1::2] = 9
+    tokens, counts = _logits_run(c)
+    assert vc.compare(tokens, counts, _logits_want(c), c["cu"]) >= 20
+
+
+@pytest.mark.parametrize("l,q", [("f32", "none"), ("f32", "f32"), ("bf16", "bf16")])
+def test_logits_peaked_rows_at_low_temperatures(l, q):
+    def edit(z, temp):
+        rng = np.random.default_rng(52)
+        R, V = z.shape
+        temp[:] = np.geomspace(0.05, 1.0, R).astype(np.float32)
+        z[np.arange(R), rng.integers(0, V, R)] += rng.uniform(12.0, 30.0, R)
+    c = _logits_case(53, 40, 50021, l, q, most=3, edit=edit)
+    tokens, counts = _logits_run(c)
+    assert vc.compare(tokens, counts, _logits_want(c), c["cu"]) >= 30
+    lo, hi = c["cu"][:-1], c["cu"][1:]
+    assert all(tokens[a + n - 1] >= 0 for a, b, n in zip(lo, hi, counts) if b > a)
