@@ -202,6 +202,7 @@ struct Cta {
   uint32_t ring;       // [MAIN][DEPTH] slots
   float4* red;         // [ML_BUFS][MAIN][RT * NACC][32]
   uint32_t full, empty;  // mbarriers [ML_BUFS]: partial sums written, and read
+  uint32_t* top;         // [ML_MAX_G] all_rows: the largest |t| by which stage_all scaled each token's row, as bits
   volatile int* abort;   // a bounded wait ran out: no one waits any more
   uint32_t seq;        // tiles so far, over all shares
 };
@@ -408,7 +409,11 @@ struct Experts {
         ss += s_part[2 * (grp * split + k) + 1];
       }
       const float r = a.gamma ? rsqrtf(__fdividef(ss, static_cast<float>(a.H)) + a.eps) : 1.0f;
-      const float mult = FP4 ? pow2_field(scale_exponent(__float_as_uint(mx * r))) : 1.f;
+      // the products' scale is taken out again by this same value: another order of the sum of squares may
+      // give another last bit, and next to a power of two another exponent
+      const uint32_t top = __float_as_uint(mx * r);
+      if (part == 0 && lane == 0) cta.top[t] = top;
+      const float mult = FP4 ? pow2_field(scale_exponent(top)) : 1.f;
 #pragma unroll 2
       for (int k = (part * 32 + lane) * 8; k < kpad; k += split * 256) {
         float v[8] = {};
@@ -673,7 +678,9 @@ struct Experts {
         if (tok0 + j < size) {
           pair[j] = plan.list[first + tok0 + j];
           if (FP4)
-            am[j] = PHASE == 1 ? __float_as_uint(__ldcg(&a.stats[pair[j] / a.S].y)) : __ldcg(a.amax + pair[j]);
+            am[j] = PHASE == 2   ? __ldcg(a.amax + pair[j])
+                    : a.all_rows ? cta.top[pair[j] / a.S]
+                                 : __float_as_uint(__ldcg(&a.stats[pair[j] / a.S].y));
         }
     }
     wait();
@@ -893,6 +900,7 @@ __global__ void __launch_bounds__(32 * (MAIN + ML_FINISH), 1)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t s_bar[2 * ML_BUFS];
   __shared__ float s_part[2 * ML_MAX_WARPS];
+  __shared__ uint32_t s_top[ML_MAX_G];
   __shared__ uint32_t s_ticket;
   __shared__ int s_abort;
   const int tid = threadIdx.x;
@@ -913,6 +921,7 @@ __global__ void __launch_bounds__(32 * (MAIN + ML_FINISH), 1)
   cta.ring = smem_u32(red) + ML_BUFS * MAIN * RT * (NB == 4 ? 2 : 1) * 512;
   cta.full = smem_u32(s_bar);
   cta.empty = cta.full + 8 * ML_BUFS;
+  cta.top = s_top;
   cta.abort = &s_abort;
   cta.seq = 0;
   if (tid == 0) {
@@ -1112,7 +1121,7 @@ MoeLayerPlan plan_moe_layer(int T, int topk, int nsh, int E, int H, int I, int N
   // room for the tokens that share an expert when they spread evenly, and three standard deviations
   const float mean = static_cast<float>(T) * topk / E;
   const float room = mean + 3.0f * sqrtf(mean);
-  const int most = nsh > 0 ? 16 : room <= 4.0f ? 4 : room <= 8.0f ? 8 : 16;
+  const int most = nsh > 0 ? ML_MAX_G : room <= 4.0f ? 4 : room <= 8.0f ? 8 : ML_MAX_G;
   p.G = T < most ? T : most;
   for (;; --p.G) {
     const int nb = columns_of(p.G);

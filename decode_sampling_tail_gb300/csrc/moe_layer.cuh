@@ -39,6 +39,7 @@ constexpr int ML_FINISH = 4;  // warps that add the partial sums and finish the 
 constexpr int ML_MAX_WARPS = 16;
 constexpr int ML_BUFS = 4;    // tiles whose partial sums may wait for a finishing warp
 constexpr int ML_MAX_T = 64;
+constexpr int ML_MAX_G = 16;  // tokens of one expert that share a pass over its weights
 constexpr int ML_MAX_EXPERTS = 512;  // routed and shared together
 constexpr int ML_MAX_TOPK = 16;
 constexpr int ML_MAX_SHARED = 8;

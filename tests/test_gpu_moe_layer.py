@@ -385,3 +385,29 @@ def test_wrapper_refuses_what_does_not_fit():
     for kw in (dict(H=40), dict(H=16400), dict(E=600), dict(topk=17), dict(t_max=65), dict(n_shared=9)):
         with pytest.raises(dst.TailError):
             dst.Moe(**{**dict(H=64, I=64, E=32, topk=2, t_max=4), **kw})
+
+
+@pytest.mark.parametrize("T,shared", [(2, 0), (3, 0), (4, 0), (13, 1)])
+def test_layer_rows_whose_largest_value_is_a_power_of_two(T, shared):
+    # 4-bit rows are scaled by a power of two of their largest |t|; neighbouring fp32 gammas carry that value over one
+    for seed in range(4):
+        c = Case(T, 2880, 32, 4, 2, w="mxfp4", shared=shared, act=RELU2, seed=100 + seed)
+        c.gamma[:] = 1.0
+        x = c.x.double()
+        at = x.abs().argmax(-1)
+        while len(set(at.tolist())) < T:  # a column of its own for each token
+            c.x[torch.arange(T, device=DEV), at] = 0.0
+            x = c.x.double()
+            at = x.abs().argmax(-1)
+        rms = torch.sqrt((x * x).mean(-1) + 1e-5)
+        top = (16.0 * rms / x[torch.arange(T, device=DEV), at].abs()).float()
+        m = c.handle()
+        for step in range(-24, 25):
+            c.gamma[at] = (top.view(torch.int32) + step).view(torch.float32)
+            out = c.outputs()
+            c.run(m, out)
+            ids, _, gap, y, bound = c.want()
+            sure = gap > 1e-5
+            err = (out["out_slots"].double() - y).abs()
+            assert (err <= bound)[sure].all(), (seed, step, ((err / bound).amax((1, 2)) > 1).tolist())
+        m.close()
