@@ -1101,7 +1101,7 @@ cudaError_t launch_as(const MoeLayerArgs& a, const MoeLayerPlan& p, cudaStream_t
 
 template <int FMT>
 cudaError_t launch_columns(const MoeLayerArgs& a, const MoeLayerPlan& p, cudaStream_t s) {
-  switch (columns_of(a.G)) {
+  switch (p.columns) {
     case 1: return launch_as<FMT, 1>(a, p, s);
     case 2: return launch_as<FMT, 2>(a, p, s);
     default: return launch_as<FMT, 4>(a, p, s);
@@ -1122,18 +1122,21 @@ MoeLayerPlan plan_moe_layer(int T, int topk, int nsh, int E, int H, int I, int N
   const float mean = static_cast<float>(T) * topk / E;
   const float room = mean + 3.0f * sqrtf(mean);
   const int most = nsh > 0 ? ML_MAX_G : room <= 4.0f ? 4 : room <= 8.0f ? 8 : ML_MAX_G;
-  p.G = T < most ? T : most;
-  for (;; --p.G) {
-    const int nb = columns_of(p.G);
-    const int rt = groups_of(p.format, nb);
-    const int red = ML_BUFS * MAIN_WARPS * rt * (nb == 4 ? 2 : 1) * 512 + MAIN_WARPS * depth_of(nb) * slot_of(p.format, rt);
-    p.all_rows = T <= p.G;
-    p.R = p.G;
-    p.smem = fixed + 2 * p.R * pitch + red;
-    if (p.smem <= max_smem || p.G == 1) break;
-  }
-  p.ok = p.smem <= max_smem;
-  const int units = (T * topk < E ? T * topk : E) + nsh, rt = groups_of(p.format, columns_of(p.G));
+  auto fits = [&](int G, int columns) {
+    const int rt = groups_of(p.format, columns);
+    p.G = p.R = G;
+    p.columns = columns;
+    p.all_rows = T <= G;
+    p.smem = fixed + 2 * G * pitch + ML_BUFS * MAIN_WARPS * rt * (columns == 4 ? 2 : 1) * 512 +
+             MAIN_WARPS * depth_of(columns) * slot_of(p.format, rt);
+    return p.smem <= max_smem;
+  };
+  p.ok = false;
+  for (int G = T < most ? T : most; G >= 1 && !p.ok; --G) p.ok = fits(G, columns_of(G));
+  // the widest rows of an odd number of 4-bit blocks: the form with the least shared memory besides them (two steps
+  // of one 16-row group in flight, 80 KB, instead of four of two, 172 KB)
+  for (int G = T < most ? T : most; G >= 1 && !p.ok; --G) p.ok = fits(G, 4);
+  const int units = (T * topk < E ? T * topk : E) + nsh, rt = groups_of(p.format, p.columns);
   p.ksplit1 = ksplit_of(p.format, rt, H, N1, units, num_sms);
   p.ksplit2 = ksplit_of(p.format, rt, I, H, units, num_sms);
   return p;

@@ -12,6 +12,7 @@ struct MoeLayerPlan {
   bool ok;
   int format;   // Format of moe_layer.cu
   int G;        // tokens of one expert that share a pass over its weights
+  int columns;  // n-tiles of the kernel's form: 1, 2 or 4
   int R;        // activation rows in shared memory
   int all_rows; // every token's rows of the first product stay there
   int smem;     // dynamic shared memory of the expert kernels

@@ -411,3 +411,9 @@ def test_layer_rows_whose_largest_value_is_a_power_of_two(T, shared):
             err = (out["out_slots"].double() - y).abs()
             assert (err <= bound)[sure].all(), (seed, step, ((err / bound).amax((1, 2)) > 1).tolist())
         m.close()
+
+
+@pytest.mark.parametrize("T,H,I,E,topk,shared", [(1, 14368, 32, 2, 1, 0), (2, 16352, 32, 2, 1, 0), (9, 32, 16352, 3, 2, 0),
+                                                (64, 11296, 32, 16, 16, 0), (64, 16352, 32, 17, 16, 8)])
+def test_layer_widest_rows_of_an_odd_number_of_blocks(T, H, I, E, topk, shared):
+    run_check(Case(T, H, I, E, topk, w="mxfp4", shared=shared, act=RELU2, seed=40))
