@@ -228,17 +228,21 @@ __device__ __forceinline__ void route_token(const MoeLayerArgs& a, int t, uint16
 // One warp: token t's weights and ids to memory, its experts known.
 __device__ __forceinline__ void write_routes(const MoeLayerArgs& a, int t, const uint16_t* pair_e) {
   const int lane = threadIdx.x & 31;
-  float w = 0.f;
+  float v = 0.f, top = -INFINITY;
   int e = 0;
   if (lane < a.topk) {
     e = pair_e[t * a.S + lane];
-    const float v = __ldcg(a.logits + static_cast<int64_t>(t) * a.E + e);
-    w = a.score ? route_score(a, v) : v + (a.br ? __ldg(a.br + e) : 0.f);
+    v = __ldcg(a.logits + static_cast<int64_t>(t) * a.E + e);
+    if (!a.score && a.br) v += __ldg(a.br + e);
+    top = a.score ? fminf(v, 0.f) : v;
   }
-  if (!a.score) {  // the first is the largest
-    const float top = __shfl_sync(0xffffffffu, w, 0);
-    w = lane < a.topk ? expf(w - top) : 0.f;
-  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  // a share does not mind a common factor: exp(-top).  sigmoid(v) = exp(min(v, 0)) / (1 + exp(-|v|)), and scores
+  // that all lie below the smallest fp32 number keep their ratios
+  float w = 0.f;
+  if (lane < a.topk)
+    w = a.score ? __fdividef(expf(fminf(v, 0.f) - top), 1.0f + expf(-fabsf(v))) : expf(v - top);
   float sum = w;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);

@@ -417,3 +417,21 @@ def test_layer_rows_whose_largest_value_is_a_power_of_two(T, shared):
                                                 (64, 11296, 32, 16, 16, 0), (64, 16352, 32, 17, 16, 8)])
 def test_layer_widest_rows_of_an_odd_number_of_blocks(T, H, I, E, topk, shared):
     run_check(Case(T, H, I, E, topk, w="mxfp4", shared=shared, act=RELU2, seed=40))
+
+
+@pytest.mark.parametrize("bias", [False, True])
+def test_layer_sigmoid_weights_of_scores_that_underflow(bias):
+    # z of about -96: sigmoid(z) is no fp32 number, its share of the sum is.  z is off by at most 13 half-steps of
+    # 2^-18 (8 products a lane, 5 additions), so a share by twice that
+    c = Case(5, 64, 32, 12, 4, act=RELU2, score="sigmoid", seed=43, gamma=False, router_bias=bias)
+    c.x[:, 0], c.router_w[:, 0] = 16.0, -6.0
+    if bias:
+        c.router_bias = torch.linspace(0.1, 0.9, 12, device=DEV)
+    out = c.outputs()
+    with c.handle() as m:
+        c.run(m, out)
+    ids, w, gap, _, _ = c.want()
+    sure = gap > 1e-5
+    assert sure.sum() >= 4 and torch.equal(out["out_ids"][sure].long(), ids[sure])
+    assert ((out["out_slot_w"].double() - w).abs()[sure] <= 2 * 13 * 2.0 ** -18 * w[sure] + 2.0 ** -22).all()
+    assert torch.isfinite(out["out_hidden"]).all()
