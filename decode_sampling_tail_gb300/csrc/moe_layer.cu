@@ -585,65 +585,86 @@ struct Experts {
     } else {
       // A block's scale relative to ref goes into its values: a power of two from 2^-8 to 2^7, so that
       // fp16 holds them exactly.  Trained weights stay in one such window for whole tiles; where they
-      // leave it, ref moves, and blocks too far apart for any window are summed quad by quad.
-      constexpr int NS = 2 * RT * PIECES;
-      auto scale = [&](int i) { return f.s[i / (2 * PIECES)][i / PIECES % 2][i % PIECES]; };
-      const uint32_t low = static_cast<uint32_t>(t.ref - 8);
-      uint32_t out = 0u;
-#pragma unroll
-      for (int i = 0; i < NS; ++i) out |= scale(i) - low;
-      bool apart = false;
-      if (__any_sync(0xffffffffu, out > 15u)) {
-        uint32_t mx = 0u, mn = 255u;
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          mx = max(mx, scale(i));
-          mn = min(mn, scale(i));
-        }
-        mx = __reduce_max_sync(0xffffffffu, mx);
-        mn = __reduce_min_sync(0xffffffffu, mn);
+      // leave it, ref moves, and blocks too far apart for any window take a pass for each window they fill.
+      // (A block far below another may still be the whole sum: the other's activations may be zero.)
+      if (__any_sync(0xffffffffu, outside(f, static_cast<uint32_t>(t.ref - 8)))) {
         flush(t);
-        apart = mx > mn + 15u || mn > 239u;  // (255 is NaN)
-        if (!apart) t.ref = static_cast<int>(mn) + 8;
-      }
-      uint32_t sc[RT][2][PIECES];
-      if (!apart) {  // 2^(scale - ref), twice
-        const uint32_t one = (15u - static_cast<uint32_t>(t.ref)) * 0x04000400u;
-#pragma unroll
-        for (int i = 0; i < NS; ++i) sc[i / (2 * PIECES)][i / PIECES % 2][i % PIECES] = scale(i) * 0x04000400u + one;
-      } else {
-#pragma unroll
-        for (int r = 0; r < 2 * RT; ++r) {
-          const int top = row_max(f.s[r >> 1][r & 1]);
-#pragma unroll
-          for (int j = 0; j < PIECES; ++j)
-            sc[r >> 1][r & 1][j] = half_pow2(static_cast<int>(f.s[r >> 1][r & 1][j]), top);
+        uint32_t todo = live(f);
+        t.ref = window(f, todo) + 8;
+        if (__any_sync(0xffffffffu, outside(f, static_cast<uint32_t>(t.ref - 8)))) {
+          products_apart<N>(f, todo, at, bp, t);
+          return;
         }
       }
+      uint32_t sc[RT][2][PIECES];  // 2^(scale - ref), twice
+      const uint32_t one = (15u - static_cast<uint32_t>(t.ref)) * 0x04000400u;
+#pragma unroll
+      for (int i = 0; i < 2 * RT * PIECES; ++i)
+        sc[i / (2 * PIECES)][i / PIECES % 2][i % PIECES] = scale_of(f, i) * 0x04000400u + one;
       products_fp4<N>(f, sc, at, bp, t.d);
-      if (apart) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const float f0 = e8m0(row_max(f.s[rt][0])), f1 = e8m0(row_max(f.s[rt][1]));
-#pragma unroll
-          for (int n = 0; n < NACC; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              t.acc[rt][n][j] = fmaf(t.d[rt][n][0][j] + t.d[rt][n][1][j], j < 2 ? f0 : f1, t.acc[rt][n][j]);
-              t.d[rt][n][0][j] = t.d[rt][n][1][j] = 0.f;
-            }
-        }
-      }
     }
   }
 
-  // the largest scale of a row's blocks in the k-step
-  static __device__ __forceinline__ int row_max(const uint32_t (&s)[PIECES]) {
-    int m = static_cast<int>(s[0]);
+  // Blocks too far apart for one window, of which `todo` hold anything: the largest window's, then the rest.
+  template <int N>
+  __device__ __forceinline__ void products_apart(const Frag<FMT, RT>& f, uint32_t todo, uint32_t at,
+                                                 const uint32_t (&bp)[NB], Sums& t) const {
+#pragma unroll 1
+    for (;;) {
+      uint32_t sc[RT][2][PIECES];
+      const uint32_t one = (15u - static_cast<uint32_t>(t.ref)) * 0x04000400u;
 #pragma unroll
-    for (int j = 1; j < PIECES; ++j) m = max(m, static_cast<int>(s[j]));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      for (int i = 0; i < 2 * RT * PIECES; ++i) {
+        const uint32_t s = scale_of(f, i);
+        const bool in = (todo >> i & 1u) && (s == 255u || s - static_cast<uint32_t>(t.ref - 8) <= 15u);
+        sc[i / (2 * PIECES)][i / PIECES % 2][i % PIECES] = !in ? 0u : s == 255u ? 0x7e007e00u : s * 0x04000400u + one;
+        if (in) todo &= ~(1u << i);
+      }
+      products_fp4<N>(f, sc, at, bp, t.d);
+      flush(t);
+      if (!__any_sync(0xffffffffu, todo != 0u)) break;
+      t.ref = window(f, todo) + 8;  // takes the largest block left at least
+    }
+  }
+
+  // block i of a lane's 2 * RT * PIECES
+  static __device__ __forceinline__ uint32_t scale_of(const Frag<FMT, RT>& f, int i) {
+    return f.s[i / (2 * PIECES)][i / PIECES % 2][i % PIECES];
+  }
+
+  // whether a scale of this lane lies outside [low, low + 15]
+  static __device__ __forceinline__ bool outside(const Frag<FMT, RT>& f, uint32_t low) {
+    uint32_t out = 0u;
+#pragma unroll
+    for (int i = 0; i < 2 * RT * PIECES; ++i) out |= scale_of(f, i) - low;
+    return out > 15u;
+  }
+
+  // the blocks of this lane that hold a value other than 0 or a scale of NaN, a bit each
+  static __device__ __forceinline__ uint32_t live(const Frag<FMT, RT>& f) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 2 * RT * PIECES; ++i) {
+      const uint32_t(&w)[4] = f.w[i / (2 * PIECES)][i / PIECES % 2][i % PIECES];
+      if (((w[0] | w[1] | w[2] | w[3]) & 0x77777777u) != 0u || scale_of(f, i) == 255u) m |= 1u << i;
+    }
+    return m;
+  }
+
+  // the lowest scale of the window for the warp's blocks `todo`: all of them, or the largest
+  static __device__ __forceinline__ int window(const Frag<FMT, RT>& f, uint32_t todo) {
+    uint32_t mx = 0u, mn = 255u;
+#pragma unroll
+    for (int i = 0; i < 2 * RT * PIECES; ++i) {
+      const uint32_t s = scale_of(f, i);
+      if ((todo >> i & 1u) && s != 255u) {
+        mx = max(mx, s);
+        mn = min(mn, s);
+      }
+    }
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    mn = __reduce_min_sync(0xffffffffu, mn);
+    return static_cast<int>(mn > mx ? 119u : mx - mn > 15u ? mx - 15u : min(mn, 239u));
   }
 
   __device__ __forceinline__ float glu(float gate, float up) const {

@@ -144,13 +144,6 @@ __device__ __forceinline__ void fp4_to_half(uint32_t w, uint32_t scale, uint32_t
   }
 }
 
-// 2^(s - ref) as an fp16 pair for s <= ref; 0 below the smallest subnormal.
-__device__ __forceinline__ uint32_t half_pow2(int s, int ref) {
-  const int d = s - ref;
-  const uint32_t b = d >= -14 ? static_cast<uint32_t>(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
-  return b | (b << 16);
-}
-
 // 2^(s - 127) of an e8m0 scale; 255 is NaN.
 __device__ __forceinline__ float e8m0(int s) {
   return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7fc00000u : static_cast<uint32_t>(s) << 23);

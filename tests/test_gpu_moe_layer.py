@@ -435,3 +435,23 @@ def test_layer_sigmoid_weights_of_scores_that_underflow(bias):
     assert sure.sum() >= 4 and torch.equal(out["out_ids"][sure].long(), ids[sure])
     assert ((out["out_slot_w"].double() - w).abs()[sure] <= 2 * 13 * 2.0 ** -18 * w[sure] + 2.0 ** -22).all()
     assert torch.isfinite(out["out_hidden"]).all()
+
+
+@pytest.mark.parametrize("H", [512, 160])
+@pytest.mark.parametrize("apart", [16, 23, 24, 26, 40, 100])
+def test_layer_large_blocks_that_meet_zeros_hide_no_small_ones(H, apart):
+    # every other block of W1 is 2^apart times its neighbours and meets activations of zero: the small ones are the sum
+    c = Case(3, H, 64, 2, 1, w="mxfp4", seed=41, gamma=False, bias=False, act=SILU, router_bias=False)
+    c.s1[:, ::2, ::2] -= apart
+    c.s1[:, 1::2, 1::2] -= apart  # the up rows hold their small blocks elsewhere
+    c.x.view(3, -1, 32)[0, 1::2] = 0.0
+    c.x.view(3, -1, 32)[1, ::2] = 0.0
+    run_check(c)
+    # blocks of 4 sizes in one step of a row, the largest all zeros, and a block that holds no value
+    c = Case(3, H, 64, 2, 1, w="mxfp4", seed=42, gamma=False, bias=False, act=RELU2, router_bias=False)
+    for i in range(4):
+        c.s1[:, :, i::4] -= (i * apart) // 3
+    c.x.view(3, -1, 32)[:, 0::4] = 0.0
+    c.w1.view(2, 64, -1, 16)[:, :, 1::4] = 0
+    c.s1[:, ::3, 1::4] = 0
+    run_check(c)
