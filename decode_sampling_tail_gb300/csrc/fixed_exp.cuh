@@ -197,6 +197,19 @@ __device__ __forceinline__ float exp_fast(float l, float m, float scale) {
   return l == m ? 1.0f : fmaxf(e, 0.0f);
 }
 
+// exp((l - m) / T) in fp32 with a relative error of a few 2^-24 whatever the exponent's size: the exponent in a
+// pair, exp2f of its first part and the second part's term of first order.
+__device__ __forceinline__ float exp_single(float l, float m, ExpScale c) {
+  if (l == m) return 1.0f;
+  const float d = l - m, dl = d - l;
+  const float err = (l - (d - dl)) + (-m - dl);
+  const float yh = d * c.h;
+  if (!(yh >= -150.0f)) return 0.0f;  // below fp32's smallest number, or NaN
+  const float yl = fmaf(d, c.h, -yh) + fmaf(d, c.l, err * c.h);
+  const float e = exp2f(yh);
+  return fmaf(e * 0x1.62e430p-1f, yl, e);  // ln 2
+}
+
 // 2^e as fp64, e a normal exponent.
 __device__ __forceinline__ double pow2_double(int e) {
   return __longlong_as_double(static_cast<long long>(1023 + e) << 52);

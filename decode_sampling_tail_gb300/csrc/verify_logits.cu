@@ -5,7 +5,9 @@
 // Three kernels, over chunks of 8192 columns, which a CTA holds in registers, or parts of them:
 //   verify_stats (chunk, row): the chunk's maximum m_c, its lowest column and sum exp((l - m_c) / T)
 //     in fp32.  Every row has to be read, since which one is settled is not known yet; this pass is
-//     bound by memory and only has to decide acceptances (a relative 2^-21 of Z).
+//     bound by memory and only has to decide acceptances.  Z is off by at most a relative 2^-17: 2^-23 for
+//     every binary order that a term lies below the maximum, in the terms' mean (their share times their orders sums
+//     to log2 V at most: 2^-18.6), and up to 46 additions of 2^-24; 2^-21 is usual.
 //   verify_settle (part, sequence): each CTA judges the sequence's rows from those statistics (all
 //     of them compute the same bits, none waits) and finds the settled row; then the sums of that row's
 //     segments (1024 columns) as integers (fixed_exp.cuh, units of 2^-49 relative to m_c).
@@ -231,7 +233,8 @@ __global__ void __launch_bounds__(VERIFY_THREADS) verify_stats_kernel(const Logi
   }
 }
 
-// One warp: whether the row's draft is accepted, and what its token is if it is settled here.
+// One warp: whether the row's draft is accepted, and what its token is if it is settled here.  The draft's own
+// weight is formed by exp_single: exp_fast would be off by 2^-23 for every binary order it lies below the maximum.
 template <typename T>
 __device__ __forceinline__ bool judge_row(const LogitsArgs& a, int row, bool bonus, Settled& s) {
   const int lane = threadIdx.x & 31;
@@ -280,7 +283,7 @@ __device__ __forceinline__ bool judge_row(const LogitsArgs& a, int row, bool bon
     for (int i = 0; i < PER; ++i) z = fmaf(cz[i], exp_fast(cm[i], m, sc.h), z);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    if (known) ex = exp_fast(lx, m, sc.h);
+    if (known) ex = exp_single(lx, m, sc);
     if (!(z > 0.f)) s.token = -1;
   }
   const bool ok = !bonus && u_a * qx * z < ex;

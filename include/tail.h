@@ -399,8 +399,12 @@ int tail_merge_shards(int32_t nshard, int32_t k_in, int32_t k, int32_t gbs, cons
  * and its token is -1 (counted).  A candidate at -inf has probability 0; among logits
  * of +inf the mass is shared.  NaN is outside the domain.  Draws are made with weights
  * of 2^-36 relative error and exact sums, so they agree with 64-bit arithmetic except
- * where u lies within about 2^-36 of a boundary (acceptances: u_accept q within 2^-36 of
- * P, tail_verify_logits 2^-20); they do not depend on the batch.  No handle and no
+ * where u lies within about 2^-36 of a boundary; they do not depend on the batch.  The
+ * weights are multiples of 2^-52 of the row's largest (tail_verify) or of 2^-44
+ * (tail_verify_logits; 2^-43 and 2^-42 beyond 2^18 and 2^19 columns): less is not drawn.  Acceptances
+ * agree with 64-bit arithmetic except where u_accept q lies within 2^-36 of P (tail_verify;
+ * P in the units above) or within a relative 2^-17 of it (tail_verify_logits, whose sum over
+ * the vocabulary is fp32; 2^-21 is usual).  No handle and no
  * allocation; the current device and `stream`.
  */
 

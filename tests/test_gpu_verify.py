@@ -474,3 +474,26 @@ def test_logits_peaked_rows_at_low_temperatures(l, q):
     assert vc.compare(tokens, counts, _logits_want(c), c["cu"]) >= 30
     lo, hi = c["cu"][:-1], c["cu"][1:]
     assert all(tokens[a + n - 1] >= 0 for a, b, n in zip(lo, hi, counts) if b > a)
+
+
+@pytest.mark.parametrize("accept,most", [(0.5, 57.0), (0.0, 140.0)])
+def test_logits_unlikely_drafts_are_judged_by_their_own_probability(accept, most):
+    # P(x) = 2^-y / (1 + ..), u q above or below it by 2^-19.5 or zero: the largest column holds all but 2^-25 of the
+    # row, so that the fp32 sum over the columns is off by less than 2^-22 and the draft's weight decides
+    rng = np.random.default_rng(60)
+    nseq, V = 400, 64
+    R = 2 * nseq
+    temp = rng.uniform(0.3, 1.5, R).astype(np.float32)
+    z = np.full((R, V), -np.inf, np.float32)
+    z[:, 3] = rng.uniform(-30.0, 30.0, R)
+    y = rng.uniform(26.0, most, R)
+    z[:, 40] = (z[:, 3] - y * temp * np.log(2.0)).astype(np.float32)
+    e = np.exp((z[:, 40].astype(np.float64) - z[:, 3]) / temp)
+    p = e / (1.0 + e)
+    q = np.zeros((R, V), np.float32)
+    q[:, 40] = 2.0 * p * (1.0 + np.where(np.arange(R) % 4 < 2, 1.0, -1.0) * 2.0 ** -19.5)
+    c = dict(cu=np.arange(0, R + 1, 2, dtype=np.int32), R=R, V=V, logits=_dev(z), temp=temp,
+             drafts=np.full(R, 40, np.int32), accept=np.full(R, accept, np.float32), u=rng.random(R, dtype=np.float32),
+             q=_dev(q))
+    tokens, counts = _logits_run(c)
+    assert vc.compare(tokens, counts, _logits_want(c), c["cu"]) == nseq
