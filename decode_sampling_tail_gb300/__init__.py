@@ -37,7 +37,8 @@ EXPORTS = ("tail_create", "tail_run", "tail_run_ex", "tail_run_host", "tail_chec
            "tail_set_wait_limit", "tail_debug_drop_stage", "tail_last_error", "tail_run_noalloc",
            "tail_merge_shards", "tail_run_moe", "tail_tap_shape", "tail_run_taps", "tail_prepare_weight",
            "tail_verify", "tail_verify_logits", "tail_verify_logits_workspace",
-           "tail_moe_create", "tail_moe_run", "tail_moe_check", "tail_moe_get_info", "tail_moe_destroy")
+           "tail_moe_create", "tail_moe_run", "tail_moe_check", "tail_moe_set_wait_limit", "tail_moe_get_info",
+           "tail_moe_destroy")
 KERNELS = ("rms_rows", "lm_head", "merge")
 
 
@@ -127,6 +128,8 @@ def lib(path: str | None = None):
         L.tail_moe_run.restype = ctypes.c_int
         L.tail_moe_check.argtypes = [P]
         L.tail_moe_check.restype = ctypes.c_int
+        L.tail_moe_set_wait_limit.argtypes = [P, ctypes.c_uint64]
+        L.tail_moe_set_wait_limit.restype = ctypes.c_int
         L.tail_moe_get_info.argtypes = [P, ctypes.POINTER(i64)]
         L.tail_moe_get_info.restype = ctypes.c_int
         L.tail_moe_destroy.argtypes = [P]

@@ -31,6 +31,7 @@ struct tail_moe_s {
   float* slot_w;
   MoeControl* ctl;  // zero between launches
   int* err;
+  uint64_t wait_limit_ns;
 };
 
 namespace {
@@ -109,6 +110,7 @@ int tail_moe_create(const tail_moe_config* cfg, int device, tail_moe_t** out) {
   m->slot_w = reinterpret_cast<float*>(p += round256(sizes[4]));
   m->ctl = reinterpret_cast<MoeControl*>(p += round256(sizes[5]));
   m->err = reinterpret_cast<int*>(p += round256(sizes[6]));
+  m->wait_limit_ns = DEFAULT_TIMEOUT_NS;
   *out = m;
   return TAIL_OK;
 }
@@ -180,7 +182,7 @@ int tail_moe_run(tail_moe_t* m, const uint16_t* x, const float* gamma_opt, const
   a.h_out = out_hidden_opt;
   a.ctl = m->ctl;
   a.err = m->err;
-  a.timeout_ns = DEFAULT_TIMEOUT_NS;
+  a.timeout_ns = m->wait_limit_ns;
   const cudaError_t e = launch_moe_layer(a, plan, s);
   if (e != cudaSuccess) return cuda_fail(e, "tail_moe_run: kernel launch");
   return TAIL_OK;
@@ -196,6 +198,12 @@ int tail_moe_check(tail_moe_t* m) {
   if (e == cudaSuccess && code != 0) e = cudaMemset(m->err, 0, sizeof(int));
   if (e != cudaSuccess) return cuda_fail(e, "tail_moe_check");
   return code != 0 ? TAIL_ERR_DEVICE : TAIL_OK;
+}
+
+int tail_moe_set_wait_limit(tail_moe_t* m, uint64_t ns) {
+  if (!m) return TAIL_ERR_INVALID_ARG;
+  m->wait_limit_ns = ns;
+  return TAIL_OK;
 }
 
 int tail_moe_get_info(const tail_moe_t* m, int64_t* scratch_bytes) {

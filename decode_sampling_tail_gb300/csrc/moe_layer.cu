@@ -969,6 +969,10 @@ __global__ void __launch_bounds__(32 * (MAIN + ML_FINISH), 1)
     __syncthreads();
     if (tid == THREADS - 1) s_ticket = atomicAdd(&a.ctl->ticket, 1u);
   };
+  // The tiles of a product; none without a plan.  Not by the word that a wait has run out: a warp that is ahead may
+  // set it while another reads it, and all have to walk the same tiles between barriers.  After it has been set no
+  // wait lasts, and what is left to do is done on whatever stands in the scratch.
+  auto tiles_of = [&](const Phase& ph) { return static_cast<uint32_t>(max(cta.plan.nunits, 0) * ph.tiles); };
   auto end_share = [&](int stage) {  // counts this one as done, and goes to the next
     __syncthreads();
     if (tid == THREADS - 32 && stage < 3) {
@@ -1002,14 +1006,14 @@ __global__ void __launch_bounds__(32 * (MAIN + ML_FINISH), 1)
 #pragma unroll 1
   while (ticket < 2 * n) {
     begin_share();
-    const uint32_t i = ticket - n, tiles = s_abort ? 0u : cta.plan.nunits * ph1.tiles;
+    const uint32_t i = ticket - n, tiles = tiles_of(ph1);
     Experts<FMT, RT, NB, 1, DEPTH, MAIN>(a, ph1, cta, ksplit1).share(cut(tiles, i), cut(tiles, i + 1), nullptr, 0u);
     end_share(1);
   }
 #pragma unroll 1
   while (ticket < 3 * n) {
     begin_share();
-    const uint32_t i = ticket - 2 * n, tiles = s_abort ? 0u : cta.plan.nunits * ph2.tiles;
+    const uint32_t i = ticket - 2 * n, tiles = tiles_of(ph2);
     Experts<FMT, RT, NB, 2, DEPTH, MAIN>(a, ph2, cta, ksplit2).share(cut(tiles, i), cut(tiles, i + 1), a.ctl->done + 1, n);
     end_share(2);
   }

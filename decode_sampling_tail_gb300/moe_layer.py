@@ -99,3 +99,9 @@ class Moe:
         rc = lib().tail_moe_check(self.h)
         if rc != TAIL_OK:
             raise TailError(rc, "tail_moe_check")
+
+    def set_wait_limit(self, ns: int):
+        """Bounds every device wait of later runs to ``ns`` nanoseconds (tail_moe_set_wait_limit; 1e9 at first)."""
+        rc = lib().tail_moe_set_wait_limit(self.h, ns)
+        if rc != TAIL_OK:
+            raise TailError(rc, "tail_moe_set_wait_limit")

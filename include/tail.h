@@ -518,6 +518,9 @@ int tail_moe_run(tail_moe_t* m, const uint16_t* x, const float* gamma_opt, const
 /* Synchronises the device and reads the handle's error word: TAIL_ERR_DEVICE (and clears it) when a
    bounded device wait of a run ran out (its outputs are then undefined), else TAIL_OK. */
 int tail_moe_check(tail_moe_t* m);
+/* Bounds every device wait of later runs to `ns` nanoseconds of GPU global time (default 1e9), as tail_set_wait_limit
+   does; a run whose wait ran out ends all the same and leaves the handle ready for the next. */
+int tail_moe_set_wait_limit(tail_moe_t* m, uint64_t ns);
 int tail_moe_get_info(const tail_moe_t* m, int64_t* scratch_bytes);
 void tail_moe_destroy(tail_moe_t* m);
 

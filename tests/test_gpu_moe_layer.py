@@ -455,3 +455,28 @@ def test_layer_large_blocks_that_meet_zeros_hide_no_small_ones(H, apart):
     c.w1.view(2, 64, -1, 16)[:, :, 1::4] = 0
     c.s1[:, ::3, 1::4] = 0
     run_check(c)
+
+
+@pytest.mark.parametrize("w", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("T", [1, 3, 40])
+def test_layer_waits_that_run_out_are_reported_and_recoverable(T, w):
+    # at a limit of 1 ns every wait that is not over at its first look runs out: each run reports it, ends, and leaves
+    # the handle as it was
+    c = Case(T, 512, 416, 12, 4, w=w, shared=1, seed=44)
+    want = run_check(c)
+    out = c.outputs()
+    with c.handle() as m:
+        c.run(m, out)
+        m.check()
+        for _ in range(3):
+            m.set_wait_limit(1)
+            c.run(m, out)
+            c.run(m, out)
+            with pytest.raises(dst.TailError) as e:
+                m.check()
+            assert e.value.args and dst.lib().tail_moe_check(m.h) == dst.TAIL_OK  # the word was cleared
+            m.set_wait_limit(1_000_000_000)
+            out = c.outputs()
+            c.run(m, out)
+            m.check()
+            assert all(torch.equal(out[k], want[k]) for k in out)

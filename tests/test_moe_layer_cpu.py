@@ -67,3 +67,7 @@ def test_struct_and_constants_mirror_the_header():
                         ("TAIL_MOE_SOFTMAX", moe_layer.SCORES["softmax"]),
                         ("TAIL_MOE_SIGMOID", moe_layer.SCORES["sigmoid"]), ("TAIL_MXFP4", dst.TAIL_MXFP4)):
         assert f"{name} = {value}" in text
+
+
+def test_wait_limit_needs_a_handle(L):
+    assert L.tail_moe_set_wait_limit(None, 1) == dst.TAIL_ERR_INVALID_ARG
