@@ -53,6 +53,12 @@ bool supported(const tail_moe_config* c) {
          c->n_shared <= ML_MAX_SHARED && c->E <= ML_MAX_EXPERTS - c->n_shared && c->t_max <= ML_MAX_T;
 }
 
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+bool meet(const Span& a, const Span& b) { return a.p && b.p && overlap(a.p, a.bytes, b.p, b.bytes); }
+
 int64_t round256(int64_t v) { return (v + 255) & ~int64_t(255); }
 
 }  // namespace
@@ -132,10 +138,23 @@ int tail_moe_run(tail_moe_t* m, const uint16_t* x, const float* gamma_opt, const
   if (!aligned(router_bias_opt, 4) || !aligned(b1_opt, 4) || !aligned(b2_opt, 4) || !aligned(out_hidden_opt, 16) ||
       !aligned(out_slots_opt, 16) || !aligned(out_slot_w_opt, 4) || !aligned(out_ids_opt, 4))
     return TAIL_ERR_INVALID_ARG;
-  // x is read again when the slots are combined: h in place of x is an element-wise replacement and
-  // allowed, any other overlap is not
-  const int64_t xb = static_cast<int64_t>(n_tokens) * c.H * 2;
-  if (out_hidden_opt && out_hidden_opt != x && overlap(out_hidden_opt, xb, x, xb)) return TAIL_ERR_INVALID_ARG;
+  // CTAs read inputs while others write outputs, so none may meet another; but x is read again where the slots are
+  // combined, and h in place of x is an element-wise replacement
+  const int64_t T = n_tokens, H = c.H, n1 = m->n_all * static_cast<int64_t>(m->N1), n2 = m->n_all * H;
+  const Span in[] = {{x, T * H * 2},          {gamma_opt, H * 4},  {router_w, c.E * H * 2}, {router_bias_opt, c.E * 4LL},
+                     {w1, fp4 ? n1 * H / 2 : n1 * H * 2},          {w1_scale, fp4 ? n1 * H / 32 : 0},
+                     {b1_opt, n1 * 4},        {w2, fp4 ? n2 * c.I / 2 : n2 * c.I * 2},
+                     {w2_scale, fp4 ? n2 * c.I / 32 : 0},          {b2_opt, n2 * 4}};
+  const Span out[] = {{out_hidden_opt, T * H * 2},
+                      {out_slots_opt, T * m->S * H * 4},
+                      {out_slot_w_opt, T * m->S * 4},
+                      {out_ids_opt, T * m->S * 4}};
+  for (const Span& o : out) {
+    for (const Span& i : in)
+      if (meet(o, i) && !(o.p == out_hidden_opt && i.p == x && o.p == i.p)) return TAIL_ERR_INVALID_ARG;
+    for (const Span* other = out; other < &o; ++other)
+      if (meet(o, *other)) return TAIL_ERR_INVALID_ARG;
+  }
   DeviceGuard guard(m->device);
   if (!guard.ok) return TAIL_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -505,7 +505,8 @@ int tail_moe_create(const tail_moe_config* cfg, int device, tail_moe_t** out);
  *   out_slots_opt  [n_tokens][S][H] fp32 y, 16-byte aligned, or NULL: with out_slot_w_opt the
  *                  `slots` and `slot_w` of tail_run_moe (n_routed = topk).  One of the two is needed.
  *   out_slot_w_opt [n_tokens][S] fp32, out_ids_opt [n_tokens][S] int32, or NULL.
- * Inputs must not alias outputs otherwise, and everything is read in stream order.  One run per handle at a time (its scratch is shared),
+ * Outputs must not overlap an input otherwise, nor one another (TAIL_ERR_INVALID_ARG), and everything is
+ * read in stream order.  One run per handle at a time (its scratch is shared),
  * also between captured graphs.  Results are deterministic, and a token's do not depend on the
  * others except through how many tokens share an expert (fp32 summation order).  Non-finite
  * activations give non-finite outputs in their own token's row only.

@@ -480,3 +480,41 @@ def test_layer_waits_that_run_out_are_reported_and_recoverable(T, w):
             c.run(m, out)
             m.check()
             assert all(torch.equal(out[k], want[k]) for k in out)
+
+
+def test_layer_refuses_outputs_over_inputs_and_each_other():
+    c = Case(3, 64, 32, 4, 2, w="mxfp4", shared=1, seed=45)
+    o = c.outputs()
+    arena = torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)
+
+    def at(byte, like):
+        return arena[byte:byte + like.numel() * like.element_size()].view(like.dtype).view(like.shape)
+
+    def moved(**kw):  # a case with one input in the arena, at byte 4096
+        d = Case(3, 64, 32, 4, 2, w="mxfp4", shared=1, seed=45)
+        for k in kw:
+            setattr(d, k, at(4096, getattr(d, k)).copy_(getattr(d, k)))
+        return d
+
+    with c.handle() as m:
+        for name, like in o.items():
+            size, step = like.numel() * like.element_size(), 16
+            for k in ("x", "gamma", "router_w", "router_bias", "w1", "s1", "b1", "w2", "s2", "b2"):
+                d = moved(**{k: 1})
+                n = getattr(d, k).numel() * getattr(d, k).element_size()
+                for byte in (4096 - size // step * step + step, 4096 + (n - 1) // step * step):
+                    if not 4096 - size < byte < 4096 + n:
+                        continue
+                    with pytest.raises(dst.TailError) as e:
+                        d.run(m, {**o, name: at(byte, like)})
+                    assert e.value.status == dst.TAIL_ERR_INVALID_ARG
+            for other in o:
+                if other != name:
+                    with pytest.raises(dst.TailError):
+                        c.run(m, {**o, name: at(8192, like), other: at(8192, o[other])})
+        d = moved(x=1)  # side by side, and h in place of x, are allowed
+        x = d.x.clone()
+        out = {k: at(16384 + 8192 * i, v) for i, (k, v) in enumerate(o.items()) if k != "out_hidden"}
+        d.run(m, {**out, "out_hidden": d.x})
+        torch.cuda.synchronize()
+        check(c, {**{k: v.clone() for k, v in out.items()}, "out_hidden": d.x}, x=x)
