@@ -19,7 +19,7 @@ def need_opt(t, what, dtype, shape, index):
 
 
 def need_matrix(t, what, rows, index):
-    """[rows, n] of a float type with unit stride along the columns: (pointer, type code, n, leading dimension)."""
+    """[rows, n >= 1] of a float type with unit stride along the columns: (pointer, type code, n, leading dimension)."""
     import torch
     code = {torch.float32: TAIL_F32, torch.float16: TAIL_F16, torch.bfloat16: TAIL_BF16}.get(t.dtype)
     if code is None:
@@ -28,6 +28,8 @@ def need_matrix(t, what, rows, index):
         raise ValueError(f"{what} must be [{rows}, n] on cuda:{index} with contiguous rows; got {tuple(t.shape)}, "
                          f"strides {t.stride()}, {t.device}")
     n = t.shape[1]
+    if n < 1:
+        raise ValueError(f"{what} must have at least one column")  # (no columns have no pointer: None to the library)
     ld = t.stride(0) if rows > 1 else n
     if ld < n:
         raise ValueError(f"{what}: rows overlap (strides {t.stride()})")

@@ -102,6 +102,15 @@ def test_wrappers_want_cuda_tensors():
         dst.verify_logits(torch.zeros(3, 10), f, i[:2], i, f, f)
 
 
+def test_probabilities_without_columns_are_refused():
+    # their pointer is null, which would stand for certain drafts
+    torch = pytest.importorskip("torch")
+    from decode_sampling_tail_gb300 import _args
+    assert _args.need_matrix(torch.zeros(3, 5), "q", 3, -1)[2:] == (5, 5)
+    with pytest.raises(ValueError):
+        _args.need_matrix(torch.zeros(3, 0), "q", 3, -1)
+
+
 # ------------------------------------------------------------------ the rule by hand
 
 def _one(target, draft, drafts, accept, u):
