@@ -14,9 +14,9 @@
 // Waits are bounded; one that runs out raises the error word, and the CTA leaves.
 //
 // Bound: bf16 by HBM, 4-bit weights by instructions.  Measured (copy rate 6.69 TB/s): bf16, 64 tokens over 128
-// experts of 2880 x 5760 and 2880 x 2880, 5.54 GB: 849-876 us, 6.3-6.5 TB/s (0.94-0.98); 8 tokens over 64 experts
-// and 2 shared, 737 MB: 122-126 us, 0.87-0.90; 5 tokens over 32 experts 0.88-0.92.  4 bits, 16 tokens over 128
-// experts, 677 MB: 200-204 us, 0.50: a 2 KB k-step of a warp takes about 350 instructions (196 of them conversions,
+// experts of 2880 x 5760 and 2880 x 2880, 5.54 GB: 849-887 us, 6.2-6.5 TB/s (0.93-0.98); 8 tokens over 64 experts
+// and 2 shared, 737 MB: 121-126 us, 0.87-0.91; 5 tokens over 32 experts 0.88-0.92.  4 bits, 16 tokens over 128
+// experts, 677 MB: 202-206 us, 0.50: a 2 KB k-step of a warp takes about 350 instructions (196 of them conversions,
 // scalings and products), a scheduler's three main warps issue on 47 % of the cycles, and neither a deeper ring
 // (3, 4, 5 or 6 steps: 204.8, 204.2, 205.4, 206.2 us) nor k-steps of 32 rows (211) move it.  One token, 54 MB:
 // 35.4 us, a chain of stage latencies and of fetching code that runs once.
@@ -289,7 +289,8 @@ struct Experts {
   }
 
   // Eight activations v times mult into shared memory, split into a high and a low 16-bit part so that
-  // the products carry them to about 2^-17 (bf16) or 2^-22 (fp16, scaled by a power of two a token).
+  // the products carry them to about 2^-17 (bf16) or 2^-22 (fp16, scaled by a power of two a token; fp16's
+  // smallest step is 2^-37 of the row's largest there).
   // What the four lanes of a row read together lies side by side.
   __device__ __forceinline__ void put8(int row, int k, const float (&v)[8], float mult) const {
     uint32_t hi[4], lo[4];

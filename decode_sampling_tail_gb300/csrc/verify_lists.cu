@@ -17,9 +17,10 @@
 // One CTA a sequence, one warp a row; every warp settles its row whole, drawing
 // before it knows whether earlier drafts held: what bounds the kernel is one
 // row's chain of loads, exponentials, scans and gathers, and rows in parallel
-// cost no more than one.  Measured: one sequence of 4 rows, k = 256: 10.7 us back to
-// back; 64 sequences of 6 rows 13.5 us; 200 of 1 to 10 rows, k = 1000: 24.7 us (a
-// chain four times as long: a lane owns 32 candidates instead of 8; 9 MB of lists,
+// cost no more than one.  Measured by graph replay: one sequence of 4 rows, k = 256:
+// 6.2 us; 64 sequences of 6 rows 8.4 us (called from Python one by one, 10.7 and
+// 12.3 to 15.7: the host's part); 200 of 1 to 10 rows, k = 1000: 24.4 us either way
+// (a chain four times as long: a lane owns 32 candidates instead of 8; 9 MB of lists,
 // DRAM 7 MB, issue slots 7 % busy).
 #include "../../include/tail.h"
 #include "abi_common.h"

@@ -22,7 +22,8 @@
 // Measured at V = 201088: 96 sequences (384 fp32 rows, and fp32 draft rows where one is refused) 164-167 us back to back, of
 // them stats 53-59 us (309 MB: 5.3-5.8 TB/s, 0.8-0.87 of the copy rate), settle 46 and draw 65: both form
 // 19 million exponentials to 2^-36, 55 to 75 instructions each, on 66 % of the issue slots; 16 sequences 42 us;
-// one sequence of 5 rows 17-18 us, the latency of three launches.
+// one sequence of 5 rows 10.7 us by graph replay, the latency of three launches (17-20 called from Python one by
+// one: the host's part).
 #include "../../include/tail.h"
 #include "abi_common.h"
 #include "verify.cuh"

@@ -461,7 +461,8 @@ int tail_verify_logits(int32_t rows, int32_t nseq, int32_t V, const void* logits
  * A selected expert's weights are read once for its tokens up to a number between 4 and 16 (as
  * many as an even spread of the call's tokens would bring it, with room; beyond 4 to 8 as shared
  * memory allows: 10 at widths of 2880, 1 at 16384); products and sums are fp32, with activations
- * carried as two 16-bit parts.
+ * carried as two 16-bit parts: to 2^-17 of each (bf16 weights), or to 2^-22 of each and no finer
+ * than 2^-37 of the row's largest (mxfp4).  4-bit values enter exactly, whatever their scales.
  */
 typedef enum { TAIL_MOE_GLU = 0, TAIL_MOE_RELU2 = 1 } tail_moe_act;
 typedef enum { TAIL_MOE_SOFTMAX = 0, TAIL_MOE_SIGMOID = 1 } tail_moe_score;
@@ -507,8 +508,9 @@ int tail_moe_create(const tail_moe_config* cfg, int device, tail_moe_t** out);
  *   out_slot_w_opt [n_tokens][S] fp32, out_ids_opt [n_tokens][S] int32, or NULL.
  * Outputs must not overlap an input otherwise, nor one another (TAIL_ERR_INVALID_ARG), and everything is
  * read in stream order.  One run per handle at a time (its scratch is shared),
- * also between captured graphs.  Results are deterministic, and a token's do not depend on the
- * others except through how many tokens share an expert (fp32 summation order).  Non-finite
+ * also between captured graphs.  Results are deterministic.  A token's depend on the others only by
+ * the order of fp32 sums, which follows n_tokens and how many tokens share an expert: in the last
+ * bits, and where two experts' scores lie that close, in which of them runs.  Non-finite
  * activations give non-finite outputs in their own token's row only.
  */
 int tail_moe_run(tail_moe_t* m, const uint16_t* x, const float* gamma_opt, const uint16_t* router_w,
