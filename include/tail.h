@@ -399,7 +399,8 @@ int tail_merge_shards(int32_t nshard, int32_t k_in, int32_t k, int32_t gbs, cons
  * and its token is -1 (counted).  A candidate at -inf has probability 0; among logits
  * of +inf the mass is shared.  NaN is outside the domain.  Draws are made with weights
  * of 2^-36 relative error and exact sums, so they agree with 64-bit arithmetic except
- * where u lies within about 2^-36 of a boundary; they do not depend on the batch.  The
+ * where u lies within about 2^-36 of a boundary (2^-36 / R in a residual that holds a share
+ * R of the row: what P - q cancels is gone); they do not depend on the batch.  The
  * weights are multiples of 2^-52 of the row's largest (tail_verify) or of 2^-44
  * (tail_verify_logits; 2^-43 and 2^-42 beyond 2^18 and 2^19 columns): less is not drawn.  Acceptances
  * agree with 64-bit arithmetic except where u_accept q lies within 2^-36 of P (tail_verify;
