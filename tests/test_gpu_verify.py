@@ -446,7 +446,7 @@ def _deep(z, temp, most=1.0):
     temp[:] = np.geomspace(0.05, most, R).astype(np.float32)
     unit = (temp.astype(np.float64) * np.log(2.0))[:, None]
     y = rng.uniform(-120.0, -75.0, (R, V))
-    y[:, 3072:4096] = rng.uniform(-59.97, -59.03, (R, 1024))
+    y[:, 4096:5120] = rng.uniform(-59.97, -59.03, (R, 1024))
     y[:, 5], y[:, 9] = 0.0, -1.0
     z[:] = (y * unit).astype(np.float32)
 
