@@ -38,7 +38,8 @@ EXPORTS = ("tail_create", "tail_run", "tail_run_ex", "tail_run_host", "tail_chec
            "tail_merge_shards", "tail_run_moe", "tail_tap_shape", "tail_run_taps", "tail_prepare_weight",
            "tail_verify", "tail_verify_logits", "tail_verify_logits_workspace",
            "tail_moe_create", "tail_moe_run", "tail_moe_check", "tail_moe_set_wait_limit", "tail_moe_get_info",
-           "tail_moe_destroy")
+           "tail_moe_destroy", "tail_token_logprobs", "tail_token_logprobs_grad", "tail_policy_loss",
+           "tail_preference_loss_workspace", "tail_preference_loss", "tail_distill_topk")
 KERNELS = ("rms_rows", "lm_head", "merge")
 
 
@@ -134,6 +135,21 @@ def lib(path: str | None = None):
         L.tail_moe_get_info.restype = ctypes.c_int
         L.tail_moe_destroy.argtypes = [P]
         L.tail_moe_destroy.restype = None
+        f32 = ctypes.c_float
+        L.tail_token_logprobs.argtypes = [i32, i32, P, i32, i64, P, f32, P, P, P, P]
+        L.tail_token_logprobs.restype = ctypes.c_int
+        L.tail_token_logprobs_grad.argtypes = [i32, i32, P, i32, i64, P, f32, P, P, P, P, P, i64, P]
+        L.tail_token_logprobs_grad.restype = ctypes.c_int
+        L.tail_policy_loss.argtypes = [i32, i32, P, i32, i64, P, f32, P, P, P, f32, f32, f32, f32, P, P, P, P, P, i64,
+                                       P]
+        L.tail_policy_loss.restype = ctypes.c_int
+        L.tail_preference_loss_workspace.argtypes = [i32, ctypes.POINTER(i64)]
+        L.tail_preference_loss_workspace.restype = ctypes.c_int
+        L.tail_preference_loss.argtypes = [i32, i32, i32, P, i32, i64, P, P, f32, P, f32, f32, f32, i32, P, P, i64, P, P,
+                                           P, i64, P]
+        L.tail_preference_loss.restype = ctypes.c_int
+        L.tail_distill_topk.argtypes = [i32, i32, i32, P, i32, i64, P, i32, i64, P, i64, f32, P, P, P, P, i64, P]
+        L.tail_distill_topk.restype = ctypes.c_int
         L.tail_check.argtypes = [P]
         L.tail_check.restype = ctypes.c_int
         L.tail_get_info.argtypes = [P, ctypes.POINTER(tail_info)]
@@ -437,3 +453,5 @@ def merge_shards(cand_vals, cand_idx, shard_offsets, k, params=None, out_tokens=
 
 from .speculative import verify, verify_logits, verify_logits_workspace  # noqa: E402,F401
 from .moe_layer import Moe  # noqa: E402,F401
+from .training import (distill_topk, policy_loss, preference_loss, preference_loss_workspace,  # noqa: E402,F401
+                       token_logprobs, token_logprobs_grad)

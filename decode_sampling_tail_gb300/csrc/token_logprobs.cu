@@ -1,0 +1,202 @@
+// Log-probabilities of given tokens under softmax(z / T), and the gradient of a sum of them and of the
+// rows' entropies.
+//
+// Forward: one pass over the logits, a cluster a row where rows are few (row_softmax.cuh).
+// Gradient: from the rows' log-sum-exps, with p_v = 2^((z_v - R) k + r), R = fp32(lse T) and r the rest of lse that
+//   R leaves (formed in 64 bits, once a row): differences from R keep their bits near the
+//   maximum, where z k - lse log2(e) would lose up to 2^-19 of p.  Every column is read and written
+//   once, by any CTA.  At the token 1 - p is -expm1(log p).
+#include "../../include/tail.h"
+#include "row_softmax.cuh"
+#include "training.h"
+
+namespace tail {
+
+namespace {
+
+template <typename T, bool ENT>
+__global__ void __launch_bounds__(512) score_kernel(const __grid_constant__ ScoreArgs a) {
+  __shared__ StatShared sh;
+  const int size = cluster_size(), rank = cluster_rank();
+  const int64_t r = blockIdx.x / size;
+  pdl_wait();
+  int t = a.tokens[r];
+  bool live = static_cast<uint32_t>(t) < static_cast<uint32_t>(a.V);
+  if (a.cu) live = live && r >= a.cu[0] && r < a.cu[a.nseq];
+  const bool first = rank == 0 && threadIdx.x == 0;
+  if (first && a.coef) a.coef[r] = 0.f;
+  if (!live) {
+    if (first) {
+      if (a.score) a.score[r] = RowScore{0.f, 0.f, 0.f, -1};
+      if (a.logprob) a.logprob[r] = 0.f;
+      if (a.lse) a.lse[r] = 0.f;
+      if (ENT) a.entropy[r] = 0.f;
+    }
+    return;
+  }
+  if (size > 1) cluster_arrive();
+  const T* row = static_cast<const T*>(a.logits) + r * a.ld;
+  const float z = Vec<T>::widen1(row[t]);
+  const RowPart p = row_part(row, a.V, rank, size);
+  RowAcc<T, ENT> acc;
+  const RowStat st = cluster_merge(stat_part(row, p, 0, a.k, acc), a.k, sh, rank, size);
+  if (!first) return;
+  const float ln = log1pf(st.s);
+  const bool empty = st.m == -INFINITY;
+  const float lp = empty ? -INFINITY : (z - st.m) * a.inv_t - ln;
+  if (a.score) a.score[r] = RowScore{st.m, st.s, empty ? 0.f : lp, empty ? -1 : t};
+  if (a.logprob) a.logprob[r] = lp;
+  if (a.lse) a.lse[r] = empty ? -INFINITY : st.m * a.inv_t + ln;
+  if (ENT) a.entropy[r] = empty ? 0.f : ln - 0.693147181f * st.u / (1.f + st.s);
+}
+
+template <typename T, bool ENT, bool SCORED>
+__global__ void __launch_bounds__(512) spread_kernel(const __grid_constant__ SpreadArgs a) {
+  const int size = cluster_size(), rank = cluster_rank();
+  const int64_t r = blockIdx.x / size;
+  pdl_wait();
+  T* grad = static_cast<T*>(a.grad) + r * a.gld;
+  const T* row = static_cast<const T*>(a.logits) + r * a.ld;
+  RowGrad g;
+  g.k = a.k;
+  bool live;
+  if (SCORED) {
+    const RowScore sc = a.score[r];
+    const float c = a.coef[r] * a.inv_t;
+    live = sc.token >= 0 && c != 0.f;
+    g.token = sc.token;
+    g.ref = sc.m;
+    g.A = -c / (1.f + sc.s);
+    g.B = 0.f;
+    if (live) {
+      const float z = Vec<T>::widen1(row[sc.token]);
+      g.at_token = c * (z == sc.m ? sc.s : 1.f + sc.s - ex2((z - sc.m) * a.k)) / (1.f + sc.s);
+    }
+  } else {
+    g.token = a.tokens[r];
+    const float da = a.a[r] * a.inv_t, db = ENT ? a.b[r] * a.inv_t : 0.f, lse = a.lse[r];
+    live = static_cast<uint32_t>(g.token) < static_cast<uint32_t>(a.V) && (da != 0.f || db != 0.f) && lse != -INFINITY;
+    if (live) {
+      g.ref = static_cast<float>(lse * a.t64);
+      const float rest = static_cast<float>((g.ref * a.inv_t64 - lse) * LOG2E);  // log2 p at z = ref
+      const float f = exp2f(rest), H = ENT ? a.entropy[r] : 0.f;
+      g.A = f * (-da - (ENT ? db * (0.693147181f * rest + H) : 0.f));
+      g.B = -f * db * 0.693147181f;
+      const float l = static_cast<float>(Vec<T>::widen1(row[g.token]) * a.inv_t64 - lse);
+      g.at_token = -da * expm1f(l);
+      if (ENT && l > -INFINITY) g.at_token -= db * expf(l) * (l + H);
+    }
+  }
+  if (!live) {
+    zero_part(grad, a.V, rank, size);
+    return;
+  }
+  // in place, another CTA of the row may write the token's column once all have read it
+  if (size > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  grad_part<T, ENT>(g, row, grad, row_part(row, a.V, rank, size), nullptr, 0);
+}
+
+template <typename T>
+cudaError_t scores(const ScoreArgs& a, int rows, cudaStream_t stream) {
+  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 0);
+  return a.entropy ? launch_rows(score_kernel<T, true>, p, rows, 0, stream, a)
+                   : launch_rows(score_kernel<T, false>, p, rows, 0, stream, a);
+}
+
+template <typename T>
+cudaError_t spread(const SpreadArgs& a, int rows, cudaStream_t stream) {
+  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 0);
+  if (a.score) return launch_rows(spread_kernel<T, false, true>, p, rows, 0, stream, a);
+  return a.b ? launch_rows(spread_kernel<T, true, false>, p, rows, 0, stream, a)
+             : launch_rows(spread_kernel<T, false, false>, p, rows, 0, stream, a);
+}
+
+const char* LIMITS = "more than 1048576 columns or 16777216 rows";
+
+}  // namespace
+
+cudaError_t launch_scores(const ScoreArgs& a, int dtype, int rows, cudaStream_t stream) {
+  return dtype == TAIL_F32   ? scores<float>(a, rows, stream)
+         : dtype == TAIL_F16 ? scores<__half>(a, rows, stream)
+                             : scores<__nv_bfloat16>(a, rows, stream);
+}
+
+cudaError_t launch_spread(const SpreadArgs& a, int dtype, int rows, cudaStream_t stream) {
+  return dtype == TAIL_F32   ? spread<float>(a, rows, stream)
+         : dtype == TAIL_F16 ? spread<__half>(a, rows, stream)
+                             : spread<__nv_bfloat16>(a, rows, stream);
+}
+
+}  // namespace tail
+
+using namespace tail;
+
+extern "C" int tail_token_logprobs(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype,
+                                   int64_t logits_ld, const int32_t* tokens, float temperature,
+                                   float* out_logprob_opt, float* out_lse_opt, float* out_entropy_opt, void* stream) {
+  const int rc = sizes_ok(rows, V, LIMITS);
+  if (rc) return rc;
+  if (!temperature_ok(temperature)) return TAIL_ERR_INVALID_ARG;
+  if (rows == 0) return TAIL_OK;
+  if (!out_logprob_opt && !out_lse_opt && !out_entropy_opt) return TAIL_ERR_INVALID_ARG;
+  if (!matrix_ok(logits, logits_dtype, logits_ld, V) || !tokens) return TAIL_ERR_INVALID_ARG;
+  if (!words_ok({tokens, out_logprob_opt, out_lse_opt, out_entropy_opt})) return TAIL_ERR_INVALID_ARG;
+  const int64_t n = 4LL * rows;
+  if (outputs_meet({{out_logprob_opt, n}, {out_lse_opt, n}, {out_entropy_opt, n}},
+                   {{tokens, n}, {logits, extent(rows, logits_ld, V, elem_bytes(logits_dtype))}}))
+    return TAIL_ERR_INVALID_ARG;
+  ScoreArgs a = {};
+  a.logits = logits;
+  a.ld = logits_ld;
+  a.tokens = tokens;
+  a.V = V;
+  a.k = static_cast<float>(LOG2E / temperature);
+  a.inv_t = static_cast<float>(1.0 / temperature);
+  a.logprob = out_logprob_opt;
+  a.lse = out_lse_opt;
+  a.entropy = out_entropy_opt;
+  const cudaError_t e = launch_scores(a, logits_dtype, rows, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TAIL_OK : cuda_fail(e, "tail_token_logprobs: kernel launch");
+}
+
+extern "C" int tail_token_logprobs_grad(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype,
+                                        int64_t logits_ld, const int32_t* tokens, float temperature, const float* lse,
+                                        const float* d_logprob, const float* d_entropy_opt, const float* entropy_opt,
+                                        void* out_grad, int64_t grad_ld, void* stream) {
+  const int rc = sizes_ok(rows, V, LIMITS);
+  if (rc) return rc;
+  if (!temperature_ok(temperature) || (d_entropy_opt != nullptr) != (entropy_opt != nullptr)) return TAIL_ERR_INVALID_ARG;
+  if (rows == 0) return TAIL_OK;
+  if (!matrix_ok(logits, logits_dtype, logits_ld, V) || !matrix_ok(out_grad, logits_dtype, grad_ld, V) || !tokens ||
+      !lse || !d_logprob)
+    return TAIL_ERR_INVALID_ARG;
+  if (!words_ok({tokens, lse, d_logprob, d_entropy_opt, entropy_opt})) return TAIL_ERR_INVALID_ARG;
+  const int64_t n = 4LL * rows;
+  const int es = elem_bytes(logits_dtype);
+  if (!grad_apart(logits, logits_ld, out_grad, grad_ld, rows, V, es) ||
+      outputs_meet({{out_grad, extent(rows, grad_ld, V, es)}},
+                   {{tokens, n}, {lse, n}, {d_logprob, n}, {d_entropy_opt, n}, {entropy_opt, n}}))
+    return TAIL_ERR_INVALID_ARG;
+  SpreadArgs a = {};
+  a.logits = logits;
+  a.ld = logits_ld;
+  a.grad = out_grad;
+  a.gld = grad_ld;
+  a.tokens = tokens;
+  a.V = V;
+  a.t64 = temperature;
+  a.inv_t64 = 1.0 / a.t64;
+  a.k = static_cast<float>(LOG2E / a.t64);
+  a.inv_t = static_cast<float>(a.inv_t64);
+  a.lse = lse;
+  a.a = d_logprob;
+  a.b = d_entropy_opt;
+  a.entropy = entropy_opt;
+  const cudaError_t e = launch_spread(a, logits_dtype, rows, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TAIL_OK : cuda_fail(e, "tail_token_logprobs_grad: kernel launch");
+}

@@ -586,6 +586,111 @@ const char* tail_status_string(int status);
    ("" when none); valid until the thread's next failing call. */
 const char* tail_last_error(void);
 
+/*
+ * Training on vocabulary logits: the losses that a policy, a preference-tuned model or a draft
+ * model is trained by, on the logits that the tail's lm_head gives, with their gradients.  The
+ * page has no counterpart.  A row r of logits z_r (V columns) has p_r = softmax(z_r / T), l_r = log p_r,
+ * H_r = -sum_v p_r(v) l_r(v), with T > 0 the call's temperature.
+ *   rows, V        rows <= 16777216 (0: nothing is done), V <= 1048576 (TAIL_ERR_UNSUPPORTED beyond).
+ *   logits         [rows][logits_ld] of logits_dtype (tail_dtype), aligned to its element; out_logits_opt of
+ *                  tail_run is such an array.  Rows whose start and whose gradient's start have the same
+ *                  address modulo 16 bytes are the fast case.
+ *   tokens         [rows] int32: the token that row r's logits predicted.  A row whose token is outside [0, V)
+ *                  (-1: a prompt position, padding) is ignored: its results are 0, its gradient is
+ *                  zeros, its logits are not read.
+ *   temperature    T, from 2^-64 to 2^64.
+ *   weight_opt     [rows] (or [pairs]) fp32 factors of the losses, NULL: 1.  A row (pair) of weight 0 is
+ *                  left out: loss and gradient 0, whatever the formula gives.
+ *   out_loss       fp32, the weight in it.
+ *   out_grad_opt   [rows][grad_ld] of logits_dtype: the gradient of the sum of out_loss by the logits; rounded
+ *                  once.  NULL: the loss alone.  It may be the logits themselves (same pointer and
+ *                  leading dimension); other overlaps are refused.
+ * Outputs must not overlap inputs otherwise, nor one another (TAIL_ERR_INVALID_ARG).  A logit of -inf has
+ * probability 0 and gradient 0.  A row without a logit above -inf has no distribution: log-probability
+ * and lse -inf, entropy 0; the losses leave it out like an ignored row.  NaN makes its own row's results NaN, and +inf is
+ * outside the domain; other rows do not change.  What a formula makes infinite is infinite (the
+ * log-probability of a token of probability 0).
+ * Sums are fp32, one instance of a row's maximum apart from the others, so that the log-probability of a
+ * likely token and its distance 1 - p keep about 2^-20 of themselves.  Results are deterministic and
+ * a row's do not depend on the others', except by the order of sums, which follows rows, V and the dtype.  No handle
+ * and no allocation; asynchronous on `stream` of the current device; everything is read in stream order.
+ */
+
+/*
+ * l_r(token), lse_r = log sum_v exp(z_rv / T) and H_r of every row, each [rows] fp32 or NULL (not all three).
+ * Ignored rows get 0.  One launch, one pass over the logits.
+ */
+int tail_token_logprobs(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype, int64_t logits_ld,
+                        const int32_t* tokens, float temperature, float* out_logprob_opt, float* out_lse_opt,
+                        float* out_entropy_opt, void* stream);
+
+/*
+ * The gradient of sum_r d_logprob[r] l_r(token) + d_entropy[r] H_r, for losses formed by the caller:
+ *   dz_v = (d_logprob (1[v = token] - p_v) - d_entropy p_v (log p_v + H)) / T,  log p_v = z_v / T - lse.
+ *   lse, entropy_opt  [rows] as tail_token_logprobs gives them; entropy_opt goes with d_entropy_opt.
+ * A row with both factors 0 gets zeros and is not read.  One launch.
+ */
+int tail_token_logprobs_grad(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype, int64_t logits_ld,
+                             const int32_t* tokens, float temperature, const float* lse, const float* d_logprob,
+                             const float* d_entropy_opt, const float* entropy_opt, void* out_grad, int64_t grad_ld,
+                             void* stream);
+
+/*
+ * The clipped policy loss of every row, with l = l_r(token), R = exp(l - old), d = ref - l:
+ *   loss = weight (max(-A R, -A min(max(R, 1 - clip_low), 1 + clip_high)) + kl_coef (exp(d) - d - 1)
+ *          - entropy_coef H);  the derivative of the maximum is that of -A R where it is not below the other.
+ *   old_logprob, advantage  [rows] fp32, A the advantage.
+ *   ref_logprob_opt         [rows] fp32; needed when kl_coef is not 0, not read otherwise.
+ *   clip_low                in [0, 1]; clip_high >= 0 (inf: no upper clip).
+ *   out_logprob_opt, out_entropy_opt  [rows] fp32 l and H, or NULL.
+ * One launch; the logits are read once.
+ */
+int tail_policy_loss(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype, int64_t logits_ld,
+                     const int32_t* tokens, float temperature, const float* old_logprob, const float* advantage,
+                     const float* ref_logprob_opt, float clip_low, float clip_high, float kl_coef, float entropy_coef,
+                     const float* weight_opt, float* out_loss, float* out_logprob_opt, float* out_entropy_opt,
+                     void* out_grad_opt, int64_t grad_ld, void* stream);
+
+/*
+ * The paired preference loss: sequences 2i (chosen) and 2i + 1 (rejected) of nseq (even), with L_s the sum (average:
+ * the mean) of l_r(token) over the sequence's counted rows (none: 0):
+ *   h = beta ((L_2i - ref_2i) - (L_2i+1 - ref_2i+1)) - margin,
+ *   loss_i = weight_i ((1 - label_smoothing) log(1 + exp(-h)) + label_smoothing log(1 + exp(h))).
+ *   cu_rows        [nseq + 1] int32 (device), non-decreasing: sequence s has the rows [cu_rows[s], cu_rows[s + 1]).  Rows
+ *                  outside [cu_rows[0], cu_rows[nseq]) are ignored: gradient zeros, not read.  (Values
+ *                  outside [0, rows] are cut.)
+ *   ref_logprob_opt  [nseq] fp32: the reference model's L_s, NULL: 0.
+ *   label_smoothing  in [0, 1];  average 0 or 1.
+ *   workspace      device memory of tail_preference_loss_workspace(rows) bytes, 16-byte aligned, any
+ *                  contents; calls that may overlap need one each.  (NULL with rows 0.)
+ *   out_loss       [nseq / 2];  out_seq_logprob_opt [nseq] L_s, or NULL.
+ * Two launches, three with the gradient.  nseq <= 16777216.
+ */
+int tail_preference_loss_workspace(int32_t rows, int64_t* bytes);
+int tail_preference_loss(int32_t rows, int32_t V, int32_t nseq, const void* logits, int32_t logits_dtype,
+                         int64_t logits_ld, const int32_t* tokens, const int32_t* cu_rows, float temperature,
+                         const float* ref_logprob_opt, float beta, float label_smoothing, float margin,
+                         int32_t average, const float* weight_opt, void* workspace, int64_t workspace_bytes,
+                         float* out_loss, float* out_seq_logprob_opt, void* out_grad_opt, int64_t grad_ld,
+                         void* stream);
+
+/*
+ * Distillation from a teacher's top logits, such as the top-k that tail_run_ex gives.  q is the softmax over the
+ * list's t_i / T and, when teacher_rest_opt is given, one more entry: the logarithm of what exp(t_v / T) of all
+ * tokens outside the list sums to (-inf: nothing).  With p the softmax of the student's z / T over all V,
+ *   loss_r = weight_r (sum_i q_i (log q_i - l_r(id_i)) + q_rest (log q_rest - log sum_{v not listed} p_v)).
+ *   k              entries a row, 1 <= k <= 1024.
+ *   topk_vals      [rows][vals_ld] t of vals_dtype (tail_dtype);  topk_idx [rows][idx_ld] int32.  Any order; an
+ *                  id outside [0, V) (-1) is no entry, an id that comes twice counts with both.
+ *   teacher_rest_opt  [rows] fp32, or NULL: q is over the list alone.
+ * A row without an entry (or whose every value and the rest are -inf) is ignored; otherwise there are no
+ * tokens.  One launch; the logits are read once.
+ */
+int tail_distill_topk(int32_t rows, int32_t V, int32_t k, const void* logits, int32_t logits_dtype, int64_t logits_ld,
+                      const void* topk_vals, int32_t vals_dtype, int64_t vals_ld, const int32_t* topk_idx,
+                      int64_t idx_ld, float temperature, const float* teacher_rest_opt, const float* weight_opt,
+                      float* out_loss, void* out_grad_opt, int64_t grad_ld, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
