@@ -135,20 +135,20 @@ def lib(path: str | None = None):
         L.tail_moe_get_info.restype = ctypes.c_int
         L.tail_moe_destroy.argtypes = [P]
         L.tail_moe_destroy.restype = None
-        f32 = ctypes.c_float
-        L.tail_token_logprobs.argtypes = [i32, i32, P, i32, i64, P, f32, P, P, P, P]
+        f32, f64 = ctypes.c_float, ctypes.c_double
+        L.tail_token_logprobs.argtypes = [i32, i32, P, i32, i64, P, f64, P, P, P, P]
         L.tail_token_logprobs.restype = ctypes.c_int
-        L.tail_token_logprobs_grad.argtypes = [i32, i32, P, i32, i64, P, f32, P, P, P, P, P, i64, P]
+        L.tail_token_logprobs_grad.argtypes = [i32, i32, P, i32, i64, P, f64, P, P, P, P, P, i64, P]
         L.tail_token_logprobs_grad.restype = ctypes.c_int
-        L.tail_policy_loss.argtypes = [i32, i32, P, i32, i64, P, f32, P, P, P, f32, f32, f32, f32, P, P, P, P, P, i64,
+        L.tail_policy_loss.argtypes = [i32, i32, P, i32, i64, P, f64, P, P, P, f32, f32, f32, f32, P, P, P, P, P, i64,
                                        P]
         L.tail_policy_loss.restype = ctypes.c_int
         L.tail_preference_loss_workspace.argtypes = [i32, ctypes.POINTER(i64)]
         L.tail_preference_loss_workspace.restype = ctypes.c_int
-        L.tail_preference_loss.argtypes = [i32, i32, i32, P, i32, i64, P, P, f32, P, f32, f32, f32, i32, P, P, i64, P, P,
+        L.tail_preference_loss.argtypes = [i32, i32, i32, P, i32, i64, P, P, f64, P, f32, f32, f32, i32, P, P, i64, P, P,
                                            P, i64, P]
         L.tail_preference_loss.restype = ctypes.c_int
-        L.tail_distill_topk.argtypes = [i32, i32, i32, P, i32, i64, P, i32, i64, P, i64, f32, P, P, P, P, i64, P]
+        L.tail_distill_topk.argtypes = [i32, i32, i32, P, i32, i64, P, i32, i64, P, i64, f64, P, P, P, P, i64, P]
         L.tail_distill_topk.restype = ctypes.c_int
         L.tail_check.argtypes = [P]
         L.tail_check.restype = ctypes.c_int

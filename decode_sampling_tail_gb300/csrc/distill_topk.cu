@@ -31,7 +31,7 @@ struct DistillArgs {
   float k, inv_t;
   double k64;
   int vals_dtype;
-  int cached, map_words;
+  int map_words, flag_words, cache_at, kept;  // cache_at, kept: in vectors
 };
 
 __device__ __forceinline__ float list_value(const DistillArgs& a, int64_t r, int i) {
@@ -47,6 +47,7 @@ struct Teacher {
   float q_rest, lq_rest;   // and its logarithm
   float q_list;            // 1 - q_rest
   bool rest_is_max;
+  bool any;  // whether there is anything to aim at
 };
 
 __device__ __forceinline__ Teacher teacher_of(const RowStat& st, const float* rest, int64_t r, float k, double k64) {
@@ -61,7 +62,9 @@ __device__ __forceinline__ Teacher teacher_of(const RowStat& st, const float* re
   t.q_list = 1.f;
   t.rest_is_max = false;
   t.ln = log1pf(st.s);
+  t.any = listed;
   if (!rest || rest[r] == -INFINITY) return t;
+  t.any = true;
   if (!listed) {  // the list's values are all -inf: everything is outside it
     t.others = 0.f, t.ln = 0.f, t.q_rest = 1.f, t.lq_rest = 0.f, t.q_list = 0.f, t.rest_is_max = true;
     return t;
@@ -72,7 +75,7 @@ __device__ __forceinline__ Teacher teacher_of(const RowStat& st, const float* re
     t.others = st.s + w;
     t.ln = log1pf(t.others);
     t.q_rest = w / (1.f + t.others);
-    t.lq_rest = d * 0.693147181f - t.ln;
+    t.lq_rest = d > -100.f ? logf(t.q_rest) : d * 0.693147181f - t.ln;
     t.q_list = in / (1.f + t.others);
   } else {
     t.rest_is_max = true;
@@ -87,174 +90,234 @@ __device__ __forceinline__ Teacher teacher_of(const RowStat& st, const float* re
   return t;
 }
 
-template <typename T, bool GRAD>
-__global__ void __launch_bounds__(512, 2) distill_kernel(const __grid_constant__ DistillArgs a) {
-  constexpr int N = Vec<T>::N;
-  extern __shared__ uint4 smem[];
-  __shared__ StatShared sh;
-  uint4* cache = smem;
-  uint32_t* map = reinterpret_cast<uint32_t*>(cache + a.cached);
-  int32_t* ids = reinterpret_cast<int32_t*>(map + a.map_words);
-  float* tv = reinterpret_cast<float*>(ids + a.k_list);  // the teacher's values
-  float* zv = tv + a.k_list;                             // the student's logits at the entries
-  const int size = cluster_size(), rank = cluster_rank(), tid = threadIdx.x, nt = blockDim.x;
-  const int64_t r = blockIdx.x / size;
-  pdl_wait();
-  const float w = a.weight ? a.weight[r] : 1.f;
-  T* grad = static_cast<T*>(a.grad) + r * a.gld;
-  const T* row = static_cast<const T*>(a.logits) + r * a.ld;
-  const RowPart p = row_part(row, a.V, rank, size);
-  const int cached = GRAD ? min(a.cached, p.count) : 0;
-  // The part's columns: [lo, hi), its bits from one vector in front of its first whole one.
-  const int body = p.head + p.first * N;
-  const int lo = rank == 0 ? 0 : body, hi = rank == size - 1 ? a.V : body + p.count * N;
-  const int origin = body - N;
+// A CTA's shared memory behind the board: the list (ids and the teacher's values), the student's logits at its
+// entries, the bit map of the part's listed columns, and a byte a thread and batch that says which of its
+// vectors have one.  What is kept of the part follows.
+struct List {
+  int32_t* ids;
+  float* t;
+  float* z;
+  uint32_t* map;
+  uint32_t* flags;
+};
 
-  for (int i = tid; i < a.map_words; i += nt) map[i] = 0;
-  bool any = false;
-  RowStat ts = no_stat();
-  for (int i = tid; i < a.k_list; i += nt) {
-    const int id = a.idx[r * a.ild + i];
-    const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.V);
-    const float v = list_value(a, r, i);
-    ids[i] = ok ? id : -1;
-    tv[i] = v;
-    any = any || ok;
-    if (ok) ts = merge(ts, stat_of(v), a.k);
-  }
-  if (!__syncthreads_or(any && w != 0.f)) {
-    if (rank == 0 && tid == 0) a.loss[r] = 0.f;
-    if (GRAD) zero_part(grad, a.V, rank, size);
-    return;
-  }
-  if (size > 1) cluster_arrive();
-  fetch_part(row, p, cache, cached);
-  // The entries of this part (the loss, on rank 0, wants all of them), their bits, and whether an id comes twice.
-  bool twice = false;
-  for (int i = tid; i < a.k_list; i += nt) {
-    const int id = ids[i];
-    if (id < 0) continue;
-    const bool mine = id >= lo && id < hi;
-    if (mine || rank == 0) zv[i] = Vec<T>::widen1(row[id]);
-    if (mine) {
-      const uint32_t bit = 1u << ((id - origin) & 31);
-      twice = (atomicOr(map + ((id - origin) >> 5), bit) & bit) || twice;
-    }
-  }
-  twice = __syncthreads_or(twice);
-  // The first of an id's entries stands for its column.
-  const auto owner = [&](int i) {
-    if (ids[i] < lo || ids[i] >= hi) return false;
-    if (twice)
-      for (int j = 0; j < i; ++j)
-        if (ids[j] == ids[i]) return false;
-    return true;
-  };
-  RowStat in = no_stat();
-  for (int i = tid; i < a.k_list; i += nt)
-    if (owner(i)) in = merge(in, stat_of(zv[i]), a.k);
-  const auto bits = [&](int i) {
+// Bits from one vector in front of a part's first whole one to the columns behind its last.
+inline int map_words(int64_t part, int n) { return static_cast<int>(((part + 2) * n + 31) / 32 + 1); }
+inline int flag_words(int64_t part, int nt) { return batches(static_cast<int>(part), nt) * nt / 4; }
+
+template <int N, int NT>
+struct ListMask {
+  const uint32_t* map;
+  const uint8_t* flag;
+  __device__ __forceinline__ uint32_t flags(int b) const { return flag[b * NT + static_cast<int>(threadIdx.x)]; }
+  __device__ __forceinline__ uint32_t bits(int i) const {
     const int at = (i + 1) * N;
     return (map[at >> 5] >> (at & 31)) & ((1u << N) - 1);
+  }
+};
+
+// What a row's gradient needs at the entries: the student's statistics over all columns, weight / T (0: no gradient).
+struct EntryGrad {
+  float m, s, wt;
+};
+
+// A row's loss and the factors of its gradient from the board, by one warp.
+__device__ __forceinline__ void distill_row(const DistillArgs& a, int64_t r, float w, const Teacher& t,
+                                            const Board<2>& board, RowGrad* g, EntryGrad* e) {
+  const int lane = threadIdx.x;
+  const RowStat o = board.stat<false>(0, a.k), n = board.stat<false>(1, a.k);
+  const RowStat all = merge(o, n, a.k);
+  const bool live = all.m != -INFINITY && t.any;  // a distribution, and something to aim at
+  const float ln = log1pf(all.s), sum = 1.f + all.s;
+  const float out_w = o.m == -INFINITY ? 0.f : (1.f + o.s) * ex2(dist(o.m, finite_ref(all.m), a.k));
+  const float in_w = n.m == -INFINITY ? 0.f : (1.f + n.s) * ex2(dist(n.m, finite_ref(all.m), a.k));
+  const float p_rest = out_w / sum;
+  if (board.rank == 0) {
+    float loss = 0.f, q = 0.f;
+    for (int i = lane; i < board.sets; i += 32) {
+      const float4 x = board.get(0, i);
+      if (!(x.w == 0.f)) loss += x.z - x.w * ((finite_ref(board.get(1, i).x) - all.m) * a.inv_t);
+      q += x.w;
+    }
+    // log q_i - l_i is a difference of two logits and of two log-sums: the logarithm of the sums' quotient does not
+    // leave each one's rounding behind
+    const float scale = 1.f + t.others;
+    const float x = t.D == 0.f ? all.s - t.others : sum * ex2(-t.D) - scale;
+    const float lead = t.D < 100.f ? log1pf(x / scale) : ln - t.ln - t.D * 0.693147181f;
+    loss = warp_sum(loss) + lead * warp_sum(q);
+    if (!(t.q_rest == 0.f)) {
+      const float lp = out_w >= in_w    ? -log1pf(in_w / out_w)
+                       : out_w > 1e-30f ? logf(p_rest)
+                                        : (o.m - all.m) * a.inv_t + log1pf(o.s) - ln;
+      loss += t.q_rest * (t.lq_rest - (o.m == -INFINITY ? -INFINITY : lp));
+    }
+    if (lane == 0) a.loss[r] = live ? w * loss : 0.f;
+  }
+  if (lane == 0) {
+    const float wt = live ? w * a.inv_t : 0.f;
+    const float off = p_rest > 0.5f && t.q_rest > 0.5f ? t.q_list - in_w / sum : p_rest - t.q_rest;
+    *g = RowGrad{finite_ref(o.m), a.k, live ? wt * off / (1.f + o.s) : 0.f, 0.f, 0.f, -1};
+    *e = EntryGrad{finite_ref(all.m), all.s, wt};
+  }
+}
+
+template <typename T, bool GRAD, int NT>
+__global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const __grid_constant__ DistillArgs a) {
+  constexpr int N = Vec<T>::N;
+  extern __shared__ uint4 smem[];
+  __shared__ RowStat s_warp[NT / 32];
+  __shared__ Teacher s_teacher;
+  __shared__ RowGrad s_grad;
+  __shared__ EntryGrad s_entry;
+  const int size = cluster_size(), rank = cluster_rank(), tid = threadIdx.x;
+  const Board<2> board = board_at<2>(smem, rank, size);
+  List l;
+  l.ids = reinterpret_cast<int32_t*>(smem + Board<2>::bytes(board.sets) / 16);
+  l.t = reinterpret_cast<float*>(l.ids + a.k_list);
+  l.z = l.t + a.k_list;
+  l.map = reinterpret_cast<uint32_t*>(l.z + a.k_list);
+  l.flags = l.map + a.map_words;
+  uint4* cache = smem + a.cache_at;
+  const int64_t r = blockIdx.x / size;
+  const T* row = static_cast<const T*>(a.logits) + r * a.ld;
+  T* grad = static_cast<T*>(a.grad) + r * a.gld;
+  const RowPart p = row_part(row, a.V, rank, size);
+  const int cached = GRAD ? min(a.kept, p.count) : 0;
+  // The part's columns [lo, hi); bit 0 of the map is one vector in front of its first whole one.
+  const int body = p.head + p.first * N, origin = body - N;
+  const int lo = rank == 0 ? 0 : body, hi = rank == size - 1 ? a.V : body + p.count * N;
+  const auto entries = [&](auto f) {  // f(entry, its column) for this thread's entries in the part
+    for (int i = tid; i < a.k_list; i += NT) {
+      const int id = l.ids[i];
+      if (id >= lo && id < hi) f(i, id);
+    }
   };
-  RowStat out = stat_cached<T, false>(row, p, cache, cached, a.k, bits);
-  const bool edge = p.edge_n && !(map[(p.edge_lo - origin) >> 5] >> ((p.edge_lo - origin) & 31) & 1);
-  if (edge) out = merge(out, stat_of(Vec<T>::widen1(row[p.edge_lo])), a.k);
+  for (int i = tid; i < a.map_words + a.flag_words; i += NT) l.map[i] = 0;  // (the flags lie behind the map)
+  pdl_wait();
 
-  ts = warp_merge(ts, a.k);
-  __syncthreads();
-  if ((tid & 31) == 0) sh.warp[tid >> 5] = ts;
-  __syncthreads();
-  ts = no_stat();
-  for (int i = 0; i < nt / 32; ++i) ts = merge(ts, sh.warp[i], a.k);
-  __syncthreads();
-  out.u = 0.f;
-  out = cluster_merge(out, a.k, sh, rank, size);
-  if (size > 1) cluster_arrive();
-  __syncthreads();
-  in = cluster_merge(in, a.k, sh, rank, size);
-
-  const Teacher t = teacher_of(ts, a.rest, r, a.k, a.k64);
-  const RowStat all = merge(out, in, a.k);
-  const bool target = ts.m != -INFINITY || t.q_rest > 0.f;
-  if (all.m == -INFINITY || !target) {  // no distribution, or nothing to aim at
+  // The list.  A row is fetched at once when its first entry is one.
+  const float w = a.weight ? a.weight[r] : 1.f;
+  const bool early = w != 0.f && static_cast<uint32_t>(a.idx[r * a.ild]) < static_cast<uint32_t>(a.V);
+  const auto fetch = [&] {
+    if (cached > 0)
+      fetch_part<T, NT>(row, p, cache, cached);
+    else
+      prefetch_part(row, p);
+  };
+  if (early) fetch();
+  bool any = false;
+  RowStat st[1] = {no_stat()};
+  if (w != 0.f)
+    for (int i = tid; i < a.k_list; i += NT) {
+      const int id = a.idx[r * a.ild + i];
+      const float v = list_value(a, r, i);
+      const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.V);
+      l.ids[i] = ok ? id : -1;
+      l.t[i] = v;
+      any = any || ok;
+      if (ok) st[0] = merge(st[0], stat_of(v), a.k);
+    }
+  st[0] = warp_merge<1, false>(st, a.k);
+  if ((tid & 31) == 0) s_warp[tid >> 5] = st[0];
+  if (!__syncthreads_or(any)) {
     if (rank == 0 && tid == 0) a.loss[r] = 0.f;
     if (GRAD) zero_part(grad, a.V, rank, size);
     return;
   }
-  const float ln = log1pf(all.s), sum = 1.f + all.s;
-  const float out_w = out.m == -INFINITY ? 0.f : (1.f + out.s) * ex2(dist(out.m, all.m, a.k));
-  const float in_w = in.m == -INFINITY ? 0.f : (1.f + in.s) * ex2(dist(in.m, all.m, a.k));
-  const float p_rest = out_w / sum;
-  const float tln = t.ln;
+  if (size > 1) cluster_arrive();
+  if (!early) fetch();
+  // The entries of this part: their bits, and whether an id comes twice.
+  bool twice = false;
+  entries([&](int i, int id) {
+    const int at = id - origin, v = at / N - 1;
+    const uint32_t bit = 1u << (at & 31);
+    twice = (atomicOr(l.map + (at >> 5), bit) & bit) || twice;
+    if (v >= 0 && v < p.count) {
+      const int f = v / (ROW_BATCH * NT) * NT + v % NT;  // its thread's byte of its batch
+      atomicOr(l.flags + (f >> 2), 1u << (v / NT % ROW_BATCH + 8 * (f & 3)));
+    }
+    l.z[i] = Vec<T>::widen1(row[id]);
+  });
+  if (tid < 32) {
+    st[0] = tid < NT / 32 ? s_warp[tid] : no_stat();
+    st[0] = warp_merge<1, false>(st, a.k);
+    if (tid == 0) s_teacher = teacher_of(st[0], a.rest, r, a.k, a.k64);
+  }
+  twice = __syncthreads_or(twice);
+  const Teacher& t = s_teacher;
+  const auto weight = [&](int i) { return ex2((l.t[i] - t.m) * a.k - t.D) / (1.f + t.others); };
+  const auto owner = [&](int i, int id) {  // the first of an id's entries stands for its column
+    if (twice)
+      for (int j = 0; j < i; ++j)
+        if (l.ids[j] == id) return false;
+    return true;
+  };
 
-  if (rank == 0) {
-    float loss = 0.f;
-    for (int i = tid; i < a.k_list; i += nt) {
-      if (ids[i] < 0) continue;
-      const float y = (tv[i] - t.m) * a.k - t.D, q = ex2(y) / (1.f + t.others);
-      if (!(q == 0.f)) loss += q * ((y * 0.693147181f - tln) - ((zv[i] - all.m) * a.inv_t - ln));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
-    if ((tid & 31) == 0) sh.warp[tid >> 5].m = loss;
-  }
-  __syncthreads();
-  if (rank == 0 && tid == 0) {
-    float loss = 0.f;
-    for (int i = 0; i < nt / 32; ++i) loss += sh.warp[i].m;
-    if (!(t.q_rest == 0.f)) {
-      const float lp = out_w >= in_w ? -log1pf(in_w / out_w)
-                                     : (out.m - all.m) * a.inv_t + log1pf(out.s) - ln;
-      loss += t.q_rest * (t.lq_rest - (out.m == -INFINITY ? -INFINITY : lp));
-    }
-    a.loss[r] = w * loss;
-  }
+  // Statistics of the columns outside the list and of the listed ones, and, relative to the latter's maximum in
+  // the warp, sum q_i (t_i - z_i) / T and sum q_i.
+  const float edge = edge_of(row, p);
+  RowStat out[1] = {stat_pass<T, false, NT>(row, p, cache, cached, a.k,
+                                            ListMask<N, NT>{l.map, reinterpret_cast<const uint8_t*>(l.flags)})};
+  if (p.edge_n && !(l.map[(p.edge_lo - origin) >> 5] >> ((p.edge_lo - origin) & 31) & 1))
+    out[0] = merge(out[0], stat_of(edge), a.k);
+  RowStat in[1] = {no_stat()};
+  entries([&](int i, int id) {
+    if (owner(i, id)) in[0] = merge(in[0], stat_of(l.z[i]), a.k);
+  });
+  out[0] = warp_merge<1, false>(out, a.k);
+  in[0] = warp_merge<1, false>(in, a.k);
+  float C = 0.f, Q = 0.f;
+  entries([&](int i, int) {
+    const float q = weight(i);
+    if (q == 0.f) return;
+    C += q * (((l.t[i] - t.m) - (l.z[i] - finite_ref(in[0].m))) * a.inv_t);
+    Q += q;
+  });
+  const float4 post[2] = {make_float4(out[0].m, out[0].s, warp_sum(C), warp_sum(Q)),
+                          make_float4(in[0].m, in[0].s, 0.f, 0.f)};
+  if (size > 1) cluster_wait();
+  board.post(post);
+  board.wait();
+  if (tid < 32) distill_row(a, r, w, t, board, &s_grad, &s_entry);
   if (!GRAD) return;
-  const float wt = w * a.inv_t;
-  RowGrad g;
-  g.ref = finite_ref(out.m);
-  g.k = a.k;
-  g.token = -1;
-  g.B = 0.f;
-  g.at_token = 0.f;
-  const float off = p_rest > 0.5f && t.q_rest > 0.5f ? t.q_list - in_w / sum : p_rest - t.q_rest;
-  g.A = wt * off / (1.f + out.s);
-  grad_part<T, false>(g, row, grad, p, cache, cached);
+  __syncthreads();
+  grad_pass<T, false, NT>(s_grad, GradRow<T>{row, grad, p, cache, cached, edge});
   __syncthreads();  // the entries' values go over what the pass has written
-  for (int i = tid; i < a.k_list; i += nt) {
-    if (!owner(i)) continue;
-    const float y = (tv[i] - t.m) * a.k - t.D;
-    float q = ex2(y) / (1.f + t.others);
-    float q_left = !t.rest_is_max && tv[i] == t.m ? t.others / (1.f + t.others) : 1.f - q;
+  const EntryGrad e = s_entry;
+  entries([&](int i, int id) {
+    if (!owner(i, id)) return;
+    float q = weight(i), q_left = 1.f - q;
     if (twice) {
       for (int j = i + 1; j < a.k_list; ++j)
-        if (ids[j] == ids[i]) q += ex2((tv[j] - t.m) * a.k - t.D) / (1.f + t.others);
+        if (l.ids[j] == id) q += weight(j);
       q_left = 1.f - q;
+    } else if (q > 0.5f && !t.rest_is_max) {
+      q_left = t.others / (1.f + t.others);  // above one half: the largest
     }
-    const float e = ex2((zv[i] - all.m) * a.k), pv = e / sum;
-    const float p_left = (zv[i] == all.m ? all.s : sum - e) / sum;
-    grad[ids[i]] = Vec<T>::narrow1(wt * (pv > 0.5f && q > 0.5f ? q_left - p_left : pv - q));
-  }
+    const float x = ex2((l.z[i] - e.m) * a.k), sum = 1.f + e.s, pv = x / sum;
+    const float p_left = (l.z[i] == e.m ? e.s : sum - x) / sum;
+    grad[id] = Vec<T>::narrow1(e.wt == 0.f ? 0.f : e.wt * (pv > 0.5f && q > 0.5f ? q_left - p_left : pv - q));
+  });
+}
+
+template <typename T, bool GRAD>
+cudaError_t launch(DistillArgs& a, int rows, cudaStream_t stream) {
+  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 16, GRAD ? 24 * 1024 : -1);
+  const int64_t part = part_of(row_vectors(a.V, sizeof(T)), p.size);
+  a.map_words = map_words(part, Vec<T>::N);
+  a.flag_words = flag_words(part, p.threads);
+  const int beside = Board<2>::bytes(p.size * p.threads / 32) + 4 * (3 * a.k_list + a.map_words + a.flag_words);
+  a.cache_at = (beside + 15) / 16;
+  a.kept = p.kept;
+  const int smem = 16 * (a.cache_at + a.kept);
+  return p.threads == 512   ? launch_rows<distill_kernel<T, GRAD, 512>>(p, smem, rows, stream, a)
+         : p.threads == 256 ? launch_rows<distill_kernel<T, GRAD, 256>>(p, smem, rows, stream, a)
+                            : launch_rows<distill_kernel<T, GRAD, 128>>(p, smem, rows, stream, a);
 }
 
 template <typename T>
 cudaError_t launch(DistillArgs& a, int rows, cudaStream_t stream) {
-  // the map takes a bit a column and the lists 12 bytes an entry of what a CTA has
-  const int lists = 12 * a.k_list;
-  const int fit = ROW_SM_SMEM / 2 - lists;
-  const RowPlan p = plan_rows(rows, a.V, sizeof(T), a.grad ? fit - fit / 16 : 0);
-  const int64_t vecs = (static_cast<int64_t>(a.V) * sizeof(T) + 15) / 16;
-  const int64_t part = (vecs + p.size - 1) / p.size;
-  a.map_words = static_cast<int>(((part + 2) * Vec<T>::N + 31) / 32 + 1);
-  a.cached = p.cached;
-  if (a.grad) {
-    const int64_t room = (ROW_SM_SMEM / 2 - lists - 4LL * a.map_words) / 16;
-    if (a.cached > room) a.cached = static_cast<int>(room < 0 ? 0 : room);
-  }
-  const int smem = a.cached * 16 + a.map_words * 4 + lists;
-  return a.grad ? launch_rows(distill_kernel<T, true>, p, rows, smem, stream, a)
-                : launch_rows(distill_kernel<T, false>, p, rows, smem, stream, a);
+  return a.grad ? launch<T, true>(a, rows, stream) : launch<T, false>(a, rows, stream);
 }
 
 }  // namespace
@@ -265,7 +328,7 @@ using namespace tail;
 
 extern "C" int tail_distill_topk(int32_t rows, int32_t V, int32_t k, const void* logits, int32_t logits_dtype,
                                  int64_t logits_ld, const void* topk_vals, int32_t vals_dtype, int64_t vals_ld,
-                                 const int32_t* topk_idx, int64_t idx_ld, float temperature,
+                                 const int32_t* topk_idx, int64_t idx_ld, double temperature,
                                  const float* teacher_rest_opt, const float* weight_opt, float* out_loss,
                                  void* out_grad_opt, int64_t grad_ld, void* stream) {
   const int rc = sizes_ok(rows, V, "more than 1048576 columns or 16777216 rows");

@@ -23,84 +23,117 @@ struct PolicyArgs {
   int V;
   float k, inv_t;
   float lo, hi, kl, ent;  // 1 - clip_low, 1 + clip_high, the terms' factors
-  int cached;
+  int kept;  // vectors of a part that shared memory holds
 };
 
-template <typename T, bool ENT>
-__global__ void __launch_bounds__(512, 2) policy_kernel(const __grid_constant__ PolicyArgs a) {
-  extern __shared__ uint4 cache[];
-  __shared__ StatShared sh;
-  const int size = cluster_size(), rank = cluster_rank();
-  const int64_t r = blockIdx.x / size;
-  pdl_wait();
-  const int t = a.tokens[r];
-  const float w = a.weight ? a.weight[r] : 1.f;
-  T* grad = static_cast<T*>(a.grad) + r * a.gld;
-  const bool first = rank == 0 && threadIdx.x == 0;
-  if (static_cast<uint32_t>(t) >= static_cast<uint32_t>(a.V) || w == 0.f) {
-    if (first) {
-      a.loss[r] = 0.f;
-      if (a.logprob) a.logprob[r] = 0.f;
-      if (a.entropy) a.entropy[r] = 0.f;
-    }
-    if (a.grad) zero_part(grad, a.V, rank, size);
-    return;
-  }
-  if (size > 1) cluster_arrive();
-  const T* row = static_cast<const T*>(a.logits) + r * a.ld;
-  const RowPart p = row_part(row, a.V, rank, size);
-  const int cached = min(a.cached, p.count);
-  fetch_part(row, p, cache, cached);
-  const float z = Vec<T>::widen1(row[t]);
-  RowStat st = stat_cached<T, ENT>(row, p, cache, cached, a.k, [](int) { return 0u; });
-  if (p.edge_n) st = merge(st, stat_of(Vec<T>::widen1(row[p.edge_lo])), a.k);
-  st = cluster_merge(st, a.k, sh, rank, size);
-  const float ln = log1pf(st.s), sum = 1.f + st.s;
-  if (st.m == -INFINITY) {  // no distribution
-    if (first) {
-      a.loss[r] = 0.f;
-      if (a.logprob) a.logprob[r] = -INFINITY;
-      if (a.entropy) a.entropy[r] = 0.f;
-    }
-    if (a.grad) zero_part(grad, a.V, rank, size);
-    return;
-  }
-  const float lp = (z - st.m) * a.inv_t - ln;
-  const float excess = ENT ? -0.693147181f * st.u / sum : 0.f;  // H - log of the sum
-  const float R = expf(lp - a.old[r]), A = a.adv[r];
-  const float open = -A * R, clipped = -A * fminf(fmaxf(R, a.lo), a.hi);
+// A row's loss and the factors of its gradient.
+struct PolicyRow {
+  int64_t r;
+  int t;
+  float w, z, old, adv, ref;
+};
+template <bool ENT>
+__device__ __forceinline__ RowGrad policy_row(const PolicyArgs& a, const PolicyRow& x, const RowStat& all, bool first) {
+  const float ln = log1pf(all.s), sum = 1.f + all.s;
+  const bool empty = all.m == -INFINITY;  // no distribution
+  const float lp = empty ? -INFINITY : (x.z - all.m) * a.inv_t - ln;
+  const float excess = ENT ? -0.693147181f * all.u / sum : 0.f;  // H - log of the sum
+  const float R = expf(lp - x.old);
+  const float open = -x.adv * R, clipped = -x.adv * fminf(fmaxf(R, a.lo), a.hi);
   float loss = fmaxf(open, clipped), c = open >= clipped ? open : 0.f;
   if (a.kl != 0.f) {
-    const float d = a.ref[r] - lp, k = expm1f(d);
+    const float d = x.ref - lp, k = expm1f(d);
     loss += a.kl * (k > 1e30f ? k : k - d);  // (k and d may both be infinite)
     c -= a.kl * k;
   }
   if (ENT) loss -= a.ent * (ln + excess);
   if (first) {
-    a.loss[r] = w * loss;
-    if (a.logprob) a.logprob[r] = lp;
-    if (ENT && a.entropy) a.entropy[r] = ln + excess;
+    a.loss[x.r] = empty ? 0.f : x.w * loss;
+    if (a.logprob) a.logprob[x.r] = lp;
+    if (ENT && a.entropy) a.entropy[x.r] = empty ? 0.f : ln + excess;
   }
-  if (!a.grad) return;
   RowGrad g;
-  g.ref = st.m;
+  g.ref = finite_ref(all.m);
   g.k = a.k;
-  g.token = t;
-  const float cw = w * c * a.inv_t, fw = ENT ? w * a.ent * a.inv_t : 0.f;
-  const float et = ex2((z - st.m) * a.k);
+  g.token = x.t;
+  const float cw = x.w * c * a.inv_t, fw = ENT ? x.w * a.ent * a.inv_t : 0.f;
+  const float et = ex2((x.z - g.ref) * a.k);
   g.A = (fw * excess - cw) / sum;
   g.B = fw * 0.693147181f / sum;
-  g.at_token = cw * (z == st.m ? st.s : sum - et) / sum;
+  g.at_token = cw * (x.z == all.m ? all.s : sum - et) / sum;
   if (ENT && et > 0.f) g.at_token += fw * (et / sum) * (lp + ln + excess);
-  grad_part<T, ENT>(g, row, grad, p, cache, cached);
+  if (empty) g.A = g.B = g.at_token = 0.f;
+  return g;
+}
+
+template <typename T, bool ENT, bool GRAD, int NT>
+__global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) policy_kernel(const __grid_constant__ PolicyArgs a) {
+  extern __shared__ uint4 smem[];
+  __shared__ RowGrad s_grad;
+  const int size = cluster_size(), rank = cluster_rank();
+  const Board<1> board = board_at<1>(smem, rank, size);
+  uint4* cache = smem + Board<1>::bytes(board.sets) / 16;
+  PolicyRow x;
+  x.r = blockIdx.x / size;
+  const T* row = static_cast<const T*>(a.logits) + x.r * a.ld;
+  T* grad = static_cast<T*>(a.grad) + x.r * a.gld;
+  const bool first = rank == 0 && threadIdx.x == 0;
+  pdl_wait();
+  x.t = a.tokens[x.r];
+  x.w = a.weight ? a.weight[x.r] : 1.f;
+  if (static_cast<uint32_t>(x.t) >= static_cast<uint32_t>(a.V) || x.w == 0.f) {
+    if (first) {
+      a.loss[x.r] = 0.f;
+      if (a.logprob) a.logprob[x.r] = 0.f;
+      if (a.entropy) a.entropy[x.r] = 0.f;
+    }
+    if (GRAD) zero_part(grad, a.V, rank, size);
+    return;
+  }
+  if (size > 1) cluster_arrive();
+  const RowPart p = row_part(row, a.V, rank, size);
+  const int cached = GRAD ? min(a.kept, p.count) : 0;
+  if (cached > 0)
+    fetch_part<T, NT>(row, p, cache, cached);
+  else
+    prefetch_part(row, p);
+  const float edge = edge_of(row, p);
+  if (threadIdx.x < 32) {
+    x.z = Vec<T>::widen1(row[x.t]);
+    x.old = a.old[x.r];
+    x.adv = a.adv[x.r];
+    x.ref = a.kl != 0.f ? a.ref[x.r] : 0.f;
+  }
+  RowStat st[1] = {stat_pass<T, ENT, NT>(row, p, cache, cached, a.k, NoMask{})};
+  if (p.edge_n) st[0] = merge(st[0], stat_of(edge), a.k);
+  st[0] = warp_merge<1, ENT>(st, a.k);
+  const float4 post[1] = {make_float4(st[0].m, st[0].s, st[0].u, 0.f)};
+  if (size > 1) cluster_wait();
+  board.post(post);
+  board.wait();
+  if (threadIdx.x < 32) {  // one warp forms the row's factors for all
+    const RowGrad g = policy_row<ENT>(a, x, board.template stat<ENT>(0, a.k), first);
+    if (GRAD && threadIdx.x == 0) s_grad = g;
+  }
+  if (!GRAD) return;
+  __syncthreads();
+  grad_pass<T, ENT, NT>(s_grad, GradRow<T>{row, grad, p, cache, cached, edge});
+}
+
+template <typename T, bool ENT, bool GRAD>
+cudaError_t launch(PolicyArgs& a, int rows, cudaStream_t stream) {
+  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 8, GRAD ? Board<1>::bytes(ROW_MAX_SETS) : -1);
+  a.kept = p.kept;
+  const int smem = Board<1>::bytes(p.size * p.threads / 32) + 16 * p.kept;
+  return p.threads == 512   ? launch_rows<policy_kernel<T, ENT, GRAD, 512>>(p, smem, rows, stream, a)
+         : p.threads == 256 ? launch_rows<policy_kernel<T, ENT, GRAD, 256>>(p, smem, rows, stream, a)
+                            : launch_rows<policy_kernel<T, ENT, GRAD, 128>>(p, smem, rows, stream, a);
 }
 
 template <typename T>
-cudaError_t launch(PolicyArgs& a, int rows, bool ent, cudaStream_t stream) {
-  const RowPlan p = plan_rows(rows, a.V, sizeof(T), a.grad ? ROW_SM_SMEM / 2 : 0);
-  a.cached = p.cached;
-  return ent ? launch_rows(policy_kernel<T, true>, p, rows, p.cached * 16, stream, a)
-             : launch_rows(policy_kernel<T, false>, p, rows, p.cached * 16, stream, a);
+cudaError_t launch(PolicyArgs& a, int rows, bool ent, cudaStream_t s) {
+  if (a.grad) return ent ? launch<T, true, true>(a, rows, s) : launch<T, false, true>(a, rows, s);
+  return ent ? launch<T, true, false>(a, rows, s) : launch<T, false, false>(a, rows, s);
 }
 
 }  // namespace
@@ -110,7 +143,7 @@ cudaError_t launch(PolicyArgs& a, int rows, bool ent, cudaStream_t stream) {
 using namespace tail;
 
 extern "C" int tail_policy_loss(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype, int64_t logits_ld,
-                                const int32_t* tokens, float temperature, const float* old_logprob,
+                                const int32_t* tokens, double temperature, const float* old_logprob,
                                 const float* advantage, const float* ref_logprob_opt, float clip_low, float clip_high,
                                 float kl_coef, float entropy_coef, const float* weight_opt, float* out_loss,
                                 float* out_logprob_opt, float* out_entropy_opt, void* out_grad_opt, int64_t grad_ld,

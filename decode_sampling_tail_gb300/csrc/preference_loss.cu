@@ -109,7 +109,7 @@ extern "C" int tail_preference_loss_workspace(int32_t rows, int64_t* bytes) {
 
 extern "C" int tail_preference_loss(int32_t rows, int32_t V, int32_t nseq, const void* logits, int32_t logits_dtype,
                                     int64_t logits_ld, const int32_t* tokens, const int32_t* cu_rows,
-                                    float temperature, const float* ref_logprob_opt, float beta, float label_smoothing,
+                                    double temperature, const float* ref_logprob_opt, float beta, float label_smoothing,
                                     float margin, int32_t average, const float* weight_opt, void* workspace,
                                     int64_t workspace_bytes, float* out_loss, float* out_seq_logprob_opt,
                                     void* out_grad_opt, int64_t grad_ld, void* stream) {
@@ -175,8 +175,7 @@ extern "C" int tail_preference_loss(int32_t rows, int32_t V, int32_t nseq, const
     a.margin = margin;
     a.average = average;
     a.grad = rows > 0 && out_grad_opt;
-    RowPlan p = {1, PAIR_THREADS, 0};
-    e = launch_rows(pair_kernel, p, pairs, 0, s, a);
+    e = launch_rows<pair_kernel>(RowPlan{1, PAIR_THREADS, 0}, 0, pairs, s, a);
   }
   if (e == cudaSuccess && rows > 0 && out_grad_opt) {
     SpreadArgs a = {};

@@ -8,14 +8,14 @@
 // it apart, -log1p(s) is a likely token's log-probability and s / (1 + s) its distance from 1 to a few
 // units of 2^-24 of themselves.  It costs a minimum a column: a running pair of maxima keeps the
 // larger of each two values, and the smaller one goes into the sum, so that every value but the
-// maxima enters exactly once.  The sums are taken 32 columns at a time against the maximum so far, so a change of
+// maxima enters exactly once.  The sums are taken 16 or 32 columns at a time against the maximum so far, so a change of
 // it costs one multiplication a batch.
 #pragma once
 
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <math.h>
 #include <stdint.h>
 
@@ -25,8 +25,9 @@
 namespace tail {
 
 constexpr int ROW_MAX_V = 1 << 20;      // columns
-constexpr int ROW_MAX_CLUSTER = 8;      // CTAs a row, the portable cluster size
-constexpr int ROW_SM_SMEM = 220 * 1024; // dynamic shared memory that the CTAs of an SM share out
+constexpr int ROW_BATCH = 4;            // vectors a thread takes at a time
+constexpr int ROW_MAX_CLUSTER = 8;      // CTAs a row, the portable size
+constexpr int ROW_SMEM = 224 * 1024;    // dynamic shared memory of a CTA at most
 
 // ---------------------------------------------------------------- arithmetic
 
@@ -258,15 +259,38 @@ struct RowAcc {
   }
 };
 
-__device__ __forceinline__ RowStat warp_merge(RowStat r, float k) {
+__device__ __forceinline__ float warp_max(float v) {  // NaN when any is
+  float y;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(v));
+  return y;
+}
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    RowStat b;
-    b.m = __shfl_xor_sync(0xffffffffu, r.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, r.s, o);
-    b.u = __shfl_xor_sync(0xffffffffu, r.u, o);
-    r = merge(r, b, k);
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The statistics of J sets a lane, the same bits in every lane: the sets are brought to the common maximum once,
+// and the first set that holds it gives the instance that stays out of the sum.
+template <int J, bool ENT>
+__device__ __forceinline__ RowStat warp_merge(const RowStat (&v)[J], float k) {
+  float mx = v[0].m;
+#pragma unroll
+  for (int j = 1; j < J; ++j) mx = max_nan(mx, v[j].m);
+  RowStat r{warp_max(mx), 0.f, 0.f};
+  const float ref = finite_ref(r.m);
+  bool found = false;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const uint32_t at = __ballot_sync(0xffffffffu, v[j].m == r.m);
+    const bool out = !found && at && static_cast<int>(threadIdx.x & 31) == __ffs(at) - 1;
+    found = found || at;
+    const float d = dist(v[j].m, ref, k), c = ex2(d);
+    r.s += c * (v[j].s + (out ? 0.f : 1.f));
+    if (ENT) r.u += c * (v[j].u + d * (1.f + v[j].s));
   }
+  r.s = warp_sum(r.s);
+  if (ENT) r.u = warp_sum(r.u);
   return r;
 }
 
@@ -341,45 +365,69 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// Writes a word to the same shared variable of CTA `rank` of the cluster.
-__device__ __forceinline__ void store_remote(float* mine, int rank, float v) {
+// Writes four words to the same shared variable of CTA `rank` of the cluster.
+__device__ __forceinline__ void store_remote(float4* mine, int rank, float4 v) {
   uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
 }
 
-struct StatShared {
-  RowStat warp[32];
-  RowStat cta[ROW_MAX_CLUSTER];
+// Where the warps of a cluster's CTAs leave W words of four each for all of them.
+constexpr int ROW_MAX_SETS = 128;  // warps of a cluster: 8 CTAs of 16
+template <int W>
+struct Board {
+  float4* at;  // [W][sets] in shared memory
+  int sets, rank, size;
+
+  static __host__ __device__ constexpr int bytes(int sets) { return W * sets * static_cast<int>(sizeof(float4)); }
+
+  // Lanes 0 .. size - 1 of each warp write to a CTA each; then the CTA arrives.  (All CTAs have started: the cluster has
+  // been synchronised before.)
+  __device__ __forceinline__ void post(const float4 (&v)[W]) const {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float4* mine = at + (sets / size) * rank + warp;
+    if (size == 1) {
+      if (lane == 0)
+#pragma unroll
+        for (int w = 0; w < W; ++w) mine[w * sets] = v[w];
+      return;
+    }
+    if (lane < size)
+#pragma unroll
+      for (int w = 0; w < W; ++w) store_remote(mine + w * sets, lane, v[w]);
+    __syncwarp();
+    cluster_arrive();
+  }
+  __device__ __forceinline__ void wait() const {
+    if (size == 1)
+      __syncthreads();
+    else
+      cluster_wait();
+  }
+  __device__ __forceinline__ float4 get(int w, int i) const {
+    return i < sets ? at[w * sets + i] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  }
+  template <int J, bool ENT>
+  __device__ __forceinline__ RowStat stat_of_sets(int w, float k) const {
+    RowStat v[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const float4 x = get(w, j * 32 + static_cast<int>(threadIdx.x & 31));
+      v[j] = RowStat{x.x, x.y, x.z};
+    }
+    return warp_merge<J, ENT>(v, k);
+  }
+  // The cluster's statistics from its warps' (word w: maximum, s, u), the same bits in every lane and CTA.
+  template <bool ENT>
+  __device__ __forceinline__ RowStat stat(int w, float k) const {
+    return sets <= 32 ? stat_of_sets<1, ENT>(w, k) : stat_of_sets<ROW_MAX_SETS / 32, ENT>(w, k);
+  }
 };
 
-// The statistics of all the cluster's threads, the same bits in each.  A cluster of more than one CTA has
-// called cluster_arrive() once before: a CTA's shared memory may be written only when it has started.
-__device__ __forceinline__ RowStat cluster_merge(RowStat r, float k, StatShared& sh, int rank, int size) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarp = blockDim.x >> 5;
-  r = warp_merge(r, k);
-  if (lane == 0) sh.warp[warp] = r;
-  __syncthreads();
-  if (warp == 0) {
-    r = lane < nwarp ? sh.warp[lane] : no_stat();
-    r = warp_merge(r, k);
-  }
-  if (size == 1) {
-    if (threadIdx.x == 0) sh.cta[0] = r;
-    __syncthreads();
-    return sh.cta[0];
-  }
-  cluster_wait();
-  if (warp == 0 && lane < size) {
-    store_remote(&sh.cta[rank].m, lane, r.m);
-    store_remote(&sh.cta[rank].s, lane, r.s);
-    store_remote(&sh.cta[rank].u, lane, r.u);
-  }
-  cluster_arrive();
-  cluster_wait();
-  r = sh.cta[0];
-  for (int i = 1; i < size; ++i) r = merge(r, sh.cta[i], k);
-  return r;
+template <int W>
+__device__ __forceinline__ Board<W> board_at(void* smem, int rank, int size) {
+  return Board<W>{static_cast<float4*>(smem), size * static_cast<int>(blockDim.x >> 5), rank, size};
 }
 
 // ---------------------------------------------------------------- gradient
@@ -412,15 +460,6 @@ __device__ __forceinline__ uint4 grad_vec(const RowGrad& g, const uint4& z) {
   return out;
 }
 
-// Puts the token's own value into the vector that holds it.
-template <typename T>
-__device__ __forceinline__ void put(uint4& v, int i, float x) {
-  T* p = reinterpret_cast<T*>(&v);
-#pragma unroll
-  for (int j = 0; j < Vec<T>::N; ++j)
-    if (j == i) p[j] = Vec<T>::narrow1(x);
-}
-
 // Whether a row's gradient lies on the same whole vectors as its logits.
 __device__ __forceinline__ bool same_phase(const void* a, const void* b) {
   return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
@@ -435,133 +474,219 @@ __device__ __forceinline__ void zero_part(T* grad, int V, int rank, int size) {
   if (p.edge_n) grad[p.edge_lo] = Vec<T>::narrow1(0.f);
 }
 
-// The gradient over this CTA's part of a row.  The first `cached` of its vectors are in shared memory
-// (`cache`, written by the thread that reads them here, or by others before a barrier).  Rows whose gradient lies elsewhere
-// in its 16-byte vectors are written column by column.
-template <typename T, bool ENT>
-__device__ __forceinline__ void grad_part(const RowGrad& g, const T* row, T* grad, const RowPart& p, const uint4* cache,
-                                          int cached) {
-  constexpr int N = Vec<T>::N;
-  const int tid = threadIdx.x, nt = blockDim.x;
-  const int body = p.head + p.first * N;  // the part's first column in a vector
-  if (same_phase(row, grad)) {
-    const uint4* in = reinterpret_cast<const uint4*>(row + p.head) + p.first;
-    uint4* out = reinterpret_cast<uint4*>(grad + p.head) + p.first;
-    const int tv = g.token >= body ? (g.token - body) / N : -1;
-    constexpr int U = 4;
-    for (int i0 = tid; i0 < p.count; i0 += U * nt) {
-      uint4 z[U];
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int i = i0 + j * nt;
-        if (i < p.count) z[j] = i < cached ? cache[i] : __ldcg(in + i);
-      }
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int i = i0 + j * nt;
-        if (i >= p.count) continue;
-        uint4 o = grad_vec<T, ENT>(g, z[j]);
-        if (i == tv) put<T>(o, g.token - body - tv * N, g.at_token);
-        __stcs(out + i, o);
-      }
-    }
-  } else {
-    const T* c = reinterpret_cast<const T*>(cache);
-    for (int i = tid; i < p.count * N; i += nt) {
-      const T z = i < cached * N ? c[i] : row[body + i];
-      grad[body + i] = Vec<T>::narrow1(body + i == g.token ? g.at_token : grad1<T, ENT>(g, z));
-    }
-  }
-  if (p.edge_n)
-    grad[p.edge_lo] = Vec<T>::narrow1(p.edge_lo == g.token ? g.at_token : grad1<T, ENT>(g, row[p.edge_lo]));
-}
-
-// ---------------------------------------------------------------- statistics of a part
-
-// Statistics over this CTA's part, straight from memory.
-template <typename T, bool ENT>
-__device__ __forceinline__ RowStat stat_part(const T* row, const RowPart& p, int from, float k, RowAcc<T, ENT>& acc) {
-  constexpr int U = 32 / Vec<T>::N;  // 32 columns a batch
-  const uint4* in = reinterpret_cast<const uint4*>(row + p.head) + p.first;
-  for (int i0 = from + threadIdx.x; i0 < p.count; i0 += U * blockDim.x) {
-    uint4 v[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int i = i0 + j * static_cast<int>(blockDim.x);
-      v[j] = i < p.count ? __ldcg(in + i) : Vec<T>::fill();
-    }
-    acc.batch(v, k);
-  }
-  RowStat r = acc.done(k);
-  if (p.edge_n) r = merge(r, stat_of(Vec<T>::widen1(row[p.edge_lo])), k);
-  return r;
-}
-
-// Requests the part's first `cached` vectors into shared memory, each by the thread that uses it, as one group a batch of
-// U vectors a thread; stat_cached takes them batch by batch as they arrive.
+// This thread's single column of a part, if it has one.
 template <typename T>
+__device__ __forceinline__ float edge_of(const T* row, const RowPart& p) {
+  return p.edge_n ? Vec<T>::widen1(row[p.edge_lo]) : -INFINITY;
+}
+
+template <typename T>
+__device__ __forceinline__ const uint4* part_vectors(const T* row, const RowPart& p) {
+  return reinterpret_cast<const uint4*>(row + p.head) + p.first;
+}
+
+// ---------------------------------------------------------------- passes over a part
+// A thread takes vectors tid, tid + NT, .. of the part, ROW_BATCH of them at a time; in all passes the same ones, so
+// that its copies into shared memory need no barrier.  Whole batches run without a bound in sight: with one, and a
+// token to look for, a vector cost more instructions than its columns' arithmetic.
+
+__host__ __device__ constexpr int batches(int n, int nt) { return (n + ROW_BATCH * nt - 1) / (ROW_BATCH * nt); }
+
+// Requests the part's first `cached` vectors into shared memory, each by the thread that takes it, one group a batch.
+template <typename T, int NT>
 __device__ __forceinline__ void fetch_part(const T* row, const RowPart& p, uint4* cache, int cached) {
-  constexpr int U = 32 / Vec<T>::N;
-  const uint4* in = reinterpret_cast<const uint4*>(row + p.head) + p.first;
-  const int nt = blockDim.x;
-  for (int b = 0; b < cached; b += U * nt) {
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int i = b + j * nt + static_cast<int>(threadIdx.x);
-      if (i < cached) copy_async16(cache + i, in + i);
-    }
+  const uint4* in = part_vectors(row, p);
+  for (int b = 0; b < batches(cached, NT); ++b) {
+    const int end = min((b + 1) * ROW_BATCH * NT, cached);
+    for (int i = b * ROW_BATCH * NT + static_cast<int>(threadIdx.x); i < end; i += NT) copy_async16(cache + i, in + i);
     copy_commit();
   }
 }
 
-// `mask(i)`: the bits of vector i's columns that count as -inf.
-template <typename T, bool ENT, typename Mask>
-__device__ __forceinline__ RowStat stat_cached(const T* row, const RowPart& p, const uint4* cache, int cached, float k,
-                                               Mask mask) {
-  constexpr int U = 32 / Vec<T>::N;
-  const uint4* in = reinterpret_cast<const uint4*>(row + p.head) + p.first;
-  const int nt = blockDim.x;
-  RowAcc<T, ENT> acc;
-  int left = (cached + U * nt - 1) / (U * nt);
-  for (int b = 0; b < p.count; b += U * nt) {
-    if (left > 0) copy_wait(--left);
+// Has the whole part brought into L2, by one instruction of one thread: the loads behind it then wait for L2 alone.
+template <typename T>
+__device__ __forceinline__ void prefetch_part(const T* row, const RowPart& p) {
+  if (threadIdx.x == 0 && p.count > 0)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(part_vectors(row, p)), "r"(p.count * 16) : "memory");
+}
+
+// Columns that count as -inf: flags(b) of this thread's batch b has a bit a vector with any, bits(i) the columns of
+// vector i.
+struct NoMask {
+  __device__ __forceinline__ uint32_t flags(int) const { return 0; }
+  __device__ __forceinline__ uint32_t bits(int) const { return 0; }
+};
+
+template <typename T, bool ENT, int NT, typename Mask>
+__device__ __forceinline__ void stat_batch(RowAcc<T, ENT>& acc, uint4 (&v)[ROW_BATCH], int b, float k,
+                                           const Mask& mask) {
+  const uint32_t f = mask.flags(b);
+  if (f)
+#pragma unroll
+    for (int j = 0; j < ROW_BATCH; ++j)
+      if (f & (1u << j))
+        Vec<T>::mask(v[j], mask.bits((b * ROW_BATCH + j) * NT + static_cast<int>(threadIdx.x)));
+  acc.batch(v, k);
+}
+
+// What lies behind the first b batches: single vectors of the last batch that is kept, then what comes from memory.
+template <typename T, bool ENT, int NT, typename Mask>
+__device__ __forceinline__ void stat_tail(RowAcc<T, ENT>& acc, const T* row, const RowPart& p, const uint4* cache,
+                                          int cached, int b, float k, const Mask& mask) {
+  constexpr int U = ROW_BATCH;
+  const int tid = threadIdx.x, whole = p.count / (U * NT);
+  const auto single = [&](const uint4& z, int i) {
+    uint4 v[1] = {z};
+    const uint32_t m = mask.bits(i);
+    if (m) Vec<T>::mask(v[0], m);
+    acc.batch(v, k);
+  };
+  for (int i = b * U * NT + tid; i < cached; i += NT) single(cache[i], i);
+  if (cached == p.count) return;
+  const uint4* in = part_vectors(row, p);
+  for (b = max(b, cached / (U * NT)); b < whole; ++b) {
     uint4 v[U];
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int i = b + j * nt + static_cast<int>(threadIdx.x);
-      v[j] = i < cached ? cache[i] : i < p.count ? __ldcg(in + i) : Vec<T>::fill();
-      const uint32_t bits = i < p.count ? mask(i) : 0;
-      if (bits) Vec<T>::mask(v[j], bits);
-    }
-    acc.batch(v, k);
+    for (int j = 0; j < U; ++j) v[j] = __ldcg(in + (b * U + j) * NT + tid);
+    stat_batch<T, ENT, NT>(acc, v, b, k, mask);
   }
+  for (int i = b * U * NT + tid; i < p.count; i += NT) single(__ldcg(in + i), i);
+}
+
+// Statistics over this CTA's part, its first `cached` vectors from shared memory as their copies arrive (the thread has
+// no other copies under way), the others from memory.  Without the thread's single column.
+template <typename T, bool ENT, int NT, typename Mask>
+__device__ __forceinline__ RowStat stat_pass(const T* row, const RowPart& p, const uint4* cache, int cached, float k,
+                                             const Mask& mask) {
+  constexpr int U = ROW_BATCH;
+  RowAcc<T, ENT> acc;
+  int left = batches(cached, NT), b = 0;
+  const uint4* c = cache + threadIdx.x;
+  for (; b < cached / (U * NT); ++b, c += U * NT) {
+    copy_wait(--left);
+    uint4 v[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) v[j] = c[j * NT];
+    stat_batch<T, ENT, NT>(acc, v, b, k, mask);
+  }
+  if (left > 0) copy_wait(0);
+  stat_tail<T, ENT, NT>(acc, row, p, cache, cached, b, k, mask);
   return acc.done(k);
+}
+
+template <typename T, bool ENT, int NT>
+__device__ __forceinline__ void grad_batch(const RowGrad& g, const uint4* c, uint4* out) {
+  uint4 z[ROW_BATCH];
+#pragma unroll
+  for (int j = 0; j < ROW_BATCH; ++j) z[j] = c[j * NT];
+#pragma unroll
+  for (int j = 0; j < ROW_BATCH; ++j) __stcs(out + j * NT, grad_vec<T, ENT>(g, z[j]));
+}
+
+// A row whose gradient is written, and where it is kept.
+template <typename T>
+struct GradRow {
+  const T* row;
+  T* grad;
+  RowPart p;
+  uint4* cache;
+  int cached;
+  float edge;
+};
+
+// The gradient behind the first b batches, with the token's column and the single one.  Rows whose gradient lies elsewhere
+// in its 16-byte vectors are written column by column (b is 0); then what the cache holds must be visible to
+// all threads.
+template <typename T, bool ENT, int NT>
+__device__ __forceinline__ void grad_tail(const RowGrad& g, const GradRow<T>& r, int b) {
+  constexpr int N = Vec<T>::N, U = ROW_BATCH;
+  const int tid = threadIdx.x;
+  const RowPart& p = r.p;
+  const int body = p.head + p.first * N;  // the part's first column in a vector
+  if (same_phase(r.row, r.grad)) {
+    uint4* out = reinterpret_cast<uint4*>(r.grad + p.head) + p.first;
+    for (int i = b * U * NT + tid; i < r.cached; i += NT) __stcs(out + i, grad_vec<T, ENT>(g, r.cache[i]));
+    if (r.cached < p.count) {
+      const uint4* in = part_vectors(r.row, p);
+      for (b = max(b, r.cached / (U * NT)); b < p.count / (U * NT); ++b) {
+        uint4 z[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) z[j] = __ldcg(in + (b * U + j) * NT + tid);
+#pragma unroll
+        for (int j = 0; j < U; ++j) __stcs(out + (b * U + j) * NT + tid, grad_vec<T, ENT>(g, z[j]));
+      }
+      for (int i = b * U * NT + tid; i < p.count; i += NT) __stcs(out + i, grad_vec<T, ENT>(g, __ldcg(in + i)));
+    }
+    // the token's column, by the thread that has written its vector
+    const int tv = g.token >= body ? (g.token - body) / N : -1;
+    if (tv >= 0 && tv < p.count && tv % NT == tid) r.grad[g.token] = Vec<T>::narrow1(g.at_token);
+  } else {
+    const T* c = reinterpret_cast<const T*>(r.cache);
+    for (int i = tid; i < p.count * N; i += NT) {
+      const T z = i < r.cached * N ? c[i] : r.row[body + i];
+      r.grad[body + i] = Vec<T>::narrow1(body + i == g.token ? g.at_token : grad1<T, ENT>(g, z));
+    }
+  }
+  if (p.edge_n)
+    r.grad[p.edge_lo] =
+        Vec<T>::narrow1(p.edge_lo == g.token ? g.at_token : grad1<T, ENT>(g, Vec<T>::narrow1(r.edge)));
+}
+
+// The gradient over this CTA's part of a row.
+template <typename T, bool ENT, int NT>
+__device__ __forceinline__ void grad_pass(const RowGrad& g, const GradRow<T>& r) {
+  constexpr int U = ROW_BATCH;
+  int b = 0;
+  if (same_phase(r.row, r.grad)) {
+    const uint4* c = r.cache + threadIdx.x;
+    uint4* out = reinterpret_cast<uint4*>(r.grad + r.p.head) + r.p.first + threadIdx.x;
+    for (; b < r.cached / (U * NT); ++b, c += U * NT, out += U * NT) grad_batch<T, ENT, NT>(g, c, out);
+  }
+  grad_tail<T, ENT, NT>(g, r, b);
 }
 
 // ---------------------------------------------------------------- host side
 
+// How a row is split, and whether its parts stay in shared memory between the passes.
 struct RowPlan {
   int size;     // CTAs a row
-  int threads;
-  int cached;   // vectors of a part that shared memory holds
+  int threads;  // 512, 256 or 128, 1024 of them a SM
+  int kept;     // vectors of a part that shared memory holds
 };
 
-// How a row is split.  `fit`: bytes of the row that one CTA should hold at most (0: the row is not kept).
-inline RowPlan plan_rows(int64_t rows, int V, int es, int64_t fit) {
-  RowPlan p;
-  const int64_t vecs = (static_cast<int64_t>(V) * es + 15) / 16;
-  p.size = 1;
-  while (p.size < ROW_MAX_CLUSTER && fit > 0 && (vecs + p.size - 1) / p.size * 16 > fit) p.size *= 2;
-  // few rows: spread each over more SMs, as long as a part still has two vectors a thread
-  while (p.size < ROW_MAX_CLUSTER && rows * p.size * 2 <= 2 * 152 && vecs / (2 * p.size) >= 1024) p.size *= 2;
-  const int64_t part = (vecs + p.size - 1) / p.size;
-  p.threads = part >= 2048 ? 512 : part >= 512 ? 256 : part >= 128 ? 128 : 64;
-  p.cached = fit > 0 ? static_cast<int>(part * 16 <= fit ? part : fit / 16) : 0;
+constexpr int ROW_SMS = 152;
+constexpr int ROW_SM_THREADS = 1024;
+
+inline int64_t row_vectors(int V, int es) { return (static_cast<int64_t>(V) * es + 15) / 16; }
+inline int64_t part_of(int64_t vecs, int size) { return (vecs + size - 1) / size; }
+
+// Bytes of rows that may be in flight at once.  What a first pass has read is there for the second as long as it
+// fits L2 beside the gradient that is written.
+constexpr int64_t ROW_FLIGHT = 62 << 20;
+
+// `least`: vectors a thread that a part keeps when rows are split to fill the device; `beside`: bytes of shared memory of a
+// CTA beside what is kept (negative: nothing is kept).
+inline RowPlan plan_rows(int64_t rows, int V, int es, int least, int beside) {
+  const int64_t vecs = row_vectors(V, es);
+  RowPlan p = {1, vecs >= 1024 ? 256 : 128, 0};
+  const int slots = ROW_SMS * (ROW_SM_THREADS / p.threads);
+  for (; p.size < ROW_MAX_CLUSTER; p.size *= 2) {
+    const int64_t part = vecs / (2 * p.size);
+    const bool spills = slots / p.size * vecs * 16 > ROW_FLIGHT && rows * p.size > slots / 2;
+    const bool few = rows * p.size < 2 * ROW_SMS && part >= p.threads;
+    const bool uneven = rows * p.size < 2 * slots && part >= least * p.threads;
+    if (!spills && !few && !uneven) break;
+  }
+  const int64_t part = part_of(vecs, p.size), a_sm = (rows * p.size + ROW_SMS - 1) / ROW_SMS;
+  if (beside >= 0 && a_sm * (part * 16 + beside + 2048) <= ROW_SMEM) p.kept = static_cast<int>(part);
   return p;
 }
 
-template <typename A>
-cudaError_t launch_rows(void (*kernel)(A), const RowPlan& p, int64_t rows, int smem, cudaStream_t stream, const A& a) {
+// A cluster a row.  Shared memory beyond the default is asked for once a device.
+template <auto KERNEL, typename A>
+cudaError_t launch_rows(const RowPlan& p, int smem, int64_t rows, cudaStream_t stream, const A& a) {
+  constexpr int DEVICES = 16;
+  static std::atomic<bool> asked[DEVICES];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * p.size));
   cfg.blockDim = dim3(p.threads);
@@ -576,11 +701,16 @@ cudaError_t launch_rows(void (*kernel)(A), const RowPlan& p, int64_t rows, int s
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (smem > 48 * 1024 - 2048) {  // with the static part; idempotent, per device
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (smem > 32 * 1024) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= DEVICES || !asked[dev].load(std::memory_order_acquire))) {
+      e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, ROW_SMEM);
+      if (e == cudaSuccess && dev < DEVICES) asked[dev].store(true, std::memory_order_release);
+    }
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return cudaLaunchKernelEx(&cfg, KERNEL, a);
 }
 
 // Bytes from a matrix's first element to its last.

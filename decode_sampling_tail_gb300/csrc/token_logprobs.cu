@@ -14,10 +14,11 @@ namespace tail {
 
 namespace {
 
-template <typename T, bool ENT>
-__global__ void __launch_bounds__(512) score_kernel(const __grid_constant__ ScoreArgs a) {
-  __shared__ StatShared sh;
+template <typename T, bool ENT, int NT>
+__global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) score_kernel(const __grid_constant__ ScoreArgs a) {
+  extern __shared__ uint4 smem[];
   const int size = cluster_size(), rank = cluster_rank();
+  const Board<1> board = board_at<1>(smem, rank, size);
   const int64_t r = blockIdx.x / size;
   pdl_wait();
   int t = a.tokens[r];
@@ -36,60 +37,75 @@ __global__ void __launch_bounds__(512) score_kernel(const __grid_constant__ Scor
   }
   if (size > 1) cluster_arrive();
   const T* row = static_cast<const T*>(a.logits) + r * a.ld;
-  const float z = Vec<T>::widen1(row[t]);
+  const float z = first ? Vec<T>::widen1(row[t]) : 0.f;
   const RowPart p = row_part(row, a.V, rank, size);
-  RowAcc<T, ENT> acc;
-  const RowStat st = cluster_merge(stat_part(row, p, 0, a.k, acc), a.k, sh, rank, size);
+  prefetch_part(row, p);
+  RowStat st[1] = {stat_pass<T, ENT, NT>(row, p, nullptr, 0, a.k, NoMask{})};
+  st[0] = merge(st[0], stat_of(edge_of(row, p)), a.k);
+  st[0] = warp_merge<1, ENT>(st, a.k);
+  const float4 post[1] = {make_float4(st[0].m, st[0].s, st[0].u, 0.f)};
+  if (size > 1) cluster_wait();
+  board.post(post);
+  board.wait();
+  if (rank != 0 || threadIdx.x >= 32) return;
+  const RowStat all = board.template stat<ENT>(0, a.k);
   if (!first) return;
-  const float ln = log1pf(st.s);
-  const bool empty = st.m == -INFINITY;
-  const float lp = empty ? -INFINITY : (z - st.m) * a.inv_t - ln;
-  if (a.score) a.score[r] = RowScore{st.m, st.s, empty ? 0.f : lp, empty ? -1 : t};
+  const float ln = log1pf(all.s);
+  const bool empty = all.m == -INFINITY;
+  const float lp = empty ? -INFINITY : (z - all.m) * a.inv_t - ln;
+  if (a.score) a.score[r] = RowScore{all.m, all.s, empty ? 0.f : lp, empty ? -1 : t};
   if (a.logprob) a.logprob[r] = lp;
-  if (a.lse) a.lse[r] = empty ? -INFINITY : st.m * a.inv_t + ln;
-  if (ENT) a.entropy[r] = empty ? 0.f : ln - 0.693147181f * st.u / (1.f + st.s);
+  if (a.lse) a.lse[r] = empty ? -INFINITY : all.m * a.inv_t + ln;
+  if (ENT) a.entropy[r] = empty ? 0.f : ln - 0.693147181f * all.u / (1.f + all.s);
 }
 
+// The factors of a row's gradient; false: there is none.
 template <typename T, bool ENT, bool SCORED>
-__global__ void __launch_bounds__(512) spread_kernel(const __grid_constant__ SpreadArgs a) {
-  const int size = cluster_size(), rank = cluster_rank();
-  const int64_t r = blockIdx.x / size;
-  pdl_wait();
-  T* grad = static_cast<T*>(a.grad) + r * a.gld;
-  const T* row = static_cast<const T*>(a.logits) + r * a.ld;
-  RowGrad g;
+__device__ __forceinline__ bool spread_factors(const SpreadArgs& a, int64_t r, const T* row, RowGrad& g) {
   g.k = a.k;
-  bool live;
+  g.B = 0.f;
   if (SCORED) {
     const RowScore sc = a.score[r];
     const float c = a.coef[r] * a.inv_t;
-    live = sc.token >= 0 && c != 0.f;
     g.token = sc.token;
+    if (sc.token < 0 || c == 0.f) return false;
     g.ref = sc.m;
     g.A = -c / (1.f + sc.s);
-    g.B = 0.f;
-    if (live) {
-      const float z = Vec<T>::widen1(row[sc.token]);
-      g.at_token = c * (z == sc.m ? sc.s : 1.f + sc.s - ex2((z - sc.m) * a.k)) / (1.f + sc.s);
-    }
-  } else {
-    g.token = a.tokens[r];
-    const float da = a.a[r] * a.inv_t, db = ENT ? a.b[r] * a.inv_t : 0.f, lse = a.lse[r];
-    live = static_cast<uint32_t>(g.token) < static_cast<uint32_t>(a.V) && (da != 0.f || db != 0.f) && lse != -INFINITY;
-    if (live) {
-      g.ref = static_cast<float>(lse * a.t64);
-      const float rest = static_cast<float>((g.ref * a.inv_t64 - lse) * LOG2E);  // log2 p at z = ref
-      const float f = exp2f(rest), H = ENT ? a.entropy[r] : 0.f;
-      g.A = f * (-da - (ENT ? db * (0.693147181f * rest + H) : 0.f));
-      g.B = -f * db * 0.693147181f;
-      const float l = static_cast<float>(Vec<T>::widen1(row[g.token]) * a.inv_t64 - lse);
-      g.at_token = -da * expm1f(l);
-      if (ENT && l > -INFINITY) g.at_token -= db * expf(l) * (l + H);
-    }
+    const float z = Vec<T>::widen1(row[sc.token]);
+    g.at_token = c * (z == sc.m ? sc.s : 1.f + sc.s - ex2((z - sc.m) * a.k)) / (1.f + sc.s);
+    return true;
   }
-  if (!live) {
-    zero_part(grad, a.V, rank, size);
-    return;
+  g.token = a.tokens[r];
+  const float da = a.a[r] * a.inv_t, db = ENT ? a.b[r] * a.inv_t : 0.f, lse = a.lse[r];
+  if (static_cast<uint32_t>(g.token) >= static_cast<uint32_t>(a.V) || (da == 0.f && db == 0.f) || lse == -INFINITY)
+    return false;
+  g.ref = static_cast<float>(lse * a.t64);
+  const float rest = static_cast<float>((g.ref * a.inv_t64 - lse) * LOG2E);  // log2 p at z = ref
+  const float f = exp2f(rest), H = ENT ? a.entropy[r] : 0.f;
+  g.A = f * (-da - (ENT ? db * (0.693147181f * rest + H) : 0.f));
+  g.B = -f * db * 0.693147181f;
+  const float l = static_cast<float>(Vec<T>::widen1(row[g.token]) * a.inv_t64 - lse);
+  g.at_token = -da * expm1f(l);
+  if (ENT && l > -INFINITY) g.at_token -= db * expf(l) * (l + H);
+  return true;
+}
+
+template <typename T, bool ENT, bool SCORED, int NT>
+__global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) spread_kernel(const __grid_constant__ SpreadArgs a) {
+  __shared__ RowGrad s_grad;
+  __shared__ bool s_live;
+  const int size = cluster_size(), rank = cluster_rank();
+  // after a pass over all rows the last of them are still in L2
+  const int64_t r = (SCORED ? gridDim.x - 1 - blockIdx.x : blockIdx.x) / size;
+  const T* row = static_cast<const T*>(a.logits) + r * a.ld;
+  T* grad = static_cast<T*>(a.grad) + r * a.gld;
+  const RowPart p = row_part(row, a.V, rank, size);
+  pdl_wait();
+  if (threadIdx.x == 0) {  // one thread: the 64-bit pipe is narrow
+    RowGrad g;
+    s_live = spread_factors<T, ENT, SCORED>(a, r, row, g);
+    s_grad = g;
+    if (s_live) prefetch_part(row, p);
   }
   // in place, another CTA of the row may write the token's column once all have read it
   if (size > 1) {
@@ -98,22 +114,38 @@ __global__ void __launch_bounds__(512) spread_kernel(const __grid_constant__ Spr
   } else {
     __syncthreads();
   }
-  grad_part<T, ENT>(g, row, grad, row_part(row, a.V, rank, size), nullptr, 0);
+  if (!s_live) {
+    zero_part(grad, a.V, rank, size);
+    return;
+  }
+  const RowGrad g = s_grad;
+  grad_pass<T, ENT, NT>(g, GradRow<T>{row, grad, p, nullptr, 0, edge_of(row, p)});
 }
 
+template <typename T, bool ENT>
+cudaError_t scores(const ScoreArgs& a, int rows, cudaStream_t stream) {
+  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 8, -1);
+  const int smem = Board<1>::bytes(p.size * p.threads / 32);
+  return p.threads == 512   ? launch_rows<score_kernel<T, ENT, 512>>(p, smem, rows, stream, a)
+         : p.threads == 256 ? launch_rows<score_kernel<T, ENT, 256>>(p, smem, rows, stream, a)
+                            : launch_rows<score_kernel<T, ENT, 128>>(p, smem, rows, stream, a);
+}
 template <typename T>
 cudaError_t scores(const ScoreArgs& a, int rows, cudaStream_t stream) {
-  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 0);
-  return a.entropy ? launch_rows(score_kernel<T, true>, p, rows, 0, stream, a)
-                   : launch_rows(score_kernel<T, false>, p, rows, 0, stream, a);
+  return a.entropy ? scores<T, true>(a, rows, stream) : scores<T, false>(a, rows, stream);
 }
 
+template <typename T, bool ENT, bool SCORED>
+cudaError_t spread(const SpreadArgs& a, int rows, cudaStream_t stream) {
+  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 8, -1);
+  return p.threads == 512   ? launch_rows<spread_kernel<T, ENT, SCORED, 512>>(p, 0, rows, stream, a)
+         : p.threads == 256 ? launch_rows<spread_kernel<T, ENT, SCORED, 256>>(p, 0, rows, stream, a)
+                            : launch_rows<spread_kernel<T, ENT, SCORED, 128>>(p, 0, rows, stream, a);
+}
 template <typename T>
 cudaError_t spread(const SpreadArgs& a, int rows, cudaStream_t stream) {
-  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 0);
-  if (a.score) return launch_rows(spread_kernel<T, false, true>, p, rows, 0, stream, a);
-  return a.b ? launch_rows(spread_kernel<T, true, false>, p, rows, 0, stream, a)
-             : launch_rows(spread_kernel<T, false, false>, p, rows, 0, stream, a);
+  if (a.score) return spread<T, false, true>(a, rows, stream);
+  return a.b ? spread<T, true, false>(a, rows, stream) : spread<T, false, false>(a, rows, stream);
 }
 
 const char* LIMITS = "more than 1048576 columns or 16777216 rows";
@@ -137,7 +169,7 @@ cudaError_t launch_spread(const SpreadArgs& a, int dtype, int rows, cudaStream_t
 using namespace tail;
 
 extern "C" int tail_token_logprobs(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype,
-                                   int64_t logits_ld, const int32_t* tokens, float temperature,
+                                   int64_t logits_ld, const int32_t* tokens, double temperature,
                                    float* out_logprob_opt, float* out_lse_opt, float* out_entropy_opt, void* stream) {
   const int rc = sizes_ok(rows, V, LIMITS);
   if (rc) return rc;
@@ -165,7 +197,7 @@ extern "C" int tail_token_logprobs(int32_t rows, int32_t V, const void* logits, 
 }
 
 extern "C" int tail_token_logprobs_grad(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype,
-                                        int64_t logits_ld, const int32_t* tokens, float temperature, const float* lse,
+                                        int64_t logits_ld, const int32_t* tokens, double temperature, const float* lse,
                                         const float* d_logprob, const float* d_entropy_opt, const float* entropy_opt,
                                         void* out_grad, int64_t grad_ld, void* stream) {
   const int rc = sizes_ok(rows, V, LIMITS);

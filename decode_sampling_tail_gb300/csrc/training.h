@@ -84,7 +84,7 @@ inline bool matrix_ok(const void* p, int dtype, int64_t ld, int V) {
 }
 
 // Temperatures whose inverse and log2(e) / T are ordinary fp32 numbers.
-inline bool temperature_ok(float t) { return t >= 0x1p-64f && t <= 0x1p64f; }
+inline bool temperature_ok(double t) { return t >= 0x1p-64 && t <= 0x1p64; }
 
 inline int sizes_ok(int rows, int V, const char* what) {
   if (rows < 0 || V < 1) return TAIL_ERR_INVALID_ARG;

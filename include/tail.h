@@ -598,7 +598,7 @@ const char* tail_last_error(void);
  *   tokens         [rows] int32: the token that row r's logits predicted.  A row whose token is outside [0, V)
  *                  (-1: a prompt position, padding) is ignored: its results are 0, its gradient is
  *                  zeros, its logits are not read.
- *   temperature    T, from 2^-64 to 2^64.
+ *   temperature    T, from 2^-64 to 2^64 (a double: a rounded T would shift every z / T).
  *   weight_opt     [rows] (or [pairs]) fp32 factors of the losses, NULL: 1.  A row (pair) of weight 0 is
  *                  left out: loss and gradient 0, whatever the formula gives.
  *   out_loss       fp32, the weight in it.
@@ -621,7 +621,7 @@ const char* tail_last_error(void);
  * Ignored rows get 0.  One launch, one pass over the logits.
  */
 int tail_token_logprobs(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype, int64_t logits_ld,
-                        const int32_t* tokens, float temperature, float* out_logprob_opt, float* out_lse_opt,
+                        const int32_t* tokens, double temperature, float* out_logprob_opt, float* out_lse_opt,
                         float* out_entropy_opt, void* stream);
 
 /*
@@ -631,7 +631,7 @@ int tail_token_logprobs(int32_t rows, int32_t V, const void* logits, int32_t log
  * A row with both factors 0 gets zeros and is not read.  One launch.
  */
 int tail_token_logprobs_grad(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype, int64_t logits_ld,
-                             const int32_t* tokens, float temperature, const float* lse, const float* d_logprob,
+                             const int32_t* tokens, double temperature, const float* lse, const float* d_logprob,
                              const float* d_entropy_opt, const float* entropy_opt, void* out_grad, int64_t grad_ld,
                              void* stream);
 
@@ -646,7 +646,7 @@ int tail_token_logprobs_grad(int32_t rows, int32_t V, const void* logits, int32_
  * One launch; the logits are read once.
  */
 int tail_policy_loss(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype, int64_t logits_ld,
-                     const int32_t* tokens, float temperature, const float* old_logprob, const float* advantage,
+                     const int32_t* tokens, double temperature, const float* old_logprob, const float* advantage,
                      const float* ref_logprob_opt, float clip_low, float clip_high, float kl_coef, float entropy_coef,
                      const float* weight_opt, float* out_loss, float* out_logprob_opt, float* out_entropy_opt,
                      void* out_grad_opt, int64_t grad_ld, void* stream);
@@ -668,7 +668,7 @@ int tail_policy_loss(int32_t rows, int32_t V, const void* logits, int32_t logits
  */
 int tail_preference_loss_workspace(int32_t rows, int64_t* bytes);
 int tail_preference_loss(int32_t rows, int32_t V, int32_t nseq, const void* logits, int32_t logits_dtype,
-                         int64_t logits_ld, const int32_t* tokens, const int32_t* cu_rows, float temperature,
+                         int64_t logits_ld, const int32_t* tokens, const int32_t* cu_rows, double temperature,
                          const float* ref_logprob_opt, float beta, float label_smoothing, float margin,
                          int32_t average, const float* weight_opt, void* workspace, int64_t workspace_bytes,
                          float* out_loss, float* out_seq_logprob_opt, void* out_grad_opt, int64_t grad_ld,
@@ -688,7 +688,7 @@ int tail_preference_loss(int32_t rows, int32_t V, int32_t nseq, const void* logi
  */
 int tail_distill_topk(int32_t rows, int32_t V, int32_t k, const void* logits, int32_t logits_dtype, int64_t logits_ld,
                       const void* topk_vals, int32_t vals_dtype, int64_t vals_ld, const int32_t* topk_idx,
-                      int64_t idx_ld, float temperature, const float* teacher_rest_opt, const float* weight_opt,
+                      int64_t idx_ld, double temperature, const float* teacher_rest_opt, const float* weight_opt,
                       float* out_loss, void* out_grad_opt, int64_t grad_ld, void* stream);
 
 #ifdef __cplusplus

@@ -287,6 +287,30 @@ def test_distill(rows, V, k, pad, dt, rest, T, vdt, twice):
     assert torch.equal(zt, out)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_more_rows_than_shared_memory_holds(dt):
+    # rows that pass twice through L2 instead
+    rng = np.random.default_rng(12)
+    rows, V = 330, 50021
+    z = np.tile(_logits(rng, 30, V, dt), (11, 1))
+    z[:, 0] = rng.standard_normal(rows)
+    z = _np(_dev(z, DT[dt])).astype(np.float32)
+    t = rng.integers(0, V, rows).astype(np.int32)
+    t[2::30] = V - 1
+    t[7::11] = -1
+    f = np.float32
+    old, adv = np.full(rows, -11.0, f), rng.standard_normal(rows).astype(f)
+    zt = _dev(z, DT[dt])
+    loss, lp, g = (_np(x) for x in dst.policy_loss(zt, _dev(t), _dev(old), _dev(adv)))
+    c = f32(0.2)
+    _check_rows(rng, lambda r: [x[:2] + x[3:] for x in tc.policy(z[r], t[r], 1.0, -11.0, float(adv[r]), 0.0, c, c, 0.0, 0.0,
+                                                                1.0, dt)], (loss, lp, g), ("loss", "l", "gradient"), rows)
+    vals, idx, rs = _lists(rng, z, 20, "f32", True, 1.0)
+    loss, g = (_np(x) for x in dst.distill_topk(zt, _dev(vals), _dev(idx), teacher_rest=_dev(rs)))
+    _check_rows(rng, lambda r: tc.distill(z[r], vals[r], idx[r], float(rs[r]), 1.0, 1.0, dt), (loss, g),
+                ("loss", "gradient"), rows)
+
+
 # ------------------------------------------------------------------ rows that go wrong
 
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
