@@ -58,7 +58,7 @@ def allocating_on(stream, index):
     """Allocations inside belong to the call's stream."""
     import torch
     if stream is None:
-        return torch.cuda.device(index)
+        return device_guard(index)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=index)
     return torch.cuda.stream(stream)

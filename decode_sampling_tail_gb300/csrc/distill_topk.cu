@@ -50,7 +50,7 @@ struct Teacher {
   bool any;  // whether there is anything to aim at
 };
 
-__device__ __forceinline__ Teacher teacher_of(const RowStat& st, const float* rest, int64_t r, float k, double k64) {
+__device__ __forceinline__ Teacher teacher_of(const RowStat& st, float rest, float k, double k64) {
   Teacher t;
   t.m = finite_ref(st.m);
   const bool listed = st.m != -INFINITY;
@@ -63,13 +63,13 @@ __device__ __forceinline__ Teacher teacher_of(const RowStat& st, const float* re
   t.rest_is_max = false;
   t.ln = log1pf(st.s);
   t.any = listed;
-  if (!rest || rest[r] == -INFINITY) return t;
+  if (rest == -INFINITY) return t;
   t.any = true;
   if (!listed) {  // the list's values are all -inf: everything is outside it
     t.others = 0.f, t.ln = 0.f, t.q_rest = 1.f, t.lq_rest = 0.f, t.q_list = 0.f, t.rest_is_max = true;
     return t;
   }
-  const float d = static_cast<float>(rest[r] * LOG2E - t.m * k64);  // the rest's weight is 2^d
+  const float d = static_cast<float>(rest * LOG2E - t.m * k64);  // the rest's weight is 2^d
   if (d <= 0.f) {
     const float w = ex2(fmaxf(d, -200.f));
     t.others = st.s + w;
@@ -90,7 +90,7 @@ __device__ __forceinline__ Teacher teacher_of(const RowStat& st, const float* re
   return t;
 }
 
-// A CTA's shared memory behind the board: the list (ids and the teacher's values), the student's logits at its
+// A CTA's dynamic shared memory: the list (ids and the teacher's values), the student's logits at its
 // entries, the bit map of the part's listed columns, and a byte a thread and batch that says which of its
 // vectors have one.  What is kept of the part follows.
 struct List {
@@ -121,58 +121,76 @@ struct EntryGrad {
   float m, s, wt;
 };
 
-// A row's loss and the factors of its gradient from the board, by one warp.
-__device__ __forceinline__ void distill_row(const DistillArgs& a, int64_t r, float w, const Teacher& t,
-                                            const Board<2>& board, RowGrad* g, EntryGrad* e) {
-  const int lane = threadIdx.x;
-  const RowStat o = board.stat<false>(0, a.k), n = board.stat<false>(1, a.k);
+// What a set of columns says of a row: statistics of those outside the list and of the listed ones, and, relative to the
+// latter's maximum, C = sum q_i (t_i - z_i) / T and Q = sum q_i.
+struct Sums {
+  RowStat out, in;
+  float C, Q;
+};
+__device__ __forceinline__ void pack(const Sums& s, float4 (&v)[2]) {
+  v[0] = make_float4(s.out.m, s.out.s, s.C, s.Q);
+  v[1] = make_float4(s.in.m, s.in.s, 0.f, 0.f);
+}
+__device__ __forceinline__ Sums unpack(const float4& a, const float4& b) {
+  return Sums{RowStat{a.x, a.y, 0.f}, RowStat{b.x, b.y, 0.f}, a.z, a.w};
+}
+// A warp's lanes' together.
+__device__ __forceinline__ Sums merge_sums(const Sums& s, float k, float inv_t) {
+  Sums r;
+  r.out = warp_merge<false>(s.out, k);
+  r.in = warp_merge<false>(s.in, k);
+  float C = s.C;
+  if (!(s.Q == 0.f)) C += s.Q * ((finite_ref(r.in.m) - finite_ref(s.in.m)) * inv_t);
+  r.C = warp_sum(C);
+  r.Q = warp_sum(s.Q);
+  return r;
+}
+
+// A row's loss and the factors of its gradient, by one warp.
+__device__ __forceinline__ void distill_row(const DistillArgs& a, int64_t r, float w, const Teacher& t, const Sums& x,
+                                            int rank, RowGrad* g, EntryGrad* e) {
+  const RowStat &o = x.out, &n = x.in;
   const RowStat all = merge(o, n, a.k);
   const bool live = all.m != -INFINITY && t.any;  // a distribution, and something to aim at
-  const float ln = log1pf(all.s), sum = 1.f + all.s;
+  const float ln = log1pf(all.s), sum = 1.f + all.s, inv = 1.f / sum;
   const float out_w = o.m == -INFINITY ? 0.f : (1.f + o.s) * ex2(dist(o.m, finite_ref(all.m), a.k));
   const float in_w = n.m == -INFINITY ? 0.f : (1.f + n.s) * ex2(dist(n.m, finite_ref(all.m), a.k));
-  const float p_rest = out_w / sum;
-  if (board.rank == 0) {
-    float loss = 0.f, q = 0.f;
-    for (int i = lane; i < board.sets; i += 32) {
-      const float4 x = board.get(0, i);
-      if (!(x.w == 0.f)) loss += x.z - x.w * ((finite_ref(board.get(1, i).x) - all.m) * a.inv_t);
-      q += x.w;
-    }
+  const float p_rest = out_w * inv;
+  if (threadIdx.x != 0) return;
+  if (rank == 0) {
     // log q_i - l_i is a difference of two logits and of two log-sums: the logarithm of the sums' quotient does not
     // leave each one's rounding behind
     const float scale = 1.f + t.others;
-    const float x = t.D == 0.f ? all.s - t.others : sum * ex2(-t.D) - scale;
-    const float lead = t.D < 100.f ? log1pf(x / scale) : ln - t.ln - t.D * 0.693147181f;
-    loss = warp_sum(loss) + lead * warp_sum(q);
+    const float y = t.D == 0.f ? all.s - t.others : sum * ex2(-t.D) - scale;
+    const float lead = t.D < 100.f ? log1pf(y / scale) : ln - t.ln - t.D * 0.693147181f;
+    float loss = lead * x.Q;
+    if (!(x.Q == 0.f)) loss += x.C + x.Q * ((all.m - finite_ref(n.m)) * a.inv_t);
     if (!(t.q_rest == 0.f)) {
       const float lp = out_w >= in_w    ? -log1pf(in_w / out_w)
                        : out_w > 1e-30f ? logf(p_rest)
                                         : (o.m - all.m) * a.inv_t + log1pf(o.s) - ln;
       loss += t.q_rest * (t.lq_rest - (o.m == -INFINITY ? -INFINITY : lp));
     }
-    if (lane == 0) a.loss[r] = live ? w * loss : 0.f;
+    a.loss[r] = live ? w * loss : 0.f;
   }
-  if (lane == 0) {
-    const float wt = live ? w * a.inv_t : 0.f;
-    const float off = p_rest > 0.5f && t.q_rest > 0.5f ? t.q_list - in_w / sum : p_rest - t.q_rest;
-    *g = RowGrad{finite_ref(o.m), a.k, live ? wt * off / (1.f + o.s) : 0.f, 0.f, 0.f, -1};
-    *e = EntryGrad{finite_ref(all.m), all.s, wt};
-  }
+  const float wt = live ? w * a.inv_t : 0.f;
+  const float off = p_rest > 0.5f && t.q_rest > 0.5f ? t.q_list - in_w * inv : p_rest - t.q_rest;
+  *g = RowGrad{finite_ref(o.m), a.k, live ? wt * off / (1.f + o.s) : 0.f, 0.f, 0.f, -1};
+  *e = EntryGrad{finite_ref(all.m), all.s, wt};
 }
 
 template <typename T, bool GRAD, int NT>
 __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const __grid_constant__ DistillArgs a) {
   constexpr int N = Vec<T>::N;
   extern __shared__ uint4 smem[];
+  __shared__ Board<2> board;
   __shared__ RowStat s_warp[NT / 32];
   __shared__ Teacher s_teacher;
   __shared__ RowGrad s_grad;
   __shared__ EntryGrad s_entry;
   const int size = cluster_size(), rank = cluster_rank(), tid = threadIdx.x;
-  const Board<2> board = board_at<2>(smem, rank, size);
   List l;
-  l.ids = reinterpret_cast<int32_t*>(smem + Board<2>::bytes(board.sets) / 16);
+  l.ids = reinterpret_cast<int32_t*>(smem);
   l.t = reinterpret_cast<float*>(l.ids + a.k_list);
   l.z = l.t + a.k_list;
   l.map = reinterpret_cast<uint32_t*>(l.z + a.k_list);
@@ -182,7 +200,7 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
   const T* row = static_cast<const T*>(a.logits) + r * a.ld;
   T* grad = static_cast<T*>(a.grad) + r * a.gld;
   const RowPart p = row_part(row, a.V, rank, size);
-  const int cached = GRAD ? min(a.kept, p.count) : 0;
+  const bool kept = GRAD && a.kept > 0;
   // The part's columns [lo, hi); bit 0 of the map is one vector in front of its first whole one.
   const int body = p.head + p.first * N, origin = body - N;
   const int lo = rank == 0 ? 0 : body, hi = rank == size - 1 ? a.V : body + p.count * N;
@@ -192,40 +210,51 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
       if (id >= lo && id < hi) f(i, id);
     }
   };
+  if (size > 1) board.init();
   for (int i = tid; i < a.map_words + a.flag_words; i += NT) l.map[i] = 0;  // (the flags lie behind the map)
   pdl_wait();
 
-  // The list.  A row is fetched at once when its first entry is one.
+  // The list: a thread's first entry and the logit at it are under way while the part is requested, which waits for
+  // the row's first id at most.
   const float w = a.weight ? a.weight[r] : 1.f;
-  const bool early = w != 0.f && static_cast<uint32_t>(a.idx[r * a.ild]) < static_cast<uint32_t>(a.V);
-  const auto fetch = [&] {
-    if (cached > 0)
-      fetch_part<T, NT>(row, p, cache, cached);
-    else
-      prefetch_part(row, p);
-  };
-  if (early) fetch();
-  bool any = false;
-  RowStat st[1] = {no_stat()};
-  if (w != 0.f)
-    for (int i = tid; i < a.k_list; i += NT) {
-      const int id = a.idx[r * a.ild + i];
-      const float v = list_value(a, r, i);
-      const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.V);
-      l.ids[i] = ok ? id : -1;
-      l.t[i] = v;
-      any = any || ok;
-      if (ok) st[0] = merge(st[0], stat_of(v), a.k);
-    }
-  st[0] = warp_merge<1, false>(st, a.k);
+  const int head_id = a.idx[r * a.ild];
+  const float rest = a.rest && tid == 0 ? a.rest[r] : -INFINITY;  // the first thread's
+  const bool listed = tid < a.k_list;
+  int id0 = listed ? a.idx[r * a.ild + tid] : -1;
+  const float v0 = listed ? list_value(a, r, tid) : 0.f;
+  const bool early = w != 0.f && static_cast<uint32_t>(head_id) < static_cast<uint32_t>(a.V);
+  if (kept)
+    fetch_part<T, NT>(row, p, cache);
+  else if (early)
+    prefetch_part(row, p, 0);
+  if (static_cast<uint32_t>(id0) >= static_cast<uint32_t>(a.V)) id0 = -1;
+  float z0 = 0.f;
+  if (id0 >= lo && id0 < hi) z0 = Vec<T>::widen1(row[id0]);
+  bool any = id0 >= 0;
+  RowStat st[1] = {stat_of(any ? v0 : -INFINITY)};
+  if (listed) {
+    l.ids[tid] = id0;
+    l.t[tid] = v0;
+  }
+  for (int i = tid + NT; i < a.k_list; i += NT) {
+    const int id = a.idx[r * a.ild + i];
+    const float v = list_value(a, r, i);
+    const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.V);
+    l.ids[i] = ok ? id : -1;
+    l.t[i] = v;
+    any = any || ok;
+    if (ok) st[0] = merge(st[0], stat_of(v), a.k);
+  }
+  st[0] = warp_merge<false>(st[0], a.k);
   if ((tid & 31) == 0) s_warp[tid >> 5] = st[0];
-  if (!__syncthreads_or(any)) {
+  if (!__syncthreads_or(any && w != 0.f)) {
+    if (kept) copy_wait(0);
     if (rank == 0 && tid == 0) a.loss[r] = 0.f;
     if (GRAD) zero_part(grad, a.V, rank, size);
     return;
   }
-  if (size > 1) cluster_arrive();
-  if (!early) fetch();
+  if (size > 1) cluster_started();
+  if (!kept && !early) prefetch_part(row, p, 0);
   // The entries of this part: their bits, and whether an id comes twice.
   bool twice = false;
   entries([&](int i, int id) {
@@ -236,12 +265,16 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
       const int f = v / (ROW_BATCH * NT) * NT + v % NT;  // its thread's byte of its batch
       atomicOr(l.flags + (f >> 2), 1u << (v / NT % ROW_BATCH + 8 * (f & 3)));
     }
-    l.z[i] = Vec<T>::widen1(row[id]);
+    l.z[i] = i == tid ? z0 : Vec<T>::widen1(row[id]);
   });
+  Batch v;
+  if (!kept) v.load<NT>(part_vectors(row, p), 0, p.count);
+  const float edge = edge_of(row, p);
+  if (size > 1) cluster_wait();
   if (tid < 32) {
     st[0] = tid < NT / 32 ? s_warp[tid] : no_stat();
-    st[0] = warp_merge<1, false>(st, a.k);
-    if (tid == 0) s_teacher = teacher_of(st[0], a.rest, r, a.k, a.k64);
+    st[0] = warp_merge<false>(st[0], a.k);
+    if (tid == 0) s_teacher = teacher_of(st[0], rest, a.k, a.k64);
   }
   twice = __syncthreads_or(twice);
   const Teacher& t = s_teacher;
@@ -253,35 +286,42 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
     return true;
   };
 
-  // Statistics of the columns outside the list and of the listed ones, and, relative to the latter's maximum in
-  // the warp, sum q_i (t_i - z_i) / T and sum q_i.
-  const float edge = edge_of(row, p);
-  RowStat out[1] = {stat_pass<T, false, NT>(row, p, cache, cached, a.k,
-                                            ListMask<N, NT>{l.map, reinterpret_cast<const uint8_t*>(l.flags)})};
+  Sums x;
+  x.out = stat_pass<T, false, NT>(row, p, kept ? cache : nullptr, v, a.k,
+                                  ListMask<N, NT>{l.map, reinterpret_cast<const uint8_t*>(l.flags)});
   if (p.edge_n && !(l.map[(p.edge_lo - origin) >> 5] >> ((p.edge_lo - origin) & 31) & 1))
-    out[0] = merge(out[0], stat_of(edge), a.k);
-  RowStat in[1] = {no_stat()};
+    x.out = merge(x.out, stat_of(edge), a.k);
+  if (GRAD && !kept) v.load<NT>(part_vectors(row, p), 0, p.count);  // for the second pass, while the factors are formed
+  x.in = no_stat();
   entries([&](int i, int id) {
-    if (owner(i, id)) in[0] = merge(in[0], stat_of(l.z[i]), a.k);
+    if (owner(i, id)) x.in = merge(x.in, stat_of(l.z[i]), a.k);
   });
-  out[0] = warp_merge<1, false>(out, a.k);
-  in[0] = warp_merge<1, false>(in, a.k);
-  float C = 0.f, Q = 0.f;
+  x.C = x.Q = 0.f;
   entries([&](int i, int) {
     const float q = weight(i);
     if (q == 0.f) return;
-    C += q * (((l.t[i] - t.m) - (l.z[i] - finite_ref(in[0].m))) * a.inv_t);
-    Q += q;
+    x.C += q * (((l.t[i] - t.m) - (l.z[i] - finite_ref(x.in.m))) * a.inv_t);
+    x.Q += q;
   });
-  const float4 post[2] = {make_float4(out[0].m, out[0].s, warp_sum(C), warp_sum(Q)),
-                          make_float4(in[0].m, in[0].s, 0.f, 0.f)};
-  if (size > 1) cluster_wait();
-  board.post(post);
-  board.wait();
-  if (tid < 32) distill_row(a, r, w, t, board, &s_grad, &s_entry);
+  x = merge_sums(x, a.k, a.inv_t);
+  float4 mine[2], all[2];
+  pack(x, mine);
+  if ((tid & 31) == 0) board.warp[0][tid >> 5] = mine[0], board.warp[1][tid >> 5] = mine[1];
+  __syncthreads();
+  if (tid < 32) {  // one warp forms the row's loss and factors for all
+    x = tid < NT / 32 ? unpack(board.warp[0][tid], board.warp[1][tid]) : Sums{no_stat(), no_stat(), 0.f, 0.f};
+    x = merge_sums(x, a.k, a.inv_t);
+    if (size > 1) {
+      pack(x, mine);
+      const bool ok = board.template exchange<true>(rank, size, mine, all);
+      x = merge_sums(unpack(all[0], tid < size ? all[1] : make_float4(-INFINITY, 0.f, 0.f, 0.f)), a.k, a.inv_t);
+      if (!ok) x.out.m = NAN;
+    }
+    distill_row(a, r, w, t, x, rank, &s_grad, &s_entry);
+  }
   if (!GRAD) return;
   __syncthreads();
-  grad_pass<T, false, NT>(s_grad, GradRow<T>{row, grad, p, cache, cached, edge});
+  grad_pass<T, false, NT>(s_grad, GradRow<T>{row, grad, p, kept ? cache : nullptr, edge}, v);
   __syncthreads();  // the entries' values go over what the pass has written
   const EntryGrad e = s_entry;
   entries([&](int i, int id) {
@@ -306,7 +346,7 @@ cudaError_t launch(DistillArgs& a, int rows, cudaStream_t stream) {
   const int64_t part = part_of(row_vectors(a.V, sizeof(T)), p.size);
   a.map_words = map_words(part, Vec<T>::N);
   a.flag_words = flag_words(part, p.threads);
-  const int beside = Board<2>::bytes(p.size * p.threads / 32) + 4 * (3 * a.k_list + a.map_words + a.flag_words);
+  const int beside = 4 * (3 * a.k_list + a.map_words + a.flag_words);
   a.cache_at = (beside + 15) / 16;
   a.kept = p.kept;
   const int smem = 16 * (a.cache_at + a.kept);

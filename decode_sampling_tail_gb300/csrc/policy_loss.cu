@@ -34,10 +34,10 @@ struct PolicyRow {
 };
 template <bool ENT>
 __device__ __forceinline__ RowGrad policy_row(const PolicyArgs& a, const PolicyRow& x, const RowStat& all, bool first) {
-  const float ln = log1pf(all.s), sum = 1.f + all.s;
+  const float ln = log1pf(all.s), sum = 1.f + all.s, inv = 1.f / sum;
   const bool empty = all.m == -INFINITY;  // no distribution
   const float lp = empty ? -INFINITY : (x.z - all.m) * a.inv_t - ln;
-  const float excess = ENT ? -0.693147181f * all.u / sum : 0.f;  // H - log of the sum
+  const float excess = ENT ? -0.693147181f * all.u * inv : 0.f;  // H - log of the sum
   const float R = expf(lp - x.old);
   const float open = -x.adv * R, clipped = -x.adv * fminf(fmaxf(R, a.lo), a.hi);
   float loss = fmaxf(open, clipped), c = open >= clipped ? open : 0.f;
@@ -58,30 +58,39 @@ __device__ __forceinline__ RowGrad policy_row(const PolicyArgs& a, const PolicyR
   g.token = x.t;
   const float cw = x.w * c * a.inv_t, fw = ENT ? x.w * a.ent * a.inv_t : 0.f;
   const float et = ex2((x.z - g.ref) * a.k);
-  g.A = (fw * excess - cw) / sum;
-  g.B = fw * 0.693147181f / sum;
-  g.at_token = cw * (x.z == all.m ? all.s : sum - et) / sum;
-  if (ENT && et > 0.f) g.at_token += fw * (et / sum) * (lp + ln + excess);
+  g.A = (fw * excess - cw) * inv;
+  g.B = fw * 0.693147181f * inv;
+  g.at_token = cw * (x.z == all.m ? all.s : sum - et) * inv;
+  if (ENT && et > 0.f) g.at_token += fw * (et * inv) * (lp + ln + excess);
   if (empty) g.A = g.B = g.at_token = 0.f;
   return g;
 }
 
 template <typename T, bool ENT, bool GRAD, int NT>
 __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) policy_kernel(const __grid_constant__ PolicyArgs a) {
-  extern __shared__ uint4 smem[];
+  extern __shared__ uint4 cache[];
+  __shared__ Board<1> board;
   __shared__ RowGrad s_grad;
   const int size = cluster_size(), rank = cluster_rank();
-  const Board<1> board = board_at<1>(smem, rank, size);
-  uint4* cache = smem + Board<1>::bytes(board.sets) / 16;
   PolicyRow x;
   x.r = blockIdx.x / size;
   const T* row = static_cast<const T*>(a.logits) + x.r * a.ld;
   T* grad = static_cast<T*>(a.grad) + x.r * a.gld;
   const bool first = rank == 0 && threadIdx.x == 0;
+  const RowPart p = row_part(row, a.V, rank, size);
+  const bool kept = GRAD && a.kept > 0;
+  if (size > 1) board.init();
   pdl_wait();
   x.t = a.tokens[x.r];
   x.w = a.weight ? a.weight[x.r] : 1.f;
+  // the first of the row's logits come with its token, whether they will count or not
+  Batch v;
+  if (kept)
+    fetch_part<T, NT>(row, p, cache);
+  else
+    v.load<NT>(part_vectors(row, p), 0, p.count);
   if (static_cast<uint32_t>(x.t) >= static_cast<uint32_t>(a.V) || x.w == 0.f) {
+    if (kept) copy_wait(0);
     if (first) {
       a.loss[x.r] = 0.f;
       if (a.logprob) a.logprob[x.r] = 0.f;
@@ -90,13 +99,8 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) policy_kernel(const _
     if (GRAD) zero_part(grad, a.V, rank, size);
     return;
   }
-  if (size > 1) cluster_arrive();
-  const RowPart p = row_part(row, a.V, rank, size);
-  const int cached = GRAD ? min(a.kept, p.count) : 0;
-  if (cached > 0)
-    fetch_part<T, NT>(row, p, cache, cached);
-  else
-    prefetch_part(row, p);
+  if (!kept) prefetch_part(row, p, ROW_BATCH * NT);
+  if (size > 1) cluster_started();
   const float edge = edge_of(row, p);
   if (threadIdx.x < 32) {
     x.z = Vec<T>::widen1(row[x.t]);
@@ -104,27 +108,26 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) policy_kernel(const _
     x.adv = a.adv[x.r];
     x.ref = a.kl != 0.f ? a.ref[x.r] : 0.f;
   }
-  RowStat st[1] = {stat_pass<T, ENT, NT>(row, p, cache, cached, a.k, NoMask{})};
-  if (p.edge_n) st[0] = merge(st[0], stat_of(edge), a.k);
-  st[0] = warp_merge<1, ENT>(st, a.k);
-  const float4 post[1] = {make_float4(st[0].m, st[0].s, st[0].u, 0.f)};
   if (size > 1) cluster_wait();
-  board.post(post);
-  board.wait();
-  if (threadIdx.x < 32) {  // one warp forms the row's factors for all
-    const RowGrad g = policy_row<ENT>(a, x, board.template stat<ENT>(0, a.k), first);
+  RowStat st = stat_pass<T, ENT, NT>(row, p, kept ? cache : nullptr, v, a.k, NoMask{});
+  if (p.edge_n) st = merge(st, stat_of(edge), a.k);
+  // the second pass's first vectors come while the factors are formed
+  if (GRAD && !kept) v.load<NT>(part_vectors(row, p), 0, p.count);
+  st = cluster_stat<ENT, GRAD>(board, st, a.k, rank, size);
+  if (threadIdx.x < 32 && (GRAD || rank == 0)) {  // one warp forms the row's factors for all
+    const RowGrad g = policy_row<ENT>(a, x, st, first);
     if (GRAD && threadIdx.x == 0) s_grad = g;
   }
   if (!GRAD) return;
   __syncthreads();
-  grad_pass<T, ENT, NT>(s_grad, GradRow<T>{row, grad, p, cache, cached, edge});
+  grad_pass<T, ENT, NT>(s_grad, GradRow<T>{row, grad, p, kept ? cache : nullptr, edge}, v);
 }
 
 template <typename T, bool ENT, bool GRAD>
 cudaError_t launch(PolicyArgs& a, int rows, cudaStream_t stream) {
-  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 8, GRAD ? Board<1>::bytes(ROW_MAX_SETS) : -1);
+  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 8, GRAD ? 0 : -1);
   a.kept = p.kept;
-  const int smem = Board<1>::bytes(p.size * p.threads / 32) + 16 * p.kept;
+  const int smem = 16 * p.kept;
   return p.threads == 512   ? launch_rows<policy_kernel<T, ENT, GRAD, 512>>(p, smem, rows, stream, a)
          : p.threads == 256 ? launch_rows<policy_kernel<T, ENT, GRAD, 256>>(p, smem, rows, stream, a)
                             : launch_rows<policy_kernel<T, ENT, GRAD, 128>>(p, smem, rows, stream, a);

@@ -270,27 +270,16 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// The statistics of J sets a lane, the same bits in every lane: the sets are brought to the common maximum once,
-// and the first set that holds it gives the instance that stays out of the sum.
-template <int J, bool ENT>
-__device__ __forceinline__ RowStat warp_merge(const RowStat (&v)[J], float k) {
-  float mx = v[0].m;
-#pragma unroll
-  for (int j = 1; j < J; ++j) mx = max_nan(mx, v[j].m);
-  RowStat r{warp_max(mx), 0.f, 0.f};
-  const float ref = finite_ref(r.m);
-  bool found = false;
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const uint32_t at = __ballot_sync(0xffffffffu, v[j].m == r.m);
-    const bool out = !found && at && static_cast<int>(threadIdx.x & 31) == __ffs(at) - 1;
-    found = found || at;
-    const float d = dist(v[j].m, ref, k), c = ex2(d);
-    r.s += c * (v[j].s + (out ? 0.f : 1.f));
-    if (ENT) r.u += c * (v[j].u + d * (1.f + v[j].s));
-  }
-  r.s = warp_sum(r.s);
-  if (ENT) r.u = warp_sum(r.u);
+// The statistics of a warp's lanes, the same bits in every lane: they are brought to the common maximum once, and
+// the first lane that holds it gives the instance that stays out of the sum.
+template <bool ENT>
+__device__ __forceinline__ RowStat warp_merge(const RowStat& v, float k) {
+  RowStat r{warp_max(v.m), 0.f, 0.f};
+  const uint32_t at = __ballot_sync(0xffffffffu, v.m == r.m);
+  const bool out = static_cast<int>(threadIdx.x & 31) == __ffs(at) - 1;
+  const float d = dist(v.m, finite_ref(r.m), k), c = ex2(d);
+  r.s = warp_sum(c * (v.s + (out ? 0.f : 1.f)));
+  if (ENT) r.u = warp_sum(c * (v.u + d * (1.f + v.s)));
   return r;
 }
 
@@ -330,6 +319,13 @@ __device__ __forceinline__ RowPart row_part(const T* row, int V, int rank, int s
   return p;
 }
 
+// Whether a column of the row is this CTA's.
+template <typename T>
+__device__ __forceinline__ bool has_column(const RowPart& p, int rank, int size, int col) {
+  const int lo = p.head + p.first * Vec<T>::N;
+  return (col >= lo || rank == 0) && (col < lo + p.count * Vec<T>::N || rank == size - 1);
+}
+
 // ---------------------------------------------------------------- asynchronous copies of a thread's own vectors
 
 __device__ __forceinline__ void copy_async16(uint4* dst, const uint4* src) {
@@ -362,72 +358,97 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// Says that this CTA has started (and what thread 0 has initialised); the others' shared memory may be written behind the
+// wait.  Both stand at a kernel's start, beside its first loads: a wait has every warp invalidate L1, one after another,
+// about 1 us for 8 warps where the row's statistics would wait for it.
+__device__ __forceinline__ void cluster_started() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// Writes four words to the same shared variable of CTA `rank` of the cluster.
-__device__ __forceinline__ void store_remote(float4* mine, int rank, float4 v) {
-  uint32_t at;
+// Writes four words to the same shared variable of CTA `rank` of the cluster, and counts their bytes on its barrier.
+__device__ __forceinline__ void store_remote(float4* mine, uint64_t* bar, int rank, float4 v) {
+  uint32_t at, to;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(bar)), "r"(rank));
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
+               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(to)
                : "memory");
 }
 
-// Where the warps of a cluster's CTAs leave W words of four each for all of them.
-constexpr int ROW_MAX_SETS = 128;  // warps of a cluster: 8 CTAs of 16
+constexpr uint64_t ROW_WAIT_NS = 1000000000ull;
+
+// Where a cluster's CTAs leave W words of four each for one another, by their first warps alone.
 template <int W>
 struct Board {
-  float4* at;  // [W][sets] in shared memory
-  int sets, rank, size;
+  float4 warp[W][16];              // this CTA's warps'
+  float4 cta[W][ROW_MAX_CLUSTER];  // the CTAs'
+  uint64_t bar;
 
-  static __host__ __device__ constexpr int bytes(int sets) { return W * sets * static_cast<int>(sizeof(float4)); }
-
-  // Lanes 0 .. size - 1 of each warp write to a CTA each; then the CTA arrives.  (All CTAs have started: the cluster has
-  // been synchronised before.)
-  __device__ __forceinline__ void post(const float4 (&v)[W]) const {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float4* mine = at + (sets / size) * rank + warp;
-    if (size == 1) {
-      if (lane == 0)
-#pragma unroll
-        for (int w = 0; w < W; ++w) mine[w * sets] = v[w];
-      return;
+  // All threads, at the start; then cluster_started().
+  __device__ __forceinline__ void init() {
+    if (threadIdx.x == 0) {
+      mbar_init(smem_u32(&bar), 1);
+      fence_mbar_init();
     }
-    if (lane < size)
+  }
+  __device__ __forceinline__ bool arrived() {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\nselp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(&bar))
+        : "memory");
+    return ok != 0;
+  }
+  __device__ __forceinline__ bool wait() {
+    if (arrived()) return true;
+    const uint64_t since = global_timer_ns();
+    while (!arrived())
+      if (global_timer_ns() - since > ROW_WAIT_NS) return false;
+    return true;
+  }
+  // The first warp: its CTA's words to every CTA (ALL) or to the first, and in return all the CTAs', lane i CTA i's.
+  // False when they have not come in a second.
+  template <bool ALL>
+  __device__ __forceinline__ bool exchange(int rank, int size, const float4 (&mine)[W], float4 (&all)[W]) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0 && (ALL || rank == 0)) mbar_arrive_expect_tx(smem_u32(&bar), size * W * sizeof(float4));
+    if (ALL ? lane < size : lane == 0)
 #pragma unroll
-      for (int w = 0; w < W; ++w) store_remote(mine + w * sets, lane, v[w]);
+      for (int w = 0; w < W; ++w) store_remote(&cta[w][rank], &bar, lane, mine[w]);
     __syncwarp();
-    cluster_arrive();
-  }
-  __device__ __forceinline__ void wait() const {
-    if (size == 1)
-      __syncthreads();
-    else
-      cluster_wait();
-  }
-  __device__ __forceinline__ float4 get(int w, int i) const {
-    return i < sets ? at[w * sets + i] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-  }
-  template <int J, bool ENT>
-  __device__ __forceinline__ RowStat stat_of_sets(int w, float k) const {
-    RowStat v[J];
+    if (!ALL && rank != 0) return true;
+    const bool ok = wait();
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const float4 x = get(w, j * 32 + static_cast<int>(threadIdx.x & 31));
-      v[j] = RowStat{x.x, x.y, x.z};
-    }
-    return warp_merge<J, ENT>(v, k);
-  }
-  // The cluster's statistics from its warps' (word w: maximum, s, u), the same bits in every lane and CTA.
-  template <bool ENT>
-  __device__ __forceinline__ RowStat stat(int w, float k) const {
-    return sets <= 32 ? stat_of_sets<1, ENT>(w, k) : stat_of_sets<ROW_MAX_SETS / 32, ENT>(w, k);
+    for (int w = 0; w < W; ++w) all[w] = lane < size ? cta[w][lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    return __all_sync(0xffffffffu, ok);
   }
 };
 
-template <int W>
-__device__ __forceinline__ Board<W> board_at(void* smem, int rank, int size) {
-  return Board<W>{static_cast<float4*>(smem), size * static_cast<int>(blockDim.x >> 5), rank, size};
+// The cluster's statistics in the first warp of every CTA (ALL) or of the first, from each thread's; the same bits in all
+// lanes.  NaN when another CTA's have not come.  Ends without a barrier.
+template <bool ENT, bool ALL>
+__device__ __forceinline__ RowStat cluster_stat(Board<1>& board, RowStat st, float k, int rank, int size) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  st = warp_merge<ENT>(st, k);
+  if (lane == 0) board.warp[0][warp] = make_float4(st.m, st.s, st.u, 0.f);
+  __syncthreads();
+  if (warp != 0) return st;
+  st = no_stat();
+  if (lane < static_cast<int>(blockDim.x >> 5)) {
+    const float4 x = board.warp[0][lane];
+    st = RowStat{x.x, x.y, x.z};
+  }
+  st = warp_merge<ENT>(st, k);
+  if (size == 1) return st;
+  const float4 mine[1] = {make_float4(st.m, st.s, st.u, 0.f)};
+  float4 all[1];
+  const bool ok = board.template exchange<ALL>(rank, size, mine, all);
+  if (!ALL && rank != 0) return st;
+  st = warp_merge<ENT>(RowStat{all[0].x, all[0].y, all[0].z}, k);
+  if (!ok) st.m = NAN;
+  return st;
 }
 
 // ---------------------------------------------------------------- gradient
@@ -488,27 +509,62 @@ __device__ __forceinline__ const uint4* part_vectors(const T* row, const RowPart
 // ---------------------------------------------------------------- passes over a part
 // A thread takes vectors tid, tid + NT, .. of the part, ROW_BATCH of them at a time; in all passes the same ones, so
 // that its copies into shared memory need no barrier.  Whole batches run without a bound in sight: with one, and a
-// token to look for, a vector cost more instructions than its columns' arithmetic.
+// token to look for, a vector cost more instructions than its columns' arithmetic.  A part is kept in shared memory
+// whole or not at all; what is not kept is read from L2 in each pass, into which one instruction has brought it.  A pass over
+// memory gets its first batch from the caller, who loads it before whatever else the pass has to wait for.
 
 __host__ __device__ constexpr int batches(int n, int nt) { return (n + ROW_BATCH * nt - 1) / (ROW_BATCH * nt); }
 
-// Requests the part's first `cached` vectors into shared memory, each by the thread that takes it, one group a batch.
+// Requests the whole part into shared memory, each vector by the thread that takes it, one group a batch.
 template <typename T, int NT>
-__device__ __forceinline__ void fetch_part(const T* row, const RowPart& p, uint4* cache, int cached) {
+__device__ __forceinline__ void fetch_part(const T* row, const RowPart& p, uint4* cache) {
   const uint4* in = part_vectors(row, p);
-  for (int b = 0; b < batches(cached, NT); ++b) {
-    const int end = min((b + 1) * ROW_BATCH * NT, cached);
+  for (int b = 0; b < batches(p.count, NT); ++b) {
+    const int end = min((b + 1) * ROW_BATCH * NT, p.count);
     for (int i = b * ROW_BATCH * NT + static_cast<int>(threadIdx.x); i < end; i += NT) copy_async16(cache + i, in + i);
     copy_commit();
   }
 }
 
-// Has the whole part brought into L2, by one instruction of one thread: the loads behind it then wait for L2 alone.
+// Has the part, from vector `from` on, brought into L2, by one instruction of one thread: the loads behind it then wait for
+// L2 alone.
 template <typename T>
-__device__ __forceinline__ void prefetch_part(const T* row, const RowPart& p) {
-  if (threadIdx.x == 0 && p.count > 0)
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(part_vectors(row, p)), "r"(p.count * 16) : "memory");
+__device__ __forceinline__ void prefetch_part(const T* row, const RowPart& p, int from) {
+  if (threadIdx.x == 0 && p.count > from)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(part_vectors(row, p) + from),
+                 "r"((p.count - from) * 16)
+                 : "memory");
 }
+
+// A load of what is not needed again: its place in L2 goes first.
+__device__ __forceinline__ uint4 load_last(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p), "l"(policy_evict_first())
+               : "memory");
+  return v;
+}
+
+// A thread's vectors of a batch.
+struct Batch {
+  uint4 v[ROW_BATCH];
+
+  // Batch b of n vectors in memory; those behind the end are not touched.
+  template <int NT, bool LAST = false>
+  __device__ __forceinline__ void load(const uint4* in, int b, int n) {
+    const int i0 = b * ROW_BATCH * NT + static_cast<int>(threadIdx.x);
+    const uint4* at = in + i0;
+    if ((b + 1) * ROW_BATCH * NT <= n) {
+#pragma unroll
+      for (int j = 0; j < ROW_BATCH; ++j) v[j] = LAST ? load_last(at + j * NT) : __ldcg(at + j * NT);
+    } else {
+#pragma unroll
+      for (int j = 0; j < ROW_BATCH; ++j)
+        if (i0 + j * NT < n) v[j] = LAST ? load_last(at + j * NT) : __ldcg(at + j * NT);
+    }
+  }
+};
 
 // Columns that count as -inf: flags(b) of this thread's batch b has a bit a vector with any, bits(i) the columns of
 // vector i.
@@ -529,120 +585,104 @@ __device__ __forceinline__ void stat_batch(RowAcc<T, ENT>& acc, uint4 (&v)[ROW_B
   acc.batch(v, k);
 }
 
-// What lies behind the first b batches: single vectors of the last batch that is kept, then what comes from memory.
 template <typename T, bool ENT, int NT, typename Mask>
-__device__ __forceinline__ void stat_tail(RowAcc<T, ENT>& acc, const T* row, const RowPart& p, const uint4* cache,
-                                          int cached, int b, float k, const Mask& mask) {
-  constexpr int U = ROW_BATCH;
-  const int tid = threadIdx.x, whole = p.count / (U * NT);
-  const auto single = [&](const uint4& z, int i) {
-    uint4 v[1] = {z};
-    const uint32_t m = mask.bits(i);
-    if (m) Vec<T>::mask(v[0], m);
-    acc.batch(v, k);
-  };
-  for (int i = b * U * NT + tid; i < cached; i += NT) single(cache[i], i);
-  if (cached == p.count) return;
-  const uint4* in = part_vectors(row, p);
-  for (b = max(b, cached / (U * NT)); b < whole; ++b) {
-    uint4 v[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) v[j] = __ldcg(in + (b * U + j) * NT + tid);
-    stat_batch<T, ENT, NT>(acc, v, b, k, mask);
-  }
-  for (int i = b * U * NT + tid; i < p.count; i += NT) single(__ldcg(in + i), i);
+__device__ __forceinline__ void stat_single(RowAcc<T, ENT>& acc, const uint4& z, int i, float k, const Mask& mask) {
+  uint4 v[1] = {z};
+  const uint32_t m = mask.bits(i);
+  if (m) Vec<T>::mask(v[0], m);
+  acc.batch(v, k);
 }
 
-// Statistics over this CTA's part, its first `cached` vectors from shared memory as their copies arrive (the thread has
-// no other copies under way), the others from memory.  Without the thread's single column.
+// Statistics over this CTA's part, without the thread's single column: from shared memory as its copies arrive (the
+// thread has no other copies under way), or from memory with the first batch in x.
 template <typename T, bool ENT, int NT, typename Mask>
-__device__ __forceinline__ RowStat stat_pass(const T* row, const RowPart& p, const uint4* cache, int cached, float k,
+__device__ __forceinline__ RowStat stat_pass(const T* row, const RowPart& p, const uint4* cache, Batch& x, float k,
                                              const Mask& mask) {
   constexpr int U = ROW_BATCH;
+  const int tid = threadIdx.x, whole = p.count / (U * NT), all = batches(p.count, NT);
   RowAcc<T, ENT> acc;
-  int left = batches(cached, NT), b = 0;
-  const uint4* c = cache + threadIdx.x;
-  for (; b < cached / (U * NT); ++b, c += U * NT) {
-    copy_wait(--left);
-    uint4 v[U];
+  if (cache) {
+    const uint4* c = cache + tid;
+    for (int b = 0; b < whole; ++b, c += U * NT) {
+      copy_wait(all - 1 - b);
+      uint4 v[U];
 #pragma unroll
-    for (int j = 0; j < U; ++j) v[j] = c[j * NT];
-    stat_batch<T, ENT, NT>(acc, v, b, k, mask);
+      for (int j = 0; j < U; ++j) v[j] = c[j * NT];
+      stat_batch<T, ENT, NT>(acc, v, b, k, mask);
+    }
+    copy_wait(0);
+    for (int i = whole * U * NT + tid; i < p.count; i += NT) stat_single<T, ENT, NT>(acc, cache[i], i, k, mask);
+  } else {
+    const uint4* in = part_vectors(row, p);
+    for (int b = 0; b < whole; ++b) {
+      stat_batch<T, ENT, NT>(acc, x.v, b, k, mask);
+      if (b + 1 < all) x.load<NT>(in, b + 1, p.count);
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = (whole * U + j) * NT + tid;
+      if (i < p.count) stat_single<T, ENT, NT>(acc, x.v[j], i, k, mask);
+    }
   }
-  if (left > 0) copy_wait(0);
-  stat_tail<T, ENT, NT>(acc, row, p, cache, cached, b, k, mask);
   return acc.done(k);
 }
 
-template <typename T, bool ENT, int NT>
-__device__ __forceinline__ void grad_batch(const RowGrad& g, const uint4* c, uint4* out) {
-  uint4 z[ROW_BATCH];
-#pragma unroll
-  for (int j = 0; j < ROW_BATCH; ++j) z[j] = c[j * NT];
-#pragma unroll
-  for (int j = 0; j < ROW_BATCH; ++j) __stcs(out + j * NT, grad_vec<T, ENT>(g, z[j]));
-}
-
-// A row whose gradient is written, and where it is kept.
+// A row whose gradient is written, and where its part is kept (or null).
 template <typename T>
 struct GradRow {
   const T* row;
   T* grad;
   RowPart p;
-  uint4* cache;
-  int cached;
+  const uint4* cache;
   float edge;
 };
 
-// The gradient behind the first b batches, with the token's column and the single one.  Rows whose gradient lies elsewhere
-// in its 16-byte vectors are written column by column (b is 0); then what the cache holds must be visible to
-// all threads.
-template <typename T, bool ENT, int NT>
-__device__ __forceinline__ void grad_tail(const RowGrad& g, const GradRow<T>& r, int b) {
+// The gradient over this CTA's part of a row, from shared memory or from memory with the first batch in x.  Rows whose
+// gradient lies elsewhere in its 16-byte vectors are written column by column; then what is kept must be visible
+// to all threads.
+template <typename T, bool ENT, int NT, bool LAST = false>
+__device__ __forceinline__ void grad_pass(const RowGrad& g, const GradRow<T>& r, Batch& x) {
   constexpr int N = Vec<T>::N, U = ROW_BATCH;
   const int tid = threadIdx.x;
   const RowPart& p = r.p;
   const int body = p.head + p.first * N;  // the part's first column in a vector
   if (same_phase(r.row, r.grad)) {
-    uint4* out = reinterpret_cast<uint4*>(r.grad + p.head) + p.first;
-    for (int i = b * U * NT + tid; i < r.cached; i += NT) __stcs(out + i, grad_vec<T, ENT>(g, r.cache[i]));
-    if (r.cached < p.count) {
-      const uint4* in = part_vectors(r.row, p);
-      for (b = max(b, r.cached / (U * NT)); b < p.count / (U * NT); ++b) {
-        uint4 z[U];
+    const int whole = p.count / (U * NT), all = batches(p.count, NT);
+    uint4* out = reinterpret_cast<uint4*>(r.grad + p.head) + p.first + tid;
+    const uint4* in = part_vectors(r.row, p);
+    const uint4* c = r.cache + tid;
+    int b = 0;
+    if (r.cache) {
+      for (; b < whole; ++b, c += U * NT, out += U * NT) {
 #pragma unroll
-        for (int j = 0; j < U; ++j) z[j] = __ldcg(in + (b * U + j) * NT + tid);
+        for (int j = 0; j < U; ++j) x.v[j] = c[j * NT];
 #pragma unroll
-        for (int j = 0; j < U; ++j) __stcs(out + (b * U + j) * NT + tid, grad_vec<T, ENT>(g, z[j]));
+        for (int j = 0; j < U; ++j) __stcs(out + j * NT, grad_vec<T, ENT>(g, x.v[j]));
       }
-      for (int i = b * U * NT + tid; i < p.count; i += NT) __stcs(out + i, grad_vec<T, ENT>(g, __ldcg(in + i)));
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        if ((whole * U + j) * NT + tid < p.count) x.v[j] = c[j * NT];
+    } else {
+      for (; b < whole; ++b, out += U * NT) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) __stcs(out + j * NT, grad_vec<T, ENT>(g, x.v[j]));
+        if (b + 1 < all) x.load<NT, LAST>(in, b + 1, p.count);
+      }
     }
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if ((whole * U + j) * NT + tid < p.count) __stcs(out + j * NT, grad_vec<T, ENT>(g, x.v[j]));
     // the token's column, by the thread that has written its vector
     const int tv = g.token >= body ? (g.token - body) / N : -1;
     if (tv >= 0 && tv < p.count && tv % NT == tid) r.grad[g.token] = Vec<T>::narrow1(g.at_token);
   } else {
-    const T* c = reinterpret_cast<const T*>(r.cache);
-    for (int i = tid; i < p.count * N; i += NT) {
-      const T z = i < r.cached * N ? c[i] : r.row[body + i];
-      r.grad[body + i] = Vec<T>::narrow1(body + i == g.token ? g.at_token : grad1<T, ENT>(g, z));
-    }
+    const T* c = r.cache ? reinterpret_cast<const T*>(r.cache) : r.row + body;
+    for (int i = tid; i < p.count * N; i += NT)
+      r.grad[body + i] = Vec<T>::narrow1(body + i == g.token ? g.at_token : grad1<T, ENT>(g, c[i]));
   }
   if (p.edge_n)
     r.grad[p.edge_lo] =
         Vec<T>::narrow1(p.edge_lo == g.token ? g.at_token : grad1<T, ENT>(g, Vec<T>::narrow1(r.edge)));
-}
-
-// The gradient over this CTA's part of a row.
-template <typename T, bool ENT, int NT>
-__device__ __forceinline__ void grad_pass(const RowGrad& g, const GradRow<T>& r) {
-  constexpr int U = ROW_BATCH;
-  int b = 0;
-  if (same_phase(r.row, r.grad)) {
-    const uint4* c = r.cache + threadIdx.x;
-    uint4* out = reinterpret_cast<uint4*>(r.grad + r.p.head) + r.p.first + threadIdx.x;
-    for (; b < r.cached / (U * NT); ++b, c += U * NT, out += U * NT) grad_batch<T, ENT, NT>(g, c, out);
-  }
-  grad_tail<T, ENT, NT>(g, r, b);
 }
 
 // ---------------------------------------------------------------- host side
@@ -651,7 +691,7 @@ __device__ __forceinline__ void grad_pass(const RowGrad& g, const GradRow<T>& r)
 struct RowPlan {
   int size;     // CTAs a row
   int threads;  // 512, 256 or 128, 1024 of them a SM
-  int kept;     // vectors of a part that shared memory holds
+  int kept;     // vectors of a part, if shared memory keeps them; 0: it does not
 };
 
 constexpr int ROW_SMS = 152;
@@ -660,23 +700,42 @@ constexpr int ROW_SM_THREADS = 1024;
 inline int64_t row_vectors(int V, int es) { return (static_cast<int64_t>(V) * es + 15) / 16; }
 inline int64_t part_of(int64_t vecs, int size) { return (vecs + size - 1) / size; }
 
-// Bytes of rows that may be in flight at once.  What a first pass has read is there for the second as long as it
-// fits L2 beside the gradient that is written.
+// Bytes of rows that may be in flight at once.  What a first pass has read, or a prefetch has brought, is there for the
+// pass behind it as long as it fits L2 beside the gradient that is written.
 constexpr int64_t ROW_FLIGHT = 62 << 20;
 
-// `least`: vectors a thread that a part keeps when rows are split to fill the device; `beside`: bytes of shared memory of a
-// CTA beside what is kept (negative: nothing is kept).
-inline RowPlan plan_rows(int64_t rows, int V, int es, int least, int beside) {
-  const int64_t vecs = row_vectors(V, es);
-  RowPlan p = {1, vecs >= 1024 ? 256 : 128, 0};
+// Splits rows over more CTAs while the device is not full: few rows down to two vectors a thread, more
+// of them for an even end, down to `least` vectors a thread.
+inline void fill_device(RowPlan& p, int64_t rows, int64_t vecs, int least) {
   const int slots = ROW_SMS * (ROW_SM_THREADS / p.threads);
   for (; p.size < ROW_MAX_CLUSTER; p.size *= 2) {
     const int64_t part = vecs / (2 * p.size);
-    const bool spills = slots / p.size * vecs * 16 > ROW_FLIGHT && rows * p.size > slots / 2;
-    const bool few = rows * p.size < 2 * ROW_SMS && part >= p.threads;
+    const bool few = rows * p.size < 2 * ROW_SMS && part >= 2 * p.threads;
     const bool uneven = rows * p.size < 2 * slots && part >= least * p.threads;
-    if (!spills && !few && !uneven) break;
+    if (!few && !uneven) break;
   }
+}
+
+// Rows that pass once, without a prefetch.
+inline RowPlan plan_stream(int64_t rows, int V, int es) {
+  const int64_t vecs = row_vectors(V, es);
+  RowPlan p = {1, vecs >= 4096 ? 512 : vecs >= 1024 ? 256 : 128, 0};
+  fill_device(p, rows, vecs, 8);
+  return p;
+}
+
+// Rows that are prefetched, and kept or read again.  `beside`: bytes of shared memory of a CTA beside what is kept
+// (negative: nothing is kept).
+inline RowPlan plan_rows(int64_t rows, int V, int es, int least, int beside) {
+  const int64_t vecs = row_vectors(V, es);
+  RowPlan p = {1, vecs >= 2048 || rows <= 4 * ROW_SMS ? 256 : 128, 0};
+  const int slots = ROW_SMS * (ROW_SM_THREADS / p.threads);
+  const auto flight = [&] {
+    const int64_t at_once = slots / p.size;
+    return (rows < at_once ? rows : at_once) * vecs * 16;
+  };
+  while (p.size < ROW_MAX_CLUSTER && flight() > ROW_FLIGHT) p.size *= 2;
+  fill_device(p, rows, vecs, least);
   const int64_t part = part_of(vecs, p.size), a_sm = (rows * p.size + ROW_SMS - 1) / ROW_SMS;
   if (beside >= 0 && a_sm * (part * 16 + beside + 2048) <= ROW_SMEM) p.kept = static_cast<int>(part);
   return p;
@@ -700,7 +759,7 @@ cudaError_t launch_rows(const RowPlan& p, int smem, int64_t rows, cudaStream_t s
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = p.size > 1 ? 2 : 1;
   if (smem > 32 * 1024) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

@@ -16,12 +16,16 @@ namespace {
 
 template <typename T, bool ENT, int NT>
 __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) score_kernel(const __grid_constant__ ScoreArgs a) {
-  extern __shared__ uint4 smem[];
+  __shared__ Board<1> board;
   const int size = cluster_size(), rank = cluster_rank();
-  const Board<1> board = board_at<1>(smem, rank, size);
   const int64_t r = blockIdx.x / size;
+  const T* row = static_cast<const T*>(a.logits) + r * a.ld;
+  const RowPart p = row_part(row, a.V, rank, size);
+  if (size > 1) board.init();
   pdl_wait();
-  int t = a.tokens[r];
+  const int t = a.tokens[r];
+  Batch v;  // the first of the row's logits come with its token, whether they will count or not
+  v.load<NT>(part_vectors(row, p), 0, p.count);
   bool live = static_cast<uint32_t>(t) < static_cast<uint32_t>(a.V);
   if (a.cu) live = live && r >= a.cu[0] && r < a.cu[a.nseq];
   const bool first = rank == 0 && threadIdx.x == 0;
@@ -35,20 +39,11 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) score_kernel(const __
     }
     return;
   }
-  if (size > 1) cluster_arrive();
-  const T* row = static_cast<const T*>(a.logits) + r * a.ld;
+  if (size > 1) cluster_started();
   const float z = first ? Vec<T>::widen1(row[t]) : 0.f;
-  const RowPart p = row_part(row, a.V, rank, size);
-  prefetch_part(row, p);
-  RowStat st[1] = {stat_pass<T, ENT, NT>(row, p, nullptr, 0, a.k, NoMask{})};
-  st[0] = merge(st[0], stat_of(edge_of(row, p)), a.k);
-  st[0] = warp_merge<1, ENT>(st, a.k);
-  const float4 post[1] = {make_float4(st[0].m, st[0].s, st[0].u, 0.f)};
   if (size > 1) cluster_wait();
-  board.post(post);
-  board.wait();
-  if (rank != 0 || threadIdx.x >= 32) return;
-  const RowStat all = board.template stat<ENT>(0, a.k);
+  const RowStat mine = merge(stat_pass<T, ENT, NT>(row, p, nullptr, v, a.k, NoMask{}), stat_of(edge_of(row, p)), a.k);
+  const RowStat all = cluster_stat<ENT, false>(board, mine, a.k, rank, size);
   if (!first) return;
   const float ln = log1pf(all.s);
   const bool empty = all.m == -INFINITY;
@@ -59,9 +54,10 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) score_kernel(const __
   if (ENT) a.entropy[r] = empty ? 0.f : ln - 0.693147181f * all.u / (1.f + all.s);
 }
 
-// The factors of a row's gradient; false: there is none.
+// The factors of a row's gradient; false: there is none.  (By one thread: the 64-bit pipe is narrow.)
 template <typename T, bool ENT, bool SCORED>
-__device__ __forceinline__ bool spread_factors(const SpreadArgs& a, int64_t r, const T* row, RowGrad& g) {
+__device__ __forceinline__ bool spread_factors(const SpreadArgs& a, int64_t r, const T* row, const RowPart& p, int rank,
+                                               int size, int from, RowGrad& g) {
   g.k = a.k;
   g.B = 0.f;
   if (SCORED) {
@@ -69,8 +65,10 @@ __device__ __forceinline__ bool spread_factors(const SpreadArgs& a, int64_t r, c
     const float c = a.coef[r] * a.inv_t;
     g.token = sc.token;
     if (sc.token < 0 || c == 0.f) return false;
+    prefetch_part(row, p, from);
     g.ref = sc.m;
     g.A = -c / (1.f + sc.s);
+    if (!has_column<T>(p, rank, size, sc.token)) return true;  // in place, its part's CTA may have written it
     const float z = Vec<T>::widen1(row[sc.token]);
     g.at_token = c * (z == sc.m ? sc.s : 1.f + sc.s - ex2((z - sc.m) * a.k)) / (1.f + sc.s);
     return true;
@@ -79,11 +77,13 @@ __device__ __forceinline__ bool spread_factors(const SpreadArgs& a, int64_t r, c
   const float da = a.a[r] * a.inv_t, db = ENT ? a.b[r] * a.inv_t : 0.f, lse = a.lse[r];
   if (static_cast<uint32_t>(g.token) >= static_cast<uint32_t>(a.V) || (da == 0.f && db == 0.f) || lse == -INFINITY)
     return false;
+  prefetch_part(row, p, from);
   g.ref = static_cast<float>(lse * a.t64);
   const float rest = static_cast<float>((g.ref * a.inv_t64 - lse) * LOG2E);  // log2 p at z = ref
   const float f = exp2f(rest), H = ENT ? a.entropy[r] : 0.f;
   g.A = f * (-da - (ENT ? db * (0.693147181f * rest + H) : 0.f));
   g.B = -f * db * 0.693147181f;
+  if (!has_column<T>(p, rank, size, g.token)) return true;
   const float l = static_cast<float>(Vec<T>::widen1(row[g.token]) * a.inv_t64 - lse);
   g.at_token = -da * expm1f(l);
   if (ENT && l > -INFINITY) g.at_token -= db * expf(l) * (l + H);
@@ -94,41 +94,37 @@ template <typename T, bool ENT, bool SCORED, int NT>
 __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) spread_kernel(const __grid_constant__ SpreadArgs a) {
   __shared__ RowGrad s_grad;
   __shared__ bool s_live;
-  const int size = cluster_size(), rank = cluster_rank();
+  const int size = a.size, rank = blockIdx.x % a.size;
   // after a pass over all rows the last of them are still in L2
   const int64_t r = (SCORED ? gridDim.x - 1 - blockIdx.x : blockIdx.x) / size;
   const T* row = static_cast<const T*>(a.logits) + r * a.ld;
   T* grad = static_cast<T*>(a.grad) + r * a.gld;
   const RowPart p = row_part(row, a.V, rank, size);
   pdl_wait();
-  if (threadIdx.x == 0) {  // one thread: the 64-bit pipe is narrow
+  Batch v;  // the first of the row's logits come with its factors, whether they will count or not
+  v.load<NT, SCORED>(part_vectors(row, p), 0, p.count);
+  const float edge = edge_of(row, p);
+  if (threadIdx.x == 0) {
     RowGrad g;
-    s_live = spread_factors<T, ENT, SCORED>(a, r, row, g);
+    s_live = spread_factors<T, ENT, SCORED>(a, r, row, p, rank, size, ROW_BATCH * NT, g);
     s_grad = g;
-    if (s_live) prefetch_part(row, p);
   }
-  // in place, another CTA of the row may write the token's column once all have read it
-  if (size > 1) {
-    cluster_arrive();
-    cluster_wait();
-  } else {
-    __syncthreads();
-  }
+  __syncthreads();
   if (!s_live) {
     zero_part(grad, a.V, rank, size);
     return;
   }
-  const RowGrad g = s_grad;
-  grad_pass<T, ENT, NT>(g, GradRow<T>{row, grad, p, nullptr, 0, edge_of(row, p)});
+  // the loss of pairs begins with the rows that the pass before it has read last, and lets go of what it has read: 217 us
+  // instead of 225 at 1,300 rows of 201,088 in bf16
+  grad_pass<T, ENT, NT, SCORED>(s_grad, GradRow<T>{row, grad, p, nullptr, edge}, v);
 }
 
 template <typename T, bool ENT>
 cudaError_t scores(const ScoreArgs& a, int rows, cudaStream_t stream) {
-  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 8, -1);
-  const int smem = Board<1>::bytes(p.size * p.threads / 32);
-  return p.threads == 512   ? launch_rows<score_kernel<T, ENT, 512>>(p, smem, rows, stream, a)
-         : p.threads == 256 ? launch_rows<score_kernel<T, ENT, 256>>(p, smem, rows, stream, a)
-                            : launch_rows<score_kernel<T, ENT, 128>>(p, smem, rows, stream, a);
+  const RowPlan p = plan_stream(rows, a.V, sizeof(T));
+  return p.threads == 512   ? launch_rows<score_kernel<T, ENT, 512>>(p, 0, rows, stream, a)
+         : p.threads == 256 ? launch_rows<score_kernel<T, ENT, 256>>(p, 0, rows, stream, a)
+                            : launch_rows<score_kernel<T, ENT, 128>>(p, 0, rows, stream, a);
 }
 template <typename T>
 cudaError_t scores(const ScoreArgs& a, int rows, cudaStream_t stream) {
@@ -136,11 +132,15 @@ cudaError_t scores(const ScoreArgs& a, int rows, cudaStream_t stream) {
 }
 
 template <typename T, bool ENT, bool SCORED>
-cudaError_t spread(const SpreadArgs& a, int rows, cudaStream_t stream) {
-  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 8, -1);
-  return p.threads == 512   ? launch_rows<spread_kernel<T, ENT, SCORED, 512>>(p, 0, rows, stream, a)
-         : p.threads == 256 ? launch_rows<spread_kernel<T, ENT, SCORED, 256>>(p, 0, rows, stream, a)
-                            : launch_rows<spread_kernel<T, ENT, SCORED, 128>>(p, 0, rows, stream, a);
+cudaError_t spread(const SpreadArgs& args, int rows, cudaStream_t stream) {
+  RowPlan p = plan_rows(rows, args.V, sizeof(T), 8, -1);
+  SpreadArgs a = args;
+  a.size = p.size;  // the parts of a row need nothing of one another: no cluster
+  const int64_t parts = static_cast<int64_t>(rows) * p.size;
+  p.size = 1;
+  return p.threads == 512   ? launch_rows<spread_kernel<T, ENT, SCORED, 512>>(p, 0, parts, stream, a)
+         : p.threads == 256 ? launch_rows<spread_kernel<T, ENT, SCORED, 256>>(p, 0, parts, stream, a)
+                            : launch_rows<spread_kernel<T, ENT, SCORED, 128>>(p, 0, parts, stream, a);
 }
 template <typename T>
 cudaError_t spread(const SpreadArgs& a, int rows, cudaStream_t stream) {

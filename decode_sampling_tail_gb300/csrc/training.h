@@ -49,6 +49,7 @@ struct SpreadArgs {
   const float *lse, *a, *b, *entropy;
   const RowScore* score;
   const float* coef;
+  int size;  // CTAs a row (launch_spread's)
 };
 cudaError_t launch_spread(const SpreadArgs& a, int dtype, int rows, cudaStream_t stream);
 
