@@ -1,11 +1,16 @@
-// Distillation from a teacher's top logits and its gradient, in one pass over the student's logits.
+// Distillation from a teacher's top logits and its gradient, in one launch that reads the student's logits once.
 //
 // The teacher's list (and the weight of what lies outside it) gives q; the student's p is over the whole
-// vocabulary.  Listed columns are marked in a bit map and left out of the pass, so that
+// vocabulary.  Listed columns are marked in a bit map and left out of the statistics' pass, so that
 // the weight of the others is a sum of its own: 1 - sum of the listed p would lose it where the list holds nearly
 // everything.  The listed columns' statistics come from the entries.  Outside the list dz_v is a multiple of the
 // softmax over the others, p_rest - q_rest times it; the entries' values p_i - q_i are written
 // over it afterwards.  Where both p and q are above one half their difference is taken of 1 - q and 1 - p.
+//
+// Measured (GB300, by graph replay): 8 rows of 201088 in fp32 with 256 entries 10.4 us (floor 1.9: one CTA's chain, in
+// it two dependent loads for the list and its logits); 500 rows of 50021 in bf16 with 77 entries and the rest 27 (14.3: one
+// wave of CTAs, in step); 1024 rows of 201088 in fp32 with 256 entries 268 (241; 299 before the exchange went without
+// cluster barriers, 287 with them and the list's first loads together).
 #include "../../include/tail.h"
 #include "row_softmax.cuh"
 #include "training.h"
@@ -231,7 +236,7 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
   float z0 = 0.f;
   if (id0 >= lo && id0 < hi) z0 = Vec<T>::widen1(row[id0]);
   bool any = id0 >= 0;
-  RowStat st[1] = {stat_of(any ? v0 : -INFINITY)};
+  RowStat st = stat_of(any ? v0 : -INFINITY);
   if (listed) {
     l.ids[tid] = id0;
     l.t[tid] = v0;
@@ -243,10 +248,10 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
     l.ids[i] = ok ? id : -1;
     l.t[i] = v;
     any = any || ok;
-    if (ok) st[0] = merge(st[0], stat_of(v), a.k);
+    if (ok) st = merge(st, stat_of(v), a.k);
   }
-  st[0] = warp_merge<false>(st[0], a.k);
-  if ((tid & 31) == 0) s_warp[tid >> 5] = st[0];
+  st = warp_merge<false>(st, a.k);
+  if ((tid & 31) == 0) s_warp[tid >> 5] = st;
   if (!__syncthreads_or(any && w != 0.f)) {
     if (kept) copy_wait(0);
     if (rank == 0 && tid == 0) a.loss[r] = 0.f;
@@ -268,13 +273,13 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
     l.z[i] = i == tid ? z0 : Vec<T>::widen1(row[id]);
   });
   Batch v;
-  if (!kept) v.load<NT>(part_vectors(row, p), 0, p.count);
+  if (!kept) v = Batch::from<NT>(part_vectors(row, p), 0, p.count);
   const float edge = edge_of(row, p);
   if (size > 1) cluster_wait();
   if (tid < 32) {
-    st[0] = tid < NT / 32 ? s_warp[tid] : no_stat();
-    st[0] = warp_merge<false>(st[0], a.k);
-    if (tid == 0) s_teacher = teacher_of(st[0], rest, a.k, a.k64);
+    st = tid < NT / 32 ? s_warp[tid] : no_stat();
+    st = warp_merge<false>(st, a.k);
+    if (tid == 0) s_teacher = teacher_of(st, rest, a.k, a.k64);
   }
   twice = __syncthreads_or(twice);
   const Teacher& t = s_teacher;
@@ -291,7 +296,7 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
                                   ListMask<N, NT>{l.map, reinterpret_cast<const uint8_t*>(l.flags)});
   if (p.edge_n && !(l.map[(p.edge_lo - origin) >> 5] >> ((p.edge_lo - origin) & 31) & 1))
     x.out = merge(x.out, stat_of(edge), a.k);
-  if (GRAD && !kept) v.load<NT>(part_vectors(row, p), 0, p.count);  // for the second pass, while the factors are formed
+  if (GRAD && !kept) v = Batch::from<NT>(part_vectors(row, p), 0, p.count);  // for the second pass, while the factors are formed
   x.in = no_stat();
   entries([&](int i, int id) {
     if (owner(i, id)) x.in = merge(x.in, stat_of(l.z[i]), a.k);
@@ -350,9 +355,8 @@ cudaError_t launch(DistillArgs& a, int rows, cudaStream_t stream) {
   a.cache_at = (beside + 15) / 16;
   a.kept = p.kept;
   const int smem = 16 * (a.cache_at + a.kept);
-  return p.threads == 512   ? launch_rows<distill_kernel<T, GRAD, 512>>(p, smem, rows, stream, a)
-         : p.threads == 256 ? launch_rows<distill_kernel<T, GRAD, 256>>(p, smem, rows, stream, a)
-                            : launch_rows<distill_kernel<T, GRAD, 128>>(p, smem, rows, stream, a);
+  return p.threads == 256 ? launch_rows<distill_kernel<T, GRAD, 256>>(p, smem, rows, stream, a)
+                          : launch_rows<distill_kernel<T, GRAD, 128>>(p, smem, rows, stream, a);
 }
 
 template <typename T>

@@ -1,9 +1,13 @@
-// The clipped policy loss with its KL and entropy terms, and its gradient, in one pass over the logits.
+// The clipped policy loss with its KL and entropy terms, and its gradient, in one launch that reads the logits once.
 //
-// A row's loss depends on that row alone, so a cluster that holds the row on chip reads it once: its CTAs take
-// their parts into shared memory while they form the statistics, exchange those through the cluster, and write the
-// gradient from what they hold.  The slope of the loss by the token's log-probability, c, and
-// the entropy's factor give dz_v = (c (1[v = t] - p_v) + f p_v (log p_v + H)) / T.
+// A row's loss depends on that row alone: its statistics, its token's log-probability l and its entropy H give the loss,
+// the slope c of the loss by l and the entropy's factor f, and these dz_v = (c (1[v = t] - p_v) + f p_v (log p_v + H)) / T
+// in a second pass over the row, from L2 or shared memory (row_softmax.cuh).  At the token 1 - p is s / (1 + s) where it is
+// the likeliest.  One warp forms the factors; formed by every thread they cost 1.5 instructions a column.
+//
+// Measured (GB300, by graph replay): 12 rows of 201088 in fp32 7.5 us (floor 2.9: the chain of one CTA: first loads 1.6,
+// statistics 1.5, exchange and factors 1.5, gradient 1.9); 333 rows of 50021 in fp16, a fifth ignored, 16.5 (9.0: all
+// CTAs run at once, in step); 2048 rows of 201088 in bf16 253 (234).
 #include "../../include/tail.h"
 #include "row_softmax.cuh"
 #include "training.h"
@@ -88,7 +92,7 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) policy_kernel(const _
   if (kept)
     fetch_part<T, NT>(row, p, cache);
   else
-    v.load<NT>(part_vectors(row, p), 0, p.count);
+    v = Batch::from<NT>(part_vectors(row, p), 0, p.count);
   if (static_cast<uint32_t>(x.t) >= static_cast<uint32_t>(a.V) || x.w == 0.f) {
     if (kept) copy_wait(0);
     if (first) {
@@ -99,9 +103,10 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) policy_kernel(const _
     if (GRAD) zero_part(grad, a.V, rank, size);
     return;
   }
-  if (!kept) prefetch_part(row, p, ROW_BATCH * NT);
+  if (GRAD && !kept) prefetch_part(row, p, ROW_BATCH * NT);
   if (size > 1) cluster_started();
   const float edge = edge_of(row, p);
+  x.z = 0.f;
   if (threadIdx.x < 32) {
     x.z = Vec<T>::widen1(row[x.t]);
     x.old = a.old[x.r];
@@ -112,8 +117,8 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) policy_kernel(const _
   RowStat st = stat_pass<T, ENT, NT>(row, p, kept ? cache : nullptr, v, a.k, NoMask{});
   if (p.edge_n) st = merge(st, stat_of(edge), a.k);
   // the second pass's first vectors come while the factors are formed
-  if (GRAD && !kept) v.load<NT>(part_vectors(row, p), 0, p.count);
-  st = cluster_stat<ENT, GRAD>(board, st, a.k, rank, size);
+  if (GRAD && !kept) v = Batch::from<NT>(part_vectors(row, p), 0, p.count);
+  st = cluster_stat<ENT, GRAD>(board, st, x.z, a.k, rank, size);
   if (threadIdx.x < 32 && (GRAD || rank == 0)) {  // one warp forms the row's factors for all
     const RowGrad g = policy_row<ENT>(a, x, st, first);
     if (GRAD && threadIdx.x == 0) s_grad = g;
@@ -123,20 +128,23 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) policy_kernel(const _
   grad_pass<T, ENT, NT>(s_grad, GradRow<T>{row, grad, p, kept ? cache : nullptr, edge}, v);
 }
 
-template <typename T, bool ENT, bool GRAD>
+template <typename T, bool ENT>
 cudaError_t launch(PolicyArgs& a, int rows, cudaStream_t stream) {
-  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 8, GRAD ? 0 : -1);
+  if (!a.grad) {
+    const RowPlan p = plan_stream(rows, a.V, sizeof(T));
+    return p.threads == 512   ? launch_rows<policy_kernel<T, ENT, false, 512>>(p, 0, rows, stream, a)
+           : p.threads == 256 ? launch_rows<policy_kernel<T, ENT, false, 256>>(p, 0, rows, stream, a)
+                              : launch_rows<policy_kernel<T, ENT, false, 128>>(p, 0, rows, stream, a);
+  }
+  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 8, 0);
   a.kept = p.kept;
-  const int smem = 16 * p.kept;
-  return p.threads == 512   ? launch_rows<policy_kernel<T, ENT, GRAD, 512>>(p, smem, rows, stream, a)
-         : p.threads == 256 ? launch_rows<policy_kernel<T, ENT, GRAD, 256>>(p, smem, rows, stream, a)
-                            : launch_rows<policy_kernel<T, ENT, GRAD, 128>>(p, smem, rows, stream, a);
+  return p.threads == 256 ? launch_rows<policy_kernel<T, ENT, true, 256>>(p, 16 * p.kept, rows, stream, a)
+                          : launch_rows<policy_kernel<T, ENT, true, 128>>(p, 16 * p.kept, rows, stream, a);
 }
 
 template <typename T>
 cudaError_t launch(PolicyArgs& a, int rows, bool ent, cudaStream_t s) {
-  if (a.grad) return ent ? launch<T, true, true>(a, rows, s) : launch<T, false, true>(a, rows, s);
-  return ent ? launch<T, true, false>(a, rows, s) : launch<T, false, false>(a, rows, s);
+  return ent ? launch<T, true>(a, rows, s) : launch<T, false>(a, rows, s);
 }
 
 }  // namespace

@@ -3,7 +3,11 @@
 // Three launches: the log-probabilities of all counted rows (token_logprobs.cu); a CTA a pair, which adds up
 // its two sequences' log-probabilities in row order (64-bit sums: a margin is the difference of two sums of hundreds),
 // forms the loss and leaves each row its factor; the gradient from the rows' statistics.  The factor of a row needs
-// every row of both sequences, so the logits pass twice, the second time from L2 where they fit it.
+// every row of both sequences, so the logits pass twice; the second pass begins with the rows that the first has read last,
+// which are still in L2.
+//
+// Measured (GB300, by graph replay): one pair, 26 rows of 32000 in fp16, 9.9 us (floor 0.4: three launches in a chain);
+// 8 pairs, 1300 rows of 201088 in bf16, 215 (134 for one pass of reads; 217 for two from HBM).
 #include "../../include/tail.h"
 #include "row_softmax.cuh"
 #include "training.h"

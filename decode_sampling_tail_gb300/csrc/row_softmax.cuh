@@ -2,6 +2,16 @@
 // preference_loss.cu, distill_topk.cu): a row's softmax statistics and its gradient, the row split over
 // the CTAs of a cluster.
 //
+// What bounds them is memory: 10 to 12 instructions a column leave HBM the limit of large calls, and the latency of a
+// CTA's chain (token, statistics, exchange, factors, gradient) that of small ones.  A loss that depends on its row
+// alone reads the row from HBM once: the statistics' pass is followed at once by the gradient's, which finds the
+// row in L2, as long as no more than ROW_FLIGHT bytes of rows are under way, or in shared memory when all of a call's rows fit
+// there.  Measured at 2048 rows of 201088 columns (1.57 GB of bf16 read and written): 253 us, 0.93 of the copy rate.  Before:
+// parts in shared memory by 2 CTAs an SM 341 us; 4 CTAs of 256 threads an SM that read twice 295; each part brought to
+// L2 by one bulk prefetch 266; the exchange without cluster barriers, first loads ahead of their need 256; loads a batch
+// ahead in the statistics 253.  Persistent CTAs that fetch their next row into shared memory while they write the present
+// one's gradient took 337 to 438: one or two CTAs an SM do not cover the chain.
+//
 // Statistics.  With m the row's maximum and a_v = (z_v - m) log2(e) / T <= 0:
 //   s = sum of 2^a_v over every column but one at the maximum,  u = sum of a_v 2^a_v  (fp32).
 // One instance of the maximum stays out of s, since its weight 1 would swallow what the others add up to: with
@@ -24,7 +34,6 @@
 
 namespace tail {
 
-constexpr int ROW_MAX_V = 1 << 20;      // columns
 constexpr int ROW_BATCH = 4;            // vectors a thread takes at a time
 constexpr int ROW_MAX_CLUSTER = 8;      // CTAs a row, the portable size
 constexpr int ROW_SMEM = 224 * 1024;    // dynamic shared memory of a CTA at most
@@ -96,9 +105,6 @@ struct Vec<float> {
   }
   static __device__ __forceinline__ float widen1(float v) { return v; }
   static __device__ __forceinline__ float narrow1(float v) { return v; }
-  static __device__ __forceinline__ uint4 fill() {
-    return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
-  }
   // columns whose bit is set become -inf
   static __device__ __forceinline__ void mask(uint4& v, uint32_t bits) {
     if (bits & 1) v.x = 0xff800000u;
@@ -150,9 +156,6 @@ struct Vec<__nv_bfloat16> {
   }
   static __device__ __forceinline__ float widen1(__nv_bfloat16 v) { return __bfloat162float(v); }
   static __device__ __forceinline__ __nv_bfloat16 narrow1(float v) { return __float2bfloat16_rn(v); }
-  static __device__ __forceinline__ uint4 fill() {
-    return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-  }
   static __device__ __forceinline__ void mask(uint4& v, uint32_t bits) { mask16<0xff80u>(v, bits); }
 };
 
@@ -177,9 +180,6 @@ struct Vec<__half> {
   }
   static __device__ __forceinline__ float widen1(__half v) { return __half2float(v); }
   static __device__ __forceinline__ __half narrow1(float v) { return __float2half_rn(v); }
-  static __device__ __forceinline__ uint4 fill() {
-    return make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u);
-  }
   static __device__ __forceinline__ void mask(uint4& v, uint32_t bits) { mask16<0xfc00u>(v, bits); }
 };
 
@@ -427,9 +427,10 @@ struct Board {
 };
 
 // The cluster's statistics in the first warp of every CTA (ALL) or of the first, from each thread's; the same bits in all
-// lanes.  NaN when another CTA's have not come.  Ends without a barrier.
+// lanes.  NaN when another CTA's have not come.  Ends without a barrier.  `seen`: what the first warp has read of the
+// row's other parts; it goes with its statistics, so that a CTA that has all of them may write its part in place.
 template <bool ENT, bool ALL>
-__device__ __forceinline__ RowStat cluster_stat(Board<1>& board, RowStat st, float k, int rank, int size) {
+__device__ __forceinline__ RowStat cluster_stat(Board<1>& board, RowStat st, float seen, float k, int rank, int size) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   st = warp_merge<ENT>(st, k);
   if (lane == 0) board.warp[0][warp] = make_float4(st.m, st.s, st.u, 0.f);
@@ -442,7 +443,7 @@ __device__ __forceinline__ RowStat cluster_stat(Board<1>& board, RowStat st, flo
   }
   st = warp_merge<ENT>(st, k);
   if (size == 1) return st;
-  const float4 mine[1] = {make_float4(st.m, st.s, st.u, 0.f)};
+  const float4 mine[1] = {make_float4(st.m, st.s, st.u, seen)};
   float4 all[1];
   const bool ok = board.template exchange<ALL>(rank, size, mine, all);
   if (!ALL && rank != 0) return st;
@@ -550,19 +551,21 @@ __device__ __forceinline__ uint4 load_last(const uint4* p) {
 struct Batch {
   uint4 v[ROW_BATCH];
 
-  // Batch b of n vectors in memory; those behind the end are not touched.
+  // Batch b of n vectors in memory; zeros, unread, behind the end.
   template <int NT, bool LAST = false>
-  __device__ __forceinline__ void load(const uint4* in, int b, int n) {
+  static __device__ __forceinline__ Batch from(const uint4* in, int b, int n) {
+    Batch x;
     const int i0 = b * ROW_BATCH * NT + static_cast<int>(threadIdx.x);
     const uint4* at = in + i0;
     if ((b + 1) * ROW_BATCH * NT <= n) {
 #pragma unroll
-      for (int j = 0; j < ROW_BATCH; ++j) v[j] = LAST ? load_last(at + j * NT) : __ldcg(at + j * NT);
+      for (int j = 0; j < ROW_BATCH; ++j) x.v[j] = LAST ? load_last(at + j * NT) : __ldcg(at + j * NT);
     } else {
 #pragma unroll
       for (int j = 0; j < ROW_BATCH; ++j)
-        if (i0 + j * NT < n) v[j] = LAST ? load_last(at + j * NT) : __ldcg(at + j * NT);
+        x.v[j] = i0 + j * NT >= n ? make_uint4(0, 0, 0, 0) : LAST ? load_last(at + j * NT) : __ldcg(at + j * NT);
     }
+    return x;
   }
 };
 
@@ -614,14 +617,19 @@ __device__ __forceinline__ RowStat stat_pass(const T* row, const RowPart& p, con
     for (int i = whole * U * NT + tid; i < p.count; i += NT) stat_single<T, ENT, NT>(acc, cache[i], i, k, mask);
   } else {
     const uint4* in = part_vectors(row, p);
-    for (int b = 0; b < whole; ++b) {
+    for (int b = 0; b + 1 < all; ++b) {  // a batch is under way while the one before it is taken
+      const Batch n = Batch::from<NT>(in, b + 1, p.count);
       stat_batch<T, ENT, NT>(acc, x.v, b, k, mask);
-      if (b + 1 < all) x.load<NT>(in, b + 1, p.count);
+      x = n;
     }
+    if (whole == all) {
+      if (all > 0) stat_batch<T, ENT, NT>(acc, x.v, all - 1, k, mask);
+    } else {
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int i = (whole * U + j) * NT + tid;
-      if (i < p.count) stat_single<T, ENT, NT>(acc, x.v[j], i, k, mask);
+      for (int j = 0; j < U; ++j) {
+        const int i = (whole * U + j) * NT + tid;
+        if (i < p.count) stat_single<T, ENT, NT>(acc, x.v[j], i, k, mask);
+      }
     }
   }
   return acc.done(k);
@@ -639,8 +647,8 @@ struct GradRow {
 
 // The gradient over this CTA's part of a row, from shared memory or from memory with the first batch in x.  Rows whose
 // gradient lies elsewhere in its 16-byte vectors are written column by column; then what is kept must be visible
-// to all threads.
-template <typename T, bool ENT, int NT, bool LAST = false>
+// to all threads.  DEEP: a batch is under way while the one before it is written.
+template <typename T, bool ENT, int NT, bool LAST = false, bool DEEP = false>
 __device__ __forceinline__ void grad_pass(const RowGrad& g, const GradRow<T>& r, Batch& x) {
   constexpr int N = Vec<T>::N, U = ROW_BATCH;
   const int tid = threadIdx.x;
@@ -663,10 +671,21 @@ __device__ __forceinline__ void grad_pass(const RowGrad& g, const GradRow<T>& r,
       for (int j = 0; j < U; ++j)
         if ((whole * U + j) * NT + tid < p.count) x.v[j] = c[j * NT];
     } else {
-      for (; b < whole; ++b, out += U * NT) {
+      for (; b + 1 < all; ++b, out += U * NT) {
+        if constexpr (DEEP) {
+          const Batch n = Batch::from<NT, LAST>(in, b + 1, p.count);
+#pragma unroll
+          for (int j = 0; j < U; ++j) __stcs(out + j * NT, grad_vec<T, ENT>(g, x.v[j]));
+          x = n;
+        } else {
+#pragma unroll
+          for (int j = 0; j < U; ++j) __stcs(out + j * NT, grad_vec<T, ENT>(g, x.v[j]));
+          x = Batch::from<NT, LAST>(in, b + 1, p.count);
+        }
+      }
+      if (whole == all && all > 0) {
 #pragma unroll
         for (int j = 0; j < U; ++j) __stcs(out + j * NT, grad_vec<T, ENT>(g, x.v[j]));
-        if (b + 1 < all) x.load<NT, LAST>(in, b + 1, p.count);
       }
     }
 #pragma unroll

@@ -5,7 +5,12 @@
 // Gradient: from the rows' log-sum-exps, with p_v = 2^((z_v - R) k + r), R = fp32(lse T) and r the rest of lse that
 //   R leaves (formed in 64 bits, once a row): differences from R keep their bits near the
 //   maximum, where z k - lse log2(e) would lose up to 2^-19 of p.  Every column is read and written
-//   once, by any CTA.  At the token 1 - p is -expm1(log p).
+//   once; the parts of a row need nothing of one another.  At the token 1 - p is -expm1(log p).
+//
+// Both are bound by memory.  Measured (GB300, by graph replay): 4 rows of 201088 in fp32, scored with their entropies,
+// 3.3 us (floor 0.5: one CTA's chain of launch, first load, six batches, exchange); 1536 rows of 201088 in bf16, a tenth
+// ignored, 85 (83; 91 with each batch loaded behind the one before it); the gradient of 777 rows of 50021 in bf16
+// 25.9 (22.7; 30 without the prefetch of a part, 28 with a cluster barrier before it).
 #include "../../include/tail.h"
 #include "row_softmax.cuh"
 #include "training.h"
@@ -24,8 +29,8 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) score_kernel(const __
   if (size > 1) board.init();
   pdl_wait();
   const int t = a.tokens[r];
-  Batch v;  // the first of the row's logits come with its token, whether they will count or not
-  v.load<NT>(part_vectors(row, p), 0, p.count);
+  // the first of the row's logits come with its token, whether they will count or not
+  Batch v = Batch::from<NT>(part_vectors(row, p), 0, p.count);
   bool live = static_cast<uint32_t>(t) < static_cast<uint32_t>(a.V);
   if (a.cu) live = live && r >= a.cu[0] && r < a.cu[a.nseq];
   const bool first = rank == 0 && threadIdx.x == 0;
@@ -43,7 +48,7 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) score_kernel(const __
   const float z = first ? Vec<T>::widen1(row[t]) : 0.f;
   if (size > 1) cluster_wait();
   const RowStat mine = merge(stat_pass<T, ENT, NT>(row, p, nullptr, v, a.k, NoMask{}), stat_of(edge_of(row, p)), a.k);
-  const RowStat all = cluster_stat<ENT, false>(board, mine, a.k, rank, size);
+  const RowStat all = cluster_stat<ENT, false>(board, mine, 0.f, a.k, rank, size);
   if (!first) return;
   const float ln = log1pf(all.s);
   const bool empty = all.m == -INFINITY;
@@ -101,8 +106,8 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) spread_kernel(const _
   T* grad = static_cast<T*>(a.grad) + r * a.gld;
   const RowPart p = row_part(row, a.V, rank, size);
   pdl_wait();
-  Batch v;  // the first of the row's logits come with its factors, whether they will count or not
-  v.load<NT, SCORED>(part_vectors(row, p), 0, p.count);
+  // the first of the row's logits come with its factors, whether they will count or not
+  Batch v = Batch::from<NT, SCORED>(part_vectors(row, p), 0, p.count);
   const float edge = edge_of(row, p);
   if (threadIdx.x == 0) {
     RowGrad g;
@@ -116,7 +121,7 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) spread_kernel(const _
   }
   // the loss of pairs begins with the rows that the pass before it has read last, and lets go of what it has read: 217 us
   // instead of 225 at 1,300 rows of 201,088 in bf16
-  grad_pass<T, ENT, NT, SCORED>(s_grad, GradRow<T>{row, grad, p, nullptr, edge}, v);
+  grad_pass<T, ENT, NT, SCORED, true>(s_grad, GradRow<T>{row, grad, p, nullptr, edge}, v);
 }
 
 template <typename T, bool ENT>
@@ -138,9 +143,8 @@ cudaError_t spread(const SpreadArgs& args, int rows, cudaStream_t stream) {
   a.size = p.size;  // the parts of a row need nothing of one another: no cluster
   const int64_t parts = static_cast<int64_t>(rows) * p.size;
   p.size = 1;
-  return p.threads == 512   ? launch_rows<spread_kernel<T, ENT, SCORED, 512>>(p, 0, parts, stream, a)
-         : p.threads == 256 ? launch_rows<spread_kernel<T, ENT, SCORED, 256>>(p, 0, parts, stream, a)
-                            : launch_rows<spread_kernel<T, ENT, SCORED, 128>>(p, 0, parts, stream, a);
+  return p.threads == 256 ? launch_rows<spread_kernel<T, ENT, SCORED, 256>>(p, 0, parts, stream, a)
+                          : launch_rows<spread_kernel<T, ENT, SCORED, 128>>(p, 0, parts, stream, a);
 }
 template <typename T>
 cudaError_t spread(const SpreadArgs& a, int rows, cudaStream_t stream) {

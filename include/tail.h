@@ -597,7 +597,7 @@ const char* tail_last_error(void);
  *                  address modulo 16 bytes are the fast case.
  *   tokens         [rows] int32: the token that row r's logits predicted.  A row whose token is outside [0, V)
  *                  (-1: a prompt position, padding) is ignored: its results are 0, its gradient is
- *                  zeros, its logits are not read.
+ *                  zeros, whatever its logits hold.
  *   temperature    T, from 2^-64 to 2^64 (a double: a rounded T would shift every z / T).
  *   weight_opt     [rows] (or [pairs]) fp32 factors of the losses, NULL: 1.  A row (pair) of weight 0 is
  *                  left out: loss and gradient 0, whatever the formula gives.
@@ -613,7 +613,8 @@ const char* tail_last_error(void);
  * Sums are fp32, one instance of a row's maximum apart from the others, so that the log-probability of a
  * likely token and its distance 1 - p keep about 2^-20 of themselves.  Results are deterministic and
  * a row's do not depend on the others', except by the order of sums, which follows rows, V and the dtype.  No handle
- * and no allocation; asynchronous on `stream` of the current device; everything is read in stream order.
+ * and no allocation; asynchronous on `stream` of the current device; everything is read in stream order.  The CTAs of a
+ * row wait for one another's sums for a second at most; should they not come, that row's results are NaN.
  */
 
 /*
@@ -628,7 +629,7 @@ int tail_token_logprobs(int32_t rows, int32_t V, const void* logits, int32_t log
  * The gradient of sum_r d_logprob[r] l_r(token) + d_entropy[r] H_r, for losses formed by the caller:
  *   dz_v = (d_logprob (1[v = token] - p_v) - d_entropy p_v (log p_v + H)) / T,  log p_v = z_v / T - lse.
  *   lse, entropy_opt  [rows] as tail_token_logprobs gives them; entropy_opt goes with d_entropy_opt.
- * A row with both factors 0 gets zeros and is not read.  One launch.
+ * A row with both factors 0 gets zeros, whatever its logits hold.  One launch.
  */
 int tail_token_logprobs_grad(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype, int64_t logits_ld,
                              const int32_t* tokens, double temperature, const float* lse, const float* d_logprob,
@@ -657,7 +658,7 @@ int tail_policy_loss(int32_t rows, int32_t V, const void* logits, int32_t logits
  *   h = beta ((L_2i - ref_2i) - (L_2i+1 - ref_2i+1)) - margin,
  *   loss_i = weight_i ((1 - label_smoothing) log(1 + exp(-h)) + label_smoothing log(1 + exp(h))).
  *   cu_rows        [nseq + 1] int32 (device), non-decreasing: sequence s has the rows [cu_rows[s], cu_rows[s + 1]).  Rows
- *                  outside [cu_rows[0], cu_rows[nseq]) are ignored: gradient zeros, not read.  (Values
+ *                  outside [cu_rows[0], cu_rows[nseq]) are ignored: gradient zeros.  (Values
  *                  outside [0, rows] are cut.)
  *   ref_logprob_opt  [nseq] fp32: the reference model's L_s, NULL: 0.
  *   label_smoothing  in [0, 1];  average 0 or 1.
