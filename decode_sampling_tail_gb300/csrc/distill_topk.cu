@@ -7,10 +7,10 @@
 // softmax over the others, p_rest - q_rest times it; the entries' values p_i - q_i are written
 // over it afterwards.  Where both p and q are above one half their difference is taken of 1 - q and 1 - p.
 //
-// Measured (GB300, by graph replay): 8 rows of 201088 in fp32 with 256 entries 10.4 us (floor 1.9: one CTA's chain, in
+// Measured (GB300, by graph replay): 8 rows of 201088 in fp32 with 256 entries 10.3 us (floor 1.9: one CTA's chain, in
 // it two dependent loads for the list and its logits); 500 rows of 50021 in bf16 with 77 entries and the rest 27 (14.3: one
-// wave of CTAs, in step); 1024 rows of 201088 in fp32 with 256 entries 268 (241; 299 before the exchange went without
-// cluster barriers, 287 with them and the list's first loads together).
+// wave of CTAs, in step); 1024 rows of 201088 in fp32 with 256 entries 260 (241; 299 with cluster barriers in the
+// exchange and the list's loads one after another, 264 with every warp going through the whole list).
 #include "../../include/tail.h"
 #include "row_softmax.cuh"
 #include "training.h"
@@ -51,6 +51,7 @@ struct Teacher {
   float m, D, others, ln;  // ln = log(1 + others)
   float q_rest, lq_rest;   // and its logarithm
   float q_list;            // 1 - q_rest
+  float inv;               // 1 / (1 + others)
   bool rest_is_max;
   bool any;  // whether there is anything to aim at
 };
@@ -95,8 +96,8 @@ __device__ __forceinline__ Teacher teacher_of(const RowStat& st, float rest, flo
   return t;
 }
 
-// A CTA's dynamic shared memory: the list (ids and the teacher's values), the student's logits at its
-// entries, the bit map of the part's listed columns, and a byte a thread and batch that says which of its
+// A CTA's dynamic shared memory: the list's entries in its part, in their order (ids, the teacher's values, the student's
+// logits), the bit map of the part's listed columns, and a byte a thread and batch that says which of its
 // vectors have one.  What is kept of the part follows.
 struct List {
   int32_t* ids;
@@ -139,16 +140,18 @@ __device__ __forceinline__ void pack(const Sums& s, float4 (&v)[2]) {
 __device__ __forceinline__ Sums unpack(const float4& a, const float4& b) {
   return Sums{RowStat{a.x, a.y, 0.f}, RowStat{b.x, b.y, 0.f}, a.z, a.w};
 }
-// A warp's lanes' together.
-__device__ __forceinline__ Sums merge_sums(const Sums& s, float k, float inv_t) {
-  Sums r;
-  r.out = warp_merge<false>(s.out, k);
-  r.in = warp_merge<false>(s.in, k);
-  float C = s.C;
-  if (!(s.Q == 0.f)) C += s.Q * ((finite_ref(r.in.m) - finite_ref(s.in.m)) * inv_t);
-  r.C = warp_sum(C);
-  r.Q = warp_sum(s.Q);
-  return r;
+// A warp's lanes' together: of the listed columns, and of all.
+__device__ __forceinline__ void merge_listed(Sums& s, float k, float inv_t) {
+  const RowStat in = warp_merge<false>(s.in, k);
+  if (!(s.Q == 0.f)) s.C += s.Q * ((finite_ref(in.m) - finite_ref(s.in.m)) * inv_t);
+  s.in = in;
+  s.C = warp_sum(s.C);
+  s.Q = warp_sum(s.Q);
+}
+__device__ __forceinline__ Sums merge_sums(Sums s, float k, float inv_t) {
+  s.out = warp_merge<false>(s.out, k);
+  merge_listed(s, k, inv_t);
+  return s;
 }
 
 // A row's loss and the factors of its gradient, by one warp.
@@ -189,11 +192,14 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
   constexpr int N = Vec<T>::N;
   extern __shared__ uint4 smem[];
   __shared__ Board<2> board;
-  __shared__ RowStat s_warp[NT / 32];
+  constexpr int WARPS = NT / 32;
+  static_assert(DISTILL_MAX_K / NT * WARPS <= 32, "a lane a round and warp");
+  __shared__ RowStat s_warp[WARPS];
+  __shared__ int s_count[32];  // entries in the part by round of NT and warp
   __shared__ Teacher s_teacher;
   __shared__ RowGrad s_grad;
   __shared__ EntryGrad s_entry;
-  const int size = cluster_size(), rank = cluster_rank(), tid = threadIdx.x;
+  const int size = cluster_size(), rank = cluster_rank(), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   List l;
   l.ids = reinterpret_cast<int32_t*>(smem);
   l.t = reinterpret_cast<float*>(l.ids + a.k_list);
@@ -209,12 +215,7 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
   // The part's columns [lo, hi); bit 0 of the map is one vector in front of its first whole one.
   const int body = p.head + p.first * N, origin = body - N;
   const int lo = rank == 0 ? 0 : body, hi = rank == size - 1 ? a.V : body + p.count * N;
-  const auto entries = [&](auto f) {  // f(entry, its column) for this thread's entries in the part
-    for (int i = tid; i < a.k_list; i += NT) {
-      const int id = l.ids[i];
-      if (id >= lo && id < hi) f(i, id);
-    }
-  };
+  const auto in_part = [&](int id) { return id >= lo && id < hi; };
   if (size > 1) board.init();
   for (int i = tid; i < a.map_words + a.flag_words; i += NT) l.map[i] = 0;  // (the flags lie behind the map)
   pdl_wait();
@@ -233,25 +234,26 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
   else if (early)
     prefetch_part(row, p, 0);
   if (static_cast<uint32_t>(id0) >= static_cast<uint32_t>(a.V)) id0 = -1;
-  float z0 = 0.f;
-  if (id0 >= lo && id0 < hi) z0 = Vec<T>::widen1(row[id0]);
+  const bool mine0 = in_part(id0);
+  const float z0 = mine0 ? Vec<T>::widen1(row[id0]) : 0.f;
   bool any = id0 >= 0;
   RowStat st = stat_of(any ? v0 : -INFINITY);
-  if (listed) {
-    l.ids[tid] = id0;
-    l.t[tid] = v0;
-  }
-  for (int i = tid + NT; i < a.k_list; i += NT) {
-    const int id = a.idx[r * a.ild + i];
-    const float v = list_value(a, r, i);
+  const int rounds = (a.k_list + NT - 1) / NT;
+  const auto count = [&](int j, bool mine) {
+    const uint32_t at = __ballot_sync(0xffffffffu, mine);
+    if (lane == 0) s_count[j * WARPS + warp] = __popc(at);
+  };
+  count(0, mine0);
+  for (int j = 1; j < rounds; ++j) {
+    const int i = j * NT + tid;
+    const int id = i < a.k_list ? a.idx[r * a.ild + i] : -1;
     const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.V);
-    l.ids[i] = ok ? id : -1;
-    l.t[i] = v;
     any = any || ok;
-    if (ok) st = merge(st, stat_of(v), a.k);
+    if (ok) st = merge(st, stat_of(list_value(a, r, i)), a.k);
+    count(j, ok && in_part(id));
   }
-  st = warp_merge<false>(st, a.k);
-  if ((tid & 31) == 0) s_warp[tid >> 5] = st;
+  if (warp * 32 < a.k_list) st = warp_merge<false>(st, a.k);
+  if (lane == 0) s_warp[warp] = st;
   if (!__syncthreads_or(any && w != 0.f)) {
     if (kept) copy_wait(0);
     if (rank == 0 && tid == 0) a.loss[r] = 0.f;
@@ -260,34 +262,51 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
   }
   if (size > 1) cluster_started();
   if (!kept && !early) prefetch_part(row, p, 0);
-  // The entries of this part: their bits, and whether an id comes twice.
+  // The entries of this part, in the list's order: their bits, and whether an id comes twice.
+  const int counted = lane < rounds * WARPS ? s_count[lane] : 0, n = __reduce_add_sync(0xffffffffu, counted);
   bool twice = false;
-  entries([&](int i, int id) {
-    const int at = id - origin, v = at / N - 1;
+  const auto enter = [&](int j, bool mine, int id, float v, float z) {
+    const uint32_t others = __ballot_sync(0xffffffffu, mine);
+    const int before = __reduce_add_sync(0xffffffffu, lane < j * WARPS + warp ? counted : 0);
+    if (!mine) return;
+    const int e = before + __popc(others & lanemask_lt()), at = id - origin, c = at / N - 1;
+    l.ids[e] = id;
+    l.t[e] = v;
+    l.z[e] = z;
     const uint32_t bit = 1u << (at & 31);
     twice = (atomicOr(l.map + (at >> 5), bit) & bit) || twice;
-    if (v >= 0 && v < p.count) {
-      const int f = v / (ROW_BATCH * NT) * NT + v % NT;  // its thread's byte of its batch
-      atomicOr(l.flags + (f >> 2), 1u << (v / NT % ROW_BATCH + 8 * (f & 3)));
+    if (c >= 0 && c < p.count) {
+      const int f = c / (ROW_BATCH * NT) * NT + c % NT;  // its thread's byte of its batch
+      atomicOr(l.flags + (f >> 2), 1u << (c / NT % ROW_BATCH + 8 * (f & 3)));
     }
-    l.z[i] = i == tid ? z0 : Vec<T>::widen1(row[id]);
-  });
+  };
+  if (warp * 32 < a.k_list) enter(0, mine0, id0, v0, z0);
+  for (int j = 1; j < rounds; ++j) {
+    const int i = j * NT + tid;
+    const int id = i < a.k_list ? a.idx[r * a.ild + i] : -1;
+    const bool mine = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.V) && in_part(id);
+    enter(j, mine, id, mine ? list_value(a, r, i) : 0.f, mine ? Vec<T>::widen1(row[id]) : 0.f);
+  }
   Batch v;
   if (!kept) v = Batch::from<NT>(part_vectors(row, p), 0, p.count);
   const float edge = edge_of(row, p);
   if (size > 1) cluster_wait();
   if (tid < 32) {
-    st = tid < NT / 32 ? s_warp[tid] : no_stat();
+    st = tid < WARPS ? s_warp[tid] : no_stat();
     st = warp_merge<false>(st, a.k);
-    if (tid == 0) s_teacher = teacher_of(st, rest, a.k, a.k64);
+    if (tid == 0) {
+      Teacher t = teacher_of(st, rest, a.k, a.k64);
+      t.inv = 1.f / (1.f + t.others);
+      s_teacher = t;
+    }
   }
   twice = __syncthreads_or(twice);
   const Teacher& t = s_teacher;
-  const auto weight = [&](int i) { return ex2((l.t[i] - t.m) * a.k - t.D) / (1.f + t.others); };
-  const auto owner = [&](int i, int id) {  // the first of an id's entries stands for its column
+  const auto weight = [&](int e) { return ex2((l.t[e] - t.m) * a.k - t.D) * t.inv; };
+  const auto owner = [&](int e) {  // the first of an id's entries stands for its column
     if (twice)
-      for (int j = 0; j < i; ++j)
-        if (l.ids[j] == id) return false;
+      for (int f = 0; f < e; ++f)
+        if (l.ids[f] == l.ids[e]) return false;
     return true;
   };
 
@@ -297,24 +316,26 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
   if (p.edge_n && !(l.map[(p.edge_lo - origin) >> 5] >> ((p.edge_lo - origin) & 31) & 1))
     x.out = merge(x.out, stat_of(edge), a.k);
   if (GRAD && !kept) v = Batch::from<NT>(part_vectors(row, p), 0, p.count);  // for the second pass, while the factors are formed
+  x.out = warp_merge<false>(x.out, a.k);
   x.in = no_stat();
-  entries([&](int i, int id) {
-    if (owner(i, id)) x.in = merge(x.in, stat_of(l.z[i]), a.k);
-  });
   x.C = x.Q = 0.f;
-  entries([&](int i, int) {
-    const float q = weight(i);
-    if (q == 0.f) return;
-    x.C += q * (((l.t[i] - t.m) - (l.z[i] - finite_ref(x.in.m))) * a.inv_t);
-    x.Q += q;
-  });
-  x = merge_sums(x, a.k, a.inv_t);
+  if (warp * 32 < n) {
+    for (int e = tid; e < n; e += NT)
+      if (owner(e)) x.in = merge(x.in, stat_of(l.z[e]), a.k);
+    for (int e = tid; e < n; e += NT) {
+      const float q = weight(e);
+      if (q == 0.f) continue;
+      x.C += q * (((l.t[e] - t.m) - (l.z[e] - finite_ref(x.in.m))) * a.inv_t);
+      x.Q += q;
+    }
+    merge_listed(x, a.k, a.inv_t);
+  }
   float4 mine[2], all[2];
   pack(x, mine);
-  if ((tid & 31) == 0) board.warp[0][tid >> 5] = mine[0], board.warp[1][tid >> 5] = mine[1];
+  if (lane == 0) board.warp[0][warp] = mine[0], board.warp[1][warp] = mine[1];
   __syncthreads();
   if (tid < 32) {  // one warp forms the row's loss and factors for all
-    x = tid < NT / 32 ? unpack(board.warp[0][tid], board.warp[1][tid]) : Sums{no_stat(), no_stat(), 0.f, 0.f};
+    x = tid < WARPS ? unpack(board.warp[0][tid], board.warp[1][tid]) : Sums{no_stat(), no_stat(), 0.f, 0.f};
     x = merge_sums(x, a.k, a.inv_t);
     if (size > 1) {
       pack(x, mine);
@@ -329,20 +350,20 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
   grad_pass<T, false, NT>(s_grad, GradRow<T>{row, grad, p, kept ? cache : nullptr, edge}, v);
   __syncthreads();  // the entries' values go over what the pass has written
   const EntryGrad e = s_entry;
-  entries([&](int i, int id) {
-    if (!owner(i, id)) return;
+  for (int i = tid; i < n; i += NT) {
+    if (!owner(i)) continue;
     float q = weight(i), q_left = 1.f - q;
     if (twice) {
-      for (int j = i + 1; j < a.k_list; ++j)
-        if (l.ids[j] == id) q += weight(j);
+      for (int j = i + 1; j < n; ++j)
+        if (l.ids[j] == l.ids[i]) q += weight(j);
       q_left = 1.f - q;
     } else if (q > 0.5f && !t.rest_is_max) {
-      q_left = t.others / (1.f + t.others);  // above one half: the largest
+      q_left = t.others * t.inv;  // above one half: the largest
     }
     const float x = ex2((l.z[i] - e.m) * a.k), sum = 1.f + e.s, pv = x / sum;
     const float p_left = (l.z[i] == e.m ? e.s : sum - x) / sum;
-    grad[id] = Vec<T>::narrow1(e.wt == 0.f ? 0.f : e.wt * (pv > 0.5f && q > 0.5f ? q_left - p_left : pv - q));
-  });
+    grad[l.ids[i]] = Vec<T>::narrow1(e.wt == 0.f ? 0.f : e.wt * (pv > 0.5f && q > 0.5f ? q_left - p_left : pv - q));
+  }
 }
 
 template <typename T, bool GRAD>

@@ -19,7 +19,7 @@ DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 INF = math.inf
 
 # rows, columns: single ones, odd ones, rows inside 16-byte vectors, one CTA a row and several
-SHAPES = [(1, 1), (3, 2), (5, 7), (4, 33), (6, 300), (9, 1001), (2, 50021), (400, 515), (1, 201088)]
+SHAPES = [(1, 1), (3, 2), (5, 7), (4, 33), (6, 300), (9, 1001), (2, 50021), (400, 515), (700, 515), (1, 201088)]
 
 
 def f32(x):
@@ -116,6 +116,9 @@ def test_logprobs_and_their_gradient(rows, V, dt, T, pad):
             return [g], [tol]
 
         _check_rows(rng, want, [_np(out)], ("gradient",), rows)
+    # in place: the parts of a row are written by themselves
+    dst.token_logprobs_grad(zt, _dev(t), lse, _dev(a), T, d_entropy=_dev(b), entropy=H, out_grad=zt)
+    assert torch.equal(zt, out)
 
 
 # ------------------------------------------------------------------ policy loss
@@ -259,7 +262,7 @@ def _lists(rng, z, k, vdt, rest, T, twice=False):
 
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("rows,V,k,pad", [(1, 1, 1, 0), (7, 5, 5, 0), (7, 300, 17, 3), (9, 1001, 256, 0),
-                                          (8, 1200, 1024, 1), (7, 50021, 77, 0), (400, 515, 4, 0), (1, 201088, 256, 0)])
+                                          (8, 1200, 1024, 1), (7, 50021, 77, 0), (400, 515, 4, 0), (700, 515, 200, 0), (1, 201088, 256, 0)])
 @pytest.mark.parametrize("rest,T,vdt,twice", [(False, 1.0, "f32", False), (True, f32(0.7), "f32", False),
                                               (True, f32(1.6), "bf16", True)])
 def test_distill(rows, V, k, pad, dt, rest, T, vdt, twice):
@@ -409,6 +412,33 @@ def test_rows_longer_than_shared_memory(dt):
         tc.near(dg[r], v[1], tol[1], f"gradient of row {r}")
     with pytest.raises(dst.TailError):
         dst.token_logprobs(torch.zeros((1, V + 1), device=DEV), _dev(t[:1]))
+
+
+def test_many_short_rows():
+    g = torch.Generator(device=DEV).manual_seed(4)
+    rows, V = 70001, 37
+    z = 3 * torch.randn((rows, V), generator=g, device=DEV)
+    t = torch.randint(-1, V, (rows,), generator=g, device=DEV, dtype=torch.int32)
+    old, adv = torch.full((rows,), -3.0, device=DEV), torch.randn(rows, generator=g, device=DEV)
+    loss, lp, grad = dst.policy_loss(z, t, old, adv)
+    l = torch.log_softmax(z.double(), -1)
+    live = t >= 0
+    want = torch.where(live, l.gather(1, t.clamp(min=0).long()[:, None])[:, 0], 0.0)
+    assert (lp.double() - want).abs().max().item() < 2.0 ** -17 + 2.0 ** -22 * 30
+    R = torch.exp(want + 3.0)
+    c = torch.where(live & (-adv * R >= -adv * R.clamp(1 - f32(0.2), 1 + f32(0.2))), -adv * R, 0.0)
+    one = torch.zeros_like(l).scatter_(1, t.clamp(min=0).long()[:, None], 1.0)
+    exact = c[:, None] * (one - l.exp())
+    near = ((R - 1 + f32(0.2)).abs() > 1e-4) & ((R - 1 - f32(0.2)).abs() > 1e-4)  # the slope jumps at the clip's borders
+    # of c 2^-16 (l's error, R's) and of p 2^-16
+    assert ((grad.double() - exact).abs() <= 2.0 ** -15 * c.abs()[:, None] + 1e-30)[near].all()
+    vals, idx = z.topk(5, dim=-1)
+    kl, d = dst.distill_topk(z, vals, idx.to(torch.int32), temperature=2.0)
+    q = torch.softmax(vals.double() / 2, -1)
+    p = torch.softmax(z.double() / 2, -1)
+    exact = (p - torch.zeros_like(p).scatter_(1, idx, q)) / 2
+    assert (d.double() - exact).abs().max().item() < 2.0 ** -16
+    assert (kl.double() - (q * (q.log() - p.gather(1, idx).log())).sum(-1)).abs().max().item() < 2.0 ** -15
 
 
 def test_offsets_behind_32_bits():

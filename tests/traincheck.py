@@ -83,7 +83,7 @@ def policy(z, t, T, old, adv, ref, lo, hi, kl, ent, w, dt):
     if r is None:
         return (0.0, -np.inf, 0.0, zero), (0.0, 0.0, 0.0, zero)
     p, l, lse, H, s = r
-    dl = lp_tol(l[t], s)
+    dl = lp_tol(l[t], s) if l[t] > -np.inf else 0.0
     R = np.exp(l[t] - old)
     a, b = -adv * R, -adv * min(max(R, 1 - lo), 1 + hi)
     loss, c = max(a, b), a if a >= b else 0.0
@@ -208,7 +208,7 @@ def near(got, want, tol, what=""):
     assert np.array_equal(np.isnan(got), np.isnan(want)), what + ": NaN elsewhere"
     assert np.array_equal(got[~fin & ~np.isnan(want)], want[~fin & ~np.isnan(want)]), what + ": infinities"
     if fin.any():
-        d = np.abs(got - want)[fin]
+        d = np.abs(got[fin] - want[fin])
         bad = d > tol[fin]
         if bad.any():
             at = tuple(int(x[bad][0]) for x in np.nonzero(fin))
