@@ -2,8 +2,9 @@
 from __future__ import annotations
 
 import contextlib
+import sys
 
-from . import TAIL_BF16, TAIL_ERR_UNSUPPORTED, TAIL_F16, TAIL_F32, TailError, lib
+from . import TAIL_BF16, TAIL_ERR_UNSUPPORTED, TAIL_F16, TAIL_F32, TAIL_OK, TailError, lib
 
 
 def need(t, what, dtype, shape, index):
@@ -20,7 +21,7 @@ def need_opt(t, what, dtype, shape, index):
 
 def need_matrix(t, what, rows, index):
     """[rows, n >= 1] of a float type with unit stride along the columns: (pointer, type code, n, leading dimension)."""
-    import torch
+    torch = sys.modules["torch"]  # (an import statement a check adds up: 0.2 us each)
     dtype = t.dtype
     code = (TAIL_F32 if dtype is torch.float32 else TAIL_F16 if dtype is torch.float16 else
             TAIL_BF16 if dtype is torch.bfloat16 else None)
@@ -48,7 +49,7 @@ def cuda_index(t, what):
 def raw_stream(stream, index):
     """The cudaStream_t of a torch stream, an integer, or None (the device's current stream)."""
     if stream is None:
-        import torch
+        torch = sys.modules["torch"]
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the number alone: 0.1 us instead of 1.3
         return raw(index) if raw else torch.cuda.current_stream(index).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -74,3 +75,15 @@ def fail(rc, what):
     if rc == TAIL_ERR_UNSUPPORTED:
         raise TailError(rc, what + " [" + lib().tail_last_error().decode() + "]")
     raise TailError(rc, what)
+
+
+def call(name, args, index):
+    """The library's function on the device; a status other than TAIL_OK raises."""
+    cuda, fn = sys.modules["torch"].cuda, getattr(lib(), name)
+    if cuda.current_device() == index:
+        rc = fn(*args)
+    else:
+        with cuda.device(index):
+            rc = fn(*args)
+    if rc != TAIL_OK:
+        fail(rc, name)

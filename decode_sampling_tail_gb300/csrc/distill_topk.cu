@@ -171,8 +171,7 @@ __device__ __forceinline__ void distill_row(const DistillArgs& a, int64_t r, flo
     const float scale = 1.f + t.others;
     const float y = t.D == 0.f ? all.s - t.others : sum * ex2(-t.D) - scale;
     const float lead = t.D < 100.f ? log1pf(y / scale) : ln - t.ln - t.D * 0.693147181f;
-    float loss = lead * x.Q;
-    if (!(x.Q == 0.f)) loss += x.C + x.Q * ((all.m - finite_ref(n.m)) * a.inv_t);
+    float loss = x.Q == 0.f ? 0.f : lead * x.Q + x.C + x.Q * ((all.m - finite_ref(n.m)) * a.inv_t);
     if (!(t.q_rest == 0.f)) {
       const float lp = out_w >= in_w    ? -log1pf(in_w / out_w)
                        : out_w > 1e-30f ? logf(p_rest)

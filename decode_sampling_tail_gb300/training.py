@@ -13,7 +13,7 @@ from __future__ import annotations
 import ctypes
 
 from . import TAIL_OK, lib
-from ._args import allocating_on, cuda_index, device_guard, fail, need, need_matrix, need_opt, raw_stream
+from ._args import allocating_on, call, cuda_index, fail, need, need_matrix, need_opt, raw_stream
 
 
 def _grad(out_grad, logits, rows, V, index):
@@ -55,10 +55,7 @@ def token_logprobs(logits, tokens, temperature=1.0, *, entropy=False, out_logpro
     args = (rows, V, l, code, ld, need(tokens, "tokens", torch.int32, n, index), temperature,
             need(out_logprob, "out_logprob", f32, n, index), need(out_lse, "out_lse", f32, n, index),
             need_opt(out_entropy, "out_entropy", f32, n, index), raw_stream(stream, index))
-    with device_guard(index):
-        rc = lib().tail_token_logprobs(*args)
-    if rc != TAIL_OK:
-        fail(rc, "tail_token_logprobs")
+    call("tail_token_logprobs", args, index)
     return out_logprob, out_lse, out_entropy
 
 
@@ -82,10 +79,7 @@ def token_logprobs_grad(logits, tokens, lse, d_logprob, temperature=1.0, *, d_en
             need(lse, "lse", f32, n, index), need(d_logprob, "d_logprob", f32, n, index),
             need_opt(d_entropy, "d_entropy", f32, n, index), need_opt(entropy, "entropy", f32, n, index), g, gld,
             raw_stream(stream, index))
-    with device_guard(index):
-        rc = lib().tail_token_logprobs_grad(*args)
-    if rc != TAIL_OK:
-        fail(rc, "tail_token_logprobs_grad")
+    call("tail_token_logprobs_grad", args, index)
     return out_grad
 
 
@@ -117,10 +111,7 @@ def policy_loss(logits, tokens, old_logprob, advantage, *, ref_logprob=None, tem
             need_opt(weight, "weight", f32, n, index), need(out_loss, "out_loss", f32, n, index),
             need(out_logprob, "out_logprob", f32, n, index), need_opt(out_entropy, "out_entropy", f32, n, index),
             g, gld, raw_stream(stream, index))
-    with device_guard(index):
-        rc = lib().tail_policy_loss(*args)
-    if rc != TAIL_OK:
-        fail(rc, "tail_policy_loss")
+    call("tail_policy_loss", args, index)
     return out_loss, out_logprob, out_grad
 
 
@@ -169,10 +160,7 @@ def preference_loss(logits, tokens, cu_rows, *, ref_logprob=None, beta=0.1, labe
             need(workspace, "workspace", torch.uint8, (size,), index), size,
             need(out_loss, "out_loss", f32, (nseq // 2,), index),
             need(out_seq_logprob, "out_seq_logprob", f32, (nseq,), index), g, gld, raw_stream(stream, index))
-    with device_guard(index):
-        rc = lib().tail_preference_loss(*args)
-    if rc != TAIL_OK:
-        fail(rc, "tail_preference_loss")
+    call("tail_preference_loss", args, index)
     return out_loss, out_seq_logprob, out_grad
 
 
@@ -207,8 +195,5 @@ def distill_topk(logits, topk_vals, topk_idx, *, teacher_rest=None, temperature=
     args = (rows, V, k, l, code, ld, v, vcode, vld, topk_idx.data_ptr(), ild, temperature,
             need_opt(teacher_rest, "teacher_rest", f32, n, index), need_opt(weight, "weight", f32, n, index),
             need(out_loss, "out_loss", f32, n, index), g, gld, raw_stream(stream, index))
-    with device_guard(index):
-        rc = lib().tail_distill_topk(*args)
-    if rc != TAIL_OK:
-        fail(rc, "tail_distill_topk")
+    call("tail_distill_topk", args, index)
     return out_loss, out_grad

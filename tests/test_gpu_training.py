@@ -358,6 +358,40 @@ def test_masked_and_extreme_rows(dt, V):
     assert abs(got[0][6] / tc.logprob(z[6], 11, 1.0)[0][0] - 1) < 2.0 ** -15  # log(1 - 1e-20) and the like keep their bits
 
 
+@pytest.mark.parametrize("T", [2.0 ** -60, 1e-6, 1e6, 2.0 ** 60])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_extreme_temperatures(T, dt):
+    rng = np.random.default_rng(6)
+    V = 700
+    z = _logits(rng, 4, V, dt)
+    z[3] = 1e30 * np.sign(z[3])  # logits / T beyond fp32
+    z = _np(_dev(z, DT[dt])).astype(np.float32)
+    t = np.array([int(z[0].argmax()), 5, V - 1, int(z[3].argmax())], np.int32)
+    zt = _dev(z, DT[dt])
+    got = [_np(x) for x in dst.token_logprobs(zt, _dev(t), T, entropy=True)]
+    f = np.float32
+    vals, idx, rs = _lists(rng, z[:3], 9, "f32", False, 1.0)
+    dl, dg = (_np(x) for x in dst.distill_topk(zt[:3], _dev(vals), _dev(idx), temperature=T))
+    old = np.where(got[0] > -1e30, got[0], 0.0).astype(f)
+    loss, lp, g = (_np(x) for x in dst.policy_loss(zt, _dev(t), _dev(old), _dev(np.ones(4, f)), temperature=T,
+                                                   out_entropy=torch.empty(4, device=DEV)))
+    assert np.isfinite(g).all() and np.isfinite(dg).all() and np.isfinite(got[2]).all()
+    for r in range(4):
+        (l, lse, H), (tl, ts, tH) = tc.logprob(z[r].astype(np.float64), t[r], T)
+        if abs(l) < 1e37:
+            tc.near(got[0][r], l, tl, f"l of row {r}")
+        else:
+            assert got[0][r] == -INF or abs(got[0][r] / l - 1) < 1e-6
+        tc.near(got[2][r], H, tH + 1e-30, f"H of row {r}")
+        if abs(lse) < 1e37:
+            tc.near(got[1][r], lse, ts, f"lse of row {r}")
+    for r in range(3):
+        v, tol = tc.distill(z[r], vals[r], idx[r], None, T, 1.0, dt)
+        if abs(v[0]) < 1e37:
+            # its terms are differences of numbers of |t| / T, rounded a few times each
+            tc.near(dl[r], v[0], tol[0] + 2.0 ** -20 * abs(vals[r]).max() / T, f"distillation loss of row {r}")
+
+
 def test_tokens_of_probability_zero():
     z = torch.zeros((3, 50), device=DEV)
     z[:, :20] = -INF
