@@ -43,8 +43,10 @@ __device__ __forceinline__ RowGrad policy_row(const PolicyArgs& a, const PolicyR
   const float lp = empty ? -INFINITY : (x.z - all.m) * a.inv_t - ln;
   const float excess = ENT ? -0.693147181f * all.u * inv : 0.f;  // H - log of the sum
   const float R = expf(lp - x.old);
-  const float open = -x.adv * R, clipped = -x.adv * fminf(fmaxf(R, a.lo), a.hi);
-  float loss = fmaxf(open, clipped), c = open >= clipped ? open : 0.f;
+  // an advantage of 0 gives 0 of any ratio, one behind fp32's range too; NaN of the row, or of what it is given, stays
+  const bool none = x.adv == 0.f && R == R;
+  const float open = none ? 0.f : -x.adv * R, clipped = none ? 0.f : -x.adv * min_nan(max_nan(R, a.lo), a.hi);
+  float loss = max_nan(open, clipped), c = open < clipped ? 0.f : open;
   if (a.kl != 0.f) {
     const float d = x.ref - lp, k = expm1f(d);
     loss += a.kl * (k > 1e30f ? k : k - d);  // (k and d may both be infinite)

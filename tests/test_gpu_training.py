@@ -423,6 +423,26 @@ def test_ignored_rows_are_not_read():
     assert torch.equal(loss, zero[:, 0]) and torch.equal(g, zero)
 
 
+@pytest.mark.parametrize("terms", [dict(), dict(entropy_coef=0.01), dict(kl_coef=0.1)])
+def test_policy_keeps_nan_and_takes_nothing_of_an_advantage_of_0(terms):
+    z = torch.zeros((6, 300), device=DEV)
+    z[0, 7] = math.nan
+    t = torch.full((6,), 5, dtype=torch.int32, device=DEV)
+    l = -math.log(300)
+    old = torch.full((6,), l, device=DEV)
+    adv = torch.ones(6, device=DEV)
+    old[1], adv[2] = math.nan, math.nan  # their rows' losses, without a term that has one of itself too
+    old[3], adv[3] = -200.0, 0.0         # a ratio behind fp32's range, times nothing
+    adv[4] = 0.0
+    for hi in (0.2, INF):
+        loss, lp, g = dst.policy_loss(z, t, old, adv, ref_logprob=torch.full((6,), l, device=DEV), clip_high=hi, **terms)
+        assert torch.isnan(loss[:3]).all() and torch.isnan(g[:3]).all()
+        assert math.isnan(lp[0].item()) and torch.isfinite(lp[1:]).all()
+        assert torch.isfinite(loss[3:]).all() and torch.isfinite(g[3:]).all()
+        want = terms.get("entropy_coef", 0.0) * l  # -coef H
+        assert (loss[3:5] - want).abs().max().item() < 1e-6 and abs(loss[5].item() - (want - 1)) < 1e-5
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_rows_longer_than_shared_memory(dt):
     # 2^20 columns: a part of a row that its CTA does not hold is read twice
