@@ -73,6 +73,7 @@ __device__ __forceinline__ Teacher teacher_of(const RowStat& st, float rest, flo
   t.any = true;
   if (!listed) {  // the list's values are all -inf: everything is outside it
     t.others = 0.f, t.ln = 0.f, t.q_rest = 1.f, t.lq_rest = 0.f, t.q_list = 0.f, t.rest_is_max = true;
+    if (rest != rest) t.D = t.q_rest = rest;
     return t;
   }
   const float d = static_cast<float>(rest * LOG2E - t.m * k64);  // the rest's weight is 2^d
@@ -159,7 +160,7 @@ __device__ __forceinline__ void distill_row(const DistillArgs& a, int64_t r, flo
                                             int rank, RowGrad* g, EntryGrad* e) {
   const RowStat &o = x.out, &n = x.in;
   const RowStat all = merge(o, n, a.k);
-  const bool live = all.m != -INFINITY && t.any;  // a distribution, and something to aim at
+  const bool live = all.m != -INFINITY;  // a distribution
   const float ln = log1pf(all.s), sum = 1.f + all.s, inv = 1.f / sum;
   const float out_w = o.m == -INFINITY ? 0.f : (1.f + o.s) * ex2(dist(o.m, finite_ref(all.m), a.k));
   const float in_w = n.m == -INFINITY ? 0.f : (1.f + n.s) * ex2(dist(n.m, finite_ref(all.m), a.k));
@@ -301,6 +302,12 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
   }
   twice = __syncthreads_or(twice);
   const Teacher& t = s_teacher;
+  if (!t.any) {  // the values and the rest are all -inf: whatever the logits hold
+    if (kept) copy_wait(0);
+    if (rank == 0 && tid == 0) a.loss[r] = 0.f;
+    if (GRAD) zero_part(grad, a.V, rank, size);
+    return;
+  }
   const auto weight = [&](int e) { return ex2((l.t[e] - t.m) * a.k - t.D) * t.inv; };
   const auto owner = [&](int e) {  // the first of an id's entries stands for its column
     if (twice)

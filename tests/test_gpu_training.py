@@ -423,6 +423,24 @@ def test_ignored_rows_are_not_read():
     assert torch.equal(loss, zero[:, 0]) and torch.equal(g, zero)
 
 
+@pytest.mark.parametrize("V", [300, 60000])
+def test_distill_from_lists_of_minus_infinity(V):
+    z = torch.randn((4, V), generator=torch.Generator(device=DEV).manual_seed(9), device=DEV)
+    z[0, 9], z[1, 10] = math.nan, INF
+    idx = torch.arange(3, dtype=torch.int32, device=DEV).repeat(4, 1) * 7
+    vals = torch.full((4, 3), -INF, device=DEV)
+    for rest in (None, torch.full((4,), -INF, device=DEV)):  # nothing to aim at: ignored, whatever the logits hold
+        loss, g = dst.distill_topk(z, vals, idx, teacher_rest=rest)
+        assert torch.equal(loss, torch.zeros(4, device=DEV)) and torch.equal(g, torch.zeros_like(z))
+    rest = torch.tensor([0.0, 0.0, math.nan, 0.0], device=DEV)
+    vals[1] = 1.0
+    loss, g = dst.distill_topk(z, vals, idx, teacher_rest=rest)
+    assert torch.isnan(loss[[0, 2]]).all() and torch.isnan(g[[0, 2]]).all()
+    v, tol = tc.distill(_np(z[3]), _np(vals[3]).astype(np.float32), idx[3].cpu().numpy(), 0.0, 1.0, 1.0, "f32")
+    tc.near(_np(loss[3]), v[0], tol[0], "loss")
+    tc.near(_np(g[3]), v[1], tol[1], "gradient")
+
+
 @pytest.mark.parametrize("terms", [dict(), dict(entropy_coef=0.01), dict(kl_coef=0.1)])
 def test_policy_keeps_nan_and_takes_nothing_of_an_advantage_of_0(terms):
     z = torch.zeros((6, 300), device=DEV)
