@@ -112,6 +112,11 @@ struct List {
 inline int map_words(int64_t part, int n) { return static_cast<int>(((part + 2) * n + 31) / 32 + 1); }
 inline int flag_words(int64_t part, int nt) { return batches(static_cast<int>(part), nt) * nt / 4; }
 
+// What a List takes at most beside a part that is kept: 12 bytes an entry, and of the at most 12416 vectors that then find
+// room a byte each for the map (8 columns of 16 bits) and a quarter for the flags, each rounded up: 28040 bytes.
+constexpr int DISTILL_BESIDE = 28 * 1024;
+static_assert((ROW_SMEM - DISTILL_BESIDE - 2048) / 16 == 12416 && 12 * DISTILL_MAX_K + 12416 + 12 + 13 * 256 <= DISTILL_BESIDE);
+
 template <int N, int NT>
 struct ListMask {
   const uint32_t* map;
@@ -374,7 +379,7 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
 
 template <typename T, bool GRAD>
 cudaError_t launch(DistillArgs& a, int rows, cudaStream_t stream) {
-  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 16, GRAD ? 24 * 1024 : -1);
+  const RowPlan p = plan_rows(rows, a.V, sizeof(T), 16, GRAD ? DISTILL_BESIDE : -1);
   const int64_t part = part_of(row_vectors(a.V, sizeof(T)), p.size);
   a.map_words = map_words(part, Vec<T>::N);
   a.flag_words = flag_words(part, p.threads);

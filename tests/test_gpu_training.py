@@ -486,6 +486,19 @@ def test_rows_longer_than_shared_memory(dt):
         dst.token_logprobs(torch.zeros((1, V + 1), device=DEV), _dev(t[:1]))
 
 
+@pytest.mark.parametrize("V", [8 * 8 * 12416, 8 * 8 * 12417, 811000])
+def test_distill_parts_that_just_fill_shared_memory(V):
+    # the longest part beside the longest list that is kept, the shortest that is not, and between
+    rng = np.random.default_rng(13)
+    z = _logits(rng, 2, V, "bf16")
+    vals, idx, rs = _lists(rng, z, 1024, "f32", True, 1.0)
+    loss, g = (_np(x) for x in dst.distill_topk(_dev(z, DT["bf16"]), _dev(vals), _dev(idx), teacher_rest=_dev(rs)))
+    for r in range(2):
+        v, tol = tc.distill(z[r], vals[r], idx[r], float(rs[r]), 1.0, 1.0, "bf16")
+        tc.near(loss[r], v[0], tol[0], f"loss of row {r}")
+        tc.near(g[r], v[1], tol[1], f"gradient of row {r}")
+
+
 def test_many_short_rows():
     g = torch.Generator(device=DEV).manual_seed(4)
     rows, V = 70001, 37
