@@ -34,6 +34,8 @@ def need_matrix(t, what, rows, index):
     n = shape[1]
     if n < 1:
         raise ValueError(f"{what} must have at least one column")  # (no columns have no pointer: None to the library)
+    if (rows | n) >> 31:
+        raise ValueError(f"{what} has more than 2^31 - 1 rows or columns")  # (the library takes 32 bits)
     ld = strides[0] if rows > 1 else n
     if ld < n:
         raise ValueError(f"{what}: rows overlap (strides {strides})")

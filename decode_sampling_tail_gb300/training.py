@@ -117,6 +117,8 @@ def policy_loss(logits, tokens, old_logprob, advantage, *, ref_logprob=None, tem
 
 def preference_loss_workspace(rows: int) -> int:
     """Bytes of workspace that ``preference_loss`` needs for this many rows."""
+    if rows >> 31:
+        raise ValueError(f"rows must be 0 to 2^31 - 1, not {rows}")
     n = ctypes.c_int64()
     rc = lib().tail_preference_loss_workspace(rows, ctypes.byref(n))
     if rc != TAIL_OK:
@@ -142,6 +144,8 @@ def preference_loss(logits, tokens, cu_rows, *, ref_logprob=None, beta=0.1, labe
     if cu_rows.dim() != 1 or cu_rows.shape[0] < 1 or cu_rows.shape[0] % 2 == 0:
         raise ValueError("cu_rows must be [nseq + 1] with nseq even")
     nseq = cu_rows.shape[0] - 1
+    if nseq >> 31:
+        raise ValueError("cu_rows has more than 2^31 entries")
     l, code, V, ld = need_matrix(logits, "logits", rows, index)
     if out_loss is None or out_seq_logprob is None or workspace is None or (grad and out_grad is None):
         with allocating_on(stream, index):

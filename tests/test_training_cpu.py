@@ -211,3 +211,16 @@ def test_distill_is_zero_where_student_and_teacher_agree():
     z = np.array([1.0, 2.0, 0.5, -1.0])
     (loss, g), _ = tc.distill(z, z[[1, 0]], np.array([1, 0]), float(np.logaddexp(0.5, -1.0)), 1.0, 1.0, "f32")
     assert abs(loss) < 1e-15 and np.allclose(g, 0, atol=1e-15)
+
+
+def test_sizes_behind_32_bits_are_refused(L):
+    torch = pytest.importorskip("torch")
+    from decode_sampling_tail_gb300._args import need_matrix
+    for shape in ((2 ** 31, 1), (1, 2 ** 32 + 5), (2 ** 32 + 1, 7)):
+        t = torch.empty(shape, dtype=torch.bfloat16, device="meta")
+        with pytest.raises(ValueError, match="2\\^31"):
+            need_matrix(t, "logits", shape[0], t.get_device())
+    for rows in (2 ** 31, 2 ** 32, 2 ** 32 + 1, -1):
+        with pytest.raises(ValueError, match="rows"):
+            dst.preference_loss_workspace(rows)
+    assert dst.preference_loss_workspace(0) == 0 and dst.preference_loss_workspace(1) == 512
