@@ -6,6 +6,8 @@ import sys
 
 from . import TAIL_BF16, TAIL_ERR_UNSUPPORTED, TAIL_F16, TAIL_F32, TAIL_OK, TailError, lib
 
+_HERE = contextlib.nullcontext()
+
 
 def need(t, what, dtype, shape, index):
     """The pointer of a contiguous tensor of this type and shape on CUDA device `index`."""
@@ -59,9 +61,9 @@ def raw_stream(stream, index):
 
 def allocating_on(stream, index):
     """Allocations inside belong to the call's stream."""
-    import torch
     if stream is None:
         return device_guard(index)
+    import torch
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=index)
     return torch.cuda.stream(stream)
@@ -69,8 +71,8 @@ def allocating_on(stream, index):
 
 def device_guard(index):
     """Makes the device current for the call (the entry points without a handle run on the current one)."""
-    import torch
-    return contextlib.nullcontext() if torch.cuda.current_device() == index else torch.cuda.device(index)
+    cuda = sys.modules["torch"].cuda
+    return _HERE if cuda.current_device() == index else cuda.device(index)
 
 
 def fail(rc, what):

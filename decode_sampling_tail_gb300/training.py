@@ -11,6 +11,7 @@ and overlaps.  Calls are asynchronous on ``stream`` (None: the current stream of
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import TAIL_OK, lib
 from ._args import allocating_on, call, cuda_index, fail, need, need_matrix, need_opt, raw_stream
@@ -30,8 +31,10 @@ def _grad(out_grad, logits, rows, V, index):
 
 def _empty(t, shape, wanted, like):
     """An fp32 output that the caller did not give, where it is wanted."""
+    if t is not None or not wanted:
+        return t
     import torch
-    return torch.empty(shape, dtype=torch.float32, device=like.device) if t is None and wanted else t
+    return torch.empty(shape, dtype=torch.float32, device=like.device)
 
 
 def token_logprobs(logits, tokens, temperature=1.0, *, entropy=False, out_logprob=None, out_lse=None,
@@ -115,6 +118,7 @@ def policy_loss(logits, tokens, old_logprob, advantage, *, ref_logprob=None, tem
     return out_loss, out_logprob, out_grad
 
 
+@functools.lru_cache(maxsize=64)
 def preference_loss_workspace(rows: int) -> int:
     """Bytes of workspace that ``preference_loss`` needs for this many rows."""
     if rows >> 31:
