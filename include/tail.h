@@ -599,15 +599,15 @@ const char* tail_last_error(void);
  *                  (-1: a prompt position, padding) is ignored: its results are 0, its gradient is
  *                  zeros, whatever its logits hold.
  *   temperature    T, from 2^-64 to 2^64 (a double: a rounded T would shift every z / T).
- *   weight_opt     [rows] (or [pairs]) fp32 factors of the losses, NULL: 1.  A row (pair) of weight 0 is
- *                  left out: loss and gradient 0, whatever the formula gives.
+ *   weight_opt     [rows] (or [pairs]) fp32 factors of the losses, NULL: 1.  A row of weight 0 is ignored; a
+ *                  pair of weight 0 has loss and gradient 0, whatever the formula gives, and its L_s all the same.
  *   out_loss       fp32, the weight in it.
  *   out_grad_opt   [rows][grad_ld] of logits_dtype: the gradient of the sum of out_loss by the logits; rounded
  *                  once.  NULL: the loss alone.  It may be the logits themselves (same pointer and
  *                  leading dimension); other overlaps are refused.
  * Outputs must not overlap inputs otherwise, nor one another (TAIL_ERR_INVALID_ARG).  A logit of -inf has
  * probability 0 and gradient 0.  A row without a logit above -inf has no distribution: log-probability
- * and lse -inf, entropy 0; the losses leave it out like an ignored row.  NaN makes its own row's results NaN, and +inf is
+ * and lse -inf, entropy 0; the losses leave it out like an ignored row.  NaN makes its own row's (or pair's) results NaN, and +inf is
  * outside the domain; other rows do not change.  What a formula makes infinite is infinite (the
  * log-probability of a token of probability 0).
  * Sums are fp32, one instance of a row's maximum apart from the others, so that the log-probability of a
