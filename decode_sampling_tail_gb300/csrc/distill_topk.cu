@@ -172,11 +172,12 @@ __device__ __forceinline__ void distill_row(const DistillArgs& a, int64_t r, flo
   const float p_rest = out_w * inv;
   if (threadIdx.x != 0) return;
   if (rank == 0) {
-    // log q_i - l_i is a difference of two logits and of two log-sums: the logarithm of the sums' quotient does not
-    // leave each one's rounding behind
+    // log q_i - l_i is a difference of two logits and of two log-sums: near one another these give the logarithm of
+    // their quotient, which does not leave each one's rounding behind; far below, the quotient less 1 would cancel (to -1,
+    // and a loss of -inf, once the rest outweighs the list by 2^25), while the difference is large beside its roundings
     const float scale = 1.f + t.others;
-    const float y = t.D == 0.f ? all.s - t.others : sum * ex2(-t.D) - scale;
-    const float lead = t.D < 100.f ? log1pf(y / scale) : ln - t.ln - t.D * 0.693147181f;
+    const float y = (t.D == 0.f ? all.s - t.others : sum * ex2(-t.D) - scale) / scale;
+    const float lead = y > -0.5f ? log1pf(y) : ln - t.ln - t.D * 0.693147181f;
     float loss = x.Q == 0.f ? 0.f : lead * x.Q + x.C + x.Q * ((all.m - finite_ref(n.m)) * a.inv_t);
     if (!(t.q_rest == 0.f)) {
       const float lp = out_w >= in_w    ? -log1pf(in_w / out_w)
