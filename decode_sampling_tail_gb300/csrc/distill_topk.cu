@@ -34,7 +34,7 @@ struct DistillArgs {
   float* loss;
   int V, k_list;
   float k, inv_t;
-  double k64;
+  double k64, t64;  // log2(e) / T, T
   int vals_dtype;
   int map_words, flag_words, cache_at, kept;  // cache_at, kept: in vectors
 };
@@ -56,7 +56,7 @@ struct Teacher {
   bool any;  // whether there is anything to aim at
 };
 
-__device__ __forceinline__ Teacher teacher_of(const RowStat& st, float rest, float k, double k64) {
+__device__ __forceinline__ Teacher teacher_of(const RowStat& st, float rest, double k64, double t64) {
   Teacher t;
   t.m = finite_ref(st.m);
   const bool listed = st.m != -INFINITY;
@@ -76,7 +76,8 @@ __device__ __forceinline__ Teacher teacher_of(const RowStat& st, float rest, flo
     if (rest != rest) t.D = t.q_rest = rest;
     return t;
   }
-  const float d = static_cast<float>(rest * LOG2E - t.m * k64);  // the rest's weight is 2^d
+  // the rest's weight is 2^d: rest - m / T by one rounding, since at a small T both are far larger than their difference
+  const float d = static_cast<float>(fma(static_cast<double>(rest), t64, -static_cast<double>(t.m)) * k64);
   if (d <= 0.f) {
     const float w = ex2(fmaxf(d, -200.f));
     t.others = st.s + w;
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
     st = tid < WARPS ? s_warp[tid] : no_stat();
     st = warp_merge<false>(st, a.k);
     if (tid == 0) {
-      Teacher t = teacher_of(st, rest, a.k, a.k64);
+      Teacher t = teacher_of(st, rest, a.k64, a.t64);
       t.inv = 1.f / (1.f + t.others);
       s_teacher = t;
     }
@@ -441,6 +442,7 @@ extern "C" int tail_distill_topk(int32_t rows, int32_t V, int32_t k, const void*
   a.loss = out_loss;
   a.V = V;
   a.k_list = k;
+  a.t64 = temperature;
   a.k64 = LOG2E / temperature;
   a.k = static_cast<float>(a.k64);
   a.inv_t = static_cast<float>(1.0 / temperature);

@@ -61,3 +61,70 @@ def test_distill_with_a_rest_far_from_its_list(V, dt, T):
         tc.near(g[r], v[1], tol[1], "gradient of " + what)
 
 
+# ------------------------------------------------------------------ extreme temperatures
+
+EXTREME = [2.0 ** -60, 1e-6, 1e-3, 1e6, 2.0 ** 60]
+
+
+def _extreme(dt, seed=6, V=700):
+    rng = np.random.default_rng(seed)
+    z = _logits(rng, 4, V, dt)
+    z[3] = 1e30 * np.sign(z[3])  # logits / T beyond fp32
+    z = _np(_dev(z, DT[dt])).astype(np.float32)
+    return rng, z, z.argmax(1).astype(np.int32)
+
+
+def _lost(T, size=1.0):
+    """What exponentials below the smallest normal number leave out of a gradient (2^-126, times at most 2^6 for the
+    entropy's logarithm)."""
+    return size * 2.0 ** -120 / T
+
+
+def _distill_by_logarithms(z, vals, ids, rest, T):
+    """(loss, gradient, target) of one row, its ids valid and different, by logarithms alone: what lies outside the list
+    may have any probability.  The rest is taken from the list's maximum exactly before it is divided by T."""
+    def lse(x):
+        return x.max() + math.log(np.exp(x - x.max()).sum())
+    z, v = z.astype(np.float64), vals.astype(np.float64)
+    top = v.max()
+    u = (v - top) / T
+    if rest is not None:
+        from fractions import Fraction
+        u = np.append(u, float((Fraction(rest) * Fraction(T) - Fraction(top)) / Fraction(T)))
+    lq = u - lse(u)
+    y = (z - z.max()) / T
+    l = y - lse(y)
+    target = np.zeros(z.size)
+    target[ids] = np.exp(lq[:len(ids)])
+    loss = sum(math.exp(a) * (a - b) for a, b in zip(lq, l[ids]) if a > -700)
+    if rest is not None:
+        out = np.delete(l, ids)
+        if lq[-1] > -700:
+            loss += math.exp(lq[-1]) * (lq[-1] - lse(out))
+        target[np.setdiff1d(np.arange(z.size), ids)] = np.exp(lq[-1] + (out - lse(out)))  # (out alone may be of 1e18)
+    return loss, (np.exp(l) - target) / T, target
+
+
+@pytest.mark.parametrize("T", EXTREME)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("above", [None, -3.0, 0.0, 0.5, 20.0])
+def test_distill_at_extreme_temperatures(T, dt, above):
+    rng, z, _ = _extreme(dt)
+    z = z[:3]
+    vals, idx, _ = _lists(rng, z, 9, "f32", False, 1.0)
+    rs = None if above is None else (vals.max(1).astype(np.float64) / T + above).astype(np.float32)  # (its step may be > 1)
+    loss, g = dst.distill_topk(_dev(z, DT[dt]), _dev(vals), _dev(idx), temperature=T,
+                               teacher_rest=None if rs is None else _dev(rs))
+    for r in range(3):
+        want, grad, target = _distill_by_logarithms(z[r], vals[r], idx[r], None if rs is None else float(rs[r]), T)
+        # the loss: differences of numbers of |t| / T and |z| / T, fewer than 8 roundings of 2^-24 each, and logarithms
+        # of sums, 2^-16 each
+        big = max(abs(vals[r]).max(), abs(z[r][np.isfinite(z[r])]).max()) / T
+        if abs(want) < 1e37:
+            tc.near(_np(loss)[r], want, 2.0 ** -20 * big + 2.0 ** -15, f"loss of row {r}")
+        # the gradient: p and q by 2^-16 of themselves, q also by its rest's exponent (three roundings of the number)
+        p = grad * T + target
+        tol = (2.0 ** -16 * (p + target) + 2.0 ** -22 * (0.0 if rs is None else abs(above) + 1) * target) / T
+        tc.near(_np(g)[r], grad, tol + tc.EPS[dt] * np.abs(grad) * (1 + 2.0 ** -10) + _lost(T), f"gradient of row {r}")
+
+
