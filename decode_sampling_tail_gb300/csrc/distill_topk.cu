@@ -69,6 +69,7 @@ __device__ __forceinline__ Teacher teacher_of(const RowStat& st, float rest, dou
   t.rest_is_max = false;
   t.ln = log1pf(st.s);
   t.any = listed;
+  if (st.s != st.s) t.q_rest = st.s;  // NaN in the list: no column's share of q is known
   if (rest == -INFINITY) return t;
   t.any = true;
   if (!listed) {  // the list's values are all -inf: everything is outside it

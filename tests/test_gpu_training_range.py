@@ -128,3 +128,19 @@ def test_distill_at_extreme_temperatures(T, dt, above):
         tc.near(_np(g)[r], grad, tol + tc.EPS[dt] * np.abs(grad) * (1 + 2.0 ** -10) + _lost(T), f"gradient of row {r}")
 
 
+@pytest.mark.parametrize("V", [300, 60000])
+@pytest.mark.parametrize("rest", [False, True])
+def test_distill_keeps_nan_of_a_list(V, rest):
+    rng = np.random.default_rng(V)
+    z = _logits(rng, 3, V, "f32")
+    vals, idx, rs = _lists(rng, z, 9, "f32", rest, 1.0)
+    args = dict(teacher_rest=_dev(rs) if rest else None)
+    clean = dst.distill_topk(_dev(z), _dev(vals), _dev(idx), **args)
+    vals[1, 4] = np.nan
+    loss, g = dst.distill_topk(_dev(z), _dev(vals), _dev(idx), **args)
+    assert torch.isnan(loss[1]) and torch.isnan(g[1]).all()  # its own row, and all of that
+    assert torch.equal(loss[[0, 2]], clean[0][[0, 2]]) and torch.equal(g[[0, 2]], clean[1][[0, 2]])
+    alone = dst.distill_topk(_dev(z), _dev(vals), _dev(idx), grad=False, **args)[0]
+    assert torch.isnan(alone).tolist() == [False, True, False]
+
+
