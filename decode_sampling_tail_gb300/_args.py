@@ -65,7 +65,9 @@ def allocating_on(stream, index):
         return device_guard(index)
     import torch
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=index)
+        # (0 and cudaStreamLegacy are the default stream; to ExternalStream the number 0 is any stream of torch's pool)
+        stream = (torch.cuda.default_stream(index) if int(stream) in (0, 1) else
+                  torch.cuda.ExternalStream(int(stream), device=index))
     return torch.cuda.stream(stream)
 
 

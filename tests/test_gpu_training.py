@@ -718,3 +718,20 @@ def test_tail_scores_policy_and_distillation_together():
     after = dst.distill_topk(step, vals, idx, teacher_rest=rest, grad=False)[0]
     want = -1e-2 * (d.double() ** 2).sum(-1)  # to first order
     assert torch.allclose((after - kl).double(), want, rtol=0.1, atol=1e-5)
+
+
+def test_outputs_of_a_call_on_the_default_stream_by_its_number():
+    from decode_sampling_tail_gb300._args import allocating_on
+    zero = torch.cuda.default_stream(DEV).cuda_stream
+    assert zero == 0
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with allocating_on(zero, 0):
+            assert torch.cuda.current_stream().cuda_stream == zero
+        assert torch.cuda.current_stream().cuda_stream != zero
+    z = torch.randn((4, 500), generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)
+    t = torch.arange(4, dtype=torch.int32, device=DEV)
+    want = dst.token_logprobs(z, t)
+    torch.cuda.synchronize()
+    got = dst.token_logprobs(z, t, stream=zero)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -224,3 +224,15 @@ def test_sizes_behind_32_bits_are_refused(L):
         with pytest.raises(ValueError, match="rows"):
             dst.preference_loss_workspace(rows)
     assert dst.preference_loss_workspace(0) == 0 and dst.preference_loss_workspace(1) == 512
+
+
+def test_allocations_on_the_default_stream_by_its_number(monkeypatch):
+    torch = pytest.importorskip("torch")
+    from decode_sampling_tail_gb300._args import allocating_on
+    used = []
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: used.append(s))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: ("default", device))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda pointer, device=None: ("other", pointer, device))
+    for number in (0, 1, 0x7f0012340000):  # what a default stream's cuda_stream is; cudaStreamLegacy; any other
+        allocating_on(number, 3)
+    assert used == [("default", 3), ("default", 3), ("other", 0x7f0012340000, 3)]
