@@ -178,10 +178,21 @@ def distill_topk(logits, topk_vals, topk_idx, *, teacher_rest=None, temperature=
 
     logits [rows, V] and topk_vals [rows, k] float32, float16 or bfloat16, topk_idx [rows, k] int32 (outside [0, V): no
     entry; all three may have strided rows), as ``Tail.run`` writes them for the teacher; teacher_rest [rows] float32:
-    the log-sum-exp of the teacher's other logits / temperature (from its lse: ``rest = lse +
-    log1p(-exp(topk_vals / temperature - lse).sum(-1))`` in float64); weight [rows] float32.  Returns (loss [rows] float32,
+    the log-sum-exp of the teacher's other logits / temperature; weight [rows] float32.  Returns (loss [rows] float32,
     grad [rows, V] of the logits' type: the gradient of loss.sum()), allocated when not given, grad None with
-    ``grad=False``."""
+    ``grad=False``.
+
+    The rest comes from the teacher's logits without the listed ones (every id a valid one), whatever the list holds::
+
+        others = teacher_logits.scatter(1, topk_idx.long(), -math.inf)
+        rest = token_logprobs(others, topk_idx[:, 0].contiguous(), temperature)[1]
+
+    Where only the teacher's lse (``token_logprobs``) and the list are left, it is known to about 2^-24 |lse| of all
+    tokens' weight, and may come out below nothing::
+
+        listed = torch.exp(topk_vals.double() / temperature - lse.double()[:, None]).sum(-1)
+        rest = (lse.double() + torch.log(torch.clamp(1 - listed, min=0))).float()
+    """
     import torch
     f32 = torch.float32
     index = cuda_index(logits, "logits")

@@ -735,3 +735,47 @@ def test_outputs_of_a_call_on_the_default_stream_by_its_number():
     got = dst.token_logprobs(z, t, stream=zero)
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_the_rest_of_confident_teachers():
+    """The tail's top-k of rows that hold all but 10^-1 to 10^-12 of the weight, their rests both ways that distill_topk
+    documents, and a student's loss against 64 bits."""
+    g = torch.Generator(device=DEV).manual_seed(7)
+    H, V, k, n, T = 256, 8192, 64, 8, f32(0.9)
+    x = torch.randn((n, H), generator=g, device=DEV).to(torch.bfloat16)
+    w = torch.randn((H, V), generator=g, device=DEV) * 0.15
+    unit = x.float() / x.float().pow(2).mean(-1, keepdim=True).sqrt()
+    for r in range(n):  # logit of column 100 + r in row r
+        w[:, 100 + r] = unit[r] * (13.0 + 3.5 * r) / H
+    logits, tokens = torch.empty((n, V), device=DEV), torch.empty(n, dtype=torch.int32, device=DEV)
+    vals, idx = torch.empty((n, k), device=DEV), torch.empty((n, k), dtype=torch.int32, device=DEV)
+    with dst.Tail(H, V, k, n, hidden_dtype="bf16") as tail:
+        tail.run(x, torch.ones(H, device=DEV), w.to(torch.bfloat16), torch.tensor([[0, 1.0, T, 0.5]] * n, device=DEV),
+                 out_tokens=tokens, out_logits=logits, out_topk_vals=vals, out_topk_idx=idx)
+        tail.check()
+    y = logits.double() / T
+    exact = torch.logsumexp(y.scatter(1, idx.long(), -INF), -1)
+    left = (exact - torch.logsumexp(y, -1)).exp()
+    assert left.max().item() > 1e-3 and 0 < left.min().item() < 1e-8
+
+    others = logits.scatter(1, idx.long(), -INF)
+    rest = dst.token_logprobs(others, idx[:, 0].contiguous(), T)[1]
+    # 2^-17 of the sum, and half a step
+    assert ((rest.double() - exact).abs() <= 2.0 ** -17 + 2.0 ** -22 * exact.abs()).all()
+    lse = dst.token_logprobs(logits, tokens, T)[1]
+    listed = torch.exp(vals.double() / T - lse.double()[:, None]).sum(-1)
+    rough = (lse.double() + torch.log(torch.clamp(1 - listed, min=0))).float()
+    # what is left, by lse's error of the whole weight: 2^-17 min(1, s) of its sum, and its rounding
+    off = (torch.exp(rough.double() - torch.logsumexp(y, -1)) - left).abs()
+    s = torch.expm1(torch.logsumexp(y, -1) - y.amax(-1)).clamp(max=1)
+    assert (off <= 2.0 ** -17 * s + 2.0 ** -22 * (lse.abs().double() + 1)).all()
+
+    student = logits + 0.5 * torch.randn((n, V), generator=g, device=DEV)
+    for some in (rest, rough):
+        loss, d = (_np(a) for a in dst.distill_topk(student, vals, idx, teacher_rest=some, temperature=T))
+        assert np.isfinite(loss).all() and np.isfinite(d).all()
+        for r in range(n):
+            v, tol = tc.distill(_np(student[r]), _np(vals[r]).astype(np.float32), idx[r].cpu().numpy(), float(some[r]), T,
+                                1.0, "f32")
+            tc.near(loss[r], v[0], tol[0], f"loss of row {r}")
+            tc.near(d[r], v[1], tol[1], f"gradient of row {r}")
