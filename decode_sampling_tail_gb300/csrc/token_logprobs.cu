@@ -55,7 +55,8 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) score_kernel(const __
   const float lp = empty ? -INFINITY : (z - all.m) * a.inv_t - ln;
   if (a.score) a.score[r] = RowScore{all.m, all.s, empty ? 0.f : lp, empty ? -1 : t};
   if (a.logprob) a.logprob[r] = lp;
-  if (a.lse) a.lse[r] = empty ? -INFINITY : all.m * a.inv_t + ln;
+  // rounded once: the gradient takes every p from it
+  if (a.lse) a.lse[r] = empty ? -INFINITY : static_cast<float>(all.m * a.inv_t64 + ln);
   if (ENT) a.entropy[r] = empty ? 0.f : ln - 0.693147181f * all.u / (1.f + all.s);
 }
 
@@ -192,7 +193,8 @@ extern "C" int tail_token_logprobs(int32_t rows, int32_t V, const void* logits, 
   a.tokens = tokens;
   a.V = V;
   a.k = static_cast<float>(LOG2E / temperature);
-  a.inv_t = static_cast<float>(1.0 / temperature);
+  a.inv_t64 = 1.0 / temperature;
+  a.inv_t = static_cast<float>(a.inv_t64);
   a.logprob = out_logprob_opt;
   a.lse = out_lse_opt;
   a.entropy = out_entropy_opt;

@@ -28,6 +28,7 @@ struct ScoreArgs {
   const int32_t* tokens;
   int V;
   float k, inv_t;  // log2(e) / T, 1 / T
+  double inv_t64;  // 1 / T, where lse is asked for
   float *logprob, *lse, *entropy;
   RowScore* score;
   float* coef;

@@ -144,3 +144,22 @@ def test_distill_keeps_nan_of_a_list(V, rest):
     assert torch.isnan(alone).tolist() == [False, True, False]
 
 
+# ------------------------------------------------------------------ what a log-sum-exp keeps
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T", [1.0, f32(0.7), 0.05, 1.3])
+def test_lse_is_rounded_once(T, dt):
+    # rows whose likely token is e^20 times the others: log(1 + s) adds less than 2^-28 of error, and what is left is the
+    # rounding of lse itself, half a step
+    rng = np.random.default_rng(5)
+    rows, V = 400, 500
+    z = rng.standard_normal((rows, V)).astype(np.float32) * min(1.0, T)
+    at = rng.integers(0, V, rows).astype(np.int32)
+    z[np.arange(rows), at] = rng.uniform(26 * max(1.0, T), 60, rows).astype(np.float32)
+    z = _np(_dev(z, DT[dt])).astype(np.float32)
+    lse = _np(dst.token_logprobs(_dev(z, DT[dt]), _dev(at), T)[1])
+    for r in range(rows):
+        (_, want, _), _ = tc.logprob(z[r], at[r], T)
+        tc.near(lse[r], want, 2.0 ** -24 * abs(want) * (1 + 2.0 ** -10) + 2.0 ** -28, f"lse of row {r}")
+
+
