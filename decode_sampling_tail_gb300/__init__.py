@@ -38,7 +38,8 @@ EXPORTS = ("tail_create", "tail_run", "tail_run_ex", "tail_run_host", "tail_chec
            "tail_merge_shards", "tail_run_moe", "tail_tap_shape", "tail_run_taps", "tail_prepare_weight",
            "tail_verify", "tail_verify_logits", "tail_verify_logits_workspace",
            "tail_moe_create", "tail_moe_run", "tail_moe_check", "tail_moe_set_wait_limit", "tail_moe_get_info",
-           "tail_moe_destroy", "tail_token_logprobs", "tail_token_logprobs_grad", "tail_policy_loss",
+           "tail_moe_destroy", "tail_token_logprobs", "tail_token_logprobs_ex",
+           "tail_token_logprobs_grad", "tail_token_logprobs_grad_ex", "tail_policy_loss",
            "tail_preference_loss_workspace", "tail_preference_loss", "tail_distill_topk")
 KERNELS = ("rms_rows", "lm_head", "merge")
 
@@ -138,8 +139,12 @@ def lib(path: str | None = None):
         f32, f64 = ctypes.c_float, ctypes.c_double
         L.tail_token_logprobs.argtypes = [i32, i32, P, i32, i64, P, f64, P, P, P, P]
         L.tail_token_logprobs.restype = ctypes.c_int
+        L.tail_token_logprobs_ex.argtypes = [i32, i32, P, i32, i64, P, f64, P, P, P, P, P]
+        L.tail_token_logprobs_ex.restype = ctypes.c_int
         L.tail_token_logprobs_grad.argtypes = [i32, i32, P, i32, i64, P, f64, P, P, P, P, P, i64, P]
         L.tail_token_logprobs_grad.restype = ctypes.c_int
+        L.tail_token_logprobs_grad_ex.argtypes = [i32, i32, P, i32, i64, P, f64, P, P, P, P, P, P, i64, P]
+        L.tail_token_logprobs_grad_ex.restype = ctypes.c_int
         L.tail_policy_loss.argtypes = [i32, i32, P, i32, i64, P, f64, P, P, P, f32, f32, f32, f32, P, P, P, P, P, i64,
                                        P]
         L.tail_policy_loss.restype = ctypes.c_int

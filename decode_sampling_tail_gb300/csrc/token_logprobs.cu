@@ -2,10 +2,12 @@
 // rows' entropies.
 //
 // Forward: one pass over the logits, a cluster a row where rows are few (row_softmax.cuh).
-// Gradient: from the rows' log-sum-exps, with p_v = 2^((z_v - R) k + r), R = fp32(lse T) and r the rest of lse that
+// Gradient: from the rows' statistics (maximum m, log(1 + s)) with p_v = 2^((z_v - m) k) / (1 + s), as exact as the losses'
+//   own; or from their log-sum-exps alone, with p_v = 2^((z_v - R) k + r), R = fp32(lse T) and r the rest of lse that
 //   R leaves (formed in 64 bits, once a row): differences from R keep their bits near the
-//   maximum, where z k - lse log2(e) would lose up to 2^-19 of p.  Every column is read and written
-//   once; the parts of a row need nothing of one another.  At the token 1 - p is -expm1(log p).
+//   maximum, where z k - lse log2(e) would lose up to 2^-19 of p; what lse's own rounding takes, 2^-24 |lse| of every p, is
+//   lost.  Every column is read and written once; the parts of a row need nothing of one another.  At the token 1 - p is
+//   -expm1(log p).
 //
 // Both are bound by memory.  Measured (GB300, by graph replay): 4 rows of 201088 in fp32, scored with their entropies,
 // 3.3 us (floor 0.5: one CTA's chain of launch, first load, six batches, exchange); 1536 rows of 201088 in bf16, a tenth
@@ -40,6 +42,7 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) score_kernel(const __
       if (a.score) a.score[r] = RowScore{0.f, 0.f, 0.f, -1};
       if (a.logprob) a.logprob[r] = 0.f;
       if (a.lse) a.lse[r] = 0.f;
+      if (a.stats) a.stats[2 * r] = a.stats[2 * r + 1] = 0.f;
       if (ENT) a.entropy[r] = 0.f;
     }
     return;
@@ -55,8 +58,9 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) score_kernel(const __
   const float lp = empty ? -INFINITY : (z - all.m) * a.inv_t - ln;
   if (a.score) a.score[r] = RowScore{all.m, all.s, empty ? 0.f : lp, empty ? -1 : t};
   if (a.logprob) a.logprob[r] = lp;
-  // rounded once: the gradient takes every p from it
-  if (a.lse) a.lse[r] = empty ? -INFINITY : static_cast<float>(all.m * a.inv_t64 + ln);
+  // m / T enters exactly: a gradient may take every p from lse
+  if (a.lse) a.lse[r] = empty ? -INFINITY : fmaf(all.m, a.inv_t, fmaf(all.m, a.inv_t_low, ln));
+  if (a.stats) a.stats[2 * r] = all.m, a.stats[2 * r + 1] = empty ? 0.f : ln;
   if (ENT) a.entropy[r] = empty ? 0.f : ln - 0.693147181f * all.u / (1.f + all.s);
 }
 
@@ -80,17 +84,19 @@ __device__ __forceinline__ bool spread_factors(const SpreadArgs& a, int64_t r, c
     return true;
   }
   g.token = a.tokens[r];
-  const float da = a.a[r] * a.inv_t, db = ENT ? a.b[r] * a.inv_t : 0.f, lse = a.lse[r];
-  if (static_cast<uint32_t>(g.token) >= static_cast<uint32_t>(a.V) || (da == 0.f && db == 0.f) || lse == -INFINITY)
+  const float da = a.a[r] * a.inv_t, db = ENT ? a.b[r] * a.inv_t : 0.f, H = ENT ? a.entropy[r] : 0.f;
+  const float* st = a.stats ? a.stats + 2 * r : a.lse + r;
+  const float top = st[0], ln = st[a.stats ? 1 : 0];  // the maximum and log(1 + s), or lse twice
+  if (static_cast<uint32_t>(g.token) >= static_cast<uint32_t>(a.V) || (da == 0.f && db == 0.f) || top == -INFINITY)
     return false;
   prefetch_part(row, p, from);
-  g.ref = static_cast<float>(lse * a.t64);
-  const float rest = static_cast<float>((g.ref * a.inv_t64 - lse) * LOG2E);  // log2 p at z = ref
-  const float f = exp2f(rest), H = ENT ? a.entropy[r] : 0.f;
-  g.A = f * (-da - (ENT ? db * (0.693147181f * rest + H) : 0.f));
+  const double off = a.stats ? top : 0.f;  // log p = (z - off) / T - ln
+  g.ref = static_cast<float>(top * a.t64);
+  const float at = static_cast<float>((g.ref - off) * a.inv_t64 - ln), f = expf(at);  // log p, p at z = ref
+  g.A = f * (-da - (ENT ? db * (at + H) : 0.f));
   g.B = -f * db * 0.693147181f;
   if (!has_column<T>(p, rank, size, g.token)) return true;
-  const float l = static_cast<float>(Vec<T>::widen1(row[g.token]) * a.inv_t64 - lse);
+  const float l = static_cast<float>((Vec<T>::widen1(row[g.token]) - off) * a.inv_t64 - ln);
   g.at_token = -da * expm1f(l);
   if (ENT && l > -INFINITY) g.at_token -= db * expf(l) * (l + H);
   return true;
@@ -173,18 +179,19 @@ cudaError_t launch_spread(const SpreadArgs& a, int dtype, int rows, cudaStream_t
 
 using namespace tail;
 
-extern "C" int tail_token_logprobs(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype,
-                                   int64_t logits_ld, const int32_t* tokens, double temperature,
-                                   float* out_logprob_opt, float* out_lse_opt, float* out_entropy_opt, void* stream) {
+extern "C" int tail_token_logprobs_ex(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype,
+                                      int64_t logits_ld, const int32_t* tokens, double temperature,
+                                      float* out_logprob_opt, float* out_lse_opt, float* out_entropy_opt,
+                                      float* out_stats_opt, void* stream) {
   const int rc = sizes_ok(rows, V, LIMITS);
   if (rc) return rc;
   if (!temperature_ok(temperature)) return TAIL_ERR_INVALID_ARG;
   if (rows == 0) return TAIL_OK;
-  if (!out_logprob_opt && !out_lse_opt && !out_entropy_opt) return TAIL_ERR_INVALID_ARG;
+  if (!out_logprob_opt && !out_lse_opt && !out_entropy_opt && !out_stats_opt) return TAIL_ERR_INVALID_ARG;
   if (!matrix_ok(logits, logits_dtype, logits_ld, V) || !tokens) return TAIL_ERR_INVALID_ARG;
-  if (!words_ok({tokens, out_logprob_opt, out_lse_opt, out_entropy_opt})) return TAIL_ERR_INVALID_ARG;
+  if (!words_ok({tokens, out_logprob_opt, out_lse_opt, out_entropy_opt, out_stats_opt})) return TAIL_ERR_INVALID_ARG;
   const int64_t n = 4LL * rows;
-  if (outputs_meet({{out_logprob_opt, n}, {out_lse_opt, n}, {out_entropy_opt, n}},
+  if (outputs_meet({{out_logprob_opt, n}, {out_lse_opt, n}, {out_entropy_opt, n}, {out_stats_opt, 2 * n}},
                    {{tokens, n}, {logits, extent(rows, logits_ld, V, elem_bytes(logits_dtype))}}))
     return TAIL_ERR_INVALID_ARG;
   ScoreArgs a = {};
@@ -193,32 +200,41 @@ extern "C" int tail_token_logprobs(int32_t rows, int32_t V, const void* logits, 
   a.tokens = tokens;
   a.V = V;
   a.k = static_cast<float>(LOG2E / temperature);
-  a.inv_t64 = 1.0 / temperature;
-  a.inv_t = static_cast<float>(a.inv_t64);
+  a.inv_t = static_cast<float>(1.0 / temperature);
+  a.inv_t_low = static_cast<float>(1.0 / temperature - a.inv_t);
   a.logprob = out_logprob_opt;
   a.lse = out_lse_opt;
   a.entropy = out_entropy_opt;
+  a.stats = out_stats_opt;
   const cudaError_t e = launch_scores(a, logits_dtype, rows, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? TAIL_OK : cuda_fail(e, "tail_token_logprobs: kernel launch");
 }
 
-extern "C" int tail_token_logprobs_grad(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype,
-                                        int64_t logits_ld, const int32_t* tokens, double temperature, const float* lse,
-                                        const float* d_logprob, const float* d_entropy_opt, const float* entropy_opt,
-                                        void* out_grad, int64_t grad_ld, void* stream) {
+extern "C" int tail_token_logprobs(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype,
+                                   int64_t logits_ld, const int32_t* tokens, double temperature,
+                                   float* out_logprob_opt, float* out_lse_opt, float* out_entropy_opt, void* stream) {
+  return tail_token_logprobs_ex(rows, V, logits, logits_dtype, logits_ld, tokens, temperature, out_logprob_opt,
+                                out_lse_opt, out_entropy_opt, nullptr, stream);
+}
+
+extern "C" int tail_token_logprobs_grad_ex(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype,
+                                           int64_t logits_ld, const int32_t* tokens, double temperature,
+                                           const float* lse_opt, const float* stats_opt, const float* d_logprob,
+                                           const float* d_entropy_opt, const float* entropy_opt, void* out_grad,
+                                           int64_t grad_ld, void* stream) {
   const int rc = sizes_ok(rows, V, LIMITS);
   if (rc) return rc;
   if (!temperature_ok(temperature) || (d_entropy_opt != nullptr) != (entropy_opt != nullptr)) return TAIL_ERR_INVALID_ARG;
   if (rows == 0) return TAIL_OK;
   if (!matrix_ok(logits, logits_dtype, logits_ld, V) || !matrix_ok(out_grad, logits_dtype, grad_ld, V) || !tokens ||
-      !lse || !d_logprob)
+      (!lse_opt && !stats_opt) || !d_logprob)
     return TAIL_ERR_INVALID_ARG;
-  if (!words_ok({tokens, lse, d_logprob, d_entropy_opt, entropy_opt})) return TAIL_ERR_INVALID_ARG;
+  if (!words_ok({tokens, lse_opt, stats_opt, d_logprob, d_entropy_opt, entropy_opt})) return TAIL_ERR_INVALID_ARG;
   const int64_t n = 4LL * rows;
   const int es = elem_bytes(logits_dtype);
   if (!grad_apart(logits, logits_ld, out_grad, grad_ld, rows, V, es) ||
       outputs_meet({{out_grad, extent(rows, grad_ld, V, es)}},
-                   {{tokens, n}, {lse, n}, {d_logprob, n}, {d_entropy_opt, n}, {entropy_opt, n}}))
+                   {{tokens, n}, {lse_opt, n}, {stats_opt, 2 * n}, {d_logprob, n}, {d_entropy_opt, n}, {entropy_opt, n}}))
     return TAIL_ERR_INVALID_ARG;
   SpreadArgs a = {};
   a.logits = logits;
@@ -227,14 +243,23 @@ extern "C" int tail_token_logprobs_grad(int32_t rows, int32_t V, const void* log
   a.gld = grad_ld;
   a.tokens = tokens;
   a.V = V;
-  a.t64 = temperature;
-  a.inv_t64 = 1.0 / a.t64;
-  a.k = static_cast<float>(LOG2E / a.t64);
+  a.t64 = stats_opt ? 1.0 : temperature;
+  a.inv_t64 = 1.0 / temperature;
+  a.k = static_cast<float>(LOG2E / temperature);
   a.inv_t = static_cast<float>(a.inv_t64);
-  a.lse = lse;
+  a.lse = lse_opt;
+  a.stats = stats_opt;
   a.a = d_logprob;
   a.b = d_entropy_opt;
   a.entropy = entropy_opt;
   const cudaError_t e = launch_spread(a, logits_dtype, rows, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? TAIL_OK : cuda_fail(e, "tail_token_logprobs_grad: kernel launch");
+}
+
+extern "C" int tail_token_logprobs_grad(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype,
+                                        int64_t logits_ld, const int32_t* tokens, double temperature, const float* lse,
+                                        const float* d_logprob, const float* d_entropy_opt, const float* entropy_opt,
+                                        void* out_grad, int64_t grad_ld, void* stream) {
+  return tail_token_logprobs_grad_ex(rows, V, logits, logits_dtype, logits_ld, tokens, temperature, lse, nullptr,
+                                     d_logprob, d_entropy_opt, entropy_opt, out_grad, grad_ld, stream);
 }

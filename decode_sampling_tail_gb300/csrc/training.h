@@ -21,15 +21,15 @@ struct RowScore {
 };
 
 // Log-probabilities of the rows' tokens.  `score` (with `cu`: rows outside [cu[0], cu[nseq]) are not
-// counted, and `coef` is cleared), or the three arrays.
+// counted, and `coef` is cleared), or the four arrays.
 struct ScoreArgs {
   const void* logits;
   int64_t ld;
   const int32_t* tokens;
   int V;
   float k, inv_t;  // log2(e) / T, 1 / T
-  double inv_t64;  // 1 / T, where lse is asked for
-  float *logprob, *lse, *entropy;
+  float inv_t_low;  // what inv_t leaves of 1 / T, where lse is asked for
+  float *logprob, *lse, *entropy, *stats;
   RowScore* score;
   float* coef;
   const int32_t* cu;
@@ -37,7 +37,8 @@ struct ScoreArgs {
 };
 cudaError_t launch_scores(const ScoreArgs& a, int dtype, int rows, cudaStream_t stream);
 
-// The gradient of sum a logprob + b entropy from the rows' log-sum-exps, or of sum coef logprob from their scores.
+// The gradient of sum a logprob + b entropy from the rows' statistics or log-sum-exps, or of sum coef logprob from their
+// scores.
 struct SpreadArgs {
   const void* logits;
   int64_t ld;
@@ -46,8 +47,8 @@ struct SpreadArgs {
   const int32_t* tokens;
   int V;
   float k, inv_t;
-  double t64, inv_t64;
-  const float *lse, *a, *b, *entropy;
+  double t64, inv_t64;  // T (1 with statistics), 1 / T
+  const float *lse, *stats, *a, *b, *entropy;
   const RowScore* score;
   const float* coef;
   int size;  // CTAs a row (launch_spread's)

@@ -38,12 +38,13 @@ def _empty(t, shape, wanted, like):
 
 
 def token_logprobs(logits, tokens, temperature=1.0, *, entropy=False, out_logprob=None, out_lse=None,
-                   out_entropy=None, stream=None):
-    """Log-probabilities of ``tokens`` under softmax(logits / temperature) (tail_token_logprobs).
+                   out_entropy=None, out_stats=None, stream=None):
+    """Log-probabilities of ``tokens`` under softmax(logits / temperature) (tail_token_logprobs_ex).
 
     logits [rows, V] float32, float16 or bfloat16 (rows may be strided), tokens [rows] int32 (outside [0, V): an
     ignored row).  Returns (logprob, lse, entropy), each [rows] float32, allocated when not given; entropy is None
-    unless asked for (``entropy=True`` or ``out_entropy``)."""
+    unless asked for (``entropy=True`` or ``out_entropy``).  ``out_stats`` [rows, 2] float32 receives what
+    ``token_logprobs_grad`` needs to give a likely token's gradient to all its digits."""
     import torch
     f32 = torch.float32
     index = cuda_index(logits, "logits")
@@ -57,17 +58,20 @@ def token_logprobs(logits, tokens, temperature=1.0, *, entropy=False, out_logpro
     n = (rows,)
     args = (rows, V, l, code, ld, need(tokens, "tokens", torch.int32, n, index), temperature,
             need(out_logprob, "out_logprob", f32, n, index), need(out_lse, "out_lse", f32, n, index),
-            need_opt(out_entropy, "out_entropy", f32, n, index), raw_stream(stream, index))
-    call("tail_token_logprobs", args, index)
+            need_opt(out_entropy, "out_entropy", f32, n, index), need_opt(out_stats, "out_stats", f32, (rows, 2), index),
+            raw_stream(stream, index))
+    call("tail_token_logprobs_ex", args, index)
     return out_logprob, out_lse, out_entropy
 
 
 def token_logprobs_grad(logits, tokens, lse, d_logprob, temperature=1.0, *, d_entropy=None, entropy=None,
-                        out_grad=None, stream=None):
-    """The gradient of sum(d_logprob * logprob + d_entropy * entropy) by the logits (tail_token_logprobs_grad).
+                        stats=None, out_grad=None, stream=None):
+    """The gradient of sum(d_logprob * logprob + d_entropy * entropy) by the logits (tail_token_logprobs_grad_ex).
 
-    lse and entropy as ``token_logprobs`` gave them, d_logprob and d_entropy [rows] float32 (d_entropy goes with
-    entropy).  Returns out_grad, [rows, V] of the logits' type, allocated when not given (may be the logits)."""
+    lse, entropy and stats as ``token_logprobs`` gave them, d_logprob and d_entropy [rows] float32 (d_entropy goes with
+    entropy).  With ``stats`` lse is not read (None will do) and the gradient is exact to about 2^-16 of itself.  Without it
+    every probability is off by lse's rounding, up to 2^-24 |lse| of itself: a token whose 1 - p is near that or below
+    loses its gradient, and temperatures that make |logits| / temperature large lose the others'.  Returns out_grad, [rows, V] of the logits' type, allocated when not given (may be the logits)."""
     import torch
     f32 = torch.float32
     index = cuda_index(logits, "logits")
@@ -79,10 +83,11 @@ def token_logprobs_grad(logits, tokens, lse, d_logprob, temperature=1.0, *, d_en
     g, gld = _grad(out_grad, logits, rows, V, index)
     n = (rows,)
     args = (rows, V, l, code, ld, need(tokens, "tokens", torch.int32, n, index), temperature,
-            need(lse, "lse", f32, n, index), need(d_logprob, "d_logprob", f32, n, index),
+            need(lse, "lse", f32, n, index) if stats is None else need_opt(lse, "lse", f32, n, index),
+            need_opt(stats, "stats", f32, (rows, 2), index), need(d_logprob, "d_logprob", f32, n, index),
             need_opt(d_entropy, "d_entropy", f32, n, index), need_opt(entropy, "entropy", f32, n, index), g, gld,
             raw_stream(stream, index))
-    call("tail_token_logprobs_grad", args, index)
+    call("tail_token_logprobs_grad_ex", args, index)
     return out_grad
 
 

@@ -620,21 +620,35 @@ const char* tail_last_error(void);
 /*
  * l_r(token), lse_r = log sum_v exp(z_rv / T) and H_r of every row, each [rows] fp32 or NULL (not all three).
  * Ignored rows get 0.  One launch, one pass over the logits.
+ *   out_stats_opt  (_ex) [rows][2] fp32 or NULL: the row's maximum m, and log(1 + s) with s the sum of the others'
+ *                  exp((z_v - m) / T), so that lse = m / T + log(1 + s) without lse's rounding.  -inf and 0 without a
+ *                  distribution.
  */
 int tail_token_logprobs(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype, int64_t logits_ld,
                         const int32_t* tokens, double temperature, float* out_logprob_opt, float* out_lse_opt,
                         float* out_entropy_opt, void* stream);
+int tail_token_logprobs_ex(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype, int64_t logits_ld,
+                           const int32_t* tokens, double temperature, float* out_logprob_opt, float* out_lse_opt,
+                           float* out_entropy_opt, float* out_stats_opt, void* stream);
 
 /*
  * The gradient of sum_r d_logprob[r] l_r(token) + d_entropy[r] H_r, for losses formed by the caller:
  *   dz_v = (d_logprob (1[v = token] - p_v) - d_entropy p_v (log p_v + H)) / T,  log p_v = z_v / T - lse.
  *   lse, entropy_opt  [rows] as tail_token_logprobs gives them; entropy_opt goes with d_entropy_opt.
+ *   stats_opt         (_ex) [rows][2] as tail_token_logprobs_ex gives them; lse_opt is not read then (one of the two is
+ *                     needed).  The gradient keeps about 2^-16 of itself.
+ * From lse alone every p_v is off by lse's rounding, up to 2^-24 |lse| of itself, and a likely token's 1 - p by as much of
+ * 1: nothing is left of a 1 - p below that, nor of any p_v where |lse| passes 2^24 (a small T).
  * A row with both factors 0 gets zeros, whatever its logits hold.  One launch.
  */
 int tail_token_logprobs_grad(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype, int64_t logits_ld,
                              const int32_t* tokens, double temperature, const float* lse, const float* d_logprob,
                              const float* d_entropy_opt, const float* entropy_opt, void* out_grad, int64_t grad_ld,
                              void* stream);
+int tail_token_logprobs_grad_ex(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype, int64_t logits_ld,
+                                const int32_t* tokens, double temperature, const float* lse_opt, const float* stats_opt,
+                                const float* d_logprob, const float* d_entropy_opt, const float* entropy_opt,
+                                void* out_grad, int64_t grad_ld, void* stream);
 
 /*
  * The clipped policy loss of every row, with l = l_r(token), R = exp(l - old), d = ref - l:

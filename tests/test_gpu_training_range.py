@@ -163,3 +163,65 @@ def test_lse_is_rounded_once(T, dt):
         tc.near(lse[r], want, 2.0 ** -24 * abs(want) * (1 + 2.0 ** -10) + 2.0 ** -28, f"lse of row {r}")
 
 
+# ------------------------------------------------------------------ the gradient of likely tokens, forward and back
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("V", [300, 60000])
+@pytest.mark.parametrize("T", [1.0, f32(0.7), 0.05])
+@pytest.mark.parametrize("with_entropy", [False, True])
+def test_gradient_from_the_statistics(V, dt, T, with_entropy):
+    # 1 - p from 1 / 2 down to 1e-11, and tokens that are not the likely one
+    rng = np.random.default_rng(V)
+    rows = 12
+    z = rng.standard_normal((rows, V)).astype(np.float32) * min(1.0, 2 * T)
+    t = rng.integers(0, V, rows).astype(np.int32)
+    z[np.arange(rows), t] = T * (math.log(V) + np.linspace(0.0, 25.0, rows))
+    z[3, :V // 3] = -INF
+    z[3, t[3]] = 8.0
+    t[1] = (t[1] + 1) % V
+    t[6], t[7] = -1, V
+    z[8] = -INF
+    z = _np(_dev(z, DT[dt])).astype(np.float32)
+    zt = _dev(z, DT[dt])
+    stats = torch.empty((rows, 2), device=DEV)
+    lp, lse, H = dst.token_logprobs(zt, _dev(t), T, entropy=True, out_stats=stats)
+    for r in range(rows):
+        if 0 <= t[r] < V and r != 8:
+            s = tc.row(z[r], T)[4]  # (of its V terms those below 2^-126, which fp32 does not hold, count as 0)
+            tc.near(_np(stats[r]), [z[r].max(), math.log1p(s)],
+                    [0.0, 2.0 ** -17 * min(1.0, s) + 2.0 ** -22 * math.log1p(s) + V * 2.0 ** -126], f"statistics of row {r}")
+    assert stats[6].tolist() == [0, 0] and stats[7].tolist() == [0, 0] and stats[8].tolist() == [-INF, 0]
+    a, b = rng.standard_normal(rows).astype(np.float32), rng.standard_normal(rows).astype(np.float32)
+    a[9] = b[9] = 0
+    more = dict(d_entropy=_dev(b), entropy=H) if with_entropy else {}
+    g = dst.token_logprobs_grad(zt, _dev(t), None, _dev(a), T, stats=stats, **more)
+    for r in range(rows):
+        if r in (6, 7, 8, 9):
+            assert torch.count_nonzero(g[r]).item() == 0
+            continue
+        want, tol = tc.spread(z[r], t[r], T, float(a[r]), float(b[r]) if with_entropy else 0.0, dt)
+        tc.near(_np(g[r]), want, tol, f"gradient of row {r}")
+    # a lse beside them is not read; in place the same
+    nan = torch.full((rows,), math.nan, device=DEV)
+    assert torch.equal(dst.token_logprobs_grad(zt, _dev(t), nan, _dev(a), T, stats=stats, **more), g)
+    assert torch.equal(dst.token_logprobs_grad(zt, _dev(t), None, _dev(a), T, stats=stats, out_grad=zt, **more), g)
+    with pytest.raises(ValueError):
+        dst.token_logprobs_grad(zt, _dev(t), None, _dev(a), T, stats=stats[:, 0])
+    with pytest.raises(dst.TailError):
+        dst.token_logprobs(zt, _dev(t), T, out_logprob=stats.view(-1)[:rows], out_stats=stats)
+
+
+@pytest.mark.parametrize("T", EXTREME)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_gradient_from_the_statistics_at_extreme_temperatures(T, dt):
+    rng, z, t = _extreme(dt)
+    t[1] = 5  # not the likely one
+    stats = torch.empty((4, 2), device=DEV)
+    H = dst.token_logprobs(_dev(z, DT[dt]), _dev(t), T, entropy=True, out_stats=stats)[2]
+    a, b = rng.standard_normal(4).astype(np.float32), rng.standard_normal(4).astype(np.float32)
+    g = dst.token_logprobs_grad(_dev(z, DT[dt]), _dev(t), None, _dev(a), T, stats=stats, d_entropy=_dev(b), entropy=H)
+    for r in range(4):
+        want, tol = tc.spread(z[r], t[r], T, float(a[r]), float(b[r]), dt)
+        tc.near(_np(g[r]), want, tol + _lost(T, 4.0), f"gradient of row {r}")
+
+

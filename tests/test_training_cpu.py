@@ -236,3 +236,16 @@ def test_allocations_on_the_default_stream_by_its_number(monkeypatch):
     for number in (0, 1, 0x7f0012340000):  # what a default stream's cuda_stream is; cudaStreamLegacy; any other
         allocating_on(number, 3)
     assert used == [("default", 3), ("default", 3), ("other", 0x7f0012340000, 3)]
+
+
+def test_statistics_refusals(L):
+    S = 1 << 28  # [rows][2]
+    scores = lambda **k: (lambda a: L.tail_token_logprobs_ex(4, 100, P, 0, 100, P, 1.0, a["lp"], a["lse"], a["H"],  # noqa: E731
+                                                             a["s"], None))({**dict(lp=O1, lse=O2, H=O3, s=S), **k})
+    for bad in (dict(s=S + 2), dict(s=P), dict(s=P + 1592), dict(lp=S + 28), dict(lp=None, lse=None, H=None, s=None)):
+        assert scores(**bad) == dst.TAIL_ERR_INVALID_ARG
+    grad = lambda **k: (lambda a: L.tail_token_logprobs_grad_ex(4, 100, P, 0, 100, P, a["T"], a["lse"], a["s"], a["a"],  # noqa: E731
+                                                                None, None, G, 100, None))(
+        {**dict(T=1.0, lse=None, s=S, a=P), **k})
+    for bad in (dict(s=None), dict(s=S + 1), dict(s=G - 28), dict(a=None), dict(T=0.0), dict(lse=P + 2)):
+        assert grad(**bad) == dst.TAIL_ERR_INVALID_ARG
