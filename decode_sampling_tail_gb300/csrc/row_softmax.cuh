@@ -18,8 +18,12 @@
 // it apart, -log1p(s) is a likely token's log-probability and s / (1 + s) its distance from 1 to a few
 // units of 2^-24 of themselves.  It costs a minimum a column: a running pair of maxima keeps the
 // larger of each two values, and the smaller one goes into the sum, so that every value but the
-// maxima enters exactly once.  The sums are taken 16 or 32 columns at a time against the maximum so far, so a change of
-// it costs one multiplication a batch.
+// maxima enters exactly once.  The sums are taken 16 or 32 columns at a time against the maximum so far, and a batch's own
+// sum enters the running one by one fused operation, which also takes a change of the maximum.  So a term passes at most 8 or
+// 16 additions in its batch, one a batch behind it (25 of fp32, 13 of 16 bits at 201088 columns and 512 threads), and 19
+// merges of pairs, lanes, warps and CTAs, each 2^-24 of the sum; with its exponential (2^-22) and its argument's three
+// roundings (20 ln 2 of 3 2^-24 in the mean) s is within 2^-17 of itself up to 2^18 columns, 2^-16 up to 2^20.  Measured, from
+// 32000 to 2^20 columns of all spreads: 2^-20.7 at most.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -236,17 +240,19 @@ struct RowAcc {
     const float mx = max_nan(t.x, t.y), ref = finite_ref(mx);
     const float d = dist(m, ref, k), c = ex2(d);
     m = mx;
-    if (ENT) u = mul2(fma2(s, make_float2(d, d), u), make_float2(c, c));
-    s = mul2(s, make_float2(c, c));
+    if (ENT) u = fma2(s, make_float2(d, d), u);
     const float2 off = {-ref, -ref}, kk = {k, k};
+    float2 sb, ub;  // the batch's own sums: one addition a batch to the running ones, however many columns it has
 #pragma unroll
     for (int i = 0; i < U * V::PAIRS; ++i) {
       float2 a = mul2(add2(V::widen(w[i]), off), kk);
       if (ENT) a.x = max_nan(a.x, -200.f), a.y = max_nan(a.y, -200.f);
       const float2 e = {ex2(a.x), ex2(a.y)};
-      s = add2(s, e);
-      if (ENT) u = fma2(e, a, u);
+      sb = i ? add2(sb, e) : e;
+      if (ENT) ub = i ? fma2(e, a, ub) : mul2(e, a);
     }
+    s = fma2(s, make_float2(c, c), sb);
+    if (ENT) u = fma2(u, make_float2(c, c), ub);
   }
 
   __device__ __forceinline__ RowStat done(float k) const {

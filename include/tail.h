@@ -611,7 +611,8 @@ const char* tail_last_error(void);
  * outside the domain; other rows do not change.  What a formula makes infinite is infinite (the
  * log-probability of a token of probability 0).
  * Sums are fp32, one instance of a row's maximum apart from the others, so that the log-probability of a
- * likely token and its distance 1 - p keep about 2^-20 of themselves.  Results are deterministic and
+ * likely token and its distance 1 - p keep about 2^-20 of themselves as measured; counted by their roundings the sums are
+ * within 2^-17 of themselves up to 2^18 columns, 2^-16 up to 2^20.  Results are deterministic and
  * a row's do not depend on the others', except by the order of sums, which follows rows, V and the dtype.  No handle
  * and no allocation; asynchronous on `stream` of the current device; everything is read in stream order.  The CTAs of a
  * row wait for one another's sums for a second at most; should they not come, that row's results are NaN.

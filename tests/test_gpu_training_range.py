@@ -225,3 +225,30 @@ def test_gradient_from_the_statistics_at_extreme_temperatures(T, dt):
         tc.near(_np(g[r]), want, tol + _lost(T, 4.0), f"gradient of row {r}")
 
 
+# ------------------------------------------------------------------ sums of very unlike terms
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_small_terms_reach_a_sum_that_began_large(dt):
+    # 608 rows, a CTA of 512 threads each.  Every thread's first vectors hold five zeros a lane, everything behind them
+    # exp(-15.25), just below half a step of the 4 that the zeros make: added one after another they leave no trace, and s
+    # loses 9e-6 of itself.  Bound: a term passes 16 additions in its batch, 25 batches and 10 merges, each 2^-24, and the
+    # logarithm's rounding.
+    rows, V = 608, 201088
+    n = 16 // DT[dt].itemsize  # columns a vector
+    z = torch.full((V,), -15.25, device=DEV)
+    full = 8 // n  # vectors of zeros; behind them a pair
+    z[:512 * n * full] = 0
+    z[512 * n * full:512 * n * (full + 1)].view(512, n)[:, :2] = 0
+    zeros = int((z == 0).sum())
+    assert zeros == 512 * 10
+    want = -math.log(zeros + (V - zeros) * math.exp(-15.25))
+    z = z.to(DT[dt]).expand(rows, V).contiguous()
+    lp, lse, H = dst.token_logprobs(z, torch.zeros(rows, dtype=torch.int32, device=DEV), entropy=True)
+    tol = 51 * 2.0 ** -24 + 2.0 ** -22 * abs(want)
+    tc.near(_np(lp), np.full(rows, want), tol, "l")
+    tc.near(_np(lse), np.full(rows, -want), tol, "lse")
+    p = math.exp(-15.25 + want)
+    entropy = -want + (V - zeros) * p * 15.25  # H = lse - sum p z
+    tc.near(_np(H), np.full(rows, entropy), tol + 51 * 2.0 ** -24, "H")
+
+
