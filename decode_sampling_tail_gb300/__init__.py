@@ -40,7 +40,8 @@ EXPORTS = ("tail_create", "tail_run", "tail_run_ex", "tail_run_host", "tail_chec
            "tail_moe_create", "tail_moe_run", "tail_moe_check", "tail_moe_set_wait_limit", "tail_moe_get_info",
            "tail_moe_destroy", "tail_token_logprobs", "tail_token_logprobs_ex",
            "tail_token_logprobs_grad", "tail_token_logprobs_grad_ex", "tail_policy_loss",
-           "tail_preference_loss_workspace", "tail_preference_loss", "tail_distill_topk")
+           "tail_preference_loss_workspace", "tail_preference_loss", "tail_distill_topk",
+           "tail_training_set_wait_limit")
 KERNELS = ("rms_rows", "lm_head", "merge")
 
 
@@ -155,6 +156,8 @@ def lib(path: str | None = None):
         L.tail_preference_loss.restype = ctypes.c_int
         L.tail_distill_topk.argtypes = [i32, i32, i32, P, i32, i64, P, i32, i64, P, i64, f64, P, P, P, P, i64, P]
         L.tail_distill_topk.restype = ctypes.c_int
+        L.tail_training_set_wait_limit.argtypes = [ctypes.c_uint64]
+        L.tail_training_set_wait_limit.restype = ctypes.c_int
         L.tail_check.argtypes = [P]
         L.tail_check.restype = ctypes.c_int
         L.tail_get_info.argtypes = [P, ctypes.POINTER(tail_info)]
@@ -459,4 +462,4 @@ def merge_shards(cand_vals, cand_idx, shard_offsets, k, params=None, out_tokens=
 from .speculative import verify, verify_logits, verify_logits_workspace  # noqa: E402,F401
 from .moe_layer import Moe  # noqa: E402,F401
 from .training import (distill_topk, policy_loss, preference_loss, preference_loss_workspace,  # noqa: E402,F401
-                       token_logprobs, token_logprobs_grad)
+                       set_training_wait_limit, token_logprobs, token_logprobs_grad)

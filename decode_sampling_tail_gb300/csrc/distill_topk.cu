@@ -37,6 +37,7 @@ struct DistillArgs {
   double k64, t64;  // log2(e) / T, T
   int vals_dtype;
   int map_words, flag_words, cache_at, kept;  // cache_at, kept: in vectors
+  uint64_t wait_ns;
 };
 
 __device__ __forceinline__ float list_value(const DistillArgs& a, int64_t r, int i) {
@@ -353,9 +354,12 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
     x = merge_sums(x, a.k, a.inv_t);
     if (size > 1) {
       pack(x, mine);
-      const bool ok = board.template exchange<true>(rank, size, mine, all);
+      const bool ok = board.template exchange<true>(rank, size, mine, all, a.wait_ns);
       x = merge_sums(unpack(all[0], tid < size ? all[1] : make_float4(-INFINITY, 0.f, 0.f, 0.f)), a.k, a.inv_t);
-      if (!ok) x.out.m = NAN;
+      if (!ok) {
+        x.out.m = NAN;
+        if (!GRAD) board.leave();  // (the other warps are done)
+      }
     }
     distill_row(a, r, w, t, x, rank, &s_grad, &s_entry);
   }
@@ -378,6 +382,7 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
     const float p_left = (l.z[i] == e.m ? e.s : sum - x) / sum;
     grad[l.ids[i]] = Vec<T>::narrow1(e.wt == 0.f ? 0.f : e.wt * (pv > 0.5f && q > 0.5f ? q_left - p_left : pv - q));
   }
+  if (tid < 32 && s_grad.ref != s_grad.ref) board.leave();  // its wait may have run out
 }
 
 template <typename T, bool GRAD>
@@ -447,6 +452,7 @@ extern "C" int tail_distill_topk(int32_t rows, int32_t V, int32_t k, const void*
   a.k64 = LOG2E / temperature;
   a.k = static_cast<float>(a.k64);
   a.inv_t = static_cast<float>(1.0 / temperature);
+  a.wait_ns = row_wait_limit();
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = logits_dtype == TAIL_F32   ? launch<float>(a, rows, s)
                         : logits_dtype == TAIL_F16 ? launch<__half>(a, rows, s)

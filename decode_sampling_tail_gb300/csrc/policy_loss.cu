@@ -28,6 +28,7 @@ struct PolicyArgs {
   float k, inv_t;
   float lo, hi, kl, ent;  // 1 - clip_low, 1 + clip_high, the terms' factors
   int kept;  // vectors of a part that shared memory holds
+  uint64_t wait_ns;
 };
 
 // A row's loss and the factors of its gradient.
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) policy_kernel(const _
   if (p.edge_n) st = merge(st, stat_of(edge), a.k);
   // the second pass's first vectors come while the factors are formed
   if (GRAD && !kept) v = Batch::from<NT>(part_vectors(row, p), 0, p.count);
-  st = cluster_stat<ENT, GRAD>(board, st, x.z, a.k, rank, size);
+  st = cluster_stat<ENT, GRAD>(board, st, x.z, a.k, rank, size, a.wait_ns);
   if (threadIdx.x < 32 && (GRAD || rank == 0)) {  // one warp forms the row's factors for all
     const RowGrad g = policy_row<ENT>(a, x, st, first);
     if (GRAD && threadIdx.x == 0) s_grad = g;
@@ -128,6 +129,7 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) policy_kernel(const _
   if (!GRAD) return;
   __syncthreads();
   grad_pass<T, ENT, NT>(s_grad, GradRow<T>{row, grad, p, kept ? cache : nullptr, edge}, v);
+  if (threadIdx.x < 32 && s_grad.ref != s_grad.ref) board.leave();  // its wait may have run out
 }
 
 template <typename T, bool ENT>
@@ -201,6 +203,7 @@ extern "C" int tail_policy_loss(int32_t rows, int32_t V, const void* logits, int
   a.hi = static_cast<float>(1.0 + clip_high);
   a.kl = kl_coef;
   a.ent = entropy_coef;
+  a.wait_ns = row_wait_limit();
   const bool ent = entropy_coef != 0.f || out_entropy_opt;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = logits_dtype == TAIL_F32   ? launch<float>(a, rows, ent, s)

@@ -41,6 +41,7 @@ namespace tail {
 constexpr int ROW_BATCH = 4;            // vectors a thread takes at a time
 constexpr int ROW_MAX_CLUSTER = 8;      // CTAs a row, the portable size
 constexpr int ROW_SMEM = 224 * 1024;    // dynamic shared memory of a CTA at most
+constexpr uint64_t ROW_WAIT_NS = 1000000000ull;  // how long a row's CTAs wait for one another, if not set otherwise
 
 // ---------------------------------------------------------------- arithmetic
 
@@ -382,8 +383,6 @@ __device__ __forceinline__ void store_remote(float4* mine, uint64_t* bar, int ra
                : "memory");
 }
 
-constexpr uint64_t ROW_WAIT_NS = 1000000000ull;
-
 // Where a cluster's CTAs leave W words of four each for one another, by their first warps alone.
 template <int W>
 struct Board {
@@ -407,17 +406,28 @@ struct Board {
         : "memory");
     return ok != 0;
   }
-  __device__ __forceinline__ bool wait() {
+  // (0: one look, since arrived() may itself wait for as long as the device sees fit)
+  __device__ __forceinline__ bool wait(uint64_t ns) {
+    if (ns == 0) {
+      uint32_t ok;
+      asm volatile(
+          "{\n.reg .pred p;\nmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\nselp.u32 %0, 1, 0, p;\n}"
+          : "=r"(ok)
+          : "r"(smem_u32(&bar))
+          : "memory");
+      return ok != 0;
+    }
     if (arrived()) return true;
     const uint64_t since = global_timer_ns();
     while (!arrived())
-      if (global_timer_ns() - since > ROW_WAIT_NS) return false;
+      if (global_timer_ns() - since > ns) return false;
     return true;
   }
   // The first warp: its CTA's words to every CTA (ALL) or to the first, and in return all the CTAs', lane i CTA i's.
-  // False when they have not come in a second.
+  // False when they have not come in wait_ns; then leave() has to end the kernel for this warp.
   template <bool ALL>
-  __device__ __forceinline__ bool exchange(int rank, int size, const float4 (&mine)[W], float4 (&all)[W]) {
+  __device__ __forceinline__ bool exchange(int rank, int size, const float4 (&mine)[W], float4 (&all)[W],
+                                           uint64_t wait_ns) {
     const int lane = threadIdx.x & 31;
     if (lane == 0 && (ALL || rank == 0)) mbar_arrive_expect_tx(smem_u32(&bar), size * W * sizeof(float4));
     if (ALL ? lane < size : lane == 0)
@@ -425,18 +435,30 @@ struct Board {
       for (int w = 0; w < W; ++w) store_remote(&cta[w][rank], &bar, lane, mine[w]);
     __syncwarp();
     if (!ALL && rank != 0) return true;
-    const bool ok = wait();
+    const bool ok = __all_sync(0xffffffffu, wait(wait_ns));
 #pragma unroll
     for (int w = 0; w < W; ++w) all[w] = lane < size ? cta[w][lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    return __all_sync(0xffffffffu, ok);
+    return ok;
+  }
+  // The first warp's last step where its wait has run out, behind every barrier of its CTA: the others may still write to
+  // this CTA's shared memory, which goes when the CTA ends.  It stays until every thread of the cluster has ended or waits
+  // here too, so that all of them have sent what they send, and then until that has come.  (The barrier counts ended threads
+  // as arrived; nobody else waits for it, and every other wait is bounded.)
+  __device__ __forceinline__ void leave() {
+    if (cluster_size() == 1) return;
+    cluster_started();
+    cluster_wait();
+    wait(ROW_WAIT_NS);
   }
 };
 
 // The cluster's statistics in the first warp of every CTA (ALL) or of the first, from each thread's; the same bits in all
-// lanes.  NaN when another CTA's have not come.  Ends without a barrier.  `seen`: what the first warp has read of the
+// lanes.  NaN when another CTA's have not come in wait_ns (ALL: the first warp ends by board.leave()).  Ends without a
+// barrier.  `seen`: what the first warp has read of the
 // row's other parts; it goes with its statistics, so that a CTA that has all of them may write its part in place.
 template <bool ENT, bool ALL>
-__device__ __forceinline__ RowStat cluster_stat(Board<1>& board, RowStat st, float seen, float k, int rank, int size) {
+__device__ __forceinline__ RowStat cluster_stat(Board<1>& board, RowStat st, float seen, float k, int rank, int size,
+                                                uint64_t wait_ns) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   st = warp_merge<ENT>(st, k);
   if (lane == 0) board.warp[0][warp] = make_float4(st.m, st.s, st.u, 0.f);
@@ -451,10 +473,13 @@ __device__ __forceinline__ RowStat cluster_stat(Board<1>& board, RowStat st, flo
   if (size == 1) return st;
   const float4 mine[1] = {make_float4(st.m, st.s, st.u, seen)};
   float4 all[1];
-  const bool ok = board.template exchange<ALL>(rank, size, mine, all);
+  const bool ok = board.template exchange<ALL>(rank, size, mine, all, wait_ns);
   if (!ALL && rank != 0) return st;
   st = warp_merge<ENT>(RowStat{all[0].x, all[0].y, all[0].z}, k);
-  if (!ok) st.m = NAN;
+  if (!ok) {
+    st.m = st.s = st.u = NAN;
+    if (!ALL) board.leave();  // (the other warps are done)
+  }
   return st;
 }
 

@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) score_kernel(const __
   const float z = first ? Vec<T>::widen1(row[t]) : 0.f;
   if (size > 1) cluster_wait();
   const RowStat mine = merge(stat_pass<T, ENT, NT>(row, p, nullptr, v, a.k, NoMask{}), stat_of(edge_of(row, p)), a.k);
-  const RowStat all = cluster_stat<ENT, false>(board, mine, 0.f, a.k, rank, size);
+  const RowStat all = cluster_stat<ENT, false>(board, mine, 0.f, a.k, rank, size, a.wait_ns);
   if (!first) return;
   const float ln = log1pf(all.s);
   const bool empty = all.m == -INFINITY;
@@ -163,7 +163,13 @@ const char* LIMITS = "more than 1048576 columns or 16777216 rows";
 
 }  // namespace
 
-cudaError_t launch_scores(const ScoreArgs& a, int dtype, int rows, cudaStream_t stream) {
+std::atomic<uint64_t> wait_limit{ROW_WAIT_NS};
+
+uint64_t row_wait_limit() { return wait_limit.load(std::memory_order_relaxed); }
+
+cudaError_t launch_scores(const ScoreArgs& args, int dtype, int rows, cudaStream_t stream) {
+  ScoreArgs a = args;
+  a.wait_ns = row_wait_limit();
   return dtype == TAIL_F32   ? scores<float>(a, rows, stream)
          : dtype == TAIL_F16 ? scores<__half>(a, rows, stream)
                              : scores<__nv_bfloat16>(a, rows, stream);
@@ -178,6 +184,11 @@ cudaError_t launch_spread(const SpreadArgs& a, int dtype, int rows, cudaStream_t
 }  // namespace tail
 
 using namespace tail;
+
+extern "C" int tail_training_set_wait_limit(uint64_t ns) {
+  wait_limit.store(ns, std::memory_order_relaxed);
+  return TAIL_OK;
+}
 
 extern "C" int tail_token_logprobs_ex(int32_t rows, int32_t V, const void* logits, int32_t logits_dtype,
                                       int64_t logits_ld, const int32_t* tokens, double temperature,

@@ -34,6 +34,7 @@ struct ScoreArgs {
   float* coef;
   const int32_t* cu;
   int nseq;
+  uint64_t wait_ns;  // (launch_scores')
 };
 cudaError_t launch_scores(const ScoreArgs& a, int dtype, int rows, cudaStream_t stream);
 
@@ -54,6 +55,9 @@ struct SpreadArgs {
   int size;  // CTAs a row (launch_spread's)
 };
 cudaError_t launch_spread(const SpreadArgs& a, int dtype, int rows, cudaStream_t stream);
+
+// How long the CTAs of a row wait for one another's sums, in ns (tail_training_set_wait_limit's).
+uint64_t row_wait_limit();
 
 // ---------------------------------------------------------------- argument checks
 

@@ -37,6 +37,16 @@ def _empty(t, shape, wanted, like):
     return torch.empty(shape, dtype=torch.float32, device=like.device)
 
 
+def set_training_wait_limit(ns: int):
+    """Bounds the waits of later calls' CTAs for one another to ``ns`` nanoseconds (tail_training_set_wait_limit; 1e9 at
+    first)."""
+    if not 0 <= ns < 1 << 64:
+        raise ValueError(f"ns must be 0 to 2^64 - 1, not {ns}")
+    rc = lib().tail_training_set_wait_limit(ns)
+    if rc != TAIL_OK:
+        fail(rc, "tail_training_set_wait_limit")
+
+
 def token_logprobs(logits, tokens, temperature=1.0, *, entropy=False, out_logprob=None, out_lse=None,
                    out_entropy=None, out_stats=None, stream=None):
     """Log-probabilities of ``tokens`` under softmax(logits / temperature) (tail_token_logprobs_ex).

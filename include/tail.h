@@ -615,8 +615,14 @@ const char* tail_last_error(void);
  * within 2^-17 of themselves up to 2^18 columns, 2^-16 up to 2^20.  Results are deterministic and
  * a row's do not depend on the others', except by the order of sums, which follows rows, V and the dtype.  No handle
  * and no allocation; asynchronous on `stream` of the current device; everything is read in stream order.  The CTAs of a
- * row wait for one another's sums for a second at most; should they not come, that row's results are NaN.
+ * row wait for one another's sums for a second at most (a GPU taken from the process for longer, say).  A CTA whose wait has
+ * run out writes NaN: that row's results, parts of its gradient, or both; the launch ends, and the call's results are to be
+ * thrown away.
  */
+
+/* Bounds those waits in later calls, of all threads, to `ns` nanoseconds of GPU global time (1e9 at first; 0: they look
+   once). */
+int tail_training_set_wait_limit(uint64_t ns);
 
 /*
  * l_r(token), lse_r = log sum_v exp(z_rv / T) and H_r of every row, each [rows] fp32 or NULL (not all three).

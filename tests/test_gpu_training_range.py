@@ -252,3 +252,37 @@ def test_small_terms_reach_a_sum_that_began_large(dt):
     tc.near(_np(H), np.full(rows, entropy), tol + 51 * 2.0 ** -24, "H")
 
 
+# ------------------------------------------------------------------ waits that run out
+
+@pytest.mark.parametrize("grad", [True, False])
+def test_rows_whose_wait_runs_out_are_nan(grad):
+    rng = np.random.default_rng(1)
+    rows, V = 5, 60000  # a cluster a row
+    z = _logits(rng, rows, V, "bf16")
+    vals, idx, rs = _lists(rng, z, 20, "f32", True, 1.0)
+    zt, t = _dev(z, DT["bf16"]), _dev(np.array([7, -1, V - 1, 30, 9], np.int32))
+    old, adv = torch.full((rows,), -9.0, device=DEV), torch.ones(rows, device=DEV)
+    cu = torch.tensor([0, 2, rows], dtype=torch.int32, device=DEV)
+    v, i, r = _dev(vals), _dev(idx), _dev(rs)
+
+    def calls():
+        out = [*dst.token_logprobs(zt, t, entropy=True), *dst.policy_loss(zt, t, old, adv, grad=grad),
+               *dst.preference_loss(zt, t, cu, grad=grad), *dst.distill_topk(zt, v, i, teacher_rest=r, grad=grad)]
+        return [x for x in out if x is not None]
+
+    want, late = calls(), 0
+    try:
+        dst.set_training_wait_limit(0)
+        got = [calls() for _ in range(100)]
+        torch.cuda.synchronize()  # every launch has ended
+    finally:
+        dst.set_training_wait_limit(1_000_000_000)
+    for one in got:
+        for x, y in zip(one, want):
+            assert ((x == y) | torch.isnan(x)).all()
+            late += int(torch.isnan(x).any())
+        assert one[0][1].item() == 0  # an ignored row waits for nobody
+    assert late  # (about three outputs of four)
+    assert all(torch.equal(x, y) for x, y in zip(calls(), want))
+
+

@@ -249,3 +249,9 @@ def test_statistics_refusals(L):
         {**dict(T=1.0, lse=None, s=S, a=P), **k})
     for bad in (dict(s=None), dict(s=S + 1), dict(s=G - 28), dict(a=None), dict(T=0.0), dict(lse=P + 2)):
         assert grad(**bad) == dst.TAIL_ERR_INVALID_ARG
+
+
+def test_wait_limit(L):
+    for ns in (-1, 1 << 64):
+        with pytest.raises(ValueError):
+            dst.set_training_wait_limit(ns)
