@@ -370,14 +370,10 @@ __global__ void __launch_bounds__(NT, ROW_SM_THREADS / NT) distill_kernel(const 
   const EntryGrad e = s_entry;
   for (int i = tid; i < n; i += NT) {
     if (!owner(i)) continue;
-    float q = weight(i), q_left = 1.f - q;
-    if (twice) {
+    float q = weight(i), q_left = q > 0.5f && !t.rest_is_max ? t.others * t.inv : 1.f - q;  // above one half: the largest
+    if (twice)
       for (int j = i + 1; j < n; ++j)
-        if (l.ids[j] == l.ids[i]) q += weight(j);
-      q_left = 1.f - q;
-    } else if (q > 0.5f && !t.rest_is_max) {
-      q_left = t.others * t.inv;  // above one half: the largest
-    }
+        if (l.ids[j] == l.ids[i]) q += weight(j), q_left = 1.f - q;
     const float x = ex2((l.z[i] - e.m) * a.k), sum = 1.f + e.s, pv = x / sum;
     const float p_left = (l.z[i] == e.m ? e.s : sum - x) / sum;
     grad[l.ids[i]] = Vec<T>::narrow1(e.wt == 0.f ? 0.f : e.wt * (pv > 0.5f && q > 0.5f ? q_left - p_left : pv - q));

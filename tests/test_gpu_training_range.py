@@ -286,3 +286,30 @@ def test_rows_whose_wait_runs_out_are_nan(grad):
     assert all(torch.equal(x, y) for x, y in zip(calls(), want))
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [300, 60000])
+@pytest.mark.parametrize("twice", ["others", "likely", "both"])
+@pytest.mark.parametrize("with_rest", [False, True])
+def test_distill_of_likely_tokens_from_lists_with_an_id_twice(V, dt, twice, with_rest):
+    # student and teacher both sure of one token: the gradient there is a difference of 1 - q and 1 - p, down to 1e-9
+    rng = np.random.default_rng(V)
+    rows, k = 10, 40
+    z = rng.standard_normal((rows, V)).astype(np.float32)
+    idx = np.stack([rng.permutation(V)[:k] for _ in range(rows)]).astype(np.int32)
+    vals = rng.standard_normal((rows, k)).astype(np.float32)
+    z[np.arange(rows), idx[:, 5]] = math.log(V) + np.linspace(0.0, 21.0, rows)
+    vals[:, 5] = math.log(k) + np.linspace(1.0, 21.0, rows)
+    if twice != "likely":
+        idx[:, 9] = idx[:, 30]
+    if twice != "others":
+        idx[:, 17], vals[:, 17] = idx[:, 5], vals[:, 5] - 0.5
+    rest = np.linspace(1.0, -3.0, rows).astype(np.float32) if with_rest else None
+    z = _np(_dev(z, DT[dt])).astype(np.float32)
+    loss, g = (_np(x) for x in dst.distill_topk(_dev(z, DT[dt]), _dev(vals), _dev(idx),
+                                                teacher_rest=_dev(rest) if with_rest else None))
+    for r in range(rows):
+        v, tol = tc.distill(z[r], vals[r], idx[r], float(rest[r]) if with_rest else None, 1.0, 1.0, dt)
+        tc.near(loss[r], v[0], tol[0], f"loss of row {r}")
+        tc.near(g[r], v[1], tol[1], f"gradient of row {r}")
+
+
