@@ -128,6 +128,42 @@ def test_distill_at_extreme_temperatures(T, dt, above):
         tc.near(_np(g)[r], grad, tol + tc.EPS[dt] * np.abs(grad) * (1 + 2.0 ** -10) + _lost(T), f"gradient of row {r}")
 
 
+@pytest.mark.parametrize("T", EXTREME)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("ent,kl", [(0.0, 0.0), (0.01, 0.05)])
+def test_policy_at_extreme_temperatures(T, dt, ent, kl):
+    rng, z, t = _extreme(dt)
+    l = np.array([tc.logprob(z[r], t[r], T)[0][0] for r in range(4)])
+    old, ref = (l - 0.1).astype(np.float32), (l + 0.3).astype(np.float32)
+    adv = np.array([1.0, -1.0, 0.5, -2.0], np.float32)
+    H = torch.empty(4, device=DEV)
+    loss, lp, g = dst.policy_loss(_dev(z, DT[dt]), _dev(t), _dev(old), _dev(adv), ref_logprob=_dev(ref), temperature=T,
+                                  kl_coef=kl, entropy_coef=ent, out_entropy=H)
+    c = f32(0.2)
+    for r in range(4):
+        v, tol = tc.policy(z[r], t[r], T, float(old[r]), float(adv[r]), float(ref[r]), c, c, f32(kl), f32(ent), 1.0, dt)
+        for name, a, b, e in zip(("loss", "l", "H", "gradient"), (loss, lp, H, g), v, tol):
+            # (terms below 2^-126 count as 0)
+            low = _lost(T, 4.0) if name == "gradient" else 2.0 ** -100
+            tc.near(_np(a)[r], b, e + low, f"{name} of row {r}")
+
+
+@pytest.mark.parametrize("T", EXTREME)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("average", [False, True])
+def test_preference_at_extreme_temperatures(T, dt, average):
+    rng, z, t = _extreme(dt)
+    cu = np.array([0, 1, 4], np.int32)
+    L = [tc.logprob(z[r], t[r], T)[0][0] for r in range(4)]
+    ref = np.array([L[0] + 1, sum(L[1:]) / (3 if average else 1)], np.float32)
+    loss, seq, g = dst.preference_loss(_dev(z, DT[dt]), _dev(t), _dev(cu), ref_logprob=_dev(ref), beta=0.5,
+                                       average=average, temperature=T)
+    (wl, wL, wg), (tl, tL, tg) = tc.preference(z, t, cu, T, ref, 0.5, 0.0, 0.0, average, None, dt)
+    tc.near(_np(loss), wl, tl, "loss")
+    tc.near(_np(seq), wL, tL + 4 * z.shape[1] * 2.0 ** -126, "L")  # (terms below 2^-126 count as 0)
+    tc.near(_np(g), wg, tg + _lost(T), "gradient")
+
+
 @pytest.mark.parametrize("V", [300, 60000])
 @pytest.mark.parametrize("rest", [False, True])
 def test_distill_keeps_nan_of_a_list(V, rest):
