@@ -3,7 +3,9 @@
 ``token_logprobs`` scores given tokens (a rollout's old and reference log-probabilities), ``token_logprobs_grad``
 gives the gradient of any loss formed of them; ``policy_loss``, ``preference_loss`` and ``distill_topk`` form a
 loss and its gradient in one call.  ``include/tail.h`` states the formulas.  A gradient is handed on with
-``logits.backward(grad)``, or written over the logits themselves (``out_grad=logits``).
+``logits.backward(grad)``, or written over the logits themselves (``out_grad=logits``).  Outputs that the caller gives are
+written through their pointers: autograd's version counters do not see it, so logits that some function has saved for its
+backward pass must not be written over.
 
 The tensors are checked here (type, shape, device, strides; ValueError); the library checks sizes, factors
 and overlaps.  Calls are asynchronous on ``stream`` (None: the current stream of the tensors' device).
@@ -87,15 +89,16 @@ def token_logprobs_grad(logits, tokens, lse, d_logprob, temperature=1.0, *, d_en
     index = cuda_index(logits, "logits")
     rows = logits.shape[0]
     l, code, V, ld = need_matrix(logits, "logits", rows, index)
+    if lse is None and stats is None:
+        raise ValueError("lse or stats must be given")
     if out_grad is None:
         with allocating_on(stream, index):
             out_grad = torch.empty((rows, V), dtype=logits.dtype, device=logits.device)
     g, gld = _grad(out_grad, logits, rows, V, index)
     n = (rows,)
     args = (rows, V, l, code, ld, need(tokens, "tokens", torch.int32, n, index), temperature,
-            need(lse, "lse", f32, n, index) if stats is None else need_opt(lse, "lse", f32, n, index),
-            need_opt(stats, "stats", f32, (rows, 2), index), need(d_logprob, "d_logprob", f32, n, index),
-            need_opt(d_entropy, "d_entropy", f32, n, index), need_opt(entropy, "entropy", f32, n, index), g, gld,
+            need_opt(lse, "lse", f32, n, index), need_opt(stats, "stats", f32, (rows, 2), index),
+            need(d_logprob, "d_logprob", f32, n, index), need_opt(d_entropy, "d_entropy", f32, n, index), need_opt(entropy, "entropy", f32, n, index), g, gld,
             raw_stream(stream, index))
     call("tail_token_logprobs_grad_ex", args, index)
     return out_grad

@@ -241,8 +241,9 @@ def test_gradient_from_the_statistics(V, dt, T, with_entropy):
     nan = torch.full((rows,), math.nan, device=DEV)
     assert torch.equal(dst.token_logprobs_grad(zt, _dev(t), nan, _dev(a), T, stats=stats, **more), g)
     assert torch.equal(dst.token_logprobs_grad(zt, _dev(t), None, _dev(a), T, stats=stats, out_grad=zt, **more), g)
-    with pytest.raises(ValueError):
-        dst.token_logprobs_grad(zt, _dev(t), None, _dev(a), T, stats=stats[:, 0])
+    for bad in (stats[:, 0], None):
+        with pytest.raises(ValueError):
+            dst.token_logprobs_grad(zt, _dev(t), None, _dev(a), T, stats=bad)
     with pytest.raises(dst.TailError):
         dst.token_logprobs(zt, _dev(t), T, out_logprob=stats.view(-1)[:rows], out_stats=stats)
 
