@@ -6,8 +6,10 @@
 // the likeliest.  One warp forms the factors; formed by every thread they cost 1.5 instructions a column.
 //
 // Measured (GB300, by graph replay): 12 rows of 201088 in fp32 7.5 us (floor 2.9: the chain of one CTA: first loads 1.6,
-// statistics 1.5, exchange and factors 1.5, gradient 1.9); 333 rows of 50021 in fp16, a fifth ignored, 16.5 (9.0: all
-// CTAs run at once, in step); 2048 rows of 201088 in bf16 253 (234).
+// statistics 1.5, exchange and factors 1.5, gradient 1.9); 333 rows of 50021 in fp16 with the entropy term, a fifth ignored,
+// 16.6 (9.0: 533 counted parts in 608 places, so that reads, chain and writes follow one another in each, and half of the
+// time goes to issuing 14,300 instructions a scheduler); 2048 rows of 201088 in bf16 254 (234).  The loss alone: 5.4 (1.4),
+// 8.9 (4.0) and 118 (111).
 #include "../../include/tail.h"
 #include "row_softmax.cuh"
 #include "training.h"

@@ -7,7 +7,7 @@
 // which are still in L2.
 //
 // Measured (GB300, by graph replay): one pair, 26 rows of 32000 in fp16, 9.9 us (floor 0.4: three launches in a chain);
-// 8 pairs, 1300 rows of 201088 in bf16, 215 (134 for one pass of reads; 217 for two from HBM).
+// 8 pairs, 1300 rows of 201088 in bf16, 216 (134 for one pass of reads; 217 for two from HBM).
 #include "../../include/tail.h"
 #include "row_softmax.cuh"
 #include "training.h"

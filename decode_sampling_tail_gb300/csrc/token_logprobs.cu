@@ -10,9 +10,9 @@
 //   -expm1(log p).
 //
 // Both are bound by memory.  Measured (GB300, by graph replay): 4 rows of 201088 in fp32, scored with their entropies,
-// 3.3 us (floor 0.5: one CTA's chain of launch, first load, six batches, exchange); 1536 rows of 201088 in bf16, a tenth
-// ignored, 85 (83; 91 with each batch loaded behind the one before it); the gradient of 777 rows of 50021 in bf16
-// 25.9 (22.7; 30 without the prefetch of a part, 28 with a cluster barrier before it).
+// 3.4 us (floor 0.5: one CTA's chain of launch, first load, six batches, exchange); 1536 rows of 201088 in bf16, a tenth
+// ignored, 87 (83; 91 with each batch loaded behind the one before it); the gradient of 777 rows of 50021 in bf16
+// 25.1 (22.7; 30 without the prefetch of a part, 28 with a cluster barrier before it).
 #include "../../include/tail.h"
 #include "row_softmax.cuh"
 #include "training.h"
