@@ -83,7 +83,8 @@ def token_logprobs_grad(logits, tokens, lse, d_logprob, temperature=1.0, *, d_en
     lse, entropy and stats as ``token_logprobs`` gave them, d_logprob and d_entropy [rows] float32 (d_entropy goes with
     entropy).  With ``stats`` lse is not read (None will do) and the gradient is exact to about 2^-16 of itself.  Without it
     every probability is off by lse's rounding, up to 2^-24 |lse| of itself: a token whose 1 - p is near that or below
-    loses its gradient, and temperatures that make |logits| / temperature large lose the others'.  Returns out_grad, [rows, V] of the logits' type, allocated when not given (may be the logits)."""
+    loses its gradient, and temperatures that make |logits| / temperature large lose the others'.  Returns out_grad,
+    [rows, V] of the logits' type, allocated when not given (may be the logits)."""
     import torch
     f32 = torch.float32
     index = cuda_index(logits, "logits")
@@ -98,8 +99,8 @@ def token_logprobs_grad(logits, tokens, lse, d_logprob, temperature=1.0, *, d_en
     n = (rows,)
     args = (rows, V, l, code, ld, need(tokens, "tokens", torch.int32, n, index), temperature,
             need_opt(lse, "lse", f32, n, index), need_opt(stats, "stats", f32, (rows, 2), index),
-            need(d_logprob, "d_logprob", f32, n, index), need_opt(d_entropy, "d_entropy", f32, n, index), need_opt(entropy, "entropy", f32, n, index), g, gld,
-            raw_stream(stream, index))
+            need(d_logprob, "d_logprob", f32, n, index), need_opt(d_entropy, "d_entropy", f32, n, index),
+            need_opt(entropy, "entropy", f32, n, index), g, gld, raw_stream(stream, index))
     call("tail_token_logprobs_grad_ex", args, index)
     return out_grad
 

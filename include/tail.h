@@ -606,18 +606,20 @@ const char* tail_last_error(void);
  *                  once.  NULL: the loss alone.  It may be the logits themselves (same pointer and
  *                  leading dimension); other overlaps are refused.
  * Outputs must not overlap inputs otherwise, nor one another (TAIL_ERR_INVALID_ARG).  A logit of -inf has
- * probability 0, and gradient 0 unless it is the token's.  A row without a logit above -inf has no distribution: log-probability
- * and lse -inf, entropy 0; the losses leave it out like an ignored row.  NaN makes its own row's (or pair's) results NaN, and +inf is
- * outside the domain; other rows do not change.  What a formula makes infinite is infinite (the
- * log-probability of a token of probability 0); the gradient of a row whose factor is infinite holds infinities and NaN.
+ * probability 0, and gradient 0 unless it is the token's.  A row without a logit above -inf has no distribution:
+ * log-probability and lse -inf, entropy 0; the losses leave it out like an ignored row.  NaN makes its own row's (or
+ * pair's) results NaN, and +inf is outside the domain; other rows do not change.  What a formula makes infinite is
+ * infinite (the log-probability of a token of probability 0); the gradient of a row whose factor is infinite holds
+ * infinities and NaN.
  * Sums are fp32, one instance of a row's maximum apart from the others, so that the log-probability of a
- * likely token and its distance 1 - p keep about 2^-20 of themselves as measured; counted by their roundings the sums are
- * within 2^-17 of themselves up to 2^18 columns, 2^-16 up to 2^20.  Results are deterministic and
- * a row's do not depend on the others', except by the order of sums, which follows rows, V, the dtype, the row's address
- * modulo 16 and, for the policy and the distillation loss, whether a gradient is asked for.  No handle and no allocation; asynchronous on `stream` of the current device; everything is read in stream order.  The CTAs of a
- * row wait for one another's sums for a second at most (a GPU taken from the process for longer, say).  A CTA whose wait has
- * run out writes NaN: that row's results, parts of its gradient, or both; the launch ends, and the call's results are to be
- * thrown away.
+ * likely token and its distance 1 - p keep about 2^-20 of themselves as measured; counted by their roundings the
+ * sums are within 2^-17 of themselves up to 2^18 columns, 2^-16 up to 2^20.
+ * Results are deterministic and a row's do not depend on the others', except by the order of sums, which follows rows,
+ * V, the dtype, the row's address modulo 16 and, for the policy and the distillation loss, whether a gradient is asked
+ * for.  No handle and no allocation; asynchronous on `stream` of the current device; everything is read in stream order.
+ * The CTAs of a row wait for one another's sums for a second at most (a GPU taken from the process for longer, say).  A
+ * CTA whose wait has run out writes NaN: that row's results, parts of its gradient, or both; the launch ends, and the
+ * call's results are to be thrown away.
  */
 
 /* Bounds those waits in later calls, of all threads, to `ns` nanoseconds of GPU global time (1e9 at first; 0: they look
